@@ -123,7 +123,8 @@ typedef struct {
 #define FORGE_ERR_HYPER (-6)       /* step < 1, unknown optimizer, non-finite or out-of-range hyper-parameter */
 #define FORGE_ERR_HIP (-7)         /* kernel launch failed (HIP error) */
 #define FORGE_ERR_ALIAS (-8)       /* output tensors overlap each other or an input */
-#define FORGE_ERR_SCRATCH (-9)     /* forge_linear_wgrad_unfused_noalloc: out*in > 2^24 (its scratch) */
+#define FORGE_ERR_SCRATCH (-9)     /* forge_linear_wgrad_unfused_noalloc: out*in > 2^24 (its scratch); a workspace
+                                      smaller than the call needs */
 
 /*
  * Dynamic 8-bit moment code (FORGE_I8_DYN / FORGE_U8_DYN; §2 "Precision and
@@ -261,6 +262,130 @@ int forge_linear_wgrad_unfused(const forge_tensor* X, const forge_tensor* dY, fo
 int forge_linear_wgrad_unfused_noalloc(const forge_tensor* X, const forge_tensor* dY, forge_tensor* W,
                                        forge_tensor* m, forge_tensor* v, int32_t opt, const forge_hyper* hyper,
                                        int64_t step, uint64_t seed, forge_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the fused step: the linear layer's forward product with an
+ * epilogue, the gated feed-forward block and the softmax cross entropy of a linear
+ * head, each with its gradient. They are no part of the pages' method; they are what a
+ * training step runs before and after it.
+ *   - Operands are all FORGE_F32 or all FORGE_BF16 (FP8 returns FORGE_ERR_UNSUPPORTED);
+ *     every sum is taken in FP32, bfloat16 results are rounded to nearest-even once.
+ *   - The conventions at the top of this file hold: row pitches, 16-byte alignment,
+ *     columns in multiples of 8 (bf16) or 4 (fp32), fewer than 2^31 bytes per tensor, no
+ *     allocation, no synchronisation, checks before anything is enqueued, outputs that
+ *     overlap nothing else the call uses (FORGE_ERR_ALIAS), fixed summation order.
+ *   - Any number of rows from 0 on. A workspace is caller-owned device memory, 16-byte
+ *     aligned; calls that may overlap in time need one each.
+ * ---------------------------------------------------------------------------
+ */
+typedef enum {
+  FORGE_ACT_NONE = 0,
+  FORGE_ACT_RELU = 1,
+  FORGE_ACT_SILU = 2,      /* z / (1 + e^-z) */
+  FORGE_ACT_GELU = 3,      /* z Phi(z), Phi the normal distribution function */
+  FORGE_ACT_GELU_TANH = 4  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+} forge_act;
+
+/*
+ * Y = act(X W^T + bias) + R. X [T, in], W [out, in], Y and R [T, out]; bias [1, out] in
+ * the operands' type or FORGE_F32, or NULL; R (the residual) or NULL. Z [T, out], if not
+ * NULL, receives the pre-activation X W^T + bias for forge_linear_act_backward.
+ * An unknown act is FORGE_ERR_UNSUPPORTED.
+ */
+int forge_linear_forward(const forge_tensor* X, const forge_tensor* W, const forge_tensor* bias, int32_t act,
+                         const forge_tensor* R, forge_tensor* Y, forge_tensor* Z, forge_stream_t stream);
+
+/*
+ * Backward of that epilogue: dZ = dY act'(Z), dbias[o] = sum over the tokens of dZ[., o]
+ * (float32, from the unrounded products). Then dX = dZ W (forge_linear_dgrad) and the
+ * fused step on (X, dZ); the residual's gradient is dY itself. With FORGE_ACT_NONE Z may
+ * be NULL and dZ may be NULL (dZ = dY). dbias: out contiguous floats, or NULL if not
+ * wanted. Workspace: forge_linear_act_backward_workspace(T, out) bytes (0 if dbias is
+ * NULL), else FORGE_ERR_SCRATCH.
+ */
+int64_t forge_linear_act_backward_workspace(int64_t T, int64_t out);
+int forge_linear_act_backward(const forge_tensor* dY, const forge_tensor* Z, int32_t act, forge_tensor* dZ,
+                              float* dbias, void* workspace, int64_t workspace_bytes, forge_stream_t stream);
+
+/*
+ * Gated block, H = act(X Wg^T) * (X Wu^T): both products, the activation and the product
+ * in one pass. X [T, in], Wg and Wu [hid, in], H [T, hid]. G = X Wg^T and U = X Wu^T
+ * [T, hid] are written too if both are given (FORGE_ERR_NULL for only one): the backward
+ * pass reads them.
+ */
+int forge_gated_forward(const forge_tensor* X, const forge_tensor* Wg, const forge_tensor* Wu, int32_t act,
+                        forge_tensor* H, forge_tensor* G, forge_tensor* U, forge_stream_t stream);
+
+/*
+ * Backward of the gated product: dG = dH * U * act'(G), dU = dH * act(G), all [T, hid],
+ * and, if H is not NULL, H = act(G) * U again (the input of the next layer's weight
+ * gradient, so the forward pass need not keep it).
+ * forge_gated_backward takes dH; forge_gated_dgrad takes the gradient dY [T, out] of the
+ * linear layer behind the block and its weights Wd [out, hid]: dH = dY Wd is formed tile
+ * by tile in registers (on the old Wd, so before its update) and never stored.
+ * Afterwards dX = dG Wg + dU Wu (forge_linear_dgrad_group) and the fused steps of Wg and
+ * Wu (forge_linear_wgrad_step_group on dG, dU).
+ */
+int forge_gated_backward(const forge_tensor* dH, const forge_tensor* G, const forge_tensor* U, int32_t act,
+                         forge_tensor* dG, forge_tensor* dU, forge_tensor* H, forge_stream_t stream);
+int forge_gated_dgrad(const forge_tensor* dY, const forge_tensor* Wd, const forge_tensor* G, const forge_tensor* U,
+                      int32_t act, forge_tensor* dG, forge_tensor* dU, forge_tensor* H, forge_stream_t stream);
+
+/*
+ * dX = sum over l of dY[l] W[l]: the input gradient of the layers that read the same X
+ * (gate and up; q, k, v), in one accumulation, rounded once. dY[l] [T, out_l],
+ * W[l] [out_l, in], dX [T, in], 1 <= n_layers <= FORGE_MAX_GROUP. Before the layers'
+ * fused steps, as forge_linear_dgrad.
+ */
+int forge_linear_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, forge_tensor* dX,
+                             forge_stream_t stream);
+
+/*
+ * Softmax cross entropy of a linear head, without storing the logits z = X W^T:
+ *   lse[t] = log sum_v exp(z[t, v]),  loss[t] = lse[t] - z[t, target[t]].
+ * X [T, in], W [vocab, in] (vocab: any number from 1 on; W may exceed 2^31 bytes), target: T int64 in
+ * [0, vocab), or `ignore` for tokens that do not count (loss 0, no gradient). Any other
+ * target makes that token's loss and gradients NaN. loss (or NULL) and lse: T floats;
+ * total: 3 floats, {sum of the losses, tokens counted, their mean (NaN for none)}.
+ * Workspace: forge_linear_xent_workspace(T, in, vocab, dtype, 0, 0) bytes, else
+ * FORGE_ERR_SCRATCH.
+ */
+int64_t forge_linear_xent_workspace(int64_t T, int64_t in, int64_t vocab, int32_t dtype, int32_t backward,
+                                    int64_t piece);
+int forge_linear_xent_forward(const forge_tensor* X, const forge_tensor* W, const int64_t* target, int64_t ignore,
+                              float* loss, float* lse, float* total, void* workspace, int64_t workspace_bytes,
+                              forge_stream_t stream);
+
+/*
+ * Its gradients. With g[t] the gradient of the objective by loss[t] - dloss[0], or
+ * dloss[t] if per_token, divided by total[1] if total is given (a mean) -
+ *   dz[t, v] = (exp(z[t, v] - lse[t]) - [v = target[t]]) g[t],  dX = dz W,  dW = dz^T X,
+ * in pieces of the vocabulary: a piece's logits are formed again, its dz [T, piece] goes
+ * to the workspace in the operands' type, and its part of dX and its rows of dW follow.
+ * dX [T, in] and dW [vocab, in] in the operands' type, either may be NULL. A common g is
+ * applied in FP32 to the finished sums. `piece`: vocabulary entries per piece, a multiple
+ * of 8 (0: chosen by the library, about 1 GiB of dz); workspace:
+ * forge_linear_xent_workspace(T, in, vocab, dtype, 1, piece) bytes. lse and total are
+ * forge_linear_xent_forward's.
+ */
+int forge_linear_xent_backward(const forge_tensor* X, const forge_tensor* W, const int64_t* target, int64_t ignore,
+                               const float* lse, const float* dloss, int32_t per_token, const float* total,
+                               forge_tensor* dX, forge_tensor* dW, int64_t piece, void* workspace,
+                               int64_t workspace_bytes, forge_stream_t stream);
+
+/*
+ * The same with the head's optimizer step in the place of dW: each piece's rows of W take
+ * the fused step of forge_linear_wgrad_step (dW never stored) as soon as their part of dX
+ * is done, so dX is of the old W. opt, hyper, step, seed, m and v as there (with the same
+ * element indices and random streams as a step of the whole W); g is applied to dz before
+ * its rounding. dX may be NULL. W, m and v span less than 2^31 bytes each here.
+ */
+int forge_linear_xent_step(const forge_tensor* X, forge_tensor* W, forge_tensor* m, forge_tensor* v, int32_t opt,
+                           const forge_hyper* hyper, int64_t step, uint64_t seed, const int64_t* target,
+                           int64_t ignore, const float* lse, const float* dloss, int32_t per_token,
+                           const float* total, forge_tensor* dX, int64_t piece, void* workspace,
+                           int64_t workspace_bytes, forge_stream_t stream);
 
 /* Host-only helpers (no GPU work). */
 

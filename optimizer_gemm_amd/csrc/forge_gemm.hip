@@ -28,8 +28,10 @@ FORGE_EXTERN_F8_ALL(1)
 
 hipError_t launch_wgrad_fused_bf16(int state_fmt, int opt, int sr, const void* X, const void* dY, const GemmDims& d,
                                    const OptArgs& a, hipStream_t st) {
+  // a dY row may be wider than its columns by up to 7 elements of padding (a piece of a
+  // vocabulary): the last row's 16-byte chunk that holds the last columns counts as a whole
   GArgs g{X, dY, d.ldx, d.lddy,
-          d.in, d.out, d.T, nullptr, 0, extent(d.T, d.in, d.ldx, 2), extent(d.T, d.out, d.lddy, 2), 0};
+          d.in, d.out, d.T, nullptr, 0, extent(d.T, d.in, d.ldx, 2), extent(d.T, (d.out + 7) / 8 * 8, d.lddy, 2), 0};
   switch (opt) {
     case FORGE_ADAMW: return wgrad_fused_bf16_opt<FORGE_ADAMW>(state_fmt, sr, g, a, st);
     case FORGE_SGD: return wgrad_fused_bf16_opt<FORGE_SGD>(state_fmt, sr, g, a, st);

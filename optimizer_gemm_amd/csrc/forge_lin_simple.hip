@@ -1,0 +1,240 @@
+// Products with an epilogue, general form: 64x64 tiles, float32 or bfloat16 operands,
+// either index of either operand fast. One kernel covers every operator of forge_ops.h.
+//
+// A workgroup of 4 waves (2 x 2 of 32x32) stages BK = 32 k of both operands in LDS as rows
+// of k (operands whose k is slow are transposed on the way in), and multiplies them with
+// v_mfma_f32_32x32x16_bf16 or v_mfma_f32_32x32x2_f32, FP32 accumulators in both cases. The
+// next stage's global loads are in flight (in registers) during the current stage's
+// products. The finished tile goes through LDS as float rows of the output, so that the
+// epilogue reads and writes whole row segments.
+// Bound: LDS staging (each operand element is read from LDS for 32 rows of the other), so
+// this form serves the float32 operands and the products too small for larger tiles.
+#include "forge_gemm_kernel.h"
+#include "forge_ops.h"
+
+namespace forge {
+namespace {
+
+constexpr int S_B = 64, S_BK = 32, S_NT = 256;
+// workgroups of a launch at most (each walks several tiles beyond that): a grid holds fewer
+// than 2^32 threads
+constexpr int64_t kSimpleGrid = 1 << 20;
+
+template <class T>
+struct SimpleTraits;
+template <>
+struct SimpleTraits<uint16_t> {
+  static constexpr int VE = 8, PAD = 8;
+};
+template <>
+struct SimpleTraits<float> {
+  static constexpr int VE = 4, PAD = 4;
+};
+
+// 16 bytes of an operand: KS: its rows are k (row k0 + r, columns c..), else its rows are
+// the output index (row r, k = k0 + c ..). Zero outside.
+template <class T>
+__device__ __forceinline__ u32x4 load16(const T* base, int64_t ld, int row, int rows, int col, int cols) {
+  u32x4 z{0u, 0u, 0u, 0u};
+  if (row < rows && col < cols) z = *reinterpret_cast<const u32x4*>(base + (int64_t)row * ld + col);
+  return z;
+}
+
+// One operand's stage: 64 output indexes x 32 k, as rows of k of pitch S_BK + PAD.
+template <class T, bool TR>
+struct Stage {
+  static constexpr int VE = SimpleTraits<T>::VE, LD = S_BK + SimpleTraits<T>::PAD;
+  static constexpr int CH = S_B * S_BK / VE / S_NT;  // 16-byte chunks per thread
+  u32x4 r[CH];
+  // r0: first output index of the tile, R: how many there are
+  __device__ __forceinline__ void load(const T* p, int64_t ld, int r0, int R, int k0, int K, int tid) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = tid + j * S_NT;
+      if constexpr (TR) {
+        const int kr = c / (S_B / VE), col = (c % (S_B / VE)) * VE;
+        // a chunk may reach past R inside its row's pitch (R need not be a multiple of VE
+        // where the row is padded); those elements feed outputs that are never stored
+        r[j] = load16(p, ld, k0 + kr, K, r0 + col, R);
+      } else {
+        const int row = c / (S_BK / VE), kc = (c % (S_BK / VE)) * VE;
+        r[j] = load16(p, ld, r0 + row, R, k0 + kc, K);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* s, int tid) const {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = tid + j * S_NT;
+      if constexpr (TR) {
+        const int kr = c / (S_B / VE), col = (c % (S_B / VE)) * VE;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+          for (int i = 0; i < VE; ++i) s[(col + i) * LD + kr] = (T)(r[j][i / 2] >> (16 * (i & 1)));
+        } else {
+#pragma unroll
+          for (int i = 0; i < VE; ++i) s[(col + i) * LD + kr] = bits_f32(r[j][i]);
+        }
+      } else {
+        const int row = c / (S_BK / VE), kc = (c % (S_BK / VE)) * VE;
+        *reinterpret_cast<u32x4*>(s + row * LD + kc) = r[j];
+      }
+    }
+  }
+};
+
+template <class T>
+__device__ __forceinline__ void mma32(f32x16& acc, const T* as, const T* bs, int row_a, int row_b, int hi) {
+  constexpr int LD = S_BK + SimpleTraits<T>::PAD;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int k = 0; k < S_BK; k += 16) {
+      const bf16x8 a = *reinterpret_cast<const bf16x8*>(as + row_a * LD + k + 8 * hi);
+      const bf16x8 b = *reinterpret_cast<const bf16x8*>(bs + row_b * LD + k + 8 * hi);
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < S_BK; k += 2)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(as[row_a * LD + k + hi], bs[row_b * LD + k + hi], acc, 0, 0, 0);
+  }
+}
+
+template <class T, int EPI, bool TA, bool TB>
+__global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
+  constexpr bool TWO = EPI == L_GATED;
+  constexpr int LD = S_BK + SimpleTraits<T>::PAD, LDE = S_B + 4;
+  constexpr int OP = S_B * LD * (int)sizeof(T);
+  constexpr int EB = (TWO ? 2 : 1) * S_B * LDE * 4, OB = (TWO ? 3 : 2) * OP;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[EB > OB ? EB : OB];
+  T* as = reinterpret_cast<T*>(smem);
+  T* bs = reinterpret_cast<T*>(smem + OP);
+  T* as2 = reinterpret_cast<T*>(smem + (TWO ? 2 * OP : 0));
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, hi = lane >> 5;
+  const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
+  const float sc = (EPI == L_ACC || EPI == L_DLOGIT) ? epi_scale(g.e) : 1.f;
+
+  const int tiles_m = (epi_width<EPI>(g.M) - g.m_off + S_B - 1) / S_B, tiles_n = (g.N - g.n_off + S_B - 1) / S_B;
+  for (int64_t tile = blockIdx.x; tile < (int64_t)tiles_m * tiles_n; tile += gridDim.x) {
+  const int m0 = g.m_off + (int)(tile % tiles_m) * S_B, n0 = g.n_off + (int)(tile / tiles_m) * S_B;
+  f32x16 acc, acc2;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc2[i] = 0.f;
+  Stage<T, TA> sa, sa2;
+  Stage<T, TB> sb;
+  for (int s = 0; s < g.nsrc; ++s) {
+    const T* A = static_cast<const T*>(g.A[s]);
+    const T* A2 = static_cast<const T*>(g.A[TWO ? 1 : 0]);
+    const T* B = static_cast<const T*>(g.B[s]);
+    const int K = g.K[s];
+    auto fetch = [&](int k0) {
+      sa.load(A, g.lda[s], m0, g.M, k0, K, tid);
+      if constexpr (TWO) sa2.load(A2, g.lda[1], m0, g.M, k0, K, tid);
+      sb.load(B, g.ldb[s], n0, g.N, k0, K, tid);
+    };
+    if (K > 0) fetch(0);
+    for (int k0 = 0; k0 < K; k0 += S_BK) {
+      __syncthreads();  // the previous stage is consumed
+      sa.store(as, tid);
+      if constexpr (TWO) sa2.store(as2, tid);
+      sb.store(bs, tid);
+      __syncthreads();
+      if (k0 + S_BK < K) fetch(k0 + S_BK);
+      mma32<T>(acc, as, bs, wm + l32, wn + l32, hi);
+      if constexpr (TWO) mma32<T>(acc2, as2, bs, wm + l32, wn + l32, hi);
+    }
+  }
+  __syncthreads();
+  // lane holds C[m = 8q + 4 hi + j][n = l32] of its 32x32 block: rows of the output in LDS
+  float* E = reinterpret_cast<float*>(smem);
+  float* E2 = E + (TWO ? S_B * LDE : 0);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int at = (wn + l32) * LDE + wm + 8 * q + 4 * hi;
+    *reinterpret_cast<f32x4*>(E + at) = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+    if constexpr (TWO)
+      *reinterpret_cast<f32x4*>(E2 + at) = f32x4{acc2[4 * q], acc2[4 * q + 1], acc2[4 * q + 2], acc2[4 * q + 3]};
+  }
+  __syncthreads();
+  if constexpr (EPI == L_LSE) {
+    // four threads per output row, 16 of the tile's 64 entries each
+    const int n = n0 + (tid >> 2), c0 = (tid & 3) * 16;
+    const float* row = E + (tid >> 2) * LDE + c0;
+    const int left = g.M - m0 - c0;  // entries inside the vocabulary
+    float mx = -__builtin_huge_valf();
+    for (int j = 0; j < 16; ++j)
+      if (j < left) mx = fmaxf(mx, row[j]);
+    mx = fmaxf(mx, __shfl_xor(mx, 1));
+    mx = fmaxf(mx, __shfl_xor(mx, 2));
+    float sum = 0.f;
+    const float ref = mx > -__builtin_huge_valf() ? mx : 0.f;  // an empty or all -inf block sums to 0
+    for (int j = 0; j < 16; ++j)
+      if (j < left) sum += __expf(row[j] - ref);
+    sum += __shfl_xor(sum, 1);
+    sum += __shfl_xor(sum, 2);
+    if (n < g.N) {
+      const int64_t y = g.e.target[n], hit = y - (m0 + c0);
+      if (y >= 0 && hit >= 0 && hit < 16 && hit < left) g.e.tlogit[n] = row[hit];
+      if ((tid & 3) == 0) {
+        float* o = g.e.part + ((int64_t)(m0 / S_B) * g.e.part_ld + n) * 2;
+        o[0] = mx;
+        o[1] = sum;
+      }
+    }
+  } else {
+    const int Mw = epi_width<EPI>(g.M);
+#pragma unroll
+    for (int j = 0; j < S_B * S_B / 4 / S_NT; ++j) {
+      const int v = tid + j * S_NT, r = v / (S_B / 4), c = (v % (S_B / 4)) * 4;
+      const int n = n0 + r, m = m0 + c;
+      if (n >= g.N || m >= Mw) continue;
+      const f32x4 x = *reinterpret_cast<const f32x4*>(E + r * LDE + c);
+      f32x4 x2 = x;
+      if constexpr (TWO) x2 = *reinterpret_cast<const f32x4*>(E2 + r * LDE + c);
+      epi_vec<T, EPI>(g.e, n, m, g.M, x, x2, sc);
+    }
+  }
+  }
+}
+
+template <class T, int EPI, bool TA, bool TB>
+hipError_t run(const LinArgs& g, hipStream_t st) {
+  const int64_t gx = (epi_width<EPI>(g.M) - g.m_off + S_B - 1) / S_B, gy = (g.N - g.n_off + S_B - 1) / S_B;
+  if (gx <= 0 || gy <= 0) return hipSuccess;
+  const int64_t tiles = gx * gy;
+  hipLaunchKernelGGL((lin_simple_kernel<T, EPI, TA, TB>), dim3((uint32_t)(tiles < kSimpleGrid ? tiles : kSimpleGrid)),
+                     dim3(S_NT), 0, st, g);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t pick(int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
+  if (!ta && !tb) {
+    switch (epi) {
+      case L_LINEAR: return run<T, L_LINEAR, false, false>(g, st);
+      case L_GATED: return run<T, L_GATED, false, false>(g, st);
+      case L_LSE: return run<T, L_LSE, false, false>(g, st);
+      case L_DLOGIT: return run<T, L_DLOGIT, false, false>(g, st);
+    }
+  } else if (ta && !tb) {
+    switch (epi) {
+      case L_DGATE: return run<T, L_DGATE, true, false>(g, st);
+      case L_ACC: return run<T, L_ACC, true, false>(g, st);
+    }
+  } else if (ta && tb && epi == L_ACC) {
+    return run<T, L_ACC, true, true>(g, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
+  return bf16 ? pick<uint16_t>(epi, ta, tb, g, st) : pick<float>(epi, ta, tb, g, st);
+}
+
+int lin_lse_block(int, int, int) { return S_B; }
+
+}  // namespace forge

@@ -1,0 +1,256 @@
+// Internal: the operators around the fused weight-gradient step: products with an
+// epilogue (linear forward, gated block, their gradients, softmax cross entropy of a
+// linear head). This file holds their arguments, the activations and the epilogues;
+// the kernels are in forge_lin_simple.hip and forge_ops_rows.hip.
+//
+// Every product here is C[m][n] = sum_k A[m][k] B[n][k] with m the output's columns
+// (features, contiguous in memory) and n its rows (tokens), so a lane's four consecutive
+// accumulator rows are four neighbouring elements of one output row:
+//   forward      m = out, n = tokens, k = in:   A = W (k fast), B = X (k fast)
+//   input grad.  m = in, n = tokens, k = out:   A = W (k slow: its rows are k), B = dY (k fast)
+//   weight grad. m = in, n = out, k = tokens:   A = X (k slow), B = dY (k slow)
+#pragma once
+
+#include "forge_internal.h"
+
+namespace forge {
+
+// ---------------------------------------------------------------------------
+// activations (FP32): value and derivative
+// ---------------------------------------------------------------------------
+// 1 / (1 + e^-z) on the hardware exponential and reciprocal (each within about an ulp);
+// z -> -inf gives 1 / inf = 0.
+__device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+
+// Phi(z), the normal distribution function, and e^(-z^2/2), which its derivative needs as
+// well: erfc(x) = t (a1 + t (a2 + ... )) e^(-x^2), t = 1 / (1 + 0.3275911 x), absolute error
+// below 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26). The
+// erfc form keeps the relative accuracy of the left tail up to that absolute error; one
+// exponential serves both results.
+__device__ __forceinline__ float normal_cdf_f(float z, float& gauss) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  gauss = __expf(-0.5f * z * z);
+  float p = fmaf(t, 1.061405429f, -1.453152027f);
+  p = fmaf(t, p, 1.421413741f);
+  p = fmaf(t, p, -0.284496736f);
+  p = fmaf(t, p, 0.254829592f);
+  const float half_erfc = 0.5f * t * p * gauss;
+  return z < 0.f ? half_erfc : 1.f - half_erfc;
+}
+
+constexpr float kGeluC = 0.79788456080286536f;  // sqrt(2 / pi)
+constexpr float kGeluK = 0.044715f;
+
+__device__ __forceinline__ float act_f(float z, int act) {
+  switch (act) {
+    case FORGE_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);  // NaN stays NaN
+    case FORGE_ACT_SILU: return z * sigmoid_f(z);
+    case FORGE_ACT_GELU: {
+      float e;
+      return z * normal_cdf_f(z, e);
+    }
+    case FORGE_ACT_GELU_TANH:  // z (1 + tanh u) / 2 = z sigmoid(2u)
+      return z * sigmoid_f(2.f * kGeluC * z * fmaf(kGeluK * z, z, 1.f));
+    default: return z;
+  }
+}
+// value a and derivative d
+__device__ __forceinline__ void act_vd(float z, int act, float& a, float& d) {
+  switch (act) {
+    case FORGE_ACT_RELU:
+      a = z > 0.f ? z : (z != z ? z : 0.f);
+      d = z > 0.f ? 1.f : (z != z ? z : 0.f);
+      return;
+    case FORGE_ACT_SILU: {
+      const float s = sigmoid_f(z);
+      a = z * s;
+      d = fmaf(a, 1.f - s, s);
+      return;
+    }
+    case FORGE_ACT_GELU: {
+      float e;
+      const float c = normal_cdf_f(z, e);
+      a = z * c;
+      d = fmaf(z * 0.39894228040143268f, e, c);
+      return;
+    }
+    case FORGE_ACT_GELU_TANH: {
+      const float s = sigmoid_f(2.f * kGeluC * z * fmaf(kGeluK * z, z, 1.f));
+      a = z * s;
+      d = fmaf(2.f * a * (1.f - s), kGeluC * fmaf(3.f * kGeluK * z, z, 1.f), s);
+      return;
+    }
+    default:
+      a = z;
+      d = 1.f;
+      return;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// element access: T = uint16_t holds bfloat16 bits, T = float holds float32
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ f32x4 load4(const uint16_t* p) {
+  const u32x2 r = *reinterpret_cast<const u32x2*>(p);
+  return f32x4{bits_f32(r.x << 16), bits_f32(r.x & 0xFFFF0000u), bits_f32(r.y << 16), bits_f32(r.y & 0xFFFF0000u)};
+}
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 x) {
+  *reinterpret_cast<u32x2*>(p) = u32x2{rne_bf16_bits(x.x) | (rne_bf16_bits(x.y) << 16),
+                                       rne_bf16_bits(x.z) | (rne_bf16_bits(x.w) << 16)};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
+
+// ---------------------------------------------------------------------------
+// arguments
+// ---------------------------------------------------------------------------
+// Epilogues of the products.
+enum LinEpi {
+  L_LINEAR = 0,  // out = act(x + bias) + in1; out2 = x + bias (the pre-activation), if asked for
+  L_GATED = 1,   // two products g, u: out = act(g) u; out2 = g, out3 = u, if asked for
+  L_DGATE = 2,   // x = dH: out = dG, out2 = dU, out3 = H (if asked for) from in1 = G, in2 = U
+  L_ACC = 3,     // out = (x + acc) * scale, or acc = x (+ acc): products summed over pieces
+  L_LSE = 4,     // per output row: the tile's maximum and sum of exponentials, the target's logit
+  L_DLOGIT = 5,  // out = (exp(x - lse) - [m is the target]) * the token's weight
+};
+
+struct LinEpiArgs {
+  int32_t act;
+  void* out;
+  void* out2;
+  void* out3;
+  int64_t ldo, ldo2, ldo3;
+  const void* in1;
+  const void* in2;
+  int64_t ld1, ld2;
+  const void* bias;  // one element per output column, float32 (bias_f32) or the operands' type
+  int32_t bias_f32;
+  // L_ACC: float32 sums over pieces; read and / or written instead of out
+  float* acc;
+  int64_t ldacc;
+  int32_t acc_read, acc_write;
+  // a factor held in device memory: scale[0] (1 where there is none), divided by count[0]
+  // where count is given (0 where that count is 0)
+  const float* scale;
+  const float* count;
+  // cross entropy (L_DLOGIT: m counts the entries of a piece whose first one is entry v0)
+  const int64_t* target;
+  int64_t ignore, v0, vocab;
+  const float* lse;
+  const float* weight;  // L_DLOGIT: one factor per token, or NULL
+  float* part;          // L_LSE: [blocks of the vocabulary][tokens][2]: maximum, sum of exponentials
+  int64_t part_ld;      // tokens
+  float* tlogit;        // L_LSE: logit of each token's target
+};
+
+constexpr int kMaxSrc = FORGE_MAX_GROUP;
+struct LinArgs {
+  // operand pairs whose products are summed (L_GATED: A[0] and A[1] are gate and up, one B)
+  const void* A[kMaxSrc];
+  const void* B[kMaxSrc];
+  int64_t lda[kMaxSrc], ldb[kMaxSrc];
+  int32_t K[kMaxSrc];
+  int32_t nsrc;
+  int32_t M, N;
+  int32_t m_off, n_off;  // origin of this launch's tiles
+  LinEpiArgs e;
+};
+
+// the factor of L_ACC / L_DLOGIT
+__device__ __forceinline__ float epi_scale(const LinEpiArgs& e) {
+  float s = e.scale ? e.scale[0] : 1.f;
+  if (e.count) s = e.count[0] > 0.f ? s / e.count[0] : 0.f;
+  return s;
+}
+
+// One 4-vector of the output: row n, columns m..m+3 (all inside the output's padded
+// width); x the product, x2 the second product of L_GATED; sc = epi_scale.
+template <class T, int EPI>
+__device__ __forceinline__ void epi_vec(const LinEpiArgs& e, int n, int m, int M, f32x4 x, f32x4 x2, float sc) {
+  if constexpr (EPI == L_LINEAR) {
+    if (e.bias) {
+      const f32x4 b = e.bias_f32 ? load4(static_cast<const float*>(e.bias) + m) : load4(static_cast<const T*>(e.bias) + m);
+      x = x + b;
+    }
+    if (e.out2) store4(static_cast<T*>(e.out2) + (int64_t)n * e.ldo2 + m, x);
+    f32x4 y{act_f(x.x, e.act), act_f(x.y, e.act), act_f(x.z, e.act), act_f(x.w, e.act)};
+    if (e.in1) y = y + load4(static_cast<const T*>(e.in1) + (int64_t)n * e.ld1 + m);
+    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, y);
+  } else if constexpr (EPI == L_GATED) {
+    const f32x4 h{act_f(x.x, e.act) * x2.x, act_f(x.y, e.act) * x2.y, act_f(x.z, e.act) * x2.z,
+                  act_f(x.w, e.act) * x2.w};
+    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, h);
+    if (e.out2) store4(static_cast<T*>(e.out2) + (int64_t)n * e.ldo2 + m, x);
+    if (e.out3) store4(static_cast<T*>(e.out3) + (int64_t)n * e.ldo3 + m, x2);
+  } else if constexpr (EPI == L_DGATE) {
+    const f32x4 g = load4(static_cast<const T*>(e.in1) + (int64_t)n * e.ld1 + m);
+    const f32x4 u = load4(static_cast<const T*>(e.in2) + (int64_t)n * e.ld2 + m);
+    f32x4 dg, du, h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a, d;
+      act_vd(g[j], e.act, a, d);
+      dg[j] = x[j] * (u[j] * d);
+      du[j] = x[j] * a;
+      h[j] = a * u[j];
+    }
+    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, dg);
+    store4(static_cast<T*>(e.out2) + (int64_t)n * e.ldo2 + m, du);
+    if (e.out3) store4(static_cast<T*>(e.out3) + (int64_t)n * e.ldo3 + m, h);
+  } else if constexpr (EPI == L_ACC) {
+    if (e.acc_read) x = x + load4(e.acc + (int64_t)n * e.ldacc + m);
+    if (e.acc_write)
+      store4(e.acc + (int64_t)n * e.ldacc + m, x);
+    else
+      store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, x * sc);
+  } else if constexpr (EPI == L_DLOGIT) {
+    const int64_t y = e.target[n];
+    f32x4 d{0.f, 0.f, 0.f, 0.f};
+    if (y != e.ignore) {
+      // a target outside the vocabulary has no gradient to give: the row becomes NaN
+      const bool bad = y < 0 || y >= e.vocab;
+      const float w = bad ? __builtin_nanf("") : (e.weight ? e.weight[n] * sc : sc);
+      const float l = e.lse[n];
+      const int64_t hit = bad ? -1 : y - e.v0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = __expf(x[j] - l);
+        // columns past the piece's last entry pad the row to its pitch: zeros
+        d[j] = m + j < M ? (p - (hit == m + j ? 1.f : 0.f)) * w : 0.f;
+      }
+    }
+    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, d);
+  }
+}
+
+// width of an output row that the epilogue writes: L_DLOGIT pads its rows with zeros to a
+// multiple of 8 entries, which the products that read them take as whole 16-byte chunks
+template <int EPI>
+__host__ __device__ constexpr int epi_width(int M) {
+  return EPI == L_DLOGIT ? (M + 7) / 8 * 8 : M;
+}
+
+// Host-side launchers. bf16: operands in bfloat16, else float32. ta / tb: the operand's
+// slow index is k (its rows are k), else k is the fast index.
+hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st);
+// vocabulary entries per partial result that launch_lin(L_LSE) writes for this product
+// (never fewer than kLseBlockMin)
+constexpr int kLseBlockMin = 64;
+int lin_lse_block(int bf16, int M, int N);
+
+// dZ = dY act'(Z) and db = its column sums in float32 (partial sums of blocks of rows go to
+// ws, rows_blocks(T, out) x out floats, when there is more than one block)
+int act_backward_blocks(int64_t T, int64_t out);
+hipError_t launch_act_backward(int bf16, int act, const void* dY, int64_t lddy, const void* Z, int64_t ldz, void* dZ,
+                               int64_t lddz, float* db, float* ws, int T, int out, hipStream_t st);
+// dG, dU and (if H) H from dH, G, U
+hipError_t launch_gated_backward(int bf16, const void* dH, int64_t lddh, const LinEpiArgs& e, int T, int hid,
+                                 hipStream_t st);
+// joins the partial maxima and sums of nblk vocabulary blocks: lse, the per-token loss, and
+// total = {sum of the losses, tokens counted, mean}; tsum: 2 * lse_join_groups(T) doubles
+int lse_join_groups(int64_t T);
+hipError_t launch_lse_join(const float* part, int64_t nblk, const float* tlogit, const int64_t* target, int64_t ignore,
+                           int64_t vocab, float* loss, float* lse, float* total, double* tsum, int T, hipStream_t st);
+
+}  // namespace forge

@@ -1,0 +1,231 @@
+// The operators' passes over rows that hold no product: the backward pass of the linear
+// epilogue (gradient through the activation, bias gradient), the gated product's backward
+// pass, and the join of the cross entropy's partial sums. All are bound by memory.
+#include "forge_ops.h"
+
+namespace forge {
+namespace {
+
+typedef uint16_t bf16_t;
+
+// ---- dZ = dY act'(Z), db = column sums ------------------------------------
+// A wave covers 64 x 4 columns (one 4-vector per lane), the 4 waves of a workgroup take
+// every fourth row of the workgroup's block of rows; a lane's column sums stay in float32
+// registers and are joined over the waves through LDS, then over the blocks of rows by
+// act_bias_join, both in a fixed order. bf16: 8 bytes per lane and row.
+constexpr int AB_COLS = 256, AB_NT = 256;
+
+template <class T>
+__global__ __launch_bounds__(AB_NT) void act_backward_kernel(int act, const T* dY, int64_t lddy, const T* Z, int64_t ldz,
+                                                             T* dZ, int64_t lddz, float* part, int R, int out,
+                                                             int rows_per) {
+  __shared__ __attribute__((aligned(16))) float red[3][AB_COLS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * AB_COLS + lane * 4;
+  const int r0 = blockIdx.y * rows_per, r1 = min(R, r0 + rows_per);
+  f32x4 sum{0.f, 0.f, 0.f, 0.f};
+  if (c < out) {
+#pragma unroll 4
+    for (int r = r0 + wave; r < r1; r += 4) {
+      f32x4 d = load4(dY + (int64_t)r * lddy + c);
+      if (act != FORGE_ACT_NONE) {
+        const f32x4 z = load4(Z + (int64_t)r * ldz + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float a, g;
+          act_vd(z[j], act, a, g);
+          d[j] *= g;
+        }
+      }
+      if (dZ) store4(dZ + (int64_t)r * lddz + c, d);
+      sum = sum + d;
+    }
+  }
+  if (!part) return;
+  if (wave) *reinterpret_cast<f32x4*>(&red[wave - 1][lane * 4]) = sum;
+  __syncthreads();
+  if (wave == 0 && c < out) {
+#pragma unroll
+    for (int w = 0; w < 3; ++w) sum = sum + *reinterpret_cast<const f32x4*>(&red[w][lane * 4]);
+    *reinterpret_cast<f32x4*>(part + (int64_t)blockIdx.y * out + c) = sum;
+  }
+}
+
+__global__ __launch_bounds__(256) void act_bias_join(const float* part, int blocks, float* db, int out) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= out) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * out + c];
+  db[c] = s;
+}
+
+// ---- gated product's backward ---------------------------------------------
+template <class T>
+__global__ __launch_bounds__(256) void gated_backward_kernel(const T* dH, int64_t lddh, LinEpiArgs e, int R, int hid) {
+  const int per = hid / 4;  // 4-vectors per row
+  const int64_t total = (int64_t)R * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int n = (int)(i / per), m = (int)(i - (int64_t)n * per) * 4;
+    const f32x4 x = load4(dH + (int64_t)n * lddh + m);
+    epi_vec<T, L_DGATE>(e, n, m, hid, x, x, 1.f);
+  }
+}
+
+// ---- join of the cross entropy's partial results --------------------------
+// lse = M + log sum_b s_b e^(m_b - M) over the vocabulary blocks' (maximum, sum) pairs. 16
+// tokens per workgroup, 16 threads of it (stride 16) share a token's blocks; the pairs of
+// neighbouring tokens are neighbours in memory. The losses' sum is taken in double.
+constexpr int LJ_T = 16, LJ_G = 16;
+
+__device__ __forceinline__ void lse_add(float& m, float& s, float m2, float s2) {
+  const float M = fmaxf(m, m2);
+  if (M == -__builtin_huge_valf()) {  // nothing yet (a NaN sum stays one)
+    s += s2;
+    return;
+  }
+  s = s * __expf(m - M) + s2 * __expf(m2 - M);
+  m = M;
+}
+
+__global__ __launch_bounds__(256) void lse_join_kernel(const float* part, int64_t nblk, const float* tlogit,
+                                                       const int64_t* target, int64_t ignore, int64_t vocab, float* loss,
+                                                       float* lse, double* tsum, float* total, int R) {
+  __shared__ float sm[LJ_G][LJ_T], ss[LJ_G][LJ_T];
+  __shared__ float ls[LJ_T], cnt[LJ_T];
+  const int t = threadIdx.x % LJ_T, grp = threadIdx.x / LJ_T, n = blockIdx.x * LJ_T + t;
+  float m = -__builtin_huge_valf(), s = 0.f;
+  if (n < R) {
+#pragma unroll 4
+    for (int64_t b = grp; b < nblk; b += LJ_G) {
+      const float2 p = *reinterpret_cast<const float2*>(part + (b * R + n) * 2);
+      lse_add(m, s, p.x, p.y);
+    }
+  }
+  sm[grp][t] = m;
+  ss[grp][t] = s;
+  __syncthreads();
+  if (grp == 0) {
+    for (int k = 1; k < LJ_G; ++k) lse_add(m, s, sm[k][t], ss[k][t]);
+    float l = 0.f, c = 0.f;
+    if (n < R) {
+      // no finite logit: m = -inf, s = 0: log 0 = -inf, as the sum says
+      const float v = (m == -__builtin_huge_valf() ? 0.f : m) + logf(s);
+      lse[n] = v;
+      const int64_t y = target[n];
+      if (y != ignore) {
+        c = 1.f;
+        l = (y >= 0 && y < vocab) ? v - tlogit[n] : __builtin_nanf("");
+      }
+      if (loss) loss[n] = l;
+    }
+    ls[t] = l;
+    cnt[t] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double a = 0.0, c = 0.0;
+    for (int k = 0; k < LJ_T; ++k) {
+      a += ls[k];
+      c += cnt[k];
+    }
+    if (gridDim.x == 1) {
+      total[0] = (float)a;
+      total[1] = (float)c;
+      total[2] = (float)(a / c);
+    } else {
+      tsum[2 * blockIdx.x] = a;
+      tsum[2 * blockIdx.x + 1] = c;
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void lse_total_kernel(const double* tsum, int groups, float* total) {
+  __shared__ double sa[256], sc[256];
+  double a = 0.0, c = 0.0;
+  for (int k = threadIdx.x; k < groups; k += 256) {
+    a += tsum[2 * k];
+    c += tsum[2 * k + 1];
+  }
+  sa[threadIdx.x] = a;
+  sc[threadIdx.x] = c;
+  __syncthreads();
+  for (int h = 128; h > 0; h >>= 1) {
+    if ((int)threadIdx.x < h) {
+      sa[threadIdx.x] += sa[threadIdx.x + h];
+      sc[threadIdx.x] += sc[threadIdx.x + h];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    total[0] = (float)sa[0];
+    total[1] = (float)sc[0];
+    total[2] = (float)(sa[0] / sc[0]);  // no token counted: NaN, as the mean of nothing
+  }
+}
+
+template <class T>
+hipError_t act_backward(int act, const void* dY, int64_t lddy, const void* Z, int64_t ldz, void* dZ, int64_t lddz,
+                        float* db, float* ws, int R, int out, hipStream_t st) {
+  const int blocks = db ? act_backward_blocks(R, out) : act_backward_blocks(R, out);
+  const int rows_per = (R + blocks - 1) / blocks;
+  float* part = !db ? nullptr : (blocks == 1 ? db : ws);
+  hipLaunchKernelGGL((act_backward_kernel<T>), dim3((out + AB_COLS - 1) / AB_COLS, blocks), dim3(AB_NT), 0, st, act,
+                     static_cast<const T*>(dY), lddy, static_cast<const T*>(Z), ldz, static_cast<T*>(dZ), lddz, part, R,
+                     out, rows_per);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !db || blocks == 1) return e;
+  hipLaunchKernelGGL(act_bias_join, dim3((out + 255) / 256), dim3(256), 0, st, ws, blocks, db, out);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Blocks of rows: enough workgroups to fill the chip several times, at least 16 rows each.
+int act_backward_blocks(int64_t T, int64_t out) {
+  const int64_t cols = (out + AB_COLS - 1) / AB_COLS;
+  int64_t b = cols > 0 ? (2048 + cols - 1) / cols : 1;
+  const int64_t most = (T + 15) / 16;
+  if (b > most) b = most;
+  if (b > 1024) b = 1024;
+  if (b < 1) b = 1;
+  // no empty block at the end: the last of ceil(T / rows_per) blocks holds a row
+  const int64_t rows_per = T > 0 ? (T + b - 1) / b : 1;
+  return (int)(T > 0 ? (T + rows_per - 1) / rows_per : 1);
+}
+
+hipError_t launch_act_backward(int bf16, int act, const void* dY, int64_t lddy, const void* Z, int64_t ldz, void* dZ,
+                               int64_t lddz, float* db, float* ws, int T, int out, hipStream_t st) {
+  return bf16 ? act_backward<bf16_t>(act, dY, lddy, Z, ldz, dZ, lddz, db, ws, T, out, st)
+              : act_backward<float>(act, dY, lddy, Z, ldz, dZ, lddz, db, ws, T, out, st);
+}
+
+hipError_t launch_gated_backward(int bf16, const void* dH, int64_t lddh, const LinEpiArgs& e, int T, int hid,
+                                 hipStream_t st) {
+  const int64_t vecs = (int64_t)T * (hid / 4);
+  if (vecs == 0) return hipSuccess;
+  const int64_t want = (vecs + 255) / 256;
+  const int grid = (int)(want < 4096 ? want : 4096);
+  if (bf16)
+    hipLaunchKernelGGL((gated_backward_kernel<bf16_t>), dim3(grid), dim3(256), 0, st, static_cast<const bf16_t*>(dH), lddh,
+                       e, T, hid);
+  else
+    hipLaunchKernelGGL((gated_backward_kernel<float>), dim3(grid), dim3(256), 0, st, static_cast<const float*>(dH), lddh, e,
+                       T, hid);
+  return hipGetLastError();
+}
+
+int lse_join_groups(int64_t T) { return (int)((T + LJ_T - 1) / LJ_T); }
+
+hipError_t launch_lse_join(const float* part, int64_t nblk, const float* tlogit, const int64_t* target, int64_t ignore,
+                           int64_t vocab, float* loss, float* lse, float* total, double* tsum, int T, hipStream_t st) {
+  const int groups = T > 0 ? lse_join_groups(T) : 1;  // no tokens: one group writes the empty total
+  hipLaunchKernelGGL(lse_join_kernel, dim3(groups), dim3(256), 0, st, part, nblk, tlogit, target, ignore, vocab, loss, lse,
+                     tsum, total, T);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || groups == 1) return e;
+  hipLaunchKernelGGL(lse_total_kernel, dim3(1), dim3(256), 0, st, tsum, groups, total);
+  return hipGetLastError();
+}
+
+}  // namespace forge

@@ -87,6 +87,31 @@ def _load() -> ctypes.CDLL:
         "forge_mfma_peak_flops": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_double),
         "forge_dyn_encode": ([ctypes.c_int32, ctypes.c_float], ctypes.c_int32),
         "forge_version": ([], ctypes.c_int),
+        "forge_linear_forward": ([P(ForgeTensor)] * 3 + [ctypes.c_int32] + [P(ForgeTensor)] * 3 + [ctypes.c_void_p],
+                                 ctypes.c_int),
+        "forge_linear_act_backward_workspace": ([ctypes.c_int64] * 2, ctypes.c_int64),
+        "forge_linear_act_backward": ([P(ForgeTensor)] * 2 + [ctypes.c_int32, P(ForgeTensor), ctypes.c_void_p,
+                                                              ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p],
+                                      ctypes.c_int),
+        "forge_gated_forward": ([P(ForgeTensor)] * 3 + [ctypes.c_int32] + [P(ForgeTensor)] * 3 + [ctypes.c_void_p],
+                                ctypes.c_int),
+        "forge_gated_backward": ([P(ForgeTensor)] * 3 + [ctypes.c_int32] + [P(ForgeTensor)] * 3 + [ctypes.c_void_p],
+                                 ctypes.c_int),
+        "forge_gated_dgrad": ([P(ForgeTensor)] * 4 + [ctypes.c_int32] + [P(ForgeTensor)] * 3 + [ctypes.c_void_p],
+                              ctypes.c_int),
+        "forge_linear_dgrad_group": ([ctypes.c_int32] + [P(ForgeTensor)] * 3 + [ctypes.c_void_p], ctypes.c_int),
+        "forge_linear_xent_workspace": ([ctypes.c_int64] * 3 + [ctypes.c_int32] * 2 + [ctypes.c_int64], ctypes.c_int64),
+        "forge_linear_xent_forward": ([P(ForgeTensor)] * 2 + [ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 4 +
+                                      [ctypes.c_int64, ctypes.c_void_p], ctypes.c_int),
+        "forge_linear_xent_backward": ([P(ForgeTensor)] * 2 + [ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 2 +
+                                       [ctypes.c_int32, ctypes.c_void_p] + [P(ForgeTensor)] * 2 +
+                                       [ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p],
+                                       ctypes.c_int),
+        "forge_linear_xent_step": ([P(ForgeTensor)] * 4 + [ctypes.c_int32, P(ForgeHyper), ctypes.c_int64,
+                                                           ctypes.c_uint64, ctypes.c_void_p, ctypes.c_int64] +
+                                   [ctypes.c_void_p] * 2 + [ctypes.c_int32, ctypes.c_void_p, P(ForgeTensor),
+                                                            ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                                            ctypes.c_void_p], ctypes.c_int),
     }
     for name, (argt, rest) in sigs.items():
         fn = getattr(lib, name)
@@ -406,3 +431,264 @@ def new_states(W: torch.Tensor, opt: str = "adamw", fmt: str = "f32"):
     else:
         raise ValueError(fmt)
     return m, v, ms, vs
+
+
+# ---------------------------------------------------------------------------
+# operators around the fused step
+# ---------------------------------------------------------------------------
+ACTS = ("none", "relu", "silu", "gelu", "gelu_tanh")
+ACT_ID = {name: k for k, name in enumerate(ACTS)}
+
+
+def _act(act: str) -> int:
+    if act not in ACT_ID:
+        raise ValueError(f"unknown activation {act!r}; one of {', '.join(ACTS)}")
+    return ACT_ID[act]
+
+
+class _On:
+    """The device and stream of a call: every tensor on one device, which is made current for
+    the call; the work goes to `stream`, or to that device's current stream."""
+
+    def __init__(self, stream, *tensors):
+        given = [t for t in tensors if t is not None]
+        self.device = given[0].device
+        for t in given:
+            if t.device != self.device:
+                raise ValueError("the tensors of a call live on one device")
+        if self.device.type != "cuda":
+            raise ValueError("forge kernels take device tensors")
+        if isinstance(stream, torch.cuda.Stream) and stream.device != self.device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self._given = stream
+        self._guard = torch.cuda.device(self.device)
+
+    def __enter__(self):
+        self._guard.__enter__()
+        self.stream = _stream(self._given)
+        return self
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        """A new tensor for this call. On a stream other than the current one the memory is
+        kept from being handed out again before that stream is done with it."""
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self._given is not None and self.stream != torch.cuda.current_stream().cuda_stream:
+            t.record_stream(torch.cuda.ExternalStream(self.stream))
+        return t
+
+
+def _same(on: "_On", out: Optional[torch.Tensor], shape, dtype) -> torch.Tensor:
+    return on.empty(shape, dtype) if out is None else out
+
+
+def _check(st: int, what: str) -> None:
+    if st:
+        raise ForgeError(st, what)
+
+
+def _row(b: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    if b is None:
+        return None
+    if b.dim() != 1 or not b.is_contiguous():
+        raise ValueError("bias is a contiguous vector")
+    return b.unsqueeze(0)
+
+
+def _vec(t: torch.Tensor, n: int, dtype: torch.dtype, what: str) -> torch.Tensor:
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous {dtype} values wanted")
+    return t
+
+
+def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+           residual: Optional[torch.Tensor] = None, save: bool = False, out: Optional[torch.Tensor] = None,
+           stream=None):
+    """Y = act(X W^T + bias) + residual, one kernel (forge_linear_forward). X [T, in], W [out, in],
+    both bfloat16 or both float32; bias [out] in that type or float32; residual [T, out];
+    act one of ACTS. With save=True returns (Y, Z), Z = X W^T + bias, which
+    linear_act_backward needs for an activation."""
+    a = _act(act)
+    with _On(stream, X, W, bias, residual, out) as on:
+        Y = _same(on, out, (X.shape[0], W.shape[0]), W.dtype)
+        Z = on.empty((X.shape[0], W.shape[0]), W.dtype) if save else None
+        _check(_lib.forge_linear_forward(_ref(describe(X)), _ref(describe(W)), _ref(describe(_row(bias))), a,
+                                         _ref(describe(residual)), _ref(describe(Y)), _ref(describe(Z)), on.stream),
+               "forge_linear_forward")
+    return (Y, Z) if save else Y
+
+
+def linear_act_backward(dY: torch.Tensor, Z: Optional[torch.Tensor] = None, act: str = "none",
+                        want_bias: bool = True, dZ: Optional[torch.Tensor] = None, stream=None):
+    """Backward of linear's epilogue (forge_linear_act_backward): (dZ, dbias) with
+    dZ = dY * act'(Z) and dbias its float32 sum over the tokens (None with want_bias=False).
+    act="none": dZ is dY itself."""
+    a = _act(act)
+    if act != "none" and Z is None:
+        raise ValueError("the gradient through an activation needs Z")
+    with _On(stream, dY, Z, dZ) as on:
+        T, out = dY.shape
+        dZ = _same(on, dZ, (T, out), dY.dtype) if act != "none" else None
+        db = ws = None
+        need = 0
+        if want_bias:
+            db = on.empty((out,), torch.float32)
+            need = _lib.forge_linear_act_backward_workspace(T, out)
+            if need:
+                ws = on.empty((need,), torch.uint8)
+        _check(_lib.forge_linear_act_backward(_ref(describe(dY)), _ref(describe(Z)), a, _ref(describe(dZ)),
+                                              db.data_ptr() if db is not None and out else None,
+                                              ws.data_ptr() if ws is not None else None, need, on.stream),
+               "forge_linear_act_backward")
+    return (dY if dZ is None else dZ), db
+
+
+def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", save: bool = False,
+          out: Optional[torch.Tensor] = None, stream=None):
+    """H = act(X Wg^T) * (X Wu^T), one kernel (forge_gated_forward): X [T, in], Wg and Wu
+    [hidden, in]. With save=True returns (H, G, U), the projections the backward pass reads."""
+    a = _act(act)
+    with _On(stream, X, Wg, Wu, out) as on:
+        shape = (X.shape[0], Wg.shape[0])
+        H = _same(on, out, shape, Wg.dtype)
+        G, U = (on.empty(shape, Wg.dtype), on.empty(shape, Wg.dtype)) if save else (None, None)
+        _check(_lib.forge_gated_forward(_ref(describe(X)), _ref(describe(Wg)), _ref(describe(Wu)), a,
+                                        _ref(describe(H)), _ref(describe(G)), _ref(describe(U)), on.stream),
+               "forge_gated_forward")
+    return (H, G, U) if save else H
+
+
+def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, act: str = "silu", want_h: bool = True,
+                   stream=None):
+    """Backward of the gated product from dH: (dG, dU, H), dG = dH * U * act'(G),
+    dU = dH * act(G), H = act(G) * U (None with want_h=False)."""
+    a = _act(act)
+    with _On(stream, dH, G, U) as on:
+        dG, dU = on.empty(dH.shape, dH.dtype), on.empty(dH.shape, dH.dtype)
+        H = on.empty(dH.shape, dH.dtype) if want_h else None
+        _check(_lib.forge_gated_backward(_ref(describe(dH)), _ref(describe(G)), _ref(describe(U)), a,
+                                         _ref(describe(dG)), _ref(describe(dU)), _ref(describe(H)), on.stream),
+               "forge_gated_backward")
+    return dG, dU, H
+
+
+def gated_dgrad(dY: torch.Tensor, Wd: torch.Tensor, G: torch.Tensor, U: torch.Tensor, act: str = "silu",
+                want_h: bool = True, stream=None):
+    """gated_backward with dH = dY Wd (the linear layer behind the block, its weights as they
+    are now) formed in registers and never stored (forge_gated_dgrad): (dG, dU, H)."""
+    a = _act(act)
+    with _On(stream, dY, Wd, G, U) as on:
+        shape = (dY.shape[0], Wd.shape[1])
+        dG, dU = on.empty(shape, Wd.dtype), on.empty(shape, Wd.dtype)
+        H = on.empty(shape, Wd.dtype) if want_h else None
+        _check(_lib.forge_gated_dgrad(_ref(describe(dY)), _ref(describe(Wd)), _ref(describe(G)), _ref(describe(U)), a,
+                                      _ref(describe(dG)), _ref(describe(dU)), _ref(describe(H)), on.stream),
+               "forge_gated_dgrad")
+    return dG, dU, H
+
+
+def dgrad_group(dYs, Ws, dX: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dX = sum_l dYs[l] Ws[l] for layers that read the same input, in one accumulation
+    (forge_linear_dgrad_group; from the weights as they are now)."""
+    n = len(Ws)
+    if len(dYs) != n or not 1 <= n <= MAX_GROUP:
+        raise ValueError(f"a group holds 1..{MAX_GROUP} layers, each with its dY and W")
+    with _On(stream, *dYs, *Ws, dX) as on:
+        dX = _same(on, dX, (dYs[0].shape[0], Ws[0].shape[1]), Ws[0].dtype)
+        dy_a = (ForgeTensor * n)(*[describe(t) for t in dYs])
+        w_a = (ForgeTensor * n)(*[describe(t) for t in Ws])
+        _check(_lib.forge_linear_dgrad_group(n, dy_a, w_a, _ref(describe(dX)), on.stream), "forge_linear_dgrad_group")
+    return dX
+
+
+_REDUCTIONS = ("mean", "sum", "none")
+
+
+def _reduction(reduction: str) -> str:
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"unknown reduction {reduction!r}; one of {', '.join(_REDUCTIONS)}")
+    return reduction
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return t.data_ptr() if t is not None and t.numel() else None
+
+
+def linear_cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+                         reduction: str = "mean", stream=None):
+    """Softmax cross entropy of the logits X W^T against `targets`, the logits never stored
+    (forge_linear_xent_forward). X [T, in], W [vocab, in]; targets: T int64 in [0, vocab) or
+    ignore_index (another value makes the loss NaN). Returns (loss, lse, total): the loss by
+    `reduction` ("mean" over the tokens that count, "sum", or "none": one per token, 0 where
+    ignored), each token's log sum of exponentials, and total = (sum of the losses, tokens
+    counted, mean); linear_cross_entropy_backward takes the last two."""
+    _reduction(reduction)
+    with _On(stream, X, W, targets) as on:
+        T = X.shape[0]
+        _vec(targets, T, torch.int64, "targets")
+        loss = on.empty((T,), torch.float32) if reduction == "none" else None
+        lse, total = on.empty((T,), torch.float32), on.empty((3,), torch.float32)
+        need = _lib.forge_linear_xent_workspace(T, X.shape[1], W.shape[0], _DT.get(W.dtype, -1), 0, 0)
+        ws = on.empty((need,), torch.uint8)
+        _check(_lib.forge_linear_xent_forward(_ref(describe(X)), _ref(describe(W)), _ptr(targets), int(ignore_index),
+                                              _ptr(loss), _ptr(lse), total.data_ptr(), _ptr(ws), need, on.stream),
+               "forge_linear_xent_forward")
+    return (loss if reduction == "none" else total[2 if reduction == "mean" else 0]), lse, total
+
+
+def _xent_grad_args(on, X, W, targets, lse, dloss, reduction, total, piece):
+    T = X.shape[0]
+    _vec(targets, T, torch.int64, "targets")
+    _vec(lse, T, torch.float32, "lse")
+    _vec(dloss, T if reduction == "none" else 1, torch.float32, "dloss")
+    if reduction == "mean":
+        if total is None:
+            raise ValueError("the gradient of a mean needs `total` of the forward pass")
+        _vec(total, 3, torch.float32, "total")
+    need = _lib.forge_linear_xent_workspace(T, X.shape[1], W.shape[0], _DT.get(W.dtype, -1), 1, int(piece))
+    return need, on.empty((need,), torch.uint8), (total if reduction == "mean" else None)
+
+
+def linear_cross_entropy_backward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                                  dloss: torch.Tensor, ignore_index: int = -100, reduction: str = "mean",
+                                  total: Optional[torch.Tensor] = None, want_dx: bool = True, want_dw: bool = True,
+                                  piece: int = 0, stream=None):
+    """Gradients of linear_cross_entropy (forge_linear_xent_backward): (dX, dW) in the operands'
+    type, None where not wanted. dloss: float32 device scalar, or T values with
+    reduction="none"; lse and total as linear_cross_entropy returned them. Works through the
+    vocabulary `piece` entries at a time (0: the library's choice)."""
+    _reduction(reduction)
+    with _On(stream, X, W, targets, lse, dloss, total) as on:
+        need, ws, tot = _xent_grad_args(on, X, W, targets, lse, dloss, reduction, total, piece)
+        dX = on.empty(X.shape, X.dtype) if want_dx else None
+        dW = on.empty(W.shape, W.dtype) if want_dw else None
+        _check(_lib.forge_linear_xent_backward(_ref(describe(X)), _ref(describe(W)), _ptr(targets), int(ignore_index),
+                                               _ptr(lse), _ptr(dloss), int(reduction == "none"), _ptr(tot),
+                                               _ref(describe(dX)), _ref(describe(dW)), int(piece), _ptr(ws), need,
+                                               on.stream), "forge_linear_xent_backward")
+    return dX, dW
+
+
+def linear_cross_entropy_step(X: torch.Tensor, W: torch.Tensor, m: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                              targets: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor, opt: str = "adamw",
+                              hyper=None, step: int = 1, seed: int = 0, m_scale: Optional[torch.Tensor] = None,
+                              v_scale: Optional[torch.Tensor] = None, code: str = "linear", ignore_index: int = -100,
+                              reduction: str = "mean", total: Optional[torch.Tensor] = None, want_dx: bool = True,
+                              piece: int = 0, stream=None) -> Optional[torch.Tensor]:
+    """linear_cross_entropy_backward with the head's fused optimizer step in the place of dW
+    (forge_linear_xent_step): W, m, v (and scales) updated in place piece by piece; returns
+    dX (from the old W) or None. Optimizer arguments as in wgrad_step."""
+    _reduction(reduction)
+    h = _hyper(opt, hyper)
+    with _On(stream, X, W, m, v, targets, lse, dloss, m_scale, v_scale, total) as on:
+        need, ws, tot = _xent_grad_args(on, X, W, targets, lse, dloss, reduction, total, piece)
+        dX = on.empty(X.shape, X.dtype) if want_dx else None
+        _check(_lib.forge_linear_xent_step(_ref(describe(X)), _ref(describe(W)), _ref(describe(m, m_scale, code=code)),
+                                           _ref(describe(v, v_scale, code=code)), OPT_ID[opt], ctypes.byref(h),
+                                           int(step), seed & (2 ** 64 - 1), _ptr(targets), int(ignore_index),
+                                           _ptr(lse), _ptr(dloss), int(reduction == "none"), _ptr(tot),
+                                           _ref(describe(dX)), int(piece), _ptr(ws), need, on.stream),
+               "forge_linear_xent_step")
+    return dX

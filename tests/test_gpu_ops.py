@@ -1,0 +1,384 @@
+"""GPU parity of the operators around the fused step against their float64 forms: the linear
+layer's epilogue, the gated block, the grouped input gradient and the cross entropy of a
+linear head, at ragged sizes, one token, no token, pitched rows, in bfloat16 and float32.
+Tolerances are derived in tests/_ops64.py."""
+import pytest
+import torch
+
+import optimizer_gemm_amd as forge
+from _ops64 import (act64, close, gated64, gated_back64, linear64, mm64, xent64, xent_grad64)
+
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+DT = {"bf16": BF, "f32": F}
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def rnd(g, *shape, dtype=BF, std=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda", dtype=F) * std).to(dtype)
+
+
+def pitched(t, extra=16):
+    """The same values as a view with wider rows, whose padding holds NaN."""
+    big = torch.full((t.shape[0], t.shape[1] + extra), float("nan"), device=t.device, dtype=t.dtype)
+    view = big[:, : t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+# tokens, in, out: one token; odd tokens; sizes that are no multiple of any tile; tiles in
+# every direction; more tiles than compute units
+SIZES = [(1, 8, 8), (1, 512, 264), (3, 72, 40), (7, 4096, 128), (33, 136, 1032), (130, 264, 520), (257, 96, 328),
+         (511, 1000, 776), (1000, 256, 2056), (2049, 520, 1288)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t,i,o", SIZES)
+def test_linear(t, i, o, dt):
+    g = gen(t * 7 + i + o)
+    X, W = rnd(g, t, i, dtype=DT[dt]), rnd(g, o, i, dtype=DT[dt], std=i ** -0.5)
+    b, R = rnd(g, o, dtype=DT[dt]), rnd(g, t, o, dtype=DT[dt])
+    act = forge.ACTS[(t + o) % 5]
+    Y, Z = forge.linear(X, W, bias=b, act=act, residual=R, save=True)
+    y, dy, z, dz = linear64(X, W, b, act, R)
+    close(f"Y {act}", Y, y, dy)
+    close("Z", Z, z, dz)
+    close("plain", forge.linear(X, W), *linear64(X, W)[:2])
+
+
+@pytest.mark.parametrize("act", forge.ACTS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_linear_activations_and_parts(act, dt):
+    g = gen(5)
+    X, W = rnd(g, 150, 200, dtype=DT[dt], std=2.0), rnd(g, 344, 200, dtype=DT[dt], std=0.2)
+    b, R = rnd(g, 344, dtype=F), rnd(g, 150, 344, dtype=DT[dt])
+    for bias in (None, b):
+        for res in (None, R):
+            Y = forge.linear(X, W, bias=bias, act=act, residual=res)
+            close(f"{act} {bias is not None} {res is not None}", Y, *linear64(X, W, bias, act, res)[:2])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [1, 5, 300])
+def test_linear_pitched_rows(t, dt):
+    g = gen(11)
+    X, W, R = rnd(g, t, 264, dtype=DT[dt]), rnd(g, 392, 264, dtype=DT[dt], std=0.06), rnd(g, t, 392, dtype=DT[dt])
+    out = torch.full((t, 400), 7.0, device="cuda", dtype=DT[dt])
+    forge.linear(pitched(X), pitched(W, 8), residual=pitched(R), act="silu", out=out[:, :392])
+    close("Y", out[:, :392], *linear64(X, W, None, "silu", R)[:2])
+    assert torch.all(out[:, 392:] == 7.0)
+
+
+def test_linear_extreme_values():
+    """Saturated activations keep their limits; a NaN or an infinity stays in its own row."""
+    X = torch.zeros(5, 8, device="cuda", dtype=BF)
+    X[:, 0] = torch.tensor([60.0, -60.0, 3e38, -3e38, float("nan")], device="cuda")
+    W = torch.zeros(8, 8, device="cuda", dtype=BF)
+    W[:, 0] = 1.0
+    for act in forge.ACTS:
+        Y = forge.linear(X, W, act=act)
+        assert torch.all(Y[0] == 60.0), act
+        # silu's left tail is -60 e^-60 = -5.25e-25, no zero: half a bfloat16 step and the
+        # exponential's argument (60 1.45 2^-24); the others' tails are below every float
+        want = act64(torch.tensor(-60.0, dtype=torch.float64), act)[0].item()
+        if abs(want) < 1e-45:
+            assert torch.all(Y[1].float().abs() < 1e-37), act
+        else:
+            assert torch.all((Y[1].double() / want - 1).abs() <= 2.0 ** -8 + 100 * 2.0 ** -24), act
+        assert torch.all(Y[2].float() > 1e38), act
+        if act != "none":
+            assert torch.all(Y[3].float() == 0.0), act
+        assert torch.all(torch.isnan(Y[4])), act
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t,o", [(1, 8), (2, 264), (17, 1000), (1025, 2056), (4099, 40)])
+def test_linear_act_backward(t, o, dt):
+    g = gen(t + o)
+    dY, Z = rnd(g, t, o, dtype=DT[dt]), rnd(g, t, o, dtype=DT[dt], std=2.0)
+    for act in forge.ACTS:
+        dZ, db = forge.linear_act_backward(dY, Z, act=act)
+        a, d = act64(Z.double(), act)
+        want = dY.double() * d
+        err = dY.double().abs() * (48 * 2.0 ** -24) * (1 + Z.double().abs()) + 2.0 ** -24 * want.abs()
+        if act == "none":
+            assert dZ is dY
+        else:
+            close(f"dZ {act}", dZ, want, err)
+        close(f"db {act}", db, want.sum(0), err.sum(0) + t * 2.0 ** -24 * want.abs().sum(0))
+    dZ, db = forge.linear_act_backward(pitched(dY), pitched(Z), act="silu", want_bias=False)
+    assert db is None
+    assert torch.equal(dZ, forge.linear_act_backward(dY, Z, act="silu")[0])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t,i,o", SIZES)
+def test_gated(t, i, o, dt):
+    g = gen(t + i * 3 + o)
+    X = rnd(g, t, i, dtype=DT[dt])
+    Wg, Wu = rnd(g, o, i, dtype=DT[dt], std=i ** -0.5), rnd(g, o, i, dtype=DT[dt], std=i ** -0.5)
+    act = forge.ACTS[(t + o) % 4 + 1]
+    H, G, U = forge.gated(X, Wg, Wu, act=act, save=True)
+    h, dh, gg, dg, uu, du = gated64(X, Wg, Wu, act)
+    close(f"H {act}", H, h, dh)
+    close("G", G, gg, dg)
+    close("U", U, uu, du)
+    assert torch.equal(forge.gated(X, Wg, Wu, act=act), H)
+    assert torch.equal(forge.gated(pitched(X), pitched(Wg), pitched(Wu, 8), act=act), H)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t,i,o", SIZES)
+def test_gated_backward(t, i, o, dt):
+    """dH = dY Wd formed in registers, the same from a given dH, then dX of both projections."""
+    g = gen(t + i + o * 3)
+    dY, Wd = rnd(g, t, i, dtype=DT[dt]), rnd(g, i, o, dtype=DT[dt], std=o ** -0.5)
+    G, U = rnd(g, t, o, dtype=DT[dt], std=2.0), rnd(g, t, o, dtype=DT[dt])
+    act = forge.ACTS[(t + o) % 4 + 1]
+    dG, dU, H = forge.gated_dgrad(dY, Wd, G, U, act=act)
+    dh, ddh = mm64(dY, Wd)
+    dg, eg, du, eu, h, eh = gated_back64(dh, ddh, G, U, act)
+    close(f"dG {act}", dG, dg, eg)
+    close("dU", dU, du, eu)
+    close("H", H, h, eh)
+    dH = rnd(g, t, o, dtype=DT[dt])
+    dG2, dU2, H2 = forge.gated_backward(dH, pitched(G), U, act=act)
+    dg, eg, du, eu, h, eh = gated_back64(dH.double(), torch.zeros_like(dh), G, U, act)
+    close("dG of dH", dG2, dg, eg)
+    close("dU of dH", dU2, du, eu)
+    close("H of dH", H2, h, eh)
+    a, b, none = forge.gated_dgrad(pitched(dY), pitched(Wd), pitched(G), pitched(U), act=act, want_h=False)
+    assert none is None and torch.equal(a, dG) and torch.equal(b, dU)
+    Wg, Wu = rnd(g, o, i, dtype=DT[dt]), rnd(g, o, i, dtype=DT[dt])
+    dX = forge.dgrad_group([dG, dU], [Wg, Wu])
+    x1, e1 = mm64(dG, Wg)
+    x2, e2 = mm64(dU, Wu)
+    close("dX", dX, x1 + x2, 2 * (e1 + e2))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("outs", [(8,), (264, 40), (1032, 264, 264), (72, 8, 200, 520)])
+def test_dgrad_group(outs, dt):
+    g = gen(sum(outs))
+    t, i = 205, 456
+    dYs = [rnd(g, t, o, dtype=DT[dt]) for o in outs]
+    Ws = [rnd(g, o, i, dtype=DT[dt]) for o in outs]
+    want, bound = 0, 0
+    for d, w in zip(dYs, Ws):
+        x, e = mm64(d, w)
+        want, bound = want + x, bound + len(outs) * e
+    close("dX", forge.dgrad_group([pitched(d) for d in dYs], [pitched(w) for w in Ws]), want, bound)
+
+
+def head(seed, t, i, v, dtype, ignored=0.2, ignore=-100):
+    g = gen(seed)
+    W = rnd(g, v, i, dtype=dtype, std=2.0 * i ** -0.5)
+    y = torch.randint(0, v, (t,), generator=g, device="cuda")
+    X = (torch.randn(t, i, generator=g, device="cuda") + 2.0 * W[y].float()).to(dtype)
+    drop = torch.rand(t, generator=g, device="cuda") < ignored
+    return X, W, torch.where(drop, torch.full_like(y, ignore), y)
+
+
+# tokens, in, vocabulary (odd and tiny ones; a single entry: its loss is 0)
+HEADS = [(1, 8, 1), (1, 64, 7), (2, 136, 1000), (65, 264, 513), (130, 72, 2051), (300, 520, 4099), (1025, 256, 5003)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t,i,v", HEADS)
+def test_cross_entropy(t, i, v, dt):
+    X, W, y = head(t + v, t, i, v, DT[dt])
+    loss, dl, lse, de, _, _, keep = xent64(X, W, y, -100)
+    for red in ("none", "sum", "mean"):
+        got, got_lse, total = forge.linear_cross_entropy(pitched(X), pitched(W), y, reduction=red)
+        close("lse", got_lse, lse, de, F)
+        n = int(keep.sum())
+        assert float(total[1]) == n
+        if red == "none":
+            close("loss", got, loss, dl, F)
+        elif red == "sum":
+            close("sum", got, loss.sum(), dl.sum(), F)
+        elif n:
+            close("mean", got, loss.sum() / n, dl.sum() / n + 2.0 ** -23 * loss.sum() / n, F)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("red", ["mean", "sum", "none"])
+@pytest.mark.parametrize("t,i,v", HEADS)
+def test_cross_entropy_gradients(t, i, v, red, dt):
+    X, W, y = head(t * 3 + v, t, i, v, DT[dt])
+    y[0] = v - 1
+    keep = y != -100
+    n = int(keep.sum())
+    g = gen(17)
+    dloss = torch.rand(t if red == "none" else 1, generator=g, device="cuda") + 0.5
+    f = dloss.double() / (n if red == "mean" else 1)
+    f = (f if red == "none" else f.expand(t)) * keep
+    dx, ex, dw, ew = xent_grad64(X, W, y, -100, f, DT[dt])
+    _, lse, total = forge.linear_cross_entropy(X, W, y, reduction=red)
+    for piece in (0, 8, 264):
+        dX, dW = forge.linear_cross_entropy_backward(pitched(X), pitched(W), y, lse, dloss, reduction=red, total=total,
+                                                     piece=piece)
+        if piece == 8 and v > 600:
+            continue
+        close(f"dX {piece}", dX, dx, ex)
+        close(f"dW {piece}", dW, dw, ew)
+    only_x, none = forge.linear_cross_entropy_backward(X, W, y, lse, dloss, reduction=red, total=total, want_dw=False)
+    none2, only_w = forge.linear_cross_entropy_backward(X, W, y, lse, dloss, reduction=red, total=total, want_dx=False)
+    both = forge.linear_cross_entropy_backward(X, W, y, lse, dloss, reduction=red, total=total)
+    assert none is None and none2 is None
+    assert torch.equal(only_x, both[0]) and torch.equal(only_w, both[1])
+    assert torch.all(both[0][~keep] == 0)
+
+
+def test_cross_entropy_against_differences():
+    """The float32 gradient against central differences of the float32 loss."""
+    X, W, y = head(3, 6, 16, 37, F, ignored=0.0)
+    y[2] = -100
+    _, lse, total = forge.linear_cross_entropy(X, W, y)
+    one = torch.ones((), device="cuda")
+    dX, dW = forge.linear_cross_entropy_backward(X, W, y, lse, one, total=total)
+    h = 2.0 ** -7
+    for t, grad in ((X, dX), (W, dW)):
+        for k in (0, 5, 33, t.numel() - 1):
+            flat = t.view(-1)
+            keep = float(flat[k])
+            flat[k] = keep + h
+            up = float(forge.linear_cross_entropy(X, W, y)[0])
+            flat[k] = keep - h
+            down = float(forge.linear_cross_entropy(X, W, y)[0])
+            flat[k] = keep
+            # third differences of a softmax loss are below max|W|^3 (or |X|^3) h^2 / 6; the
+            # loss (about 5) is held to 2^-21 or so, twice, over 2 h
+            other = W if t is X else X
+            tol = float(other.abs().max()) ** 3 * h * h / 6 + 2 * 5 * 2.0 ** -21 / (2 * h)
+            assert abs((up - down) / (2 * h) - float(grad.view(-1)[k])) <= tol
+
+
+def test_cross_entropy_masks():
+    X, W, y = head(9, 40, 64, 300, BF, ignored=0.0)
+    # nothing counts: the mean of nothing is NaN, the sum 0, the gradients 0
+    none = torch.full_like(y, -100)
+    one = torch.ones((), device="cuda")
+    loss, lse, total = forge.linear_cross_entropy(X, W, none)
+    assert torch.isnan(loss) and float(total[0]) == 0 and float(total[1]) == 0
+    dX, dW = forge.linear_cross_entropy_backward(X, W, none, lse, one, total=total)
+    assert torch.all(dX == 0) and torch.all(dW == 0)
+    # an ignored index inside the vocabulary
+    l5, _, t5 = forge.linear_cross_entropy(X, W, y, ignore_index=int(y[3]), reduction="none")
+    assert float(t5[1]) == int((y != y[3]).sum()) and torch.all(l5[y == y[3]] == 0)
+    # targets outside the vocabulary: that token's loss and gradient are NaN, the others' are not
+    for bad in (300, -1, 2 ** 62, -2 ** 63):
+        z = y.clone()
+        z[7] = bad
+        lb, lse_b, tb = forge.linear_cross_entropy(X, W, z, reduction="none")
+        ok = torch.arange(40, device="cuda") != 7
+        assert torch.isnan(lb[7]) and torch.isfinite(lb[ok]).all()
+        dXb, _ = forge.linear_cross_entropy_backward(X, W, z, lse_b, one, reduction="sum")
+        assert torch.isnan(dXb[7]).all() and torch.isfinite(dXb[ok]).all()
+    # a NaN or an infinity in an ignored token's hidden state reaches no other token
+    Xn = X.clone()
+    Xn[5], Xn[6] = float("nan"), float("inf")
+    z = y.clone()
+    z[5] = z[6] = -100
+    ln, lse_n, tn = forge.linear_cross_entropy(Xn, W, z, reduction="none")
+    assert torch.isfinite(ln).all() and torch.all(ln[5:7] == 0)
+    dXn, _ = forge.linear_cross_entropy_backward(Xn, W, z, lse_n, one, reduction="sum", want_dw=False)
+    assert torch.isfinite(dXn).all() and torch.all(dXn[5:7] == 0)
+
+
+def test_cross_entropy_large_logits():
+    """Logits of +-600: no exponential overflows, a certain token's loss is 0."""
+    X = torch.zeros(3, 8, device="cuda", dtype=BF)
+    W = torch.zeros(200, 8, device="cuda", dtype=BF)
+    X[:, 0] = torch.tensor([600.0, -600.0, 0.0], device="cuda")
+    W[17, 0] = 1.0
+    y = torch.tensor([17, 17, 3], device="cuda")
+    loss, lse, _ = forge.linear_cross_entropy(X, W, y, reduction="none")
+    want = torch.logsumexp(X.double() @ W.double().t(), 1)
+    assert torch.allclose(lse.double(), want, rtol=1e-6)
+    assert torch.allclose(loss.double(), torch.tensor([0.0, 600.0 + float(want[1]), float(want[2])], device="cuda",
+                                                      dtype=torch.float64), rtol=1e-6, atol=1e-4)
+
+
+def test_empty_sizes():
+    z = lambda *s: torch.zeros(*s, device="cuda", dtype=BF)  # noqa: E731
+    assert forge.linear(z(0, 64), z(32, 64)).shape == (0, 32)
+    assert forge.gated(z(0, 64), z(32, 64), z(32, 64)).shape == (0, 32)
+    b = torch.randn(32, device="cuda").to(BF)
+    # no inner dimension: what is left is act(bias) + residual
+    R = torch.randn(4, 32, device="cuda").to(BF)
+    got = forge.linear(z(4, 0), z(32, 0), bias=b, act="silu", residual=R)
+    close("no inner dimension", got, *linear64(z(4, 0), z(32, 0), b, "silu", R)[:2])
+    dZ, db = forge.linear_act_backward(z(0, 32), z(0, 32), act="silu")
+    assert dZ.shape == (0, 32) and torch.all(db == 0)
+    assert torch.all(forge.dgrad_group([z(5, 0)], [z(0, 16)]) == 0)
+    y = torch.zeros(0, device="cuda", dtype=torch.int64)
+    loss, lse, total = forge.linear_cross_entropy(z(0, 64), z(100, 64), y)
+    assert torch.isnan(loss) and lse.numel() == 0 and float(total[0]) == 0 and float(total[1]) == 0
+    dX, dW = forge.linear_cross_entropy_backward(z(0, 64), z(100, 64), y, lse, torch.ones((), device="cuda"),
+                                                 total=total)
+    assert dX.shape == (0, 64) and torch.all(dW == 0)
+
+
+STEP_OPTS = [("adamw", "f32"), ("sgd", "f32"), ("lion", "bf16"), ("adamw", "q8"), ("adamw", "q8dyn"),
+             ("rmsprop", "f32")]
+
+
+@pytest.mark.parametrize("opt,states", STEP_OPTS)
+@pytest.mark.parametrize("v", [1000, 1003])
+def test_cross_entropy_step(opt, states, v):
+    """The head's fused step in pieces of the vocabulary equals the fused step of the whole W on
+    the same dz (bit for bit: same element indices and random streams), and dX is of the old W."""
+    t, i = 190, 128
+    X, W, y = head(v, t, i, v, BF)
+    dloss = torch.full((), 0.75, device="cuda")
+    code = "dynamic" if states == "q8dyn" else "linear"
+    _, lse, total = forge.linear_cross_entropy(X, W, y)
+    old = W.clone()
+
+    def run(piece):
+        w = old.clone()
+        m, vv, ms, vs = forge.new_states(w, opt, states)
+        outs = []
+        for step in (1, 2):
+            outs.append(forge.linear_cross_entropy_step(X, w, m, vv, y, lse, dloss, opt, None, step, 99, ms, vs,
+                                                        code=code, total=total, piece=piece))
+        return outs + [t_ for t_ in (w, m, vv, ms, vs) if t_ is not None]
+
+    whole = run(0)
+    dx, ex, _, _ = xent_grad64(X, old, y, -100, dloss.double() / total[1].double() * (y != -100), BF)
+    close("dX", whole[0], dx, ex)
+    assert not torch.equal(whole[2], old)
+    for piece in (256, 520):
+        part = run(piece)
+        for a, b in zip(whole[2:], part[2:]):
+            # the tile shape, and with it the order of the token sum, follows the piece's size:
+            # 190 tokens give one order of tokens in every configuration but the k-split ones
+            assert a.shape == b.shape
+        # dX of a piecewise sum differs by its float32 order only
+        close(f"dX of pieces {piece}", part[0], dx, ex)
+        # weights: within the step that a gradient error of the FP32 sum can make
+        d = (whole[2].float() - part[2].float()).abs()
+        assert float(d.max()) <= 2.0 ** -7 * float(old.abs().max()) * 2
+
+
+def test_step_on_a_multiple_of_eight_equals_wgrad_step():
+    """One piece: the head's step is wgrad_step on the dz that the plain gradient call forms."""
+    t, i, v = 100, 64, 264
+    X, W, y = head(5, t, i, v, F, ignored=0.0)
+    _, lse, total = forge.linear_cross_entropy(X, W, y, reduction="sum")
+    one = torch.ones((), device="cuda")
+    w = W.clone()
+    forge.linear_cross_entropy_step(X, w, None, None, y, lse, one, "sgd", {"lr": 1.0, "stochastic_round": 0}, 1, 0,
+                                    reduction="sum")
+    _, dW = forge.linear_cross_entropy_backward(X, W, y, lse, one, reduction="sum")
+    # the fp32 GEMMs differ in their order of summation only
+    _, _, _, ew = xent_grad64(X, W, y, -100, torch.ones(t, device="cuda", dtype=torch.float64), F)
+    err = ((W - w).double() - dW.double()).abs()
+    assert torch.all(err <= 2 * ew + 2.0 ** -23 * W.double().abs() + 2.0 ** -22 * dW.double().abs())

@@ -1,0 +1,200 @@
+"""Host checks of the operators around the fused step, on the CPU: every refusal the C ABI
+documents is returned before anything is enqueued (the descriptors hold made-up addresses),
+workspace sizes, and the Python layer's own argument checks."""
+import ctypes
+
+import pytest
+import torch
+
+import optimizer_gemm_amd as forge
+from optimizer_gemm_amd.forge import BF16, E4M3, F32, ForgeTensor
+
+NULL, SHAPE, DTYPE, ALIGN, UNSUP, HYPER, ALIAS, SCRATCH = -1, -2, -3, -4, -5, -6, -8, -9
+L = forge.lib()
+BASE = 1 << 32
+
+
+def ten(k, rows, cols, dt=BF16, ld=None, off=0):
+    """descriptor number k, far from the others'"""
+    return ForgeTensor(BASE + (k << 33) + off, dt, 0, rows, cols, cols if ld is None else ld, None)
+
+
+def ref(t):
+    return ctypes.byref(t) if t is not None else None
+
+
+def linear(X=None, W=None, bias=None, act=0, R=None, Y=None, Z=None):
+    X = X or ten(0, 16, 64)
+    W = W or ten(1, 32, 64)
+    Y = Y or ten(2, 16, 32)
+    return L.forge_linear_forward(ref(X), ref(W), ref(bias), act, ref(R), ref(Y), ref(Z), None)
+
+
+def test_linear_refusals():
+    assert L.forge_linear_forward(None, ref(ten(1, 32, 64)), None, 0, None, ref(ten(2, 16, 32)), None, None) == NULL
+    assert linear(act=5) == UNSUP and linear(act=-1) == UNSUP
+    assert linear(X=ten(0, 16, 72)) == SHAPE
+    assert linear(Y=ten(2, 16, 40)) == SHAPE and linear(Y=ten(2, 8, 32)) == SHAPE
+    assert linear(X=ten(0, 16, 64, F32)) == DTYPE
+    assert linear(X=ten(0, 16, 64, E4M3), W=ten(1, 32, 64, E4M3)) == UNSUP
+    assert linear(W=ten(1, 32, 64, 2)) == DTYPE
+    assert linear(X=ten(0, 16, 64, ld=68)) == ALIGN and linear(X=ten(0, 16, 64, off=8)) == ALIGN
+    assert linear(W=ten(1, 36, 64), Y=ten(2, 16, 36)) == ALIGN
+    assert linear(X=ten(0, 16, 64, ld=56)) == SHAPE
+    assert linear(bias=ten(3, 1, 40)) == SHAPE and linear(bias=ten(3, 2, 32)) == SHAPE
+    assert linear(bias=ten(3, 1, 32, 2)) == DTYPE
+    assert linear(R=ten(3, 16, 24)) == SHAPE and linear(R=ten(3, 16, 32, F32)) == DTYPE
+    assert linear(Y=ten(0, 16, 32)) == ALIAS
+    assert linear(R=ten(2, 16, 32)) == ALIAS
+    assert linear(Z=ten(2, 16, 32, off=32)) == ALIAS
+    assert linear(X=ten(0, 1 << 25, 64), Y=ten(2, 1 << 25, 32)) == UNSUP
+
+
+def test_act_backward_refusals():
+    dY, Z, dZ = ten(0, 4096, 64), ten(1, 4096, 64), ten(2, 4096, 64)
+    need = L.forge_linear_act_backward_workspace(4096, 64)
+    assert need > 0 and need % 16 == 0 and L.forge_linear_act_backward_workspace(1, 64) == 0
+
+    def call(dY=dY, Z=Z, act=2, dZ=dZ, db=BASE + (5 << 33), ws=BASE + (6 << 33), n=need):
+        return L.forge_linear_act_backward(ref(dY), ref(Z), act, ref(dZ), db, ws, n, None)
+
+    assert call(act=9) == UNSUP
+    assert call(Z=None) == NULL and call(dZ=None) == NULL and call(ws=None) == NULL
+    assert call(n=need - 1) == SCRATCH
+    assert call(ws=BASE + (6 << 33) + 4) == ALIGN and call(db=BASE + 4) == ALIGN
+    assert call(Z=ten(1, 4096, 72)) == SHAPE
+    assert call(dZ=ten(0, 4096, 64)) == ALIAS
+    assert call(db=BASE + (6 << 33)) == ALIAS
+    assert call(dY=ten(0, 4096, 64, E4M3)) == UNSUP
+
+
+def test_gated_refusals():
+    X, Wg, Wu, H = ten(0, 16, 64), ten(1, 32, 64), ten(2, 32, 64), ten(3, 16, 32)
+
+    def call(X=X, Wg=Wg, Wu=Wu, act=2, H=H, G=None, U=None):
+        return L.forge_gated_forward(ref(X), ref(Wg), ref(Wu), act, ref(H), ref(G), ref(U), None)
+
+    assert call(G=ten(4, 16, 32)) == NULL and call(U=ten(4, 16, 32)) == NULL
+    assert call(act=7) == UNSUP
+    assert call(Wu=ten(2, 40, 64)) == SHAPE and call(Wu=ten(2, 32, 56)) == SHAPE
+    assert call(G=ten(4, 16, 32), U=ten(5, 16, 40)) == SHAPE
+    assert call(G=ten(4, 16, 32), U=ten(4, 16, 32)) == ALIAS
+    assert call(H=ten(1, 16, 32)) == ALIAS
+    assert call(Wu=ten(2, 32, 64, F32)) == DTYPE
+
+
+def test_gated_backward_refusals():
+    a = [ten(k, 16, 32) for k in range(6)]
+
+    def call(**kw):
+        t = dict(zip(("dH", "G", "U", "dG", "dU", "H"), a), **kw)
+        return L.forge_gated_backward(ref(t["dH"]), ref(t["G"]), ref(t["U"]), 2, ref(t["dG"]), ref(t["dU"]), ref(t["H"]),
+                                      None)
+
+    assert call(G=None) == NULL and call(dU=None) == NULL and call(dH=None) == NULL
+    assert call(U=ten(2, 16, 40)) == SHAPE
+    assert call(dG=a[0]) == ALIAS and call(dU=a[1]) == ALIAS and call(H=a[3]) == ALIAS
+
+    def fused(**kw):
+        t = dict(zip(("G", "U", "dG", "dU", "H"), a[1:]), dY=ten(7, 16, 48), Wd=ten(8, 48, 32), **kw)
+        t.update(kw)
+        return L.forge_gated_dgrad(ref(t["dY"]), ref(t["Wd"]), ref(t["G"]), ref(t["U"]), 2, ref(t["dG"]), ref(t["dU"]),
+                                   ref(t["H"]), None)
+
+    assert L.forge_gated_dgrad(ref(ten(7, 16, 48)), None, ref(a[1]), ref(a[2]), 2, ref(a[3]), ref(a[4]), None,
+                               None) == NULL
+    assert fused(G=ten(1, 16, 40)) == SHAPE
+    assert fused(dG=ten(8, 16, 32)) == ALIAS and fused(H=ten(7, 16, 32)) == ALIAS
+
+
+def test_dgrad_group_refusals():
+    def call(n, dys, ws, dx):
+        A = ForgeTensor * max(1, len(dys))
+        return L.forge_linear_dgrad_group(n, A(*dys), A(*ws), ref(dx), None)
+
+    dY, W, dX = ten(0, 16, 32), ten(1, 32, 64), ten(2, 16, 64)
+    assert call(0, [dY], [W], dX) == SHAPE and call(5, [dY], [W], dX) == SHAPE
+    assert call(1, [ten(0, 8, 32)], [W], dX) == SHAPE
+    assert call(2, [dY, ten(3, 16, 40)], [W, ten(4, 48, 64)], dX) == SHAPE
+    assert call(2, [dY, ten(3, 16, 40)], [W, ten(4, 40, 72)], dX) == SHAPE
+    assert call(2, [dY, ten(3, 16, 40, F32)], [W, ten(4, 40, 64)], dX) == DTYPE
+    assert call(1, [dY], [W], ten(1, 16, 64)) == ALIAS
+
+
+def test_xent_refusals():
+    T, D, V = 32, 64, 1001
+    X, W = ten(0, T, D), ten(1, V, D)
+    tgt, lse, tot, ws = (BASE + (k << 33) for k in (4, 5, 6, 7))
+    need = L.forge_linear_xent_workspace(T, D, V, BF16, 0, 0)
+
+    def fwd(X=X, W=W, tgt=tgt, loss=None, lse=lse, tot=tot, ws=ws, n=need):
+        return L.forge_linear_xent_forward(ref(X), ref(W), tgt, -100, loss, lse, tot, ws, n, None)
+
+    assert fwd(X=None) == NULL and fwd(W=None) == NULL and fwd(tgt=None) == NULL and fwd(lse=None) == NULL
+    assert fwd(tot=None) == NULL and fwd(ws=None) == NULL
+    assert fwd(n=need - 1) == SCRATCH and fwd(ws=ws + 8) == ALIGN and fwd(tgt=tgt + 4) == ALIGN
+    assert fwd(X=ten(0, T, 72)) == SHAPE and fwd(W=ten(1, 0, D)) == SHAPE
+    assert fwd(X=ten(0, T, D, F32)) == DTYPE and fwd(X=ten(0, T, D, E4M3)) == UNSUP
+    assert fwd(lse=ws) == ALIAS and fwd(loss=lse) == ALIAS and fwd(tot=tgt) == ALIAS
+
+    dX, dW = ten(2, T, D), ten(3, V, D)
+    need_b = L.forge_linear_xent_workspace(T, D, V, BF16, 1, 0)
+    dl = BASE + (8 << 33)
+
+    def bwd(X=X, W=W, lse=lse, dl=dl, per=0, tot=tot, dX=dX, dW=dW, piece=0, ws=ws, n=need_b):
+        return L.forge_linear_xent_backward(ref(X), ref(W), tgt, -100, lse, dl, per, tot, ref(dX), ref(dW), piece, ws, n,
+                                            None)
+
+    assert bwd(lse=None) == NULL and bwd(dl=None) == NULL and bwd(ws=None) == NULL
+    assert bwd(n=need_b - 1) == SCRATCH
+    assert bwd(piece=12) == SHAPE and bwd(piece=-8) == SHAPE
+    assert bwd(dX=ten(2, T, 72)) == SHAPE and bwd(dW=ten(3, V - 1, D)) == SHAPE
+    assert bwd(dX=ten(1, T, D)) == ALIAS and bwd(dW=ten(2, V, D)) == ALIAS and bwd(dl=ws) == ALIAS
+    assert bwd(dW=ten(3, V, D, F32)) == DTYPE
+
+    h = forge.make_hyper("adamw")
+    m, v = ten(9, V, D, F32), ten(10, V, D, F32)
+
+    def step(W=W, m=m, v=v, opt=0, n=need_b, t=1, dX=dX):
+        return L.forge_linear_xent_step(ref(X), ref(W), ref(m), ref(v), opt, ctypes.byref(h), t, 0, tgt, -100, lse, dl, 0,
+                                        tot, ref(dX), 0, ws, n, None)
+
+    assert step(opt=8) == HYPER and step(t=0) == HYPER
+    assert step(m=None) == NULL and step(m=ten(9, V, 72, F32)) == SHAPE and step(v=ten(10, V, D)) == DTYPE
+    assert step(n=need_b - 1) == SCRATCH
+    assert step(m=ten(1, V, D, F32)) == ALIAS and step(dX=ten(0, T, D)) == ALIAS
+    assert step(W=ten(1, 1 << 24, D), m=ten(9, 1 << 24, D, F32), v=ten(10, 1 << 24, D, F32)) == UNSUP
+
+
+def test_xent_workspace_sizes():
+    """Grows with what it holds; a piece bounds the gradient's; nonsense is 0."""
+    f = L.forge_linear_xent_workspace
+    assert f(-1, 64, 10, BF16, 0, 0) == 0 and f(4, 64, 0, BF16, 1, 0) == 0 and f(4, 64, 8, BF16, 1, -1) == 0
+    t, d, v = 8192, 4096, 131072
+    whole, small = f(t, d, v, BF16, 1, 0), f(t, d, v, BF16, 1, 1024)
+    assert small == t * 1024 * 2 + t * d * 4
+    assert whole <= (1 << 30) * 1.05 + t * d * 4 and whole > small
+    # the forward pass holds pairs per block of the vocabulary, far below the logits
+    assert f(t, d, v, BF16, 0, 0) < t * v * 2 / 10
+    # dz of a piece stays below 2^31 bytes, whatever is asked for
+    assert f(1 << 20, 64, 1 << 20, BF16, 1, 1 << 20) < (1 << 31) + (1 << 20) * 64 * 4 + 16
+
+
+def test_python_checks():
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    with pytest.raises(ValueError, match="device tensors"):
+        forge.linear(z(4, 64), z(32, 64))
+    with pytest.raises(ValueError, match="unknown activation"):
+        forge.linear(z(4, 64), z(32, 64), act="tanh")
+    with pytest.raises(ValueError, match="unknown activation"):
+        forge.gated(z(4, 64), z(32, 64), z(32, 64), act="swish")
+    with pytest.raises(ValueError, match="needs Z"):
+        forge.linear_act_backward(z(4, 64), act="relu")
+    with pytest.raises(ValueError, match="1..4 layers"):
+        forge.dgrad_group([], [])
+    with pytest.raises(ValueError, match="1..4 layers"):
+        forge.dgrad_group([z(4, 8)], [z(8, 8), z(8, 8)])
+    with pytest.raises(ValueError, match="unknown reduction"):
+        forge.linear_cross_entropy(z(4, 64), z(32, 64), torch.zeros(4, dtype=torch.int64), reduction="avg")
+    with pytest.raises(ValueError, match="one device"):
+        forge.linear(z(4, 64), torch.zeros(32, 64, dtype=torch.bfloat16, device="meta"))
