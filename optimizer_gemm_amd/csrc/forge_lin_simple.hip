@@ -9,8 +9,7 @@
 // epilogue reads and writes whole row segments.
 // Bound: LDS staging (each operand element is read from LDS for 32 rows of the other), so
 // this form serves the float32 operands and the products too small for larger tiles.
-#include "forge_gemm_kernel.h"
-#include "forge_ops.h"
+#include "forge_lin_kernel.h"
 
 namespace forge {
 namespace {
@@ -211,30 +210,40 @@ hipError_t run(const LinArgs& g, hipStream_t st) {
 
 template <class T>
 hipError_t pick(int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
-  if (!ta && !tb) {
-    switch (epi) {
-      case L_LINEAR: return run<T, L_LINEAR, false, false>(g, st);
-      case L_GATED: return run<T, L_GATED, false, false>(g, st);
-      case L_LSE: return run<T, L_LSE, false, false>(g, st);
-      case L_DLOGIT: return run<T, L_DLOGIT, false, false>(g, st);
-    }
-  } else if (ta && !tb) {
-    switch (epi) {
-      case L_DGATE: return run<T, L_DGATE, true, false>(g, st);
-      case L_ACC: return run<T, L_ACC, true, false>(g, st);
-    }
-  } else if (ta && tb && epi == L_ACC) {
-    return run<T, L_ACC, true, true>(g, st);
-  }
+#define FORGE_PICK(E, A, B) \
+  if (epi == E && ta == A && tb == B) return run<T, E, A, B>(g, st);
+  FORGE_LIN_FORMS(FORGE_PICK)
+#undef FORGE_PICK
   return hipErrorInvalidValue;
+}
+
+// tiles of 64x64: the larger kernels count theirs in 32 bits
+bool few_tiles(const LinArgs& g) {
+  return ((int64_t)g.M + S_B) / S_B * (((int64_t)g.N + S_B) / S_B) < ((int64_t)1 << 30);
 }
 
 }  // namespace
 
+#define FORGE_EXTERN_LIN(E, A, B) extern template hipError_t lin_bf16<E, A, B>(const LinArgs&, hipStream_t);
+FORGE_LIN_FORMS(FORGE_EXTERN_LIN)
+#undef FORGE_EXTERN_LIN
+
 hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
-  return bf16 ? pick<uint16_t>(epi, ta, tb, g, st) : pick<float>(epi, ta, tb, g, st);
+  if (!bf16) return pick<float>(epi, ta, tb, g, st);
+  if (!few_tiles(g)) return pick<uint16_t>(epi, ta, tb, g, st);
+#define FORGE_PICK(E, A, B) \
+  if (epi == E && ta == A && tb == B) return lin_bf16<E, A, B>(g, st);
+  FORGE_LIN_FORMS(FORGE_PICK)
+#undef FORGE_PICK
+  return hipErrorInvalidValue;
 }
 
-int lin_lse_block(int, int, int) { return S_B; }
+int lin_lse_block(int bf16, int M, int N) {
+  LinArgs g{};
+  g.M = M;
+  g.N = N;
+  if (!bf16 || !few_tiles(g)) return S_B;
+  return lin_big<L_LSE>(M, N) ? LinBig::TM : LinSmall::TM;
+}
 
 }  // namespace forge

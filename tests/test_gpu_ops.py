@@ -35,7 +35,7 @@ def pitched(t, extra=16):
 # tokens, in, out: one token; odd tokens; sizes that are no multiple of any tile; tiles in
 # every direction; more tiles than compute units
 SIZES = [(1, 8, 8), (1, 512, 264), (3, 72, 40), (7, 4096, 128), (33, 136, 1032), (130, 264, 520), (257, 96, 328),
-         (511, 1000, 776), (1000, 256, 2056), (2049, 520, 1288)]
+         (511, 1000, 776), (1000, 256, 2056), (2049, 520, 1288), (2049, 264, 4104), (16, 64, 70008)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -163,10 +163,10 @@ def test_gated_backward(t, i, o, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t,i", [(205, 456), (2049, 4104)])
 @pytest.mark.parametrize("outs", [(8,), (264, 40), (1032, 264, 264), (72, 8, 200, 520)])
-def test_dgrad_group(outs, dt):
+def test_dgrad_group(outs, t, i, dt):
     g = gen(sum(outs))
-    t, i = 205, 456
     dYs = [rnd(g, t, o, dtype=DT[dt]) for o in outs]
     Ws = [rnd(g, o, i, dtype=DT[dt]) for o in outs]
     want, bound = 0, 0
@@ -186,7 +186,8 @@ def head(seed, t, i, v, dtype, ignored=0.2, ignore=-100):
 
 
 # tokens, in, vocabulary (odd and tiny ones; a single entry: its loss is 0)
-HEADS = [(1, 8, 1), (1, 64, 7), (2, 136, 1000), (65, 264, 513), (130, 72, 2051), (300, 520, 4099), (1025, 256, 5003)]
+HEADS = [(1, 8, 1), (1, 64, 7), (2, 136, 1000), (65, 264, 513), (130, 72, 2051), (300, 520, 4099), (1025, 256, 5003),
+         (4100, 2056, 4103)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
