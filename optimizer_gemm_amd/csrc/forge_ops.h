@@ -97,8 +97,8 @@ __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
 }
 __device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 __device__ __forceinline__ void store4(uint16_t* p, f32x4 x) {
-  *reinterpret_cast<u32x2*>(p) = u32x2{rne_bf16_bits(x.x) | (rne_bf16_bits(x.y) << 16),
-                                       rne_bf16_bits(x.z) | (rne_bf16_bits(x.w) << 16)};
+  // the compiler's conversion: v_cvt_pk_bf16_f32, nearest-even, two elements per instruction
+  *reinterpret_cast<u32x2*>(p) = __builtin_bit_cast(u32x2, __builtin_convertvector(x, bf16x4));
 }
 __device__ __forceinline__ void store4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
 
@@ -164,63 +164,80 @@ __device__ __forceinline__ float epi_scale(const LinEpiArgs& e) {
   return s;
 }
 
+// The arithmetic of an epilogue on 4 neighbouring columns: x the product (x2 the second one of
+// L_GATED), a and b what it reads from in1 and in2 (zero where there is none), y0 .. y2 what it
+// writes to out .. out3.
+template <int EPI>
+__device__ __forceinline__ void epi_math(int act, f32x4 x, f32x4 x2, f32x4 a, f32x4 b, f32x4& y0, f32x4& y1, f32x4& y2) {
+  if constexpr (EPI == L_LINEAR) {  // x: bias added
+    y1 = x;
+    y0 = f32x4{act_f(x.x, act), act_f(x.y, act), act_f(x.z, act), act_f(x.w, act)} + a;
+  } else if constexpr (EPI == L_GATED) {
+    y0 = f32x4{act_f(x.x, act), act_f(x.y, act), act_f(x.z, act), act_f(x.w, act)} * x2;
+    y1 = x;
+    y2 = x2;
+  } else if constexpr (EPI == L_DGATE) {  // x = dH, a = G, b = U
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v, d;
+      act_vd(a[j], act, v, d);
+      y0[j] = x[j] * (b[j] * d);
+      y1[j] = x[j] * v;
+      y2[j] = v * b[j];
+    }
+  }
+}
+
+// dz of 4 logits x of one token: m the first one's place, M the piece's entries (past them the
+// row is padded with zeros), hit the target's place (-1: not here), l = lse, w the factor (0
+// with ignored = true, NaN for a target outside the vocabulary)
+__device__ __forceinline__ f32x4 dlogit(f32x4 x, int m, int M, int hit, float l, float w, bool ignored) {
+  f32x4 d;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float p = __expf(x[j] - l);
+    d[j] = m + j < M && !ignored ? (p - (hit == m + j ? 1.f : 0.f)) * w : 0.f;
+  }
+  return d;
+}
+// a token's target as dlogit takes it
+__device__ __forceinline__ void dlogit_row(const LinEpiArgs& e, int64_t y, float weight, float sc, int& hit, float& w,
+                                           bool& ignored) {
+  ignored = y == e.ignore;
+  const bool bad = y < 0 || y >= e.vocab;
+  const int64_t d = bad ? -1 : y - e.v0;
+  hit = d >= 0 && d < ((int64_t)1 << 30) ? (int)d : -1;
+  w = bad ? __builtin_nanf("") : weight * sc;
+}
+
 // One 4-vector of the output: row n, columns m..m+3 (all inside the output's padded
 // width); x the product, x2 the second product of L_GATED; sc = epi_scale.
 template <class T, int EPI>
 __device__ __forceinline__ void epi_vec(const LinEpiArgs& e, int n, int m, int M, f32x4 x, f32x4 x2, float sc) {
-  if constexpr (EPI == L_LINEAR) {
-    if (e.bias) {
-      const f32x4 b = e.bias_f32 ? load4(static_cast<const float*>(e.bias) + m) : load4(static_cast<const T*>(e.bias) + m);
-      x = x + b;
-    }
-    if (e.out2) store4(static_cast<T*>(e.out2) + (int64_t)n * e.ldo2 + m, x);
-    f32x4 y{act_f(x.x, e.act), act_f(x.y, e.act), act_f(x.z, e.act), act_f(x.w, e.act)};
-    if (e.in1) y = y + load4(static_cast<const T*>(e.in1) + (int64_t)n * e.ld1 + m);
-    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, y);
-  } else if constexpr (EPI == L_GATED) {
-    const f32x4 h{act_f(x.x, e.act) * x2.x, act_f(x.y, e.act) * x2.y, act_f(x.z, e.act) * x2.z,
-                  act_f(x.w, e.act) * x2.w};
-    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, h);
-    if (e.out2) store4(static_cast<T*>(e.out2) + (int64_t)n * e.ldo2 + m, x);
-    if (e.out3) store4(static_cast<T*>(e.out3) + (int64_t)n * e.ldo3 + m, x2);
-  } else if constexpr (EPI == L_DGATE) {
-    const f32x4 g = load4(static_cast<const T*>(e.in1) + (int64_t)n * e.ld1 + m);
-    const f32x4 u = load4(static_cast<const T*>(e.in2) + (int64_t)n * e.ld2 + m);
-    f32x4 dg, du, h;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float a, d;
-      act_vd(g[j], e.act, a, d);
-      dg[j] = x[j] * (u[j] * d);
-      du[j] = x[j] * a;
-      h[j] = a * u[j];
-    }
-    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, dg);
-    store4(static_cast<T*>(e.out2) + (int64_t)n * e.ldo2 + m, du);
-    if (e.out3) store4(static_cast<T*>(e.out3) + (int64_t)n * e.ldo3 + m, h);
-  } else if constexpr (EPI == L_ACC) {
+  if constexpr (EPI == L_ACC) {
     if (e.acc_read) x = x + load4(e.acc + (int64_t)n * e.ldacc + m);
     if (e.acc_write)
       store4(e.acc + (int64_t)n * e.ldacc + m, x);
     else
       store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, x * sc);
   } else if constexpr (EPI == L_DLOGIT) {
-    const int64_t y = e.target[n];
-    f32x4 d{0.f, 0.f, 0.f, 0.f};
-    if (y != e.ignore) {
-      // a target outside the vocabulary has no gradient to give: the row becomes NaN
-      const bool bad = y < 0 || y >= e.vocab;
-      const float w = bad ? __builtin_nanf("") : (e.weight ? e.weight[n] * sc : sc);
-      const float l = e.lse[n];
-      const int64_t hit = bad ? -1 : y - e.v0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = __expf(x[j] - l);
-        // columns past the piece's last entry pad the row to its pitch: zeros
-        d[j] = m + j < M ? (p - (hit == m + j ? 1.f : 0.f)) * w : 0.f;
-      }
+    int hit;
+    float w;
+    bool ignored;
+    dlogit_row(e, e.target[n], e.weight ? e.weight[n] : 1.f, sc, hit, w, ignored);
+    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, dlogit(x, m, M, hit, e.lse[n], w, ignored));
+  } else {
+    f32x4 a{0.f, 0.f, 0.f, 0.f}, b = a, y0, y1, y2;
+    if constexpr (EPI == L_LINEAR) {
+      if (e.bias)
+        x = x + (e.bias_f32 ? load4(static_cast<const float*>(e.bias) + m) : load4(static_cast<const T*>(e.bias) + m));
     }
-    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, d);
+    if (e.in1) a = load4(static_cast<const T*>(e.in1) + (int64_t)n * e.ld1 + m);
+    if (e.in2) b = load4(static_cast<const T*>(e.in2) + (int64_t)n * e.ld2 + m);
+    epi_math<EPI>(e.act, x, x2, a, b, y0, y1, y2);
+    store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, y0);
+    if (e.out2) store4(static_cast<T*>(e.out2) + (int64_t)n * e.ldo2 + m, y1);
+    if (e.out3) store4(static_cast<T*>(e.out3) + (int64_t)n * e.ldo3 + m, y2);
   }
 }
 

@@ -61,7 +61,8 @@ int check_head(const forge_tensor* X, const forge_tensor* W, const int64_t* targ
   if (is_fp8(X->dtype)) return FORGE_ERR_UNSUPPORTED;
   if ((r = check_io(W, W->dtype)) || (r = check_io(X, W->dtype))) return r;
   if (X->cols != W->cols || W->rows < 1) return FORGE_ERR_SHAPE;
-  if (!fits_31(X)) return FORGE_ERR_UNSUPPORTED;
+  // (256 of its rows are addressed by 32-bit offsets)
+  if (!fits_31(X) || W->ld * (int64_t)elem_size(W->dtype) >= ((int64_t)1 << 23)) return FORGE_ERR_UNSUPPORTED;
   if (!target && X->rows > 0) return FORGE_ERR_NULL;
   return ((uintptr_t)target & 7u) ? FORGE_ERR_ALIGN : FORGE_OK;
 }
