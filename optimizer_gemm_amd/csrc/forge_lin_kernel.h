@@ -39,21 +39,24 @@
 
 namespace forge {
 
-template <int B_, int OCC_, bool AHEAD_>
+// B x B tiles, OCC waves per SIMD, KS groups of 2 x 2 waves that share a tile's k range.
+template <int B_, int OCC_, bool AHEAD_, int KS_ = 1>
 struct LTile {
-  static constexpr int BM = B_, BN = B_, BK = 64, WM = 2, WN = 2, OCC = OCC_;
+  static constexpr int BM = B_, BN = B_, BK = 64, WM = 2, WN = 2, OCC = OCC_, KS = KS_;
   // AHEAD: the epilogue's LDS is one slot, the next tile's first stages load beside it
   static constexpr bool AHEAD = AHEAD_;
-  static constexpr int NW = WM * WN, NT = 64 * NW;
+  static constexpr int NW = WM * WN * KS, NT = 64 * NW, GT = 64 * WM * WN;  // GT: threads of a group
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   static constexpr int KST = BK / 32;  // k-steps per stage
-  // LDS: five slots of one operand's stage. Stage s has A in slot 2s mod 5, B in slot
+  // LDS: five slots of one operand's stage per group. Stage s has A in slot 2s mod 5, B in slot
   // (2s + 1) mod 5: B of stage s + 2 takes the slot that A of stage s leaves, A of stage
   // s + 3 the one that B of stage s leaves.
-  static constexpr int SLOT = B_ * BK * 2, PL = SLOT / 16 / NT;  // PL: loads per slot and wave
-  static constexpr int EPIW = 32 * 64 * 4, EPI0 = AHEAD ? 4 * SLOT : 0;
-  static constexpr int SMEM = 5 * SLOT;
-  static_assert(SMEM * (OCC * 4 / NW) <= 160 * 1024 && EPI0 + NW * EPIW <= SMEM && FM % 4 == 0 && FN % 2 == 0, "tile");
+  static constexpr int SLOT = B_ * BK * 2, PL = SLOT / 16 / GT;  // PL: loads per slot and wave
+  // epilogue: KS = 1: 32 rows x 64 floats per wave; else the whole tile as rows of BM + 4 floats
+  static constexpr int EPIW = 32 * 64 * 4, EPI0 = AHEAD ? 4 * SLOT : 0, LDE = BM + 4;
+  static constexpr int SMEM = 5 * SLOT * KS;
+  static_assert(SMEM * (OCC * 4 / NW) <= 160 * 1024, "LDS");
+  static_assert(KS > 1 ? BN * LDE * 4 <= SMEM : (EPI0 + NW * EPIW <= SMEM && FM % 4 == 0 && FN % 2 == 0), "epilogue");
 };
 
 // Layout of one operand's stage in LDS: R output indexes x BK k.
@@ -61,15 +64,16 @@ template <class C, int R, bool TR>
 struct LOper {
   static constexpr int ROWB = (TR ? R : C::BK) * 2;  // bytes per LDS row
   static constexpr int CPR = ROWB / 16;              // 16-byte chunks per row
-  static constexpr int RSTEP = C::NT / CPR;          // rows between a thread's chunks
+  static constexpr int RSTEP = C::GT / CPR;          // rows between a thread's chunks
   // transpose reads: half a wave touches 32 bytes of 8 rows (r .. r + 3 and r + 8 .. r + 11), all
   // in different 32-byte bank groups; k-fast rows (two per 256-byte bank period): 16 consecutive
   // rows in all 16 chunk groups
+  // (rows of 128 bytes, two per bank period, take the pairs of rows apart by the row's own bit)
   __host__ __device__ static constexpr int swz(int row) {
-    return TR ? 4 * (row & 3) + 2 * ((row >> 3) & 1) : (row >> 1) & 7;
+    return !TR ? (row >> 1) & 7 : (CPR >= 16 ? 4 * (row & 3) + 2 * ((row >> 3) & 1) : 4 * ((row >> 1) & 1) + 2 * ((row >> 3) & 1));
   }
-  static_assert(C::NT % CPR == 0 && (TR ? RSTEP % 8 : RSTEP % 16) == 0, "rows of a thread's chunks");
-  static_assert(TR ? CPR >= 16 : CPR == 8, "row length");
+  static_assert(C::GT % CPR == 0 && (TR ? RSTEP % 8 : RSTEP % 16) == 0, "rows of a thread's chunks");
+  static_assert(TR ? CPR >= 8 : CPR == 8, "row length");
 };
 
 // 16 bytes per lane from buffer offset off + soff into LDS at dst + 16 * lane
@@ -111,10 +115,13 @@ void lin_kernel(LinArgs g) {
   constexpr int PA = C::PL, PB = C::PL;
   static_assert(!TWO || (!TA && PA % 2 == 0), "gate and up: k fast, half of the loads each");
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::SMEM];
-  const int tid = threadIdx.x;
-  const int wave_u = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = C::KS > 1 ? static_cast<int>(threadIdx.x) % C::GT : static_cast<int>(threadIdx.x);
+  // the wave in its group, the group (its share of the k range, its ring)
+  const int wave_a = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int wave_u = C::KS > 1 ? wave_a % (C::WM * C::WN) : wave_a, grp = C::KS > 1 ? wave_a / (C::WM * C::WN) : 0;
   const int wm = wave_u % C::WM, wn = wave_u / C::WM;
-  const uint32_t lds0 = lds_addr(smem);
+  uint8_t* const ring = smem + grp * 5 * C::SLOT;
+  const uint32_t lds0 = lds_addr(smem) + (uint32_t)(grp * 5 * C::SLOT);
   const int ntm = (epi_width<EPI>(g.M) - g.m_off + OM - 1) / OM, ntn = (g.N - g.n_off + C::BN - 1) / C::BN;
   const int ntiles = ntm * ntn;
   const LinArgsPtr ga = lin_args();
@@ -123,6 +130,7 @@ void lin_kernel(LinArgs g) {
   if constexpr (MULTI) {
     for (int s = 1; s < nsrc; ++s) nst += (ga->K[s] + C::BK - 1) / C::BK;
   }
+  const int mine = C::KS > 1 ? (nst + C::KS - 1) / C::KS : nst;  // stages of a group
 
   // ---- operand loads ----
   // The stage of each operand that is loaded next (the two are one stage apart): the pair it
@@ -192,7 +200,7 @@ void lin_kernel(LinArgs g) {
   // the j-th load of an operand's next stage, into slot (0..4)
   auto dma_a = [&](int slot, auto j_c) FORGE_INLINE {
     constexpr int j = decltype(j_c)::value;
-    uint8_t* dst = smem + slot * C::SLOT + j * C::NT * 16 + wave_u * 1024;
+    uint8_t* dst = ring + slot * C::SLOT + j * C::GT * 16 + wave_u * 1024;
     const uint32_t off = fa_k + a_k + (TA ? j * OA::RSTEP : 0) < fa_K ? av[j] : kOOB;
     if constexpr (TWO && j >= PA / 2)
       dma16s(rA2, dst, off, soff(fa_k, fa_K, fa_kb));
@@ -201,7 +209,7 @@ void lin_kernel(LinArgs g) {
   };
   auto dma_b = [&](int slot, auto j_c) FORGE_INLINE {
     constexpr int j = decltype(j_c)::value;
-    uint8_t* dst = smem + slot * C::SLOT + j * C::NT * 16 + wave_u * 1024;
+    uint8_t* dst = ring + slot * C::SLOT + j * C::GT * 16 + wave_u * 1024;
     const uint32_t off = fb_k + b_k + (TB ? j * OB::RSTEP : 0) < fb_K ? bv[j] : kOOB;
     dma16s(rB, dst, off, soff(fb_k, fb_K, fb_kb));
   };
@@ -224,8 +232,17 @@ void lin_kernel(LinArgs g) {
     g_tile(tile, ntm, ntn, tm, tn);
     lm0 = g.m_off + tm * OM;
     ln0 = g.n_off + tn * C::BN;
-    source_a(0);
-    source_b(0);
+    int src0 = 0, k0 = C::KS > 1 ? grp * mine * C::BK : 0;  // the group's first stage: its pair and k
+    if constexpr (MULTI && C::KS > 1) {
+      while (src0 + 1 < nsrc && k0 >= (ga->K[src0] + C::BK - 1) / C::BK * C::BK) {
+        k0 -= (ga->K[src0] + C::BK - 1) / C::BK * C::BK;
+        ++src0;
+      }
+    }
+    source_a(src0);
+    source_b(src0);
+    fa_k = k0;
+    fb_k = k0;
     static_for<0, 2>([&](auto s_c) FORGE_INLINE {
       constexpr int s = decltype(s_c)::value;
       static_for<0, PA>([&](auto j_c) FORGE_INLINE { dma_a(2 * s, j_c); });
@@ -241,10 +258,11 @@ void lin_kernel(LinArgs g) {
   // l mod 4) reads row 8 q + r4, elements 4 c4 .. + 3 of the 16-wide fragment and receives 4 k of
   // output index l mod 16; a second read 4 rows on gives the other 4.
   const int lane = tid & 63, q16 = lane >> 4, l16 = lane & 15;
-  auto tr_addr = [&](int base, int rowb, int col0) FORGE_INLINE -> uint32_t {
+  auto tr_addr = [&](int base, int rowb, int swz, int col0) FORGE_INLINE -> uint32_t {
     const int row = 8 * q16 + (l16 >> 2), chunk = col0 / 8 + ((lane & 3) >> 1);
-    return lds0 + (uint32_t)(base + row * rowb + 16 * (chunk ^ (4 * (row & 3) + 2 * ((row >> 3) & 1))) + 8 * (lane & 1));
+    return lds0 + (uint32_t)(base + row * rowb + 16 * (chunk ^ swz) + 8 * (lane & 1));
   };
+  const int tr_row = 8 * q16 + (l16 >> 2);
   const int a_r0 = TWO ? wm * (C::TM / 2) : wm * C::TM, b_r0 = wn * C::TN;
   // k fast: one per k-step. k slow: one per fragment (the swizzle takes the column's bits); the
   // second read's row differs in bit 2, which the swizzle does not see.
@@ -252,7 +270,7 @@ void lin_kernel(LinArgs g) {
   uint32_t a_ad[NAA], b_ad[NBA];
   if constexpr (TA) {
 #pragma unroll
-    for (int f = 0; f < C::FM; ++f) a_ad[f] = tr_addr(0, OA::ROWB, a_r0 + 16 * f);
+    for (int f = 0; f < C::FM; ++f) a_ad[f] = tr_addr(0, OA::ROWB, OA::swz(tr_row), a_r0 + 16 * f);
   } else {
 #pragma unroll
     for (int kk = 0; kk < C::KST; ++kk)
@@ -260,7 +278,7 @@ void lin_kernel(LinArgs g) {
   }
   if constexpr (TB) {
 #pragma unroll
-    for (int f = 0; f < C::FN; ++f) b_ad[f] = tr_addr(C::SLOT, OB::ROWB, b_r0 + 16 * f);
+    for (int f = 0; f < C::FN; ++f) b_ad[f] = tr_addr(C::SLOT, OB::ROWB, OB::swz(tr_row), b_r0 + 16 * f);
   } else {
 #pragma unroll
     for (int kk = 0; kk < C::KST; ++kk)
@@ -385,7 +403,7 @@ void lin_kernel(LinArgs g) {
     // and a second copy of their MFMAs on another path makes the compiler move them through
     // memory; the stages past the last one are loaded too, as zeros.
 #pragma unroll 1
-    for (int s = 0; s < nst; ++s) {
+    for (int s = 0; s < mine; ++s) {
       const int slot_a2 = pb_slot, slot_b2 = sa;
       pb_slot = sb;
       lgkm_wait<0>();
@@ -420,7 +438,64 @@ void lin_kernel(LinArgs g) {
     int etid = static_cast<int>(threadIdx.x);
     asm volatile("" : "+v"(etid));
     const int e_lane = etid & 63, e_q = e_lane >> 4, e_l16 = e_lane & 15;
-    if constexpr (EPI == L_LSE) {
+    if constexpr (C::KS > 1) {
+      // the groups' partial tiles are summed in order in LDS, as rows of the output
+      float* E = reinterpret_cast<float*>(smem);
+      const int t = static_cast<int>(threadIdx.x);
+      __syncthreads();
+#pragma unroll 1
+      for (int kg = 0; kg < C::KS; ++kg) {
+        if (grp == kg) {
+#pragma unroll
+          for (int fn = 0; fn < C::FN; ++fn)
+#pragma unroll
+            for (int fm = 0; fm < C::FM; ++fm) {
+              const int col = !TWO ? wm * C::TM + 16 * fm
+                                   : (fm < C::FM / 2 ? 0 : C::BM / 2 - C::TM / 2) + wm * (C::TM / 2) + 16 * fm;
+              f32x4* p = reinterpret_cast<f32x4*>(E + (wn * C::TN + 16 * fn + e_l16) * C::LDE + col + 4 * e_q);
+              *p = kg == 0 ? acc[fm][fn] : *p + acc[fm][fn];
+            }
+        }
+        __syncthreads();
+      }
+      if constexpr (EPI == L_LSE) {
+        // NT / BN threads per token, each a stretch of its logits
+        constexpr int TP = C::NT / C::BN, W = C::BM / TP;
+        const int n = n0 + t / TP, c0 = (t % TP) * W;
+        const float* row = E + (t / TP) * C::LDE + c0;
+        const int left = g.M - m0 - c0;
+        float mx = -__builtin_huge_valf(), sum = 0.f;
+        for (int j = 0; j < W; ++j)
+          if (j < left) mx = fmaxf(mx, row[j]);
+#pragma unroll
+        for (int h = 1; h < TP; h <<= 1) mx = fmaxf(mx, __shfl_xor(mx, h));
+        const float ref = mx > -__builtin_huge_valf() ? mx : 0.f;
+        for (int j = 0; j < W; ++j)
+          if (j < left) sum += __expf(row[j] - ref);
+#pragma unroll
+        for (int h = 1; h < TP; h <<= 1) sum += __shfl_xor(sum, h);
+        if (n < g.N) {
+          const int64_t y = g.e.target[n], d = y - (m0 + c0);
+          if (y >= 0 && d >= 0 && d < W && d < left) g.e.tlogit[n] = row[d];
+          if (t % TP == 0)
+            *reinterpret_cast<float2*>(g.e.part + ((int64_t)(m0 / C::BM) * g.e.part_ld + n) * 2) = float2{mx, sum};
+        }
+      } else {
+        const float sc = (EPI == L_ACC || EPI == L_DLOGIT) ? epi_scale(g.e) : 1.f;
+        const int Mw = epi_width<EPI>(g.M);
+        act_dispatch<EPI>(g.e.act, [&](auto act_c) {
+          for (int v = t; v < C::BN * OM / 4; v += C::NT) {
+            const int row = v / (OM / 4), col = (v % (OM / 4)) * 4, n = n0 + row, m = m0 + col;
+            if (n < g.N && m < Mw) {
+              const f32x4 x = *reinterpret_cast<const f32x4*>(E + row * C::LDE + col);
+              f32x4 x2 = x;
+              if constexpr (TWO) x2 = *reinterpret_cast<const f32x4*>(E + row * C::LDE + C::BM / 2 + col);
+              epi_vec<uint16_t, EPI, decltype(act_c)::value>(g.e, n, m, g.M, x, x2, sc);
+            }
+          }
+        });
+      }
+    } else if constexpr (EPI == L_LSE) {
       next_tile();
       // lane (q, l16): logits m = 16 fm + 4 q + j of token n = l16
       const int mb = m0 + wm * C::TM;
@@ -663,13 +738,7 @@ void lin_kernel(LinArgs g) {
               if constexpr (EPI != L_LINEAR) r2[k] = pack(y2, v2);
             }
           };
-          switch (e.act) {
-            case FORGE_ACT_RELU: math(std::integral_constant<int, FORGE_ACT_RELU>{}); break;
-            case FORGE_ACT_SILU: math(std::integral_constant<int, FORGE_ACT_SILU>{}); break;
-            case FORGE_ACT_GELU: math(std::integral_constant<int, FORGE_ACT_GELU>{}); break;
-            case FORGE_ACT_GELU_TANH: math(std::integral_constant<int, FORGE_ACT_GELU_TANH>{}); break;
-            default: math(std::integral_constant<int, FORGE_ACT_NONE>{}); break;
-          }
+          act_dispatch<EPI>(e.act, math);
           put(r0, e.out, e.ldo, 2, 0, blk);
           if (e.out2) put(r1, e.out2, e.ldo2, 2, 0, blk);
           if constexpr (EPI != L_LINEAR) {
@@ -709,6 +778,8 @@ void lin_kernel(LinArgs g) {
 
 using LinBig = LTile<256, 1, true>;
 using LinSmall = LTile<128, 2, false>;
+using LinSplit = LTile<128, 2, false, 2>;
+using LinTiny = LTile<64, 4, false, 4>;
 
 template <class C, int EPI, bool TA, bool TB>
 hipError_t lin_run(const LinArgs& g, hipStream_t st) {
@@ -722,18 +793,28 @@ hipError_t lin_run(const LinArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Large tiles for more than half a round of them (one partial round of 256x256 tiles beats
-// two of 128x128 tiles, whose operand bytes per product are twice as many); else 128x128.
+// Which tiles: 256x256 for more than half a round of them (one partial round beats two of
+// 128x128 tiles, whose operand bytes per product are twice as many); 128x128, two workgroups
+// per compute unit, for more than one per unit; 128x128 with two groups of waves on a tile's k
+// range for more than half a unit's worth; else 64x64 with four groups, where the chain of
+// stages, each a trip to memory, is what takes the time.
+enum LinTileKind { LT_BIG, LT_SMALL, LT_SPLIT, LT_TINY };
 template <int EPI>
-inline bool lin_big(int64_t M, int64_t N) {
-  const int64_t OM = EPI == L_GATED ? 128 : 256;
-  return 2 * ((M + OM - 1) / OM) * ((N + 255) / 256) > g_num_cus();
+inline LinTileKind lin_tile(int64_t M, int64_t N) {
+  const int64_t cus = g_num_cus(), w = EPI == L_GATED ? 2 * M : M;
+  if (2 * ((w + 255) / 256) * ((N + 255) / 256) > cus) return LT_BIG;
+  const int64_t t = ((w + 127) / 128) * ((N + 127) / 128);
+  return t > cus ? LT_SMALL : (2 * t > cus ? LT_SPLIT : LT_TINY);
 }
 
 template <int EPI, bool TA, bool TB>
 hipError_t lin_bf16(const LinArgs& g, hipStream_t st) {
-  return lin_big<EPI>(epi_width<EPI>(g.M), g.N) ? lin_run<LinBig, EPI, TA, TB>(g, st)
-                                                : lin_run<LinSmall, EPI, TA, TB>(g, st);
+  switch (lin_tile<EPI>(epi_width<EPI>(g.M), g.N)) {
+    case LT_BIG: return lin_run<LinBig, EPI, TA, TB>(g, st);
+    case LT_SMALL: return lin_run<LinSmall, EPI, TA, TB>(g, st);
+    case LT_SPLIT: return lin_run<LinSplit, EPI, TA, TB>(g, st);
+    default: return lin_run<LinTiny, EPI, TA, TB>(g, st);
+  }
 }
 
 #define FORGE_LIN_FORMS(X)                                                                                  \

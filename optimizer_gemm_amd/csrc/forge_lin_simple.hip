@@ -184,16 +184,17 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
     }
   } else {
     const int Mw = epi_width<EPI>(g.M);
-#pragma unroll
-    for (int j = 0; j < S_B * S_B / 4 / S_NT; ++j) {
-      const int v = tid + j * S_NT, r = v / (S_B / 4), c = (v % (S_B / 4)) * 4;
-      const int n = n0 + r, m = m0 + c;
-      if (n >= g.N || m >= Mw) continue;
-      const f32x4 x = *reinterpret_cast<const f32x4*>(E + r * LDE + c);
-      f32x4 x2 = x;
-      if constexpr (TWO) x2 = *reinterpret_cast<const f32x4*>(E2 + r * LDE + c);
-      epi_vec<T, EPI>(g.e, n, m, g.M, x, x2, sc);
-    }
+    act_dispatch<EPI>(g.e.act, [&](auto act_c) {
+      for (int j = 0; j < S_B * S_B / 4 / S_NT; ++j) {
+        const int v = tid + j * S_NT, r = v / (S_B / 4), c = (v % (S_B / 4)) * 4;
+        const int n = n0 + r, m = m0 + c;
+        if (n >= g.N || m >= Mw) continue;
+        const f32x4 x = *reinterpret_cast<const f32x4*>(E + r * LDE + c);
+        f32x4 x2 = x;
+        if constexpr (TWO) x2 = *reinterpret_cast<const f32x4*>(E2 + r * LDE + c);
+        epi_vec<T, EPI, decltype(act_c)::value>(g.e, n, m, g.M, x, x2, sc);
+      }
+    });
   }
   }
 }
@@ -243,7 +244,12 @@ int lin_lse_block(int bf16, int M, int N) {
   g.M = M;
   g.N = N;
   if (!bf16 || !few_tiles(g)) return S_B;
-  return lin_big<L_LSE>(M, N) ? LinBig::TM : LinSmall::TM;
+  switch (lin_tile<L_LSE>(M, N)) {
+    case LT_BIG: return LinBig::TM;  // a wave's entries
+    case LT_SMALL: return LinSmall::TM;
+    case LT_SPLIT: return LinSplit::BM;  // a tile's
+    default: return LinTiny::BM;
+  }
 }
 
 }  // namespace forge

@@ -11,6 +11,8 @@
 //   weight grad. m = in, n = out, k = tokens:   A = X (k slow), B = dY (k slow)
 #pragma once
 
+#include <type_traits>
+
 #include "forge_internal.h"
 
 namespace forge {
@@ -210,9 +212,26 @@ __device__ __forceinline__ void dlogit_row(const LinEpiArgs& e, int64_t y, float
   w = bad ? __builtin_nanf("") : weight * sc;
 }
 
+// f(integral_constant<act>): one branch on the activation around a whole loop, where the epilogue
+// has one
+template <int EPI, class F>
+__device__ __forceinline__ void act_dispatch(int act, F&& f) {
+  if constexpr (EPI != L_LINEAR && EPI != L_GATED && EPI != L_DGATE) {
+    f(std::integral_constant<int, FORGE_ACT_NONE>{});
+  } else {
+    switch (act) {
+      case FORGE_ACT_RELU: f(std::integral_constant<int, FORGE_ACT_RELU>{}); break;
+      case FORGE_ACT_SILU: f(std::integral_constant<int, FORGE_ACT_SILU>{}); break;
+      case FORGE_ACT_GELU: f(std::integral_constant<int, FORGE_ACT_GELU>{}); break;
+      case FORGE_ACT_GELU_TANH: f(std::integral_constant<int, FORGE_ACT_GELU_TANH>{}); break;
+      default: f(std::integral_constant<int, FORGE_ACT_NONE>{}); break;
+    }
+  }
+}
+
 // One 4-vector of the output: row n, columns m..m+3 (all inside the output's padded
-// width); x the product, x2 the second product of L_GATED; sc = epi_scale.
-template <class T, int EPI>
+// width); x the product, x2 the second product of L_GATED; sc = epi_scale; ACT = e.act.
+template <class T, int EPI, int ACT>
 __device__ __forceinline__ void epi_vec(const LinEpiArgs& e, int n, int m, int M, f32x4 x, f32x4 x2, float sc) {
   if constexpr (EPI == L_ACC) {
     if (e.acc_read) x = x + load4(e.acc + (int64_t)n * e.ldacc + m);
@@ -234,7 +253,7 @@ __device__ __forceinline__ void epi_vec(const LinEpiArgs& e, int n, int m, int M
     }
     if (e.in1) a = load4(static_cast<const T*>(e.in1) + (int64_t)n * e.ld1 + m);
     if (e.in2) b = load4(static_cast<const T*>(e.in2) + (int64_t)n * e.ld2 + m);
-    epi_math<EPI>(e.act, x, x2, a, b, y0, y1, y2);
+    epi_math<EPI>(ACT, x, x2, a, b, y0, y1, y2);
     store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, y0);
     if (e.out2) store4(static_cast<T*>(e.out2) + (int64_t)n * e.ldo2 + m, y1);
     if (e.out3) store4(static_cast<T*>(e.out3) + (int64_t)n * e.ldo3 + m, y2);

@@ -25,21 +25,24 @@ __global__ __launch_bounds__(AB_NT) void act_backward_kernel(int act, const T* d
   const int r0 = blockIdx.y * rows_per, r1 = min(R, r0 + rows_per);
   f32x4 sum{0.f, 0.f, 0.f, 0.f};
   if (c < out) {
+    act_dispatch<L_DGATE>(act, [&](auto act_c) {
+      constexpr int ACT = decltype(act_c)::value;
 #pragma unroll 4
-    for (int r = r0 + wave; r < r1; r += 4) {
-      f32x4 d = load4(dY + (int64_t)r * lddy + c);
-      if (act != FORGE_ACT_NONE) {
-        const f32x4 z = load4(Z + (int64_t)r * ldz + c);
+      for (int r = r0 + wave; r < r1; r += 4) {
+        f32x4 d = load4(dY + (int64_t)r * lddy + c);
+        if constexpr (ACT != FORGE_ACT_NONE) {
+          const f32x4 z = load4(Z + (int64_t)r * ldz + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float a, g;
-          act_vd(z[j], act, a, g);
-          d[j] *= g;
+          for (int j = 0; j < 4; ++j) {
+            float a, g;
+            act_vd(z[j], ACT, a, g);
+            d[j] *= g;
+          }
         }
+        if (dZ) store4(dZ + (int64_t)r * lddz + c, d);
+        sum = sum + d;
       }
-      if (dZ) store4(dZ + (int64_t)r * lddz + c, d);
-      sum = sum + d;
-    }
+    });
   }
   if (!part) return;
   if (wave) *reinterpret_cast<f32x4*>(&red[wave - 1][lane * 4]) = sum;
@@ -65,11 +68,13 @@ template <class T>
 __global__ __launch_bounds__(256) void gated_backward_kernel(const T* dH, int64_t lddh, LinEpiArgs e, int R, int hid) {
   const int per = hid / 4;  // 4-vectors per row
   const int64_t total = (int64_t)R * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int n = (int)(i / per), m = (int)(i - (int64_t)n * per) * 4;
-    const f32x4 x = load4(dH + (int64_t)n * lddh + m);
-    epi_vec<T, L_DGATE>(e, n, m, hid, x, x, 1.f);
-  }
+  act_dispatch<L_DGATE>(e.act, [&](auto act_c) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+      const int n = (int)(i / per), m = (int)(i - (int64_t)n * per) * 4;
+      const f32x4 x = load4(dH + (int64_t)n * lddh + m);
+      epi_vec<T, L_DGATE, decltype(act_c)::value>(e, n, m, hid, x, x, 1.f);
+    }
+  });
 }
 
 // ---- join of the cross entropy's partial results --------------------------

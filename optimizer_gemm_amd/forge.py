@@ -450,34 +450,60 @@ class _On:
     """The device and stream of a call: every tensor on one device, which is made current for
     the call; the work goes to `stream`, or to that device's current stream."""
 
-    def __init__(self, stream, *tensors):
-        given = [t for t in tensors if t is not None]
-        self.device = given[0].device
-        for t in given:
-            if t.device != self.device:
+    __slots__ = ("device", "stream", "_given", "_guard", "_index")
+
+    def __init__(self, stream, first, *others):
+        self._index = index = first.get_device()
+        for t in others:
+            if t is not None and (t.get_device() != index or (index < 0 and t.device != first.device)):
                 raise ValueError("the tensors of a call live on one device")
+        self.device = first.device
         if self.device.type != "cuda":
             raise ValueError("forge kernels take device tensors")
         if isinstance(stream, torch.cuda.Stream) and stream.device != self.device:
             raise ValueError("the stream belongs to another device than the tensors")
         self._given = stream
-        self._guard = torch.cuda.device(self.device)
+        self._guard = None
 
     def __enter__(self):
-        self._guard.__enter__()
-        self.stream = _stream(self._given)
+        if torch.cuda.current_device() != self._index:
+            self._guard = torch.cuda.device(self._index)
+            self._guard.__enter__()
+        self.stream = _raw_stream(self._index) if self._given is None else _stream(self._given)
         return self
 
     def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+        return self._guard.__exit__(*exc) if self._guard is not None else None
 
     def empty(self, shape, dtype) -> torch.Tensor:
         """A new tensor for this call. On a stream other than the current one the memory is
         kept from being handed out again before that stream is done with it."""
         t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self._given is not None and self.stream != torch.cuda.current_stream().cuda_stream:
+        if self._given is not None and self.stream != _raw_stream(self._index):
             t.record_stream(torch.cuda.ExternalStream(self.stream))
         return t
+
+
+def _raw_stream(index: int) -> int:
+    """Handle of the device's current stream (torch's own short way to it, a few microseconds
+    less per call than building a Stream object)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _ten(t: Optional[torch.Tensor]):
+    """describe() for the operands of the calls below: 2-D, no scales, device checked by _On."""
+    if t is None:
+        return None
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    if rows == 0 or cols == 0:
+        return ForgeTensor(None, dt, 0, rows, cols, cols, None)
+    if s1 != 1 and cols > 1:
+        raise ValueError("rows must be contiguous (stride(1) == 1)")
+    return ForgeTensor(t.data_ptr(), dt, 0, rows, cols, s0 if rows > 1 else cols, None)
 
 
 def _same(on: "_On", out: Optional[torch.Tensor], shape, dtype) -> torch.Tensor:
@@ -514,8 +540,8 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     with _On(stream, X, W, bias, residual, out) as on:
         Y = _same(on, out, (X.shape[0], W.shape[0]), W.dtype)
         Z = on.empty((X.shape[0], W.shape[0]), W.dtype) if save else None
-        _check(_lib.forge_linear_forward(_ref(describe(X)), _ref(describe(W)), _ref(describe(_row(bias))), a,
-                                         _ref(describe(residual)), _ref(describe(Y)), _ref(describe(Z)), on.stream),
+        _check(_lib.forge_linear_forward(_ref(_ten(X)), _ref(_ten(W)), _ref(_ten(_row(bias))), a,
+                                         _ref(_ten(residual)), _ref(_ten(Y)), _ref(_ten(Z)), on.stream),
                "forge_linear_forward")
     return (Y, Z) if save else Y
 
@@ -538,7 +564,7 @@ def linear_act_backward(dY: torch.Tensor, Z: Optional[torch.Tensor] = None, act:
             need = _lib.forge_linear_act_backward_workspace(T, out)
             if need:
                 ws = on.empty((need,), torch.uint8)
-        _check(_lib.forge_linear_act_backward(_ref(describe(dY)), _ref(describe(Z)), a, _ref(describe(dZ)),
+        _check(_lib.forge_linear_act_backward(_ref(_ten(dY)), _ref(_ten(Z)), a, _ref(_ten(dZ)),
                                               db.data_ptr() if db is not None and out else None,
                                               ws.data_ptr() if ws is not None else None, need, on.stream),
                "forge_linear_act_backward")
@@ -554,8 +580,8 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
         shape = (X.shape[0], Wg.shape[0])
         H = _same(on, out, shape, Wg.dtype)
         G, U = (on.empty(shape, Wg.dtype), on.empty(shape, Wg.dtype)) if save else (None, None)
-        _check(_lib.forge_gated_forward(_ref(describe(X)), _ref(describe(Wg)), _ref(describe(Wu)), a,
-                                        _ref(describe(H)), _ref(describe(G)), _ref(describe(U)), on.stream),
+        _check(_lib.forge_gated_forward(_ref(_ten(X)), _ref(_ten(Wg)), _ref(_ten(Wu)), a,
+                                        _ref(_ten(H)), _ref(_ten(G)), _ref(_ten(U)), on.stream),
                "forge_gated_forward")
     return (H, G, U) if save else H
 
@@ -568,8 +594,8 @@ def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, act: str 
     with _On(stream, dH, G, U) as on:
         dG, dU = on.empty(dH.shape, dH.dtype), on.empty(dH.shape, dH.dtype)
         H = on.empty(dH.shape, dH.dtype) if want_h else None
-        _check(_lib.forge_gated_backward(_ref(describe(dH)), _ref(describe(G)), _ref(describe(U)), a,
-                                         _ref(describe(dG)), _ref(describe(dU)), _ref(describe(H)), on.stream),
+        _check(_lib.forge_gated_backward(_ref(_ten(dH)), _ref(_ten(G)), _ref(_ten(U)), a,
+                                         _ref(_ten(dG)), _ref(_ten(dU)), _ref(_ten(H)), on.stream),
                "forge_gated_backward")
     return dG, dU, H
 
@@ -583,8 +609,8 @@ def gated_dgrad(dY: torch.Tensor, Wd: torch.Tensor, G: torch.Tensor, U: torch.Te
         shape = (dY.shape[0], Wd.shape[1])
         dG, dU = on.empty(shape, Wd.dtype), on.empty(shape, Wd.dtype)
         H = on.empty(shape, Wd.dtype) if want_h else None
-        _check(_lib.forge_gated_dgrad(_ref(describe(dY)), _ref(describe(Wd)), _ref(describe(G)), _ref(describe(U)), a,
-                                      _ref(describe(dG)), _ref(describe(dU)), _ref(describe(H)), on.stream),
+        _check(_lib.forge_gated_dgrad(_ref(_ten(dY)), _ref(_ten(Wd)), _ref(_ten(G)), _ref(_ten(U)), a,
+                                      _ref(_ten(dG)), _ref(_ten(dU)), _ref(_ten(H)), on.stream),
                "forge_gated_dgrad")
     return dG, dU, H
 
@@ -597,9 +623,9 @@ def dgrad_group(dYs, Ws, dX: Optional[torch.Tensor] = None, stream=None) -> torc
         raise ValueError(f"a group holds 1..{MAX_GROUP} layers, each with its dY and W")
     with _On(stream, *dYs, *Ws, dX) as on:
         dX = _same(on, dX, (dYs[0].shape[0], Ws[0].shape[1]), Ws[0].dtype)
-        dy_a = (ForgeTensor * n)(*[describe(t) for t in dYs])
-        w_a = (ForgeTensor * n)(*[describe(t) for t in Ws])
-        _check(_lib.forge_linear_dgrad_group(n, dy_a, w_a, _ref(describe(dX)), on.stream), "forge_linear_dgrad_group")
+        dy_a = (ForgeTensor * n)(*[_ten(t) for t in dYs])
+        w_a = (ForgeTensor * n)(*[_ten(t) for t in Ws])
+        _check(_lib.forge_linear_dgrad_group(n, dy_a, w_a, _ref(_ten(dX)), on.stream), "forge_linear_dgrad_group")
     return dX
 
 
@@ -632,7 +658,7 @@ def linear_cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
         lse, total = on.empty((T,), torch.float32), on.empty((3,), torch.float32)
         need = _lib.forge_linear_xent_workspace(T, X.shape[1], W.shape[0], _DT.get(W.dtype, -1), 0, 0)
         ws = on.empty((need,), torch.uint8)
-        _check(_lib.forge_linear_xent_forward(_ref(describe(X)), _ref(describe(W)), _ptr(targets), int(ignore_index),
+        _check(_lib.forge_linear_xent_forward(_ref(_ten(X)), _ref(_ten(W)), _ptr(targets), int(ignore_index),
                                               _ptr(loss), _ptr(lse), total.data_ptr(), _ptr(ws), need, on.stream),
                "forge_linear_xent_forward")
     return (loss if reduction == "none" else total[2 if reduction == "mean" else 0]), lse, total
@@ -664,9 +690,9 @@ def linear_cross_entropy_backward(X: torch.Tensor, W: torch.Tensor, targets: tor
         need, ws, tot = _xent_grad_args(on, X, W, targets, lse, dloss, reduction, total, piece)
         dX = on.empty(X.shape, X.dtype) if want_dx else None
         dW = on.empty(W.shape, W.dtype) if want_dw else None
-        _check(_lib.forge_linear_xent_backward(_ref(describe(X)), _ref(describe(W)), _ptr(targets), int(ignore_index),
+        _check(_lib.forge_linear_xent_backward(_ref(_ten(X)), _ref(_ten(W)), _ptr(targets), int(ignore_index),
                                                _ptr(lse), _ptr(dloss), int(reduction == "none"), _ptr(tot),
-                                               _ref(describe(dX)), _ref(describe(dW)), int(piece), _ptr(ws), need,
+                                               _ref(_ten(dX)), _ref(_ten(dW)), int(piece), _ptr(ws), need,
                                                on.stream), "forge_linear_xent_backward")
     return dX, dW
 
@@ -685,10 +711,10 @@ def linear_cross_entropy_step(X: torch.Tensor, W: torch.Tensor, m: Optional[torc
     with _On(stream, X, W, m, v, targets, lse, dloss, m_scale, v_scale, total) as on:
         need, ws, tot = _xent_grad_args(on, X, W, targets, lse, dloss, reduction, total, piece)
         dX = on.empty(X.shape, X.dtype) if want_dx else None
-        _check(_lib.forge_linear_xent_step(_ref(describe(X)), _ref(describe(W)), _ref(describe(m, m_scale, code=code)),
+        _check(_lib.forge_linear_xent_step(_ref(_ten(X)), _ref(_ten(W)), _ref(describe(m, m_scale, code=code)),
                                            _ref(describe(v, v_scale, code=code)), OPT_ID[opt], ctypes.byref(h),
                                            int(step), seed & (2 ** 64 - 1), _ptr(targets), int(ignore_index),
                                            _ptr(lse), _ptr(dloss), int(reduction == "none"), _ptr(tot),
-                                           _ref(describe(dX)), int(piece), _ptr(ws), need, on.stream),
+                                           _ref(_ten(dX)), int(piece), _ptr(ws), need, on.stream),
                "forge_linear_xent_step")
     return dX
