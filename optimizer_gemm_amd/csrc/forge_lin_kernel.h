@@ -123,14 +123,17 @@ void lin_kernel(LinArgs g) {
   uint8_t* const ring = smem + grp * 5 * C::SLOT;
   const uint32_t lds0 = lds_addr(smem) + (uint32_t)(grp * 5 * C::SLOT);
   const int ntm = (epi_width<EPI>(g.M) - g.m_off + OM - 1) / OM, ntn = (g.N - g.n_off + C::BN - 1) / C::BN;
-  const int ntiles = ntm * ntn;
+  const int ntiles = ntm * ntn * (EPI == L_ACC && TA && !TB ? g.splits : 1);
   const LinArgsPtr ga = lin_args();
   const int nsrc = MULTI ? ga->nsrc : 1;
   int nst = (g.K[0] + C::BK - 1) / C::BK;
   if constexpr (MULTI) {
     for (int s = 1; s < nsrc; ++s) nst += (ga->K[s] + C::BK - 1) / C::BK;
   }
-  const int mine = C::KS > 1 ? (nst + C::KS - 1) / C::KS : nst;  // stages of a group
+  // SPLIT: g.splits workgroups share a tile's k range, each writing its part of the sums
+  constexpr bool SPLIT = MULTI;
+  const int splits = SPLIT ? g.splits : 1;
+  const int mine = (nst + C::KS * splits - 1) / (C::KS * splits);  // stages of a group
 
   // ---- operand loads ----
   // The stage of each operand that is loaded next (the two are one stage apart): the pair it
@@ -140,7 +143,7 @@ void lin_kernel(LinArgs g) {
   uint32_t fa_kb = 0, fb_kb = 0;
   __amdgpu_buffer_rsrc_t rA, rA2, rB;
   uint32_t av[PA], bv[PB];     // this thread's offsets in a stage
-  int lm0 = 0, ln0 = 0;        // the tile that is being loaded
+  int lm0 = 0, ln0 = 0, lsp = 0;  // the tile that is being loaded, its part of the k range
   // offsets of the loads from a panel whose first output index is the tile's (lim of them exist)
   auto ext = [&](bool tr, int64_t ld, int64_t lim, int64_t rows, int K) FORGE_INLINE -> uint32_t {
     if (K <= 0 || lim <= 0) return 0u;
@@ -228,12 +231,17 @@ void lin_kernel(LinArgs g) {
   using N0 = std::integral_constant<int, 0>;
   // stages 0 and 1 of a tile, into slots 0..3
   auto dma_begin = [&](int tile) FORGE_INLINE {
-    int tm, tn;
+    int tm, tn, part = 0;
+    if constexpr (SPLIT) {
+      part = tile % splits;
+      tile /= splits;
+    }
     g_tile(tile, ntm, ntn, tm, tn);
+    lsp = part;
     lm0 = g.m_off + tm * OM;
     ln0 = g.n_off + tn * C::BN;
-    int src0 = 0, k0 = C::KS > 1 ? grp * mine * C::BK : 0;  // the group's first stage: its pair and k
-    if constexpr (MULTI && C::KS > 1) {
+    int src0 = 0, k0 = (part * C::KS + grp) * mine * C::BK;  // the group's first stage: its pair and k
+    if constexpr (MULTI) {
       while (src0 + 1 < nsrc && k0 >= (ga->K[src0] + C::BK - 1) / C::BK * C::BK) {
         k0 -= (ga->K[src0] + C::BK - 1) / C::BK * C::BK;
         ++src0;
@@ -339,7 +347,7 @@ void lin_kernel(LinArgs g) {
   static_assert(WAIT0 <= 63, "vmcnt range");
   if (blockIdx.x < ntiles) dma_begin(blockIdx.x);
   for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-    const int m0 = lm0, n0 = ln0;
+    const int m0 = lm0, n0 = ln0, part = lsp;
     f32x4 acc[C::FM][C::FN];
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm)
@@ -490,7 +498,8 @@ void lin_kernel(LinArgs g) {
               const f32x4 x = *reinterpret_cast<const f32x4*>(E + row * C::LDE + col);
               f32x4 x2 = x;
               if constexpr (TWO) x2 = *reinterpret_cast<const f32x4*>(E + row * C::LDE + C::BM / 2 + col);
-              epi_vec<uint16_t, EPI, decltype(act_c)::value>(g.e, n, m, g.M, x, x2, sc);
+              epi_vec<uint16_t, EPI, decltype(act_c)::value>(g.e, n, m, g.M, x, x2, sc,
+                                                             SPLIT ? (int64_t)part * g.N * g.e.ldacc : 0);
             }
           }
         });
@@ -564,6 +573,7 @@ void lin_kernel(LinArgs g) {
     } else {
       const float sc = (EPI == L_ACC || EPI == L_DLOGIT) ? epi_scale(g.e) : 1.f;
       const LinEpiArgs& e = g.e;
+      float* const e_acc = e.acc + (SPLIT ? (int64_t)part * g.N * e.ldacc : 0);
       const int Mw = epi_width<EPI>(g.M);
       // blocks of 32 output rows x 64 floats of C (32 columns of gate and of up)
       constexpr int CH = C::FM / 4, OWB = TWO ? 32 : 64, NB = C::FN / 2 * CH;
@@ -573,18 +583,19 @@ void lin_kernel(LinArgs g) {
       // vector k of this lane in a block: row e_row + k * (64 / VPR), columns 8 e_col ..
       const int e_row = e_lane / VPR, e_col = e_lane % VPR;
       constexpr int RS = 64 / VPR;
-      // what the epilogue reads and writes, from the matrices' first element (each spans less
-      // than 2^31 bytes)
+      // what the epilogue reads and writes, from this wave's first row on
+      const int rows = g.N - nw < C::TN ? g.N - nw : C::TN;
       auto res = [&](const void* p, int64_t ld, int es) FORGE_INLINE -> __amdgpu_buffer_rsrc_t {
-        return make_rsrc(p, p ? (uint32_t)(((int64_t)(g.N - 1) * ld + Mw) * es) : 0u);
+        return make_rsrc(static_cast<const char*>(p) + (int64_t)nw * ld * es,
+                         rows > 0 ? (uint32_t)(((int64_t)(rows - 1) * ld + Mw) * es) : 0u);
       };
       // byte offsets of this lane's vectors of block blk in a matrix of pitch ld
       auto offs = [&](int blk, int64_t ld, int es, uint32_t (&o)[NV]) FORGE_INLINE {
-        const int n = nw + 32 * (blk / CH) + e_row, m = mw + OWB * (blk % CH) + 8 * e_col;
+        const int n = 32 * (blk / CH) + e_row, m = mw + OWB * (blk % CH) + 8 * e_col;
         const bool okm = blk < NB && m < Mw;
         const uint32_t base = (uint32_t)n * (uint32_t)(ld * es) + (uint32_t)(m * es), step = (uint32_t)(RS * ld * es);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) o[k] = okm && n + k * RS < g.N ? base + k * step : kOOB;
+        for (int k = 0; k < NV; ++k) o[k] = okm && n + k * RS < rows ? base + k * step : kOOB;
       };
       // The inputs of a block; with one wave per SIMD, which has no other to wait behind, they are
       // loaded two blocks ahead.
@@ -606,8 +617,8 @@ void lin_kernel(LinArgs g) {
           get(P.b, e.in2, e.ld2, 2, 0, blk);
         } else if constexpr (EPI == L_ACC) {
           if (e.acc_read) {
-            get(P.a, e.acc, e.ldacc, 4, 0, blk);
-            get(P.b, e.acc, e.ldacc, 4, 16, blk);
+            get(P.a, e_acc, e.ldacc, 4, 0, blk);
+            get(P.b, e_acc, e.ldacc, 4, 16, blk);
           }
         } else if constexpr (EPI == L_DLOGIT) {
 #pragma unroll
@@ -687,8 +698,8 @@ void lin_kernel(LinArgs g) {
             r2[k] = pack(x0 * sc, x1 * sc);
           }
           if (e.acc_write) {
-            put(r0, e.acc, e.ldacc, 4, 0, blk);
-            put(r1, e.acc, e.ldacc, 4, 16, blk);
+            put(r0, e_acc, e.ldacc, 4, 0, blk);
+            put(r1, e_acc, e.ldacc, 4, 16, blk);
           } else {
             put(r2, e.out, e.ldo, 2, 0, blk);
           }
@@ -785,7 +796,7 @@ template <class C, int EPI, bool TA, bool TB>
 hipError_t lin_run(const LinArgs& g, hipStream_t st) {
   constexpr int OM = EPI == L_GATED ? C::BM / 2 : C::BM;
   const int64_t ntm = (epi_width<EPI>(g.M) - g.m_off + OM - 1) / OM, ntn = (g.N - g.n_off + C::BN - 1) / C::BN;
-  const int64_t tiles = ntm * ntn;
+  const int64_t tiles = ntm * ntn * (EPI == L_ACC && TA && !TB ? g.splits : 1);
   if (tiles <= 0) return hipSuccess;
   const int64_t resident = (int64_t)(C::OCC * 4 / C::NW) * g_num_cus();
   hipLaunchKernelGGL((lin_kernel<C, EPI, TA, TB>), dim3((uint32_t)(tiles < resident ? tiles : resident)), dim3(C::NT), 0,
@@ -809,6 +820,10 @@ inline LinTileKind lin_tile(int64_t M, int64_t N) {
 
 template <int EPI, bool TA, bool TB>
 hipError_t lin_bf16(const LinArgs& g, hipStream_t st) {
+  if constexpr (EPI == L_ACC && TA && !TB) {
+    if (g.splits > 1)
+      return g.M >= 192 && g.N >= 192 ? lin_run<LinBig, EPI, TA, TB>(g, st) : lin_run<LinSmall, EPI, TA, TB>(g, st);
+  }
   switch (lin_tile<EPI>(epi_width<EPI>(g.M), g.N)) {
     case LT_BIG: return lin_run<LinBig, EPI, TA, TB>(g, st);
     case LT_SMALL: return lin_run<LinSmall, EPI, TA, TB>(g, st);

@@ -156,6 +156,9 @@ struct LinArgs {
   int32_t nsrc;
   int32_t M, N;
   int32_t m_off, n_off;  // origin of this launch's tiles
+  // L_ACC with k-slow A, bf16: parts that share a tile's k range, each with float32 sums of its
+  // own, N x ldacc apart from e.acc on (acc_write; added by launch_acc_join)
+  int32_t splits;
   LinEpiArgs e;
 };
 
@@ -230,13 +233,15 @@ __device__ __forceinline__ void act_dispatch(int act, F&& f) {
 }
 
 // One 4-vector of the output: row n, columns m..m+3 (all inside the output's padded
-// width); x the product, x2 the second product of L_GATED; sc = epi_scale; ACT = e.act.
+// width); x the product, x2 the second product of L_GATED; sc = epi_scale; ACT = e.act; acc0: offset of
+// the float32 sums.
 template <class T, int EPI, int ACT>
-__device__ __forceinline__ void epi_vec(const LinEpiArgs& e, int n, int m, int M, f32x4 x, f32x4 x2, float sc) {
+__device__ __forceinline__ void epi_vec(const LinEpiArgs& e, int n, int m, int M, f32x4 x, f32x4 x2, float sc,
+                                        int64_t acc0 = 0) {
   if constexpr (EPI == L_ACC) {
-    if (e.acc_read) x = x + load4(e.acc + (int64_t)n * e.ldacc + m);
+    if (e.acc_read) x = x + load4(e.acc + acc0 + (int64_t)n * e.ldacc + m);
     if (e.acc_write)
-      store4(e.acc + (int64_t)n * e.ldacc + m, x);
+      store4(e.acc + acc0 + (int64_t)n * e.ldacc + m, x);
     else
       store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, x * sc);
   } else if constexpr (EPI == L_DLOGIT) {
@@ -274,6 +279,12 @@ hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hip
 // (never fewer than kLseBlockMin)
 constexpr int kLseBlockMin = 64;
 int lin_lse_block(int bf16, int M, int N);
+
+// parts a product of k-slow A should be cut into (1: none): too few tiles to fill the chip with,
+// a k range long enough to share
+int lin_splits(int bf16, int64_t M, int64_t N, int64_t K);
+// out = (sum of the parts' sums, in order) * scale
+hipError_t launch_acc_join(const LinArgs& g, hipStream_t st);
 
 // dZ = dY act'(Z) and db = its column sums in float32 (partial sums of blocks of rows go to
 // ws, rows_blocks(T, out) x out floats, when there is more than one block)

@@ -97,15 +97,19 @@ FwdWs fwd_ws(int64_t T, int64_t vocab, int64_t block) {
   w.bytes = w.tsum + (int64_t)lse_join_groups(T) * 16;
   return w;
 }
-// Backward: a piece's dz (rows of up(piece, 8) entries), the sums of dX over the pieces.
+// Backward: a piece's dz (rows of up(piece, 8) entries), the sums of dX over the pieces, one set
+// per part of the k range.
 struct BwdWs {
   int64_t dz, acc, bytes;
+  int splits;
 };
-BwdWs bwd_ws(int64_t T, int64_t in, int64_t vocab, int64_t piece, int es) {
+BwdWs bwd_ws(int64_t T, int64_t in, int64_t piece, int es) {
   BwdWs w;
   w.dz = 0;
   w.acc = up(T * up(piece, 8) * es, 16);
-  w.bytes = w.acc + (piece < vocab ? T * in * 4 : 0);
+  w.splits = T > 0 && in > 0 ? lin_splits(es == 2, in, T, piece) : 1;
+  // room for them in any case: a W of wide pitch may take more, smaller pieces
+  w.bytes = w.acc + w.splits * T * in * 4;
   return w;
 }
 
@@ -174,13 +178,16 @@ int enqueue_dx(const XentCall& c, int64_t v0, int64_t n, bool folded, hipStream_
   g.e.ldo = c.dX->ld;
   g.e.acc = (float*)(c.ws + c.w.acc);
   g.e.ldacc = c.X->cols;
+  const bool last = v0 + n >= c.W->rows;
+  g.splits = c.w.splits;
   g.e.acc_read = v0 > 0;
-  g.e.acc_write = v0 + n < c.W->rows;
+  g.e.acc_write = g.splits > 1 || !last;
   if (!folded) {
     g.e.scale = c.per_token ? nullptr : c.dloss;
     g.e.count = c.total ? c.total + 1 : nullptr;
   }
-  return hip_status(launch_lin(bf16, L_ACC, true, false, g, st));
+  const int r = hip_status(launch_lin(bf16, L_ACC, true, false, g, st));
+  return r || g.splits <= 1 || !last ? r : hip_status(launch_acc_join(g, st));
 }
 
 }  // namespace
@@ -375,6 +382,7 @@ int forge_linear_dgrad_group(int32_t n_layers, const forge_tensor* dY, const for
   if (T == 0 || in == 0) return FORGE_OK;
   g.M = (int32_t)in;
   g.N = (int32_t)T;
+  g.splits = 1;
   g.e.out = dX->data;
   g.e.ldo = dX->ld;
   return hip_status(launch_lin(dt == FORGE_BF16, L_ACC, true, false, g, (hipStream_t)stream));
@@ -385,9 +393,8 @@ int64_t forge_linear_xent_workspace(int64_t T, int64_t in, int64_t vocab, int32_
   if (T < 0 || in < 0 || vocab < 1 || T >= kMaxDim || in >= kMaxDim || vocab >= kMaxDim || piece < 0) return 0;
   const int es = dtype == FORGE_BF16 ? 2 : 4;
   if (!backward) return fwd_ws(T, vocab, lin_lse_block(dtype == FORGE_BF16, (int)vocab, (int)T)).bytes;
-  // room for the sums of dX in any case: a W of wide pitch may take more, smaller pieces
   const int64_t p = piece_of(T, in, vocab, es, piece);
-  return bwd_ws(T, in, p + 1, p, es).bytes;
+  return bwd_ws(T, in, p, es).bytes;
 }
 
 int forge_linear_xent_forward(const forge_tensor* X, const forge_tensor* W, const int64_t* target, int64_t ignore,
@@ -436,7 +443,7 @@ int forge_linear_xent_backward(const forge_tensor* X, const forge_tensor* W, con
   const int64_t T = X->rows, V = W->rows, in = W->cols;
   XentCall c{X, W, target, ignore, lse, dloss, per_token != 0, total, dX, piece_of(T, W->ld, V, es, piece),
              (char*)workspace, BwdWs{}};
-  c.w = bwd_ws(T, in, V, c.piece, es);
+  c.w = bwd_ws(T, in, c.piece, es);
   if ((r = check_xent_grad(c, piece, workspace_bytes))) return r;
   if (dW) {
     if ((r = check_io(dW, W->dtype))) return r;
@@ -485,7 +492,7 @@ int forge_linear_xent_step(const forge_tensor* X, forge_tensor* W, forge_tensor*
     return FORGE_ERR_UNSUPPORTED;
   XentCall c{X, W, target, ignore, lse, dloss, per_token != 0, total, dX, piece_of(T, W->ld, V, es, piece),
              (char*)workspace, BwdWs{}};
-  c.w = bwd_ws(T, in, V, c.piece, es);
+  c.w = bwd_ws(T, in, c.piece, es);
   if ((r = check_xent_grad(c, piece, workspace_bytes))) return r;
   const forge_tensor ws = flat(workspace, c.w.bytes), tt = flat(target, T * 8), ls = flat(lse, T * 4),
                      dl = flat(dloss, per_token ? T * 4 : 4), to = flat(total, 12);

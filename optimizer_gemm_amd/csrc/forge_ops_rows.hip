@@ -77,6 +77,21 @@ __global__ __launch_bounds__(256) void gated_backward_kernel(const T* dH, int64_
   });
 }
 
+// ---- join of a split product's parts --------------------------------------
+__global__ __launch_bounds__(256) void acc_join_kernel(LinArgs g) {
+  const int per = g.M / 4;
+  const int64_t total = (int64_t)g.N * per, part = (int64_t)g.N * g.e.ldacc;
+  const float sc = epi_scale(g.e);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int n = (int)(i / per), m = (int)(i - (int64_t)n * per) * 4;
+    const float* p = g.e.acc + (int64_t)n * g.e.ldacc + m;
+    f32x4 x = load4(p);
+#pragma unroll 4
+    for (int s = 1; s < g.splits; ++s) x = x + load4(p + s * part);
+    store4(static_cast<bf16_t*>(g.e.out) + (int64_t)n * g.e.ldo + m, x * sc);
+  }
+}
+
 // ---- join of the cross entropy's partial results --------------------------
 // lse = M + log sum_b s_b e^(m_b - M) over the vocabulary blocks' (maximum, sum) pairs. 16
 // tokens per workgroup, 16 threads of it (stride 16) share a token's blocks; the pairs of
@@ -217,6 +232,12 @@ hipError_t launch_gated_backward(int bf16, const void* dH, int64_t lddh, const L
   else
     hipLaunchKernelGGL((gated_backward_kernel<float>), dim3(grid), dim3(256), 0, st, static_cast<const float*>(dH), lddh, e,
                        T, hid);
+  return hipGetLastError();
+}
+
+hipError_t launch_acc_join(const LinArgs& g, hipStream_t st) {
+  const int64_t want = ((int64_t)g.N * (g.M / 4) + 255) / 256;
+  hipLaunchKernelGGL(acc_join_kernel, dim3((uint32_t)(want < 4096 ? want : 4096)), dim3(256), 0, st, g);
   return hipGetLastError();
 }
 

@@ -186,7 +186,7 @@ def head(seed, t, i, v, dtype, ignored=0.2, ignore=-100):
 
 
 # tokens, in, vocabulary (odd and tiny ones; a single entry: its loss is 0)
-HEADS = [(1, 8, 1), (1, 64, 7), (2, 136, 1000), (65, 264, 513), (130, 72, 2051), (300, 520, 4099), (1025, 256, 5003),
+HEADS = [(1, 8, 1), (1, 64, 7), (2, 136, 1000), (65, 264, 513), (130, 72, 2051), (300, 520, 4099), (1025, 256, 5003), (260, 200, 20011),
          (4100, 2056, 4103)]
 
 
