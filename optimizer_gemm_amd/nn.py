@@ -18,6 +18,11 @@ holds until the optimizer runs) and `step_all(model)` then applies the update
 with the library's stand-alone optimizer pass. Both schedules use the same
 kernels and the same per-element update, so they differ only in when the
 gradient exists and where it lives.
+
+Around the linear layers: ForgeLinear takes a bias and an activation and adds a residual in
+its forward product's epilogue, SwiGLUBlock(joined=True) runs gate, up, activation and
+product as one kernel, and ForgeHead is a linear head whose softmax cross entropy never
+stores its logits and whose backward pass steps its weights piece by piece of the vocabulary.
 """
 from __future__ import annotations
 
@@ -75,23 +80,97 @@ class _ForgeLinearFn(torch.autograd.Function):
         return dx, None, None
 
 
+def _rows(t: torch.Tensor, cols: int, dtype: torch.dtype) -> torch.Tensor:
+    """t as contiguous rows of `cols` elements of `dtype`."""
+    t = t.reshape(-1, cols)
+    return t if t.is_contiguous() and t.dtype == dtype else t.to(dtype).contiguous()
+
+
+def _update(layers, x2: torch.Tensor, dy2s) -> None:
+    """The weight-gradient half of a backward pass for layers that read x2: their fused steps
+    (one launch for several), or, two-phase, their float32 gradients for step_all()."""
+    L0 = layers[0]
+    if not L0.fused:
+        for L, dy2 in zip(layers, dy2s):
+            g = forge.wgrad(x2, dy2)
+            if L.grad32 is None:
+                L.grad32 = g
+            else:
+                L.grad32.add_(g)
+        return
+    for L in layers:
+        L._step_count += 1
+    ev = L0.timing
+    if ev is not None:
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+    if len(layers) == 1:
+        forge.wgrad_step(x2, dy2s[0], L0.weight.detach(), L0.m, L0.v, L0.opt, L0.hyper, L0._step_count, L0.seed,
+                         L0.m_scale, L0.v_scale, code=L0.code)
+    else:
+        forge.wgrad_step_group(x2, dy2s, [L.weight.detach() for L in layers], [L.m for L in layers],
+                               [L.v for L in layers], L0.opt, L0.hyper, L0._step_count, [L.seed for L in layers],
+                               [L.m_scale for L in layers], [L.v_scale for L in layers], code=L0.code)
+    if ev is not None:
+        e1.record()
+        ev.append((e0, e1))
+
+
+class _ForgeLinearEpiFn(torch.autograd.Function):
+    """ForgeLinear with a bias, an activation or a residual: forward is one product with an
+    epilogue; backward takes the gradient through the activation, then dX, then the steps."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, layer):
+        x2 = _rows(x, weight.shape[1], weight.dtype)
+        r2 = None if residual is None else _rows(residual, weight.shape[0], weight.dtype)
+        keep = layer.act != "none"
+        y = forge.linear(x2, weight.detach(), bias=None if bias is None else bias.detach(), act=layer.act, residual=r2,
+                         save=keep)
+        y, z = y if keep else (y, None)
+        ctx.layer, ctx.x_shape, ctx.r_shape = layer, x.shape, None if residual is None else residual.shape
+        ctx.save_for_backward(x2, z)
+        return y.reshape(*x.shape[:-1], weight.shape[0])
+
+    @staticmethod
+    def backward(ctx, dy):
+        x2, z = ctx.saved_tensors
+        layer = ctx.layer
+        w = layer.weight.detach()
+        dy2 = _rows(dy, w.shape[0], w.dtype)
+        dz, db = forge.linear_act_backward(dy2, z, act=layer.act, want_bias=layer.bias is not None)
+        # old W, before the update below
+        dx = forge.dgrad(dz, w).reshape(ctx.x_shape) if ctx.needs_input_grad[0] else None
+        _update([layer], x2, [dz])
+        if db is not None:
+            layer._bias_update(db)
+        return dx, None, None, (dy.reshape(ctx.r_shape) if ctx.needs_input_grad[3] else None), None
+
+
 class ForgeLinear(torch.nn.Module):
     """Y = X W^T with the optimizer step fused into the backward pass.
 
-    weight: [out, in] bf16 or float32 parameter (bias-free, as the linear
-    layers the pages evaluate). opt / hyper: the optimizer and its
+    weight: [out, in] bf16 or float32 parameter. opt / hyper: the optimizer and its
     hyper-parameters (forge_hyper fields). states: "f32", "bf16", "q8" (INT8
     block-64, linear codes) or "q8dyn" (INT8 block-64, dynamic 8-bit code).
     fused: True for the fused step in backward; False for the two-phase schedule
     (float32 gradient kept in `grad32`, update applied by `step()`).
     timing: if a list, each fused call appends its (start, end) CUDA events.
+    bias, act: Y = act(X W^T + bias) (act one of forge.ACTS), and forward(x, residual) adds
+    `residual`, all in the product's epilogue; the bias takes the same optimizer with float32
+    moments, as a stand-alone step after the weights' (its gradient is a float32 sum over the
+    tokens; two-phase: kept in `bias_grad32`). Without any of the three the layers are bias-free,
+    as those the pages evaluate, and forward is a plain library product.
     """
 
     def __init__(self, in_features: int, out_features: int, opt: str = "adamw", hyper: Optional[dict] = None,
                  states: str = "f32", dtype: torch.dtype = torch.bfloat16, device=None, seed: int = 0,
-                 weight: Optional[torch.Tensor] = None, fused: bool = True):
+                 weight: Optional[torch.Tensor] = None, fused: bool = True, bias: bool = False, act: str = "none"):
         super().__init__()
+        if act not in forge.ACTS:
+            raise ValueError(f"unknown activation {act!r}; one of {', '.join(forge.ACTS)}")
         self.fused = bool(fused)
+        self.act = act
         self.grad32: Optional[torch.Tensor] = None
         self.timing: Optional[list] = None
         if weight is None:
@@ -109,13 +188,39 @@ class ForgeLinear(torch.nn.Module):
                 self.register_buffer(name, t)
         self.seed = (int(seed) * _SEED_MIX) & (2 ** 64 - 1)
         self._step_count = 0
+        self.bias: Optional[torch.nn.Parameter] = None
+        self.bias_grad32: Optional[torch.Tensor] = None
+        if bias:
+            self.bias = torch.nn.Parameter(torch.zeros(self.weight.shape[0], dtype=self.weight.dtype,
+                                                       device=self.weight.device))
+            bm, bv, _, _ = forge.new_states(self.bias.detach().unsqueeze(0), opt, "f32")
+            for name, t in (("bias_m", bm), ("bias_v", bv)):
+                if t is None:
+                    setattr(self, name, None)
+                else:
+                    self.register_buffer(name, t)
 
     @property
     def step_count(self) -> int:
         return self._step_count
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if self.bias is not None or self.act != "none" or residual is not None:
+            return _ForgeLinearEpiFn.apply(x, self.weight, self.bias, residual, self)
         return _ForgeLinearFn.apply(x, self.weight, self)
+
+    def _bias_update(self, db: torch.Tensor) -> None:
+        if self.fused:
+            self._bias_step(db)
+        elif self.bias_grad32 is None:
+            self.bias_grad32 = db
+        else:
+            self.bias_grad32.add_(db)
+
+    def _bias_step(self, db: torch.Tensor) -> None:
+        # the bias draws its stochastic rounding from a stream of its own
+        forge.optimizer_step(db.unsqueeze(0), self.bias.detach().unsqueeze(0), self.bias_m, self.bias_v, self.opt,
+                             self.hyper, self._step_count, self.seed ^ _SEED_MIX)
 
     def step(self) -> None:
         """Two-phase schedule: apply the optimizer to the stored gradient and free it
@@ -126,6 +231,9 @@ class ForgeLinear(torch.nn.Module):
         forge.optimizer_step(self.grad32, self.weight.detach(), self.m, self.v, self.opt, self.hyper,
                              self._step_count, self.seed, self.m_scale, self.v_scale, code=self.code)
         self.grad32 = None
+        if self.bias_grad32 is not None:
+            self._bias_step(self.bias_grad32)
+            self.bias_grad32 = None
 
 
 class _ForgeGroupFn(torch.autograd.Function):
@@ -194,6 +302,9 @@ def grouped_linear(layers, x: torch.Tensor):
     L0 = layers[0]
     if not 1 <= len(layers) <= forge.MAX_GROUP:
         raise ValueError(f"a group holds 1..{forge.MAX_GROUP} layers")
+    for L in layers:
+        if L.bias is not None or L.act != "none":
+            raise ValueError("grouped layers have no bias and no activation")
     for L in layers[1:]:
         if (L.opt, L.code, L.fused, L._step_count, L.weight.dtype) != (L0.opt, L0.code, L0.fused, L0._step_count,
                                                                          L0.weight.dtype) or \
@@ -216,6 +327,34 @@ def _rms_norm(x: torch.Tensor, eps: float = 1e-5) -> torch.Tensor:
     return (xf * torch.rsqrt(xf.pow(2).mean(-1, keepdim=True) + eps)).to(x.dtype)
 
 
+class _GatedBlockFn(torch.autograd.Function):
+    """y = r + down(silu(gate(h)) * up(h)) as two kernels: the gated product (its projections G, U
+    kept, its result not: the backward pass forms it again), and the down projection with the
+    residual r in its epilogue. Backward: dG, dU and H from dy's product with the down weights,
+    dh of both projections in one accumulation - all on the old weights - and then the steps."""
+
+    @staticmethod
+    def forward(ctx, h, r, wg, wu, wd, block):
+        h2, r2 = _rows(h, wg.shape[1], wg.dtype), _rows(r, wd.shape[0], wd.dtype)
+        H, G, U = forge.gated(h2, wg.detach(), wu.detach(), act="silu", save=True)
+        y = forge.linear(H, wd.detach(), residual=r2)
+        ctx.block, ctx.h_shape, ctx.r_shape = block, h.shape, r.shape
+        ctx.save_for_backward(h2, G, U)
+        return y.reshape(r.shape)
+
+    @staticmethod
+    def backward(ctx, dy):
+        h2, G, U = ctx.saved_tensors
+        gate, up, down = ctx.block.gate, ctx.block.up, ctx.block.down
+        wg, wu, wd = gate.weight.detach(), up.weight.detach(), down.weight.detach()
+        dy2 = _rows(dy, wd.shape[0], wd.dtype)
+        dG, dU, H = forge.gated_dgrad(dy2, wd, G, U, act="silu")
+        dh = forge.dgrad_group([dG, dU], [wg, wu]).reshape(ctx.h_shape) if ctx.needs_input_grad[0] else None
+        _update([down], H, [dy2])
+        _update([gate, up], h2, [dG, dU])
+        return dh, (dy.reshape(ctx.r_shape) if ctx.needs_input_grad[1] else None), None, None, None, None
+
+
 class SwiGLUBlock(torch.nn.Module):
     """Residual SwiGLU MLP block of a Llama-style decoder layer built from ForgeLinear:
     y = x + down(silu(gate(n(x))) * up(n(x))), with n a parameter-free RMS norm.
@@ -223,18 +362,28 @@ class SwiGLUBlock(torch.nn.Module):
     keeps only its input for backward and recomputes the rest (activation
     checkpointing); the recomputation runs before any of the block's layers steps,
     so it sees the same weights as the forward pass. With grouped=True gate and up, which
-    read the same n(x), take their fused steps in one grouped launch."""
+    read the same n(x), take their fused steps in one grouped launch. With joined=True gate,
+    up, activation and product are one kernel, the residual is added by the down projection,
+    and the backward pass is joined likewise (gate and up stepped in one launch); bf16 layers
+    (the grouped step takes no others), results as the separate layers' up to rounding."""
 
-    def __init__(self, d: int, hidden: int, checkpoint: bool = False, seed: int = 0, grouped: bool = False, **kw):
+    def __init__(self, d: int, hidden: int, checkpoint: bool = False, seed: int = 0, grouped: bool = False,
+                 joined: bool = False, **kw):
         super().__init__()
+        for name in ("bias", "act", "weight"):
+            if name in kw:
+                raise ValueError(f"SwiGLUBlock's layers take no {name}")
         self.gate = ForgeLinear(d, hidden, seed=3 * seed, **kw)
         self.up = ForgeLinear(d, hidden, seed=3 * seed + 1, **kw)
         self.down = ForgeLinear(hidden, d, seed=3 * seed + 2, **kw)
         self.checkpoint = checkpoint
         self.grouped = grouped
+        self.joined = joined
 
     def _body(self, x: torch.Tensor) -> torch.Tensor:
         h = _rms_norm(x)
+        if self.joined:
+            return _GatedBlockFn.apply(h, x, self.gate.weight, self.up.weight, self.down.weight, self)
         if self.grouped:
             g, u = grouped_linear((self.gate, self.up), h)
         else:
@@ -245,3 +394,77 @@ class SwiGLUBlock(torch.nn.Module):
         if self.checkpoint and torch.is_grad_enabled():
             return torch.utils.checkpoint.checkpoint(self._body, x, use_reentrant=False)
         return self._body(x)
+
+
+class _LinearCrossEntropyFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, targets, ignore_index, reduction, head):
+        x2 = _rows(x, weight.shape[1], weight.dtype)
+        t1 = targets.reshape(-1).contiguous()
+        loss, lse, total = forge.linear_cross_entropy(x2, weight.detach(), t1, ignore_index=ignore_index,
+                                                      reduction=reduction)
+        ctx.args, ctx.head, ctx.x_shape, ctx.w = (ignore_index, reduction), head, x.shape, weight
+        # the scalar is a part of `total`, which backward needs: a copy goes out
+        ctx.save_for_backward(x2, t1, lse, total)
+        return loss.reshape(targets.shape) if reduction == "none" else loss.clone()
+
+    @staticmethod
+    def backward(ctx, dloss):
+        x2, t1, lse, total = ctx.saved_tensors
+        ignore_index, reduction = ctx.args
+        g = dloss.float().reshape(-1).contiguous()
+        head, w = ctx.head, ctx.w.detach()
+        if head is None:
+            dx, dw = forge.linear_cross_entropy_backward(x2, w, t1, lse, g, ignore_index=ignore_index,
+                                                         reduction=reduction, total=total,
+                                                         want_dx=ctx.needs_input_grad[0],
+                                                         want_dw=ctx.needs_input_grad[1])
+        else:
+            head._step_count += 1
+            dx, dw = forge.linear_cross_entropy_step(x2, w, head.m, head.v, t1, lse, g, head.opt, head.hyper,
+                                                     head._step_count, head.seed, head.m_scale, head.v_scale,
+                                                     code=head.code, ignore_index=ignore_index, reduction=reduction,
+                                                     total=total, want_dx=ctx.needs_input_grad[0], piece=head.piece), None
+        return (None if dx is None else dx.reshape(ctx.x_shape)), dw, None, None, None, None
+
+
+def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+                         reduction: str = "mean") -> torch.Tensor:
+    """Softmax cross entropy of the logits x weight^T without storing them, differentiable by x and
+    weight (gradients in their types). x [..., d], targets [...] int64; reduction "mean" over the
+    tokens that are not ignore_index, "sum" or "none"."""
+    return _LinearCrossEntropyFn.apply(x, weight, targets, ignore_index, reduction, None)
+
+
+class ForgeHead(torch.nn.Module):
+    """Linear head with softmax cross entropy: forward(x, targets) is the loss, its logits never
+    stored; backward computes dX and steps the weights [vocab, d] piece by piece of the
+    vocabulary, the gradient never stored either. Arguments as ForgeLinear's; `piece` the
+    vocabulary entries per piece (0: the library's choice). Each backward call is one step."""
+
+    def __init__(self, d: int, vocab: int, opt: str = "adamw", hyper: Optional[dict] = None, states: str = "f32",
+                 dtype: torch.dtype = torch.bfloat16, device=None, seed: int = 0,
+                 weight: Optional[torch.Tensor] = None, ignore_index: int = -100, piece: int = 0):
+        super().__init__()
+        if weight is None:
+            weight = torch.empty(vocab, d, dtype=dtype, device=device)
+            torch.nn.init.normal_(weight, std=0.02)
+        self.weight = torch.nn.Parameter(weight, requires_grad=True)
+        self.opt, self.hyper = opt, forge.make_hyper(opt, **(hyper or {}))
+        m, v, ms, vs = forge.new_states(self.weight.detach(), opt, states)
+        self.code = "dynamic" if states == "q8dyn" else "linear"
+        for name, t in (("m", m), ("v", v), ("m_scale", ms), ("v_scale", vs)):
+            if t is None:
+                setattr(self, name, None)
+            else:
+                self.register_buffer(name, t)
+        self.seed = (int(seed) * _SEED_MIX) & (2 ** 64 - 1)
+        self.ignore_index, self.piece = int(ignore_index), int(piece)
+        self._step_count = 0
+
+    @property
+    def step_count(self) -> int:
+        return self._step_count
+
+    def forward(self, x: torch.Tensor, targets: torch.Tensor, reduction: str = "mean") -> torch.Tensor:
+        return _LinearCrossEntropyFn.apply(x, self.weight, targets, self.ignore_index, reduction, self)
