@@ -825,7 +825,34 @@ hipError_t lin_bf16(const LinArgs& g, hipStream_t st) {
       return g.M >= 192 && g.N >= 192 ? lin_run<LinBig, EPI, TA, TB>(g, st) : lin_run<LinSmall, EPI, TA, TB>(g, st);
   }
   switch (lin_tile<EPI>(epi_width<EPI>(g.M), g.N)) {
-    case LT_BIG: return lin_run<LinBig, EPI, TA, TB>(g, st);
+    case LT_BIG: {
+      // A last round of large tiles that would be at most half full: the whole rounds run as large
+      // tiles over a band of tile columns (or rows, whichever band holds more of them), the rest as
+      // 128x128 tiles in a second launch. (Not the cross entropy's maxima and sums: their blocks
+      // follow the tile.) A tile owns its output elements either way.
+      constexpr int OM = EPI == L_GATED ? 128 : 256;
+      const int cus = g_num_cus(), Mw = epi_width<EPI>(g.M);
+      const int ntm = (Mw + OM - 1) / OM, ntn = (g.N + 255) / 256;
+      const int64_t tiles = (int64_t)ntm * ntn, full = tiles / cus * cus, rem = tiles - full;
+      if (EPI != L_LSE && full > 0 && rem > 0 && 2 * rem <= cus && g.K[0] >= 512) {
+        LinArgs g1 = g, g2 = g;
+        const int mb = (int)(full / ntn), nb = (int)(full / ntm);  // whole bands the rounds hold
+        if (mb * (int64_t)ntn >= nb * (int64_t)ntm) {
+          g1.M = mb * OM;
+          g2.m_off = g1.M;
+        } else {
+          g1.N = nb * 256;
+          g2.n_off = g1.N;
+        }
+        if (g1.M > 0 && g1.N > 0) {
+          hipError_t e = lin_run<LinBig, EPI, TA, TB>(g1, st);
+          if (e != hipSuccess) return e;
+          const int64_t t = (int64_t)((Mw - g2.m_off + OM / 2 - 1) / (OM / 2)) * ((g.N - g2.n_off + 127) / 128);
+          return t > cus ? lin_run<LinSmall, EPI, TA, TB>(g2, st) : lin_run<LinSplit, EPI, TA, TB>(g2, st);
+        }
+      }
+      return lin_run<LinBig, EPI, TA, TB>(g, st);
+    }
     case LT_SMALL: return lin_run<LinSmall, EPI, TA, TB>(g, st);
     case LT_SPLIT: return lin_run<LinSplit, EPI, TA, TB>(g, st);
     default: return lin_run<LinTiny, EPI, TA, TB>(g, st);

@@ -231,6 +231,8 @@ FORGE_LIN_FORMS(FORGE_EXTERN_LIN)
 
 hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
   if (!bf16) return pick<float>(epi, ta, tb, g, st);
+  // (2^30 rows of 16 make a grid of fewer than 2^32 threads only up to 2^27 rows)
+  if ((epi == L_LINEAR || epi == L_GATED) && g.N <= kSkinny && g.M < (1 << 26)) return launch_lin_skinny(epi, g, st);
   if (!few_tiles(g)) return pick<uint16_t>(epi, ta, tb, g, st);
 #define FORGE_PICK(E, A, B) \
   if (epi == E && ta == A && tb == B) return lin_bf16<E, A, B>(g, st);
