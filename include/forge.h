@@ -340,6 +340,15 @@ int forge_gated_dgrad(const forge_tensor* dY, const forge_tensor* Wd, const forg
  */
 int forge_linear_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, forge_tensor* dX,
                              forge_stream_t stream);
+/*
+ * The same with a workspace (16-byte aligned, forge_linear_dgrad_group_workspace bytes, 0 where
+ * none is needed; rows: the sum of the out_l): with few tokens the product has too few tiles to
+ * fill the chip, and each tile's sum is shared by several workgroups, whose FP32 parts go
+ * through the workspace and are added in a fixed order.
+ */
+int64_t forge_linear_dgrad_group_workspace(int64_t T, int64_t in, int64_t rows, int32_t dtype);
+int forge_linear_dgrad_group_split(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, forge_tensor* dX,
+                                   void* workspace, int64_t workspace_bytes, forge_stream_t stream);
 
 /*
  * Softmax cross entropy of a linear head, without storing the logits z = X W^T:
@@ -364,7 +373,8 @@ int forge_linear_xent_forward(const forge_tensor* X, const forge_tensor* W, cons
  *   dz[t, v] = (exp(z[t, v] - lse[t]) - [v = target[t]]) g[t],  dX = dz W,  dW = dz^T X,
  * in pieces of the vocabulary: a piece's logits are formed again, its dz [T, piece] goes
  * to the workspace in the operands' type, and its part of dX and its rows of dW follow.
- * dX [T, in] and dW [vocab, in] in the operands' type, either may be NULL. A common g is
+ * dX [T, in] and dW [vocab, in] in the operands' type (rows of dW less than
+ * 2^23 bytes apart), either may be NULL. A common g is
  * applied in FP32 to the finished sums. `piece`: vocabulary entries per piece, a multiple
  * of 8 (0: chosen by the library, about 1 GiB of dz); workspace:
  * forge_linear_xent_workspace(T, in, vocab, dtype, 1, piece) bytes. lse and total are

@@ -87,7 +87,7 @@ __device__ __forceinline__ void dma16s(__amdgpu_buffer_rsrc_t r, uint8_t* dst, u
 // c += a b in place, in accumulation registers. Written as assembly so that the sum keeps its
 // registers: with all 256 of them in use the compiler gives the builtin's result others and
 // moves the sums around. What the compiler's hazard checks would do is done at the uses: the
-// operands come from LDS reads that have been waited for, a sum is used again 64 (16) products
+// operands come from LDS reads that have been waited for, a sum is used again 64 (16, 4) products
 // later, and mfma_drain() stands between the last product and the first read of a sum.
 __device__ __forceinline__ void mfma_acc(f32x4& c, bf16x8 a, bf16x8 b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
@@ -815,7 +815,7 @@ inline LinTileKind lin_tile(int64_t M, int64_t N) {
   const int64_t cus = g_num_cus(), w = EPI == L_GATED ? 2 * M : M;
   if (2 * ((w + 255) / 256) * ((N + 255) / 256) > cus) return LT_BIG;
   const int64_t t = ((w + 127) / 128) * ((N + 127) / 128);
-  return t > cus ? LT_SMALL : (2 * t > cus ? LT_SPLIT : LT_TINY);
+  return t > cus ? LT_SMALL : (((w + 63) / 64) * ((N + 63) / 64) > cus ? LT_SPLIT : LT_TINY);
 }
 
 template <int EPI, bool TA, bool TB>

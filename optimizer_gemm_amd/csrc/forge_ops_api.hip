@@ -52,6 +52,9 @@ void set_pair(LinArgs& g, int s, const void* A, int64_t lda, const void* B, int6
 // ---- cross entropy: sizes ----
 constexpr int64_t kPieceBytes = (int64_t)1 << 30;  // of dz, where the caller gives no size
 
+// bytes between the rows of W or dW, below this (256 of its rows are addressed by 32-bit offsets)
+constexpr int64_t kHeadPitch = (int64_t)1 << 23;
+
 // W of the head: as check_io, but any number of bytes (tiles and pieces address it by 64-bit
 // offsets) and any number of rows.
 int check_head(const forge_tensor* X, const forge_tensor* W, const int64_t* target) {
@@ -61,8 +64,7 @@ int check_head(const forge_tensor* X, const forge_tensor* W, const int64_t* targ
   if (is_fp8(X->dtype)) return FORGE_ERR_UNSUPPORTED;
   if ((r = check_io(W, W->dtype)) || (r = check_io(X, W->dtype))) return r;
   if (X->cols != W->cols || W->rows < 1) return FORGE_ERR_SHAPE;
-  // (256 of its rows are addressed by 32-bit offsets)
-  if (!fits_31(X) || W->ld * (int64_t)elem_size(W->dtype) >= ((int64_t)1 << 23)) return FORGE_ERR_UNSUPPORTED;
+  if (!fits_31(X) || W->ld * (int64_t)elem_size(W->dtype) >= kHeadPitch) return FORGE_ERR_UNSUPPORTED;
   if (!target && X->rows > 0) return FORGE_ERR_NULL;
   return ((uintptr_t)target & 7u) ? FORGE_ERR_ALIGN : FORGE_OK;
 }
@@ -137,9 +139,9 @@ int check_xent_grad(const XentCall& c, int64_t piece, int64_t ws_bytes) {
     int r = check_mat(c.dX, c.W->dtype, c.X->rows, c.X->cols);
     if (r) return r;
   }
-  // the documented size, never less than what this call uses
-  return check_workspace(c.ws, ws_bytes,
-                         forge_linear_xent_workspace(c.X->rows, c.X->cols, c.W->rows, c.W->dtype, 1, piece));
+  // the documented size (a W of wide pitch may take smaller pieces, which need less)
+  const int64_t need = forge_linear_xent_workspace(c.X->rows, c.X->cols, c.W->rows, c.W->dtype, 1, piece);
+  return check_workspace(c.ws, ws_bytes, need > c.w.bytes ? need : c.w.bytes);
 }
 
 // dz of vocabulary entries v0 .. v0 + n - 1 into the workspace. folded: the common factor
@@ -358,8 +360,9 @@ int forge_gated_dgrad(const forge_tensor* dY, const forge_tensor* Wd, const forg
   return hip_status(launch_lin(dt == FORGE_BF16, L_DGATE, true, false, g, (hipStream_t)stream));
 }
 
-int forge_linear_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, forge_tensor* dX,
-                             forge_stream_t stream) {
+// The group's product; split: with the documented workspace.
+static int dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, forge_tensor* dX, bool split,
+                       void* workspace, int64_t workspace_bytes, hipStream_t st) {
   int r;
   if (!dY || !W || !dX) return FORGE_ERR_NULL;
   if (n_layers < 1 || n_layers > FORGE_MAX_GROUP) return FORGE_ERR_SHAPE;
@@ -368,24 +371,51 @@ int forge_linear_dgrad_group(int32_t n_layers, const forge_tensor* dY, const for
   const int64_t T = dX->rows, in = dX->cols;
   LinArgs g{};
   const forge_tensor* ins[2 * FORGE_MAX_GROUP];
+  int64_t rows = 0;
   for (int l = 0; l < n_layers; ++l) {
     if ((r = op_dtype(&dY[l])) || (r = op_dtype(&W[l]))) return r;
     if ((r = check_mat(&dY[l], dt, T, W[l].rows)) || (r = check_mat(&W[l], dt, W[l].rows, in))) return r;
     ins[2 * l] = &dY[l];
     ins[2 * l + 1] = &W[l];
+    rows += W[l].rows;
     if (W[l].rows == 0) continue;  // a layer without rows adds nothing
     set_pair(g, g.nsrc++, W[l].data, W[l].ld, dY[l].data, dY[l].ld, W[l].rows);
   }
   if ((r = check_mat(dX, dt, T, in))) return r;
-  const forge_tensor* outs[1] = {dX};
-  if ((r = check_alias(outs, 1, ins, 2 * n_layers))) return r;
+  const int64_t need = split ? forge_linear_dgrad_group_workspace(T, in, rows, dt) : 0;
+  if ((r = check_workspace(workspace, workspace_bytes, need))) return r;
+  const forge_tensor ws = flat(workspace, need);
+  const forge_tensor* outs[2] = {dX, &ws};
+  if ((r = check_alias(outs, 2, ins, 2 * n_layers))) return r;
   if (T == 0 || in == 0) return FORGE_OK;
   g.M = (int32_t)in;
   g.N = (int32_t)T;
-  g.splits = 1;
   g.e.out = dX->data;
   g.e.ldo = dX->ld;
-  return hip_status(launch_lin(dt == FORGE_BF16, L_ACC, true, false, g, (hipStream_t)stream));
+  g.splits = need ? lin_splits(dt == FORGE_BF16, in, T, rows) : 1;
+  if (g.splits > 1) {
+    g.e.acc = (float*)workspace;
+    g.e.ldacc = in;
+    g.e.acc_write = true;
+  }
+  r = hip_status(launch_lin(dt == FORGE_BF16, L_ACC, true, false, g, st));
+  return r || g.splits <= 1 ? r : hip_status(launch_acc_join(g, st));
+}
+
+int forge_linear_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, forge_tensor* dX,
+                             forge_stream_t stream) {
+  return dgrad_group(n_layers, dY, W, dX, false, nullptr, 0, (hipStream_t)stream);
+}
+
+int64_t forge_linear_dgrad_group_workspace(int64_t T, int64_t in, int64_t rows, int32_t dtype) {
+  if (T <= 0 || in <= 0 || rows <= 0 || T >= kMaxDim || in >= kMaxDim || rows >= FORGE_MAX_GROUP * kMaxDim) return 0;
+  const int64_t s = lin_splits(dtype == FORGE_BF16, in, T, rows);
+  return s > 1 ? s * T * in * 4 : 0;
+}
+
+int forge_linear_dgrad_group_split(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, forge_tensor* dX,
+                                   void* workspace, int64_t workspace_bytes, forge_stream_t stream) {
+  return dgrad_group(n_layers, dY, W, dX, true, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
 int64_t forge_linear_xent_workspace(int64_t T, int64_t in, int64_t vocab, int32_t dtype, int32_t backward,
@@ -448,6 +478,7 @@ int forge_linear_xent_backward(const forge_tensor* X, const forge_tensor* W, con
   if (dW) {
     if ((r = check_io(dW, W->dtype))) return r;
     if (dW->rows != V || dW->cols != in) return FORGE_ERR_SHAPE;
+    if (dW->ld * es >= kHeadPitch) return FORGE_ERR_UNSUPPORTED;
   }
   const forge_tensor ws = flat(workspace, c.w.bytes), tt = flat(target, T * 8), ls = flat(lse, T * 4),
                      dl = flat(dloss, per_token ? T * 4 : 4), to = flat(total, 12);

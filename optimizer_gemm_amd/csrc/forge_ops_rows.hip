@@ -82,12 +82,23 @@ __global__ __launch_bounds__(AB_NT) void act_backward_kernel(int act, const T* d
   }
 }
 
-__global__ __launch_bounds__(256) void act_bias_join(const float* part, int blocks, float* db, int out) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= out) return;
+// 16 columns per workgroup, 16 threads to each: a thread adds every sixteenth block's sums, then
+// the 16 partial sums are added in order.
+constexpr int BJ_C = 16, BJ_G = 16;
+__global__ __launch_bounds__(BJ_C* BJ_G) void act_bias_join(const float* part, int blocks, float* db, int out) {
+  __shared__ float red[BJ_G][BJ_C];
+  const int t = threadIdx.x % BJ_C, grp = threadIdx.x / BJ_C, c = blockIdx.x * BJ_C + t;
   float s = 0.f;
+  if (c < out) {
 #pragma unroll 8
-  for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * out + c];
+    for (int b = grp; b < blocks; b += BJ_G) s += part[(int64_t)b * out + c];
+  }
+  red[grp][t] = s;
+  __syncthreads();
+  if (grp || c >= out) return;
+  s = 0.f;
+#pragma unroll
+  for (int k = 0; k < BJ_G; ++k) s += red[k][t];
   db[c] = s;
 }
 
@@ -223,7 +234,7 @@ hipError_t act_backward(int act, const void* dY, int64_t lddy, const void* Z, in
                      out, rows_per);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !db || blocks == 1) return e;
-  hipLaunchKernelGGL(act_bias_join, dim3((out + 255) / 256), dim3(256), 0, st, ws, blocks, db, out);
+  hipLaunchKernelGGL(act_bias_join, dim3((out + BJ_C - 1) / BJ_C), dim3(BJ_C * BJ_G), 0, st, ws, blocks, db, out);
   return hipGetLastError();
 }
 

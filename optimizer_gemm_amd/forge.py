@@ -99,6 +99,9 @@ def _load() -> ctypes.CDLL:
                                  ctypes.c_int),
         "forge_gated_dgrad": ([P(ForgeTensor)] * 4 + [ctypes.c_int32] + [P(ForgeTensor)] * 3 + [ctypes.c_void_p],
                               ctypes.c_int),
+        "forge_linear_dgrad_group_workspace": ([ctypes.c_int64] * 3 + [ctypes.c_int32], ctypes.c_int64),
+        "forge_linear_dgrad_group_split": ([ctypes.c_int32] + [P(ForgeTensor)] * 3 +
+                                           [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p], ctypes.c_int),
         "forge_linear_dgrad_group": ([ctypes.c_int32] + [P(ForgeTensor)] * 3 + [ctypes.c_void_p], ctypes.c_int),
         "forge_linear_xent_workspace": ([ctypes.c_int64] * 3 + [ctypes.c_int32] * 2 + [ctypes.c_int64], ctypes.c_int64),
         "forge_linear_xent_forward": ([P(ForgeTensor)] * 2 + [ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 4 +
@@ -617,7 +620,7 @@ def gated_dgrad(dY: torch.Tensor, Wd: torch.Tensor, G: torch.Tensor, U: torch.Te
 
 def dgrad_group(dYs, Ws, dX: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dX = sum_l dYs[l] Ws[l] for layers that read the same input, in one accumulation
-    (forge_linear_dgrad_group; from the weights as they are now)."""
+    (forge_linear_dgrad_group_split; from the weights as they are now)."""
     n = len(Ws)
     if len(dYs) != n or not 1 <= n <= MAX_GROUP:
         raise ValueError(f"a group holds 1..{MAX_GROUP} layers, each with its dY and W")
@@ -625,7 +628,10 @@ def dgrad_group(dYs, Ws, dX: Optional[torch.Tensor] = None, stream=None) -> torc
         dX = _same(on, dX, (dYs[0].shape[0], Ws[0].shape[1]), Ws[0].dtype)
         dy_a = (ForgeTensor * n)(*[_ten(t) for t in dYs])
         w_a = (ForgeTensor * n)(*[_ten(t) for t in Ws])
-        _check(_lib.forge_linear_dgrad_group(n, dy_a, w_a, _ref(_ten(dX)), on.stream), "forge_linear_dgrad_group")
+        need = _lib.forge_linear_dgrad_group_workspace(*dX.shape, sum(w.shape[0] for w in Ws), _DT.get(dX.dtype, -1))
+        ws = on.empty((need,), torch.uint8) if need else None
+        _check(_lib.forge_linear_dgrad_group_split(n, dy_a, w_a, _ref(_ten(dX)), _ptr(ws), need, on.stream),
+               "forge_linear_dgrad_group_split")
     return dX
 
 

@@ -383,3 +383,49 @@ def test_step_on_a_multiple_of_eight_equals_wgrad_step():
     _, _, _, ew = xent_grad64(X, W, y, -100, torch.ones(t, device="cuda", dtype=torch.float64), F)
     err = ((W - w).double() - dW.double()).abs()
     assert torch.all(err <= 2 * ew + 2.0 ** -23 * W.double().abs() + 2.0 ** -22 * dW.double().abs())
+
+
+@pytest.mark.parametrize("t,i,outs", [(5, 64, (6568, 6568)), (15, 5120, (11672, 11672)), (140, 672, (4824, 40, 4824)),
+                                      (700, 264, (13000,)), (1, 8, (16384, 8, 16384, 8))])
+def test_dgrad_group_of_few_tiles(t, i, outs):
+    """Few output tiles over a long sum: several workgroups share a tile's sum. The same bits
+    every time, also when a graph replays it."""
+    n = sum(outs)
+    assert forge.lib().forge_linear_dgrad_group_workspace(t, i, n, forge.forge.BF16) > 0
+    g = gen(t + n)
+    dYs = [rnd(g, t, o) for o in outs]
+    Ws = [rnd(g, o, i, std=n ** -0.5) for o in outs]
+    want, bound = 0, 0
+    for d, w in zip(dYs, Ws):
+        x, e = mm64(d, w)
+        want, bound = want + x, bound + 2 * len(outs) * e
+    dX = forge.dgrad_group([pitched(d) for d in dYs], [pitched(w) for w in Ws])
+    close("dX", dX, want, bound)
+    out = torch.full((t, i + 8), 7.0, device="cuda", dtype=BF)
+    forge.dgrad_group(dYs, Ws, dX=out[:, :i])
+    assert torch.equal(out[:, :i], dX) and torch.all(out[:, i:] == 7.0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = forge.dgrad_group(dYs, Ws)
+    for _ in range(3):
+        again.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again, dX)
+
+
+@pytest.mark.parametrize("t,o", [(7839, 144), (70001, 8), (513, 520), (16, 1536), (4099, 12)])
+def test_linear_act_backward_shapes(t, o):
+    """Narrow outputs over many rows, columns that end inside a vector's group of lanes; float32
+    and bfloat16 (whose rows are multiples of 8)."""
+    for dtype in (F, BF):
+        if dtype == BF and o % 8:
+            continue
+        g = gen(t + o)
+        dY, Z = rnd(g, t, o, dtype=dtype), rnd(g, t, o, dtype=dtype, std=2.0)
+        dZ, db = forge.linear_act_backward(dY, Z, act="gelu")
+        _, d = act64(Z.double(), "gelu")
+        want = dY.double() * d
+        err = dY.double().abs() * (48 * 2.0 ** -24) * (1 + Z.double().abs()) + 2.0 ** -24 * want.abs()
+        close("dZ", dZ, want, err)
+        close("db", db, want.sum(0), err.sum(0) + t * 2.0 ** -24 * want.abs().sum(0))

@@ -198,3 +198,36 @@ def test_python_checks():
         forge.linear_cross_entropy(z(4, 64), z(32, 64), torch.zeros(4, dtype=torch.int64), reduction="avg")
     with pytest.raises(ValueError, match="one device"):
         forge.linear(z(4, 64), torch.zeros(32, 64, dtype=torch.bfloat16, device="meta"))
+
+
+def test_dgrad_group_split_refusals():
+    A1 = ForgeTensor * 1
+    T, rows, cols = 5, 8192, 64
+    dY, W, dX, ws = ten(0, T, rows), ten(1, rows, cols), ten(2, T, cols), BASE + (3 << 33)
+    need = L.forge_linear_dgrad_group_workspace(T, cols, rows, BF16)
+    assert need > 0 and need % (T * cols * 4) == 0
+    assert L.forge_linear_dgrad_group_workspace(8192, 4096, rows, BF16) == 0  # enough tiles
+    assert L.forge_linear_dgrad_group_workspace(T, cols, 512, BF16) == 0      # a short sum
+    assert L.forge_linear_dgrad_group_workspace(T, cols, rows, F32) == 0
+    assert L.forge_linear_dgrad_group_workspace(-1, cols, rows, BF16) == 0
+
+    def call(ws=ws, n=need, dX=dX):
+        return L.forge_linear_dgrad_group_split(1, A1(dY), A1(W), ref(dX), ws, n, None)
+
+    assert call(n=need - 1) == SCRATCH and call(ws=None) == NULL and call(ws=ws + 4) == ALIGN
+    assert call(ws=BASE) == ALIAS and call(ws=BASE + (2 << 33)) == ALIAS and call(dX=ten(1, T, cols)) == ALIAS
+
+
+def test_xent_backward_refuses_distant_rows():
+    """Rows of W or dW 2^23 bytes apart or more."""
+    T, D, V = 4, 64, 100
+    tgt, lse, tot, ws, dl = (BASE + (k << 33) for k in (4, 5, 6, 7, 8))
+    n = 1 << 40
+
+    def bwd(W, dW):
+        return L.forge_linear_xent_backward(ref(ten(0, T, D)), ref(W), tgt, -100, lse, dl, 0, tot, None, ref(dW), 0, ws, n,
+                                            None)
+
+    far = 1 << 22
+    assert bwd(ten(1, V, D, ld=far), ten(3, V, D)) == UNSUP
+    assert bwd(ten(1, V, D), ten(3, V, D, ld=far)) == UNSUP
