@@ -818,11 +818,25 @@ inline LinTileKind lin_tile(int64_t M, int64_t N) {
   return t > cus ? LT_SMALL : (((w + 63) / 64) * ((N + 63) / 64) > cus ? LT_SPLIT : LT_TINY);
 }
 
+// A product of too few tiles for the chip may be shared along k (LinArgs::splits): from 96 stages
+// on, where one workgroup's chain takes longer than the join (15 x 8192 -> 512: 18 us against 23;
+// 100 x 4096 -> 1024, 64 stages: 18 against 16), at least 12 stages and at most 32 parts (their
+// join reads them all). 256x256 tiles where they fill the chip with parts of 48 stages or more
+// (1999 x 50264 -> 1024: 217 us against 277; 1000 x 16384 -> 1000, 16 stages: 60 against 50).
+constexpr int64_t kSplitStages = 96;
+inline bool lin_split_big(int64_t M, int64_t N, int64_t K) {
+  const int64_t s = g_num_cus() / (((M + 255) / 256) * ((N + 255) / 256));
+  return M >= 192 && N >= 192 && s > 0 && (K + 63) / 64 >= 48 * s;
+}
+
 template <int EPI, bool TA, bool TB>
 hipError_t lin_bf16(const LinArgs& g, hipStream_t st) {
   if constexpr (EPI == L_ACC && TA && !TB) {
-    if (g.splits > 1)
-      return g.M >= 192 && g.N >= 192 ? lin_run<LinBig, EPI, TA, TB>(g, st) : lin_run<LinSmall, EPI, TA, TB>(g, st);
+    if (g.splits > 1) {
+      int64_t k = 0;
+      for (int s = 0; s < g.nsrc; ++s) k += g.K[s];
+      return lin_split_big(g.M, g.N, k) ? lin_run<LinBig, EPI, TA, TB>(g, st) : lin_run<LinSmall, EPI, TA, TB>(g, st);
+    }
   }
   switch (lin_tile<EPI>(epi_width<EPI>(g.M), g.N)) {
     case LT_BIG: {

@@ -244,12 +244,12 @@ hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hip
 int lin_splits(int bf16, int64_t M, int64_t N, int64_t K) {
   if (!bf16) return 1;
   const LinTileKind kind = lin_tile<L_ACC>(M, N);
-  if (kind == LT_BIG || kind == LT_SMALL) return 1;
-  // parts of 256x256 tiles (128x128 ones where either side is short), 24 stages of 64 k at least
-  const int64_t b = M >= 192 && N >= 192 ? 256 : 128, slots = (int64_t)g_num_cus() * (b == 256 ? 1 : 2);
-  const int64_t tiles = ((M + b - 1) / b) * ((N + b - 1) / b), stages = (K + 63) / 64;
-  int64_t s = slots / tiles;
-  if (s > stages / 24) s = stages / 24;
+  const int64_t stages = (K + 63) / 64;
+  if (kind == LT_BIG || kind == LT_SMALL || stages < kSplitStages) return 1;
+  const int64_t b = lin_split_big(M, N, K) ? 256 : 128, slots = (int64_t)g_num_cus() * (b == 256 ? 1 : 2);
+  int64_t s = slots / (((M + b - 1) / b) * ((N + b - 1) / b));
+  if (s > stages / 12) s = stages / 12;
+  if (s > 32) s = 32;
   return s < 2 ? 1 : (int)s;
 }
 
