@@ -1,34 +1,37 @@
-// Products with an epilogue, general form: 64x64 tiles, float32 or bfloat16 operands,
-// either index of either operand fast. One kernel covers every operator of forge_ops.h.
+// Products with an epilogue, general form: float32 or bfloat16 operands, either index of either
+// operand fast, and the choice between this kernel and the bfloat16 ones. One kernel covers every
+// operator of forge_ops.h. It serves the float32 operands, and bfloat16 outputs of 2^30 tiles and
+// more, which the others do not count.
 //
-// A workgroup of 4 waves (2 x 2 of 32x32) stages BK = 32 k of both operands in LDS as rows
-// of k (operands whose k is slow are transposed on the way in), and multiplies them with
-// v_mfma_f32_32x32x16_bf16 or v_mfma_f32_32x32x2_f32, FP32 accumulators in both cases. The
-// next stage's global loads are in flight (in registers) during the current stage's
-// products. The finished tile goes through LDS as float rows of the output, so that the
-// epilogue reads and writes whole row segments.
-// Bound: LDS staging (each operand element is read from LDS for 32 rows of the other), so
-// this form serves the float32 operands and the products too small for larger tiles.
+// A workgroup of 4 waves stages BK k of both operands in LDS as rows of k (operands whose k is
+// slow are transposed on the way in), and multiplies them with v_mfma_f32_32x32x2_f32 (or
+// 32x32x16_bf16), FP32 accumulators in both cases. The next stage's global loads are in flight
+// (in registers) during the current stage's products. The finished tile goes through LDS as
+// float rows of the output, so that the epilogue reads and writes whole row segments.
+// Two tiles. 64x64, a 32x32 block per wave; and 32x32, a quarter of the stage's k per wave, where
+// the 64x64 tiles are fewer than the compute units: four times the workgroups, each with a
+// quarter of the products per k and twice the k per stage (float32, 700 x 768 -> 432: 14.1 us
+// against 26.0; 512 x 1024 -> 1024: 18.3 against 34.3).
+// Bound: a small product by its chain of stages, about 1 us each, and the launch (512 x 256 ->
+// 256: 9.9 us of which about 8 are the call); a large one by the FP32 matrix rate and LDS staging
+// (4096 x 1024 -> 4096: 100 TFLOP/s of the part's 154).
 #include "forge_lin_kernel.h"
 
 namespace forge {
 namespace {
 
-constexpr int S_B = 64, S_BK = 32, S_NT = 256;
+// B x B output elements, stages of BK k, LD: k per row of the staged operands. B = 64: the waves
+// are 2 x 2 of 32x32; B = 32: each wave takes a quarter of the stage's k for the whole tile.
+template <class T, int B_>
+struct STile {
+  static constexpr int B = B_, BK = B_ == 64 ? 32 : 64, VE = 16 / (int)sizeof(T), LD = BK + VE;
+  static constexpr int KW = B_ == 64 ? BK : BK / 4;  // k of a wave's products per stage
+  static constexpr int LDE = B + 4;
+};
+constexpr int S_B = 64, S_NT = 256;
 // workgroups of a launch at most (each walks several tiles beyond that): a grid holds fewer
 // than 2^32 threads
 constexpr int64_t kSimpleGrid = 1 << 20;
-
-template <class T>
-struct SimpleTraits;
-template <>
-struct SimpleTraits<uint16_t> {
-  static constexpr int VE = 8, PAD = 8;
-};
-template <>
-struct SimpleTraits<float> {
-  static constexpr int VE = 4, PAD = 4;
-};
 
 // 16 bytes of an operand: KS: its rows are k (row k0 + r, columns c..), else its rows are
 // the output index (row r, k = k0 + c ..). Zero outside.
@@ -39,10 +42,10 @@ __device__ __forceinline__ u32x4 load16(const T* base, int64_t ld, int row, int 
   return z;
 }
 
-// One operand's stage: 64 output indexes x 32 k, as rows of k of pitch S_BK + PAD.
-template <class T, bool TR>
+// One operand's stage: B output indexes x BK k, as rows of k of pitch LD.
+template <class T, class C, bool TR>
 struct Stage {
-  static constexpr int VE = SimpleTraits<T>::VE, LD = S_BK + SimpleTraits<T>::PAD;
+  static constexpr int VE = C::VE, LD = C::LD, S_B = C::B, S_BK = C::BK;
   static constexpr int CH = S_B * S_BK / VE / S_NT;  // 16-byte chunks per thread
   u32x4 r[CH];
   // r0: first output index of the tile, R: how many there are
@@ -82,35 +85,41 @@ struct Stage {
   }
 };
 
-template <class T>
-__device__ __forceinline__ void mma32(f32x16& acc, const T* as, const T* bs, int row_a, int row_b, int hi) {
-  constexpr int LD = S_BK + SimpleTraits<T>::PAD;
-  if constexpr (sizeof(T) == 2) {
+// 32 x 32 products over the wave's k of a stage, from 16-byte LDS reads: lane half hi holds
+// elements 8 j + 4 hi .. of both operands' rows (float32), so a product of two k takes one from
+// each half
+template <class T, class C>
+__device__ __forceinline__ void mma32(f32x16& acc, const T* as, const T* bs, int row_a, int row_b, int k0, int hi) {
 #pragma unroll
-    for (int k = 0; k < S_BK; k += 16) {
-      const bf16x8 a = *reinterpret_cast<const bf16x8*>(as + row_a * LD + k + 8 * hi);
-      const bf16x8 b = *reinterpret_cast<const bf16x8*>(bs + row_b * LD + k + 8 * hi);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
+  for (int k = 0; k < C::KW; k += 2 * C::VE) {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(as + row_a * C::LD + k0 + k + C::VE * hi);
+    const u32x4 b = *reinterpret_cast<const u32x4*>(bs + row_b * C::LD + k0 + k + C::VE * hi);
+    if constexpr (sizeof(T) == 2) {
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0,
+                                                    0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bits_f32(a[i]), bits_f32(b[i]), acc, 0, 0, 0);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < S_BK; k += 2)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(as[row_a * LD + k + hi], bs[row_b * LD + k + hi], acc, 0, 0, 0);
   }
 }
 
-template <class T, int EPI, bool TA, bool TB>
+template <class T, class C, int EPI, bool TA, bool TB>
 __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
   constexpr bool TWO = EPI == L_GATED;
-  constexpr int LD = S_BK + SimpleTraits<T>::PAD, LDE = S_B + 4;
-  constexpr int OP = S_B * LD * (int)sizeof(T);
-  constexpr int EB = (TWO ? 2 : 1) * S_B * LDE * 4, OB = (TWO ? 3 : 2) * OP;
+  constexpr int S_B = C::B, S_BK = C::BK, LDE = C::LDE;
+  constexpr int PARTS = S_B == 64 ? 1 : 4, ET = S_B * LDE;  // partial tiles of a product, floats of one
+  static_assert(EPI != L_LSE || S_B == 64, "the cross entropy's blocks are of 64 entries");
+  constexpr int OP = S_B * C::LD * (int)sizeof(T);
+  constexpr int EB = (TWO ? 2 : 1) * PARTS * ET * 4, OB = (TWO ? 3 : 2) * OP;
   __shared__ __attribute__((aligned(16))) uint8_t smem[EB > OB ? EB : OB];
   T* as = reinterpret_cast<T*>(smem);
   T* bs = reinterpret_cast<T*>(smem + OP);
   T* as2 = reinterpret_cast<T*>(smem + (TWO ? 2 * OP : 0));
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, hi = lane >> 5;
-  const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
+  const int wm = PARTS > 1 ? 0 : (wave & 1) * 32, wn = PARTS > 1 ? 0 : (wave >> 1) * 32;
+  const int wk = PARTS > 1 ? wave * C::KW : 0;
   const float sc = (EPI == L_ACC || EPI == L_DLOGIT) ? epi_scale(g.e) : 1.f;
 
   const int tiles_m = (epi_width<EPI>(g.M) - g.m_off + S_B - 1) / S_B, tiles_n = (g.N - g.n_off + S_B - 1) / S_B;
@@ -121,8 +130,8 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc2[i] = 0.f;
-  Stage<T, TA> sa, sa2;
-  Stage<T, TB> sb;
+  Stage<T, C, TA> sa, sa2;
+  Stage<T, C, TB> sb;
   for (int s = 0; s < g.nsrc; ++s) {
     const T* A = static_cast<const T*>(g.A[s]);
     const T* A2 = static_cast<const T*>(g.A[TWO ? 1 : 0]);
@@ -141,17 +150,18 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
       sb.store(bs, tid);
       __syncthreads();
       if (k0 + S_BK < K) fetch(k0 + S_BK);
-      mma32<T>(acc, as, bs, wm + l32, wn + l32, hi);
-      if constexpr (TWO) mma32<T>(acc2, as2, bs, wm + l32, wn + l32, hi);
+      mma32<T, C>(acc, as, bs, wm + l32, wn + l32, wk, hi);
+      if constexpr (TWO) mma32<T, C>(acc2, as2, bs, wm + l32, wn + l32, wk, hi);
     }
   }
   __syncthreads();
   // lane holds C[m = 8q + 4 hi + j][n = l32] of its 32x32 block: rows of the output in LDS
   float* E = reinterpret_cast<float*>(smem);
-  float* E2 = E + (TWO ? S_B * LDE : 0);
+  float* E2 = E + (TWO ? PARTS * ET : 0);
+  const int ew = PARTS > 1 ? wave * ET : 0;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int at = (wn + l32) * LDE + wm + 8 * q + 4 * hi;
+    const int at = ew + (wn + l32) * LDE + wm + 8 * q + 4 * hi;
     *reinterpret_cast<f32x4*>(E + at) = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
     if constexpr (TWO)
       *reinterpret_cast<f32x4*>(E2 + at) = f32x4{acc2[4 * q], acc2[4 * q + 1], acc2[4 * q + 2], acc2[4 * q + 3]};
@@ -189,9 +199,13 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
         const int v = tid + j * S_NT, r = v / (S_B / 4), c = (v % (S_B / 4)) * 4;
         const int n = n0 + r, m = m0 + c;
         if (n >= g.N || m >= Mw) continue;
-        const f32x4 x = *reinterpret_cast<const f32x4*>(E + r * LDE + c);
-        f32x4 x2 = x;
+        f32x4 x = *reinterpret_cast<const f32x4*>(E + r * LDE + c), x2 = x;
         if constexpr (TWO) x2 = *reinterpret_cast<const f32x4*>(E2 + r * LDE + c);
+#pragma unroll
+        for (int p = 1; p < PARTS; ++p) {  // the waves' sums, in order
+          x = x + *reinterpret_cast<const f32x4*>(E + p * ET + r * LDE + c);
+          if constexpr (TWO) x2 = x2 + *reinterpret_cast<const f32x4*>(E2 + p * ET + r * LDE + c);
+        }
         epi_vec<T, EPI, decltype(act_c)::value>(g.e, n, m, g.M, x, x2, sc);
       }
     });
@@ -199,20 +213,30 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
   }
 }
 
-template <class T, int EPI, bool TA, bool TB>
+template <class T, class C, int EPI, bool TA, bool TB>
 hipError_t run(const LinArgs& g, hipStream_t st) {
-  const int64_t gx = (epi_width<EPI>(g.M) - g.m_off + S_B - 1) / S_B, gy = (g.N - g.n_off + S_B - 1) / S_B;
+  const int64_t gx = (epi_width<EPI>(g.M) - g.m_off + C::B - 1) / C::B, gy = (g.N - g.n_off + C::B - 1) / C::B;
   if (gx <= 0 || gy <= 0) return hipSuccess;
   const int64_t tiles = gx * gy;
-  hipLaunchKernelGGL((lin_simple_kernel<T, EPI, TA, TB>), dim3((uint32_t)(tiles < kSimpleGrid ? tiles : kSimpleGrid)),
+  hipLaunchKernelGGL((lin_simple_kernel<T, C, EPI, TA, TB>), dim3((uint32_t)(tiles < kSimpleGrid ? tiles : kSimpleGrid)),
                      dim3(S_NT), 0, st, g);
   return hipGetLastError();
+}
+
+// float32: 32x32 tiles where the 64x64 ones are fewer than the compute units
+template <class T, int EPI, bool TA, bool TB>
+hipError_t size_up(const LinArgs& g, hipStream_t st) {
+  if constexpr (sizeof(T) == 4 && EPI != L_LSE) {
+    if (((int64_t)g.M + 63) / 64 * (((int64_t)g.N + 63) / 64) < g_num_cus())
+      return run<T, STile<T, 32>, EPI, TA, TB>(g, st);
+  }
+  return run<T, STile<T, 64>, EPI, TA, TB>(g, st);
 }
 
 template <class T>
 hipError_t pick(int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
 #define FORGE_PICK(E, A, B) \
-  if (epi == E && ta == A && tb == B) return run<T, E, A, B>(g, st);
+  if (epi == E && ta == A && tb == B) return size_up<T, E, A, B>(g, st);
   FORGE_LIN_FORMS(FORGE_PICK)
 #undef FORGE_PICK
   return hipErrorInvalidValue;
