@@ -432,10 +432,10 @@ void lin_kernel(LinArgs g) {
     // those reads have landed; and the zeros of the stages past the end
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     settle(F0);
-    // Every wave passed the last stage's barrier (or, with no stage, the first one), so the slots
-    // are free but for this wave's own loads, which have landed: the next tile's first stages
-    // start before this tile's epilogue (whose first inputs are asked for before them: loads
-    // return in order).
+    // Every wave passed the last stage's barrier (or, with no stage, the first one), so no slot is
+    // read any more, and of each slot the pieces that this wave's own loads write are free: those
+    // loads have landed. The next tile's first stages go there before this tile's epilogue (whose
+    // first inputs are asked for before them: loads return in order).
     auto next_tile = [&]() FORGE_INLINE {
       if constexpr (C::AHEAD) {
         if (tile + (int)gridDim.x < ntiles) dma_begin(tile + gridDim.x);
@@ -578,7 +578,11 @@ void lin_kernel(LinArgs g) {
       // blocks of 32 output rows x 64 floats of C (32 columns of gate and of up)
       constexpr int CH = C::FM / 4, OWB = TWO ? 32 : 64, NB = C::FN / 2 * CH;
       constexpr int VPR = OWB / 8, NV = 32 * VPR / 64;  // 8-vectors per row, per lane and block
-      float* Ew = reinterpret_cast<float*>(smem + C::EPI0) + wave_u * (C::EPIW / 4);
+      // This wave's region: four rows in each KiB that its own loads write in a slot. Another
+      // wave's loads of the stages past the end may still be on their way into theirs.
+      static_assert(C::EPIW == C::NW * 2048 && C::NW * 1024 == C::GT * 16, "the wave's pieces of a slot");
+      float* Ew = reinterpret_cast<float*>(smem + C::EPI0) + wave_u * 256;
+      auto e_at = [&](int row) FORGE_INLINE { return (row >> 2) * (C::GT * 4) + (row & 3) * 64; };
       const int mw = m0 + wm * (TWO ? C::TM / 2 : C::TM), nw = n0 + wn * C::TN;
       // vector k of this lane in a block: row e_row + k * (64 / VPR), columns 8 e_col ..
       const int e_row = e_lane / VPR, e_col = e_lane % VPR;
@@ -657,7 +661,7 @@ void lin_kernel(LinArgs g) {
             static_for<0, 8>([&](auto h_c) FORGE_INLINE {
               constexpr int h = decltype(h_c)::value, fn = 2 * f + h / 4, i = h % 4;
               constexpr int fm = !TWO ? 4 * c + i : (i < 2 ? 2 * c + i : C::FM / 2 + 2 * c + i - 2);
-              *reinterpret_cast<f32x4*>(Ew + (16 * (h / 4) + e_l16) * 64 + ((4 * i + e_q) ^ e_l16) * 4) = acc[fm][fn];
+              *reinterpret_cast<f32x4*>(Ew + e_at(16 * (h / 4) + e_l16) + ((4 * i + e_q) ^ e_l16) * 4) = acc[fm][fn];
             });
             // keeps the branches apart: merged, they would index the accumulators at run time,
             // which puts them into scratch memory
@@ -683,7 +687,7 @@ void lin_kernel(LinArgs g) {
         // vector k of the block, and of the second product
         auto chunk = [&](int k, int c) FORGE_INLINE -> f32x4 {
           const int row = e_row + k * RS;
-          return *reinterpret_cast<const f32x4*>(Ew + row * 64 + (c ^ (row & 15)) * 4);
+          return *reinterpret_cast<const f32x4*>(Ew + e_at(row) + (c ^ (row & 15)) * 4);
         };
         if constexpr (EPI == L_ACC) {
 #pragma unroll

@@ -429,3 +429,15 @@ def test_linear_act_backward_shapes(t, o):
         err = dY.double().abs() * (48 * 2.0 ** -24) * (1 + Z.double().abs()) + 2.0 ** -24 * want.abs()
         close("dZ", dZ, want, err)
         close("db", db, want.sum(0), err.sum(0) + t * 2.0 ** -24 * want.abs().sum(0))
+
+
+@pytest.mark.parametrize("stages", range(0, 11))
+def test_products_of_every_ring_position(stages):
+    """The 256x256 tiles keep two and a half stages of 64 k in a ring of five slots: every place in
+    it where a tile's sum can end, several tiles per workgroup, epilogues with inputs."""
+    t, o, i = 4360, 4360, 64 * stages
+    g = gen(stages)
+    X, W, R = rnd(g, t, i), rnd(g, o, i, std=max(1, i) ** -0.5), rnd(g, t, o)
+    for _ in range(2):
+        close("Y", forge.linear(X, W, act="silu", residual=R), *linear64(X, W, None, "silu", R)[:2])
+    close("dX", forge.dgrad_group([X], [W.t().contiguous()]), *mm64(X, W.t().contiguous()))
