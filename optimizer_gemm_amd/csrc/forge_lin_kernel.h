@@ -4,34 +4,44 @@
 // as its fast index (rows of W in a forward product, rows of X or dY) or as its slow index
 // (rows of W in an input gradient, rows of X and dY in a weight gradient).
 //
-// Mainloop. A workgroup of 2 x 2 waves owns a BM x BN tile. Stages of 64 k go from global
-// memory straight into LDS (buffer loads with the LDS bit, 1 KiB per wave instruction) into
-// one of two buffers. 64 k make a k-fast row 128 bytes, one cache line: with 32 k per stage
-// every line was requested twice (TCP_TCC_READ_REQ 117.8 M against 58.7 M on a 8192 x 4096
-// product over 14336), and the matrix pipes were busy 67% of the cycles. k-fast rows are read
-// with 16-byte LDS reads, k-slow rows with the LDS transpose read; XOR swizzles of the
-// 16-byte chunks keep both free of bank conflicts. v_mfma_f32_16x16x32_bf16, FP32 sums:
-// on normally distributed data the part holds a higher clock with it than with the 32x32x16
-// form (2071 against 1791 TFLOP/s from registers alone), which moves twice the accumulators
-// per product; on constant data both reach 2430.
-// Each k-step (16 k) multiplies one fragment set while the next one is read between its
-// first MFMAs. One barrier per stage, before its last k-step: by then every wave has read
-// the whole stage and its own loads of the next one have landed, so the barrier publishes
-// that stage and frees this one's buffer; the loads of the stage after next are issued
-// between the MFMAs of the last k-step, one stage's products ahead of their use.
-// The 256x256 tile has one wave per SIMD of 128x128 (256 accumulators): each fragment byte
-// read from LDS feeds twice the MFMAs of a 64-wide wave tile.
-// Several products may run into one accumulation (MULTI: their stages follow one another).
+// Mainloop. A group of 2 x 2 waves owns a B x B tile. Stages of 64 k go from global memory
+// straight into LDS (buffer loads with the LDS bit, 1 KiB per wave instruction), one operand's
+// stage to a slot, five slots in a ring: two and a half stages, all of the 160 KiB with 256x256
+// tiles. 64 k make a k-fast row 128 bytes, one cache line: with 32 k per stage every line was
+// requested twice (TCP_TCC_READ_REQ 117.8 M against 58.7 M on 8192 x 14336 -> 4096). k-fast rows
+// are read with 16-byte LDS reads, k-slow rows with the LDS transpose read; XOR swizzles of the
+// 16-byte chunks keep both free of bank conflicts. v_mfma_f32_16x16x32_bf16, FP32 sums: on
+// normally distributed data the part holds a higher clock with it than with the 32x32x16 form
+// (2071 against 1791 TFLOP/s from registers alone), which moves twice the accumulators per
+// product; on constant data both reach 2430.
+// A stage is two k-steps of 32 k. Each multiplies one fragment set while the next one is read
+// between the first half of its products. One barrier per stage, between the two: by then every
+// wave has read the whole stage and its own loads of the next one have landed but for one
+// operand's, so the barrier publishes that stage and frees this one's slots. The loads of the
+// stage after next are issued between the products of both k-steps.
+// The 256x256 tile has one wave per SIMD of 128x128 (256 accumulators): each fragment byte read
+// from LDS feeds twice the products of a 64-wide wave tile. The smaller tiles serve outputs of
+// few tiles: 128x128 with two workgroups per compute unit; and with KS > 1 that many groups of
+// waves, each with a ring of its own, share the tile's k range, whose chain of stages is what
+// takes the time there (1 x 4096 -> 4096: 30 us -> 17 with four groups on 64x64 tiles).
+// Several products may run into one accumulation (MULTI: their stages follow one another), and
+// several workgroups may share one tile's k range (SPLIT, LinArgs::splits).
 // Operands are addressed from the tile's own origin (64-bit base, 32-bit offsets), so a
 // k-fast operand may be of any size; a k-slow one spans less than 2^31 bytes. A load whose
 // row, column or k lies outside takes an offset past every extent and writes zeros.
 //
-// Epilogue. Vector epilogues hand each wave's accumulators through a private LDS region,
+// Epilogue. Vector epilogues hand each wave's accumulators through an LDS region of its own,
 // 32 output rows x 64 columns at a time, so that whole row segments are read and written
 // without a workgroup barrier; the cross entropy's maximum and sum are taken from the
-// accumulators directly (a lane holds TM / 2 of a token's logits, its partner lane the other
-// half). The 256x256 tile's region lies beside the stage buffers, so the next tile's first
-// two stages are on their way during the epilogue.
+// accumulators directly (a lane holds a quarter of a token's logits of the wave's tile). The
+// 256x256 tile's regions are the fifth slot, so the next tile's first two stages are on their way
+// during the epilogue. With KS > 1 the groups' sums are added in order in LDS.
+//
+// Measured (256x256 tiles): 8192 x 4096 -> 4096 204 us, 1350 TFLOP/s; 8192 x 14336 -> 4096 with
+// residual 671 us, 1434; 8192 x 4096 -> 2 x 14336 gated, projections kept, 1.39 ms, 1384; a large
+// library product of these shapes, without an epilogue, reaches 1295, 1598 and 1564. 1.33 to 1.4 us per stage and tile,
+// of which the products with their LDS reads alone take 0.92; with loads that return zeros
+// 1.06. The part's clock is what gives: 1.76 GHz at 72% busy matrix pipes.
 #pragma once
 
 #include "forge_gemm_kernel.h"

@@ -1,7 +1,9 @@
 // Internal: the operators around the fused weight-gradient step: products with an
 // epilogue (linear forward, gated block, their gradients, softmax cross entropy of a
 // linear head). This file holds their arguments, the activations and the epilogues;
-// the kernels are in forge_lin_simple.hip and forge_ops_rows.hip.
+// the kernels are in forge_lin_kernel.h (bfloat16 products), forge_lin_skinny.hip (a few tokens),
+// forge_lin_simple.hip (float32, and the choice between them) and forge_ops_rows.hip (passes
+// without a product).
 //
 // Every product here is C[m][n] = sum_k A[m][k] B[n][k] with m the output's columns
 // (features, contiguous in memory) and n its rows (tokens), so a lane's four consecutive
