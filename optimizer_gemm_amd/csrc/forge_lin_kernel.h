@@ -437,6 +437,7 @@ void lin_kernel(LinArgs g) {
       next_b();
     }
     mfma_drain();
+    __builtin_amdgcn_sched_barrier(0);  // (no read of a sum moves in front of it)
     hop(std::true_type{});
     // the last k-step read fragments that nothing consumes: their registers stay pinned until
     // those reads have landed; and the zeros of the stages past the end
