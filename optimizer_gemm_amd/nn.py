@@ -403,23 +403,27 @@ class _LinearCrossEntropyFn(torch.autograd.Function):
         t1 = targets.reshape(-1).contiguous()
         loss, lse, total = forge.linear_cross_entropy(x2, weight.detach(), t1, ignore_index=ignore_index,
                                                       reduction=reduction)
-        ctx.args, ctx.head, ctx.x_shape, ctx.w = (ignore_index, reduction), head, x.shape, weight
+        ctx.args, ctx.head, ctx.x_shape = (ignore_index, reduction), head, x.shape
+        ctx.step = None if head is None else head._step_count
         # the scalar is a part of `total`, which backward needs: a copy goes out
-        ctx.save_for_backward(x2, t1, lse, total)
+        ctx.save_for_backward(x2, t1, lse, total, weight)
         return loss.reshape(targets.shape) if reduction == "none" else loss.clone()
 
     @staticmethod
     def backward(ctx, dloss):
-        x2, t1, lse, total = ctx.saved_tensors
+        x2, t1, lse, total, weight = ctx.saved_tensors
         ignore_index, reduction = ctx.args
         g = dloss.float().reshape(-1).contiguous()
-        head, w = ctx.head, ctx.w.detach()
+        head, w = ctx.head, weight.detach()
         if head is None:
             dx, dw = forge.linear_cross_entropy_backward(x2, w, t1, lse, g, ignore_index=ignore_index,
                                                          reduction=reduction, total=total,
                                                          want_dx=ctx.needs_input_grad[0],
                                                          want_dw=ctx.needs_input_grad[1])
         else:
+            if head._step_count != ctx.step:
+                # lse belongs to the weights of the forward pass
+                raise RuntimeError("the head's weights were stepped after this loss was computed")
             head._step_count += 1
             dx, dw = forge.linear_cross_entropy_step(x2, w, head.m, head.v, t1, lse, g, head.opt, head.hyper,
                                                      head._step_count, head.seed, head.m_scale, head.v_scale,
@@ -440,7 +444,8 @@ class ForgeHead(torch.nn.Module):
     """Linear head with softmax cross entropy: forward(x, targets) is the loss, its logits never
     stored; backward computes dX and steps the weights [vocab, d] piece by piece of the
     vocabulary, the gradient never stored either. Arguments as ForgeLinear's; `piece` the
-    vocabulary entries per piece (0: the library's choice). Each backward call is one step."""
+    vocabulary entries per piece (0: the library's choice). Each backward call is one step, of a
+    loss computed with the weights as they are: a loss from before another one's step is refused."""
 
     def __init__(self, d: int, vocab: int, opt: str = "adamw", hyper: Optional[dict] = None, states: str = "f32",
                  dtype: torch.dtype = torch.bfloat16, device=None, seed: int = 0,

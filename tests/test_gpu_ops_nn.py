@@ -308,3 +308,24 @@ def test_same_operand_twice():
     close("twice", two, 2 * d, 4 * e)
     sq = rnd(4, 64, 64)
     close("square", forge.linear(sq, sq, residual=sq), *linear64(sq, sq, residual=sq)[:2])
+
+
+def test_loss_of_other_weights_is_refused():
+    """Backward needs the weights that the loss was computed with."""
+    head = ForgeHead(64, 500, device="cuda")
+    x = torch.randn(2, 20, 64, device="cuda").to(torch.bfloat16).requires_grad_()
+    y = torch.randint(0, 500, (2, 20), device="cuda")
+    first, second = head(x, y), head(x, y)
+    first.backward()
+    w = head.weight.detach().clone()
+    with pytest.raises(RuntimeError, match="stepped after"):
+        second.backward()
+    assert head.step_count == 1 and torch.equal(head.weight, w)
+    head(x, y).backward()
+    assert head.step_count == 2
+    weight = torch.randn(500, 64, device="cuda").to(torch.bfloat16).requires_grad_()
+    loss = linear_cross_entropy(x, weight, y)
+    with torch.no_grad():
+        weight.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
