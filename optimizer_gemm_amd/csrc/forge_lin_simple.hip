@@ -13,7 +13,7 @@
 // quarter of the products per k and twice the k per stage (float32, 700 x 768 -> 432: 14.1 us
 // against 26.0; 512 x 1024 -> 1024: 18.3 against 34.3).
 // Bound: a small product by its chain of stages, about 1 us each, and the launch (512 x 256 ->
-// 256: 9.9 us of which about 8 are the call); a large one by the FP32 matrix rate and LDS staging
+// 256: 10.0 us, 6.0 of them the kernel); a large one by the FP32 matrix rate and LDS staging
 // (4096 x 1024 -> 4096: 100 TFLOP/s of the part's 154).
 #include "forge_lin_kernel.h"
 

@@ -463,13 +463,13 @@ class _On:
         self.device = first.device
         if self.device.type != "cuda":
             raise ValueError("forge kernels take device tensors")
-        if isinstance(stream, torch.cuda.Stream) and stream.device != self.device:
+        if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device != self.device:
             raise ValueError("the stream belongs to another device than the tensors")
         self._given = stream
         self._guard = None
 
     def __enter__(self):
-        if torch.cuda.current_device() != self._index:
+        if _current_device() != self._index:
             self._guard = torch.cuda.device(self._index)
             self._guard.__enter__()
         self.stream = _raw_stream(self._index) if self._given is None else _stream(self._given)
@@ -487,14 +487,16 @@ class _On:
         return t
 
 
-def _raw_stream(index: int) -> int:
-    """Handle of the device's current stream (torch's own short way to it, a few microseconds
-    less per call than building a Stream object)."""
-    return torch._C._cuda_getCurrentRawStream(index)
+# torch's own short ways to the device's current stream and to the current device: a few
+# microseconds less per call than a Stream object and the checks around them, which a tensor on
+# the device makes needless
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _ten(t: Optional[torch.Tensor]):
-    """describe() for the operands of the calls below: 2-D, no scales, device checked by _On."""
+    """describe() for the operands of the calls below: 2-D, no scales, device checked by _On
+    (an argument of pointer type takes the structure itself)."""
     if t is None:
         return None
     rows, cols = t.shape
@@ -503,10 +505,10 @@ def _ten(t: Optional[torch.Tensor]):
     if dt is None:
         raise ValueError(f"unsupported dtype {t.dtype}")
     if rows == 0 or cols == 0:
-        return ForgeTensor(None, dt, 0, rows, cols, cols, None)
+        return ForgeTensor(None, dt, 0, rows, cols, cols)
     if s1 != 1 and cols > 1:
         raise ValueError("rows must be contiguous (stride(1) == 1)")
-    return ForgeTensor(t.data_ptr(), dt, 0, rows, cols, s0 if rows > 1 else cols, None)
+    return ForgeTensor(t.data_ptr(), dt, 0, rows, cols, s0 if rows > 1 else cols)
 
 
 def _same(on: "_On", out: Optional[torch.Tensor], shape, dtype) -> torch.Tensor:
@@ -518,12 +520,16 @@ def _check(st: int, what: str) -> None:
         raise ForgeError(st, what)
 
 
-def _row(b: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+def _row(b: Optional[torch.Tensor]):
+    """_ten() of a vector as one row"""
     if b is None:
         return None
     if b.dim() != 1 or not b.is_contiguous():
         raise ValueError("bias is a contiguous vector")
-    return b.unsqueeze(0)
+    dt, n = _DT.get(b.dtype), b.numel()
+    if dt is None:
+        raise ValueError(f"unsupported dtype {b.dtype}")
+    return ForgeTensor(b.data_ptr() if n else None, dt, 0, 1, n, n)
 
 
 def _vec(t: torch.Tensor, n: int, dtype: torch.dtype, what: str) -> torch.Tensor:
@@ -543,8 +549,8 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     with _On(stream, X, W, bias, residual, out) as on:
         Y = _same(on, out, (X.shape[0], W.shape[0]), W.dtype)
         Z = on.empty((X.shape[0], W.shape[0]), W.dtype) if save else None
-        _check(_lib.forge_linear_forward(_ref(_ten(X)), _ref(_ten(W)), _ref(_ten(_row(bias))), a,
-                                         _ref(_ten(residual)), _ref(_ten(Y)), _ref(_ten(Z)), on.stream),
+        _check(_lib.forge_linear_forward(_ten(X), _ten(W), _row(bias), a,
+                                         _ten(residual), _ten(Y), _ten(Z), on.stream),
                "forge_linear_forward")
     return (Y, Z) if save else Y
 
@@ -567,7 +573,7 @@ def linear_act_backward(dY: torch.Tensor, Z: Optional[torch.Tensor] = None, act:
             need = _lib.forge_linear_act_backward_workspace(T, out)
             if need:
                 ws = on.empty((need,), torch.uint8)
-        _check(_lib.forge_linear_act_backward(_ref(_ten(dY)), _ref(_ten(Z)), a, _ref(_ten(dZ)),
+        _check(_lib.forge_linear_act_backward(_ten(dY), _ten(Z), a, _ten(dZ),
                                               db.data_ptr() if db is not None and out else None,
                                               ws.data_ptr() if ws is not None else None, need, on.stream),
                "forge_linear_act_backward")
@@ -583,8 +589,8 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
         shape = (X.shape[0], Wg.shape[0])
         H = _same(on, out, shape, Wg.dtype)
         G, U = (on.empty(shape, Wg.dtype), on.empty(shape, Wg.dtype)) if save else (None, None)
-        _check(_lib.forge_gated_forward(_ref(_ten(X)), _ref(_ten(Wg)), _ref(_ten(Wu)), a,
-                                        _ref(_ten(H)), _ref(_ten(G)), _ref(_ten(U)), on.stream),
+        _check(_lib.forge_gated_forward(_ten(X), _ten(Wg), _ten(Wu), a,
+                                        _ten(H), _ten(G), _ten(U), on.stream),
                "forge_gated_forward")
     return (H, G, U) if save else H
 
@@ -597,8 +603,8 @@ def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, act: str 
     with _On(stream, dH, G, U) as on:
         dG, dU = on.empty(dH.shape, dH.dtype), on.empty(dH.shape, dH.dtype)
         H = on.empty(dH.shape, dH.dtype) if want_h else None
-        _check(_lib.forge_gated_backward(_ref(_ten(dH)), _ref(_ten(G)), _ref(_ten(U)), a,
-                                         _ref(_ten(dG)), _ref(_ten(dU)), _ref(_ten(H)), on.stream),
+        _check(_lib.forge_gated_backward(_ten(dH), _ten(G), _ten(U), a,
+                                         _ten(dG), _ten(dU), _ten(H), on.stream),
                "forge_gated_backward")
     return dG, dU, H
 
@@ -612,8 +618,8 @@ def gated_dgrad(dY: torch.Tensor, Wd: torch.Tensor, G: torch.Tensor, U: torch.Te
         shape = (dY.shape[0], Wd.shape[1])
         dG, dU = on.empty(shape, Wd.dtype), on.empty(shape, Wd.dtype)
         H = on.empty(shape, Wd.dtype) if want_h else None
-        _check(_lib.forge_gated_dgrad(_ref(_ten(dY)), _ref(_ten(Wd)), _ref(_ten(G)), _ref(_ten(U)), a,
-                                      _ref(_ten(dG)), _ref(_ten(dU)), _ref(_ten(H)), on.stream),
+        _check(_lib.forge_gated_dgrad(_ten(dY), _ten(Wd), _ten(G), _ten(U), a,
+                                      _ten(dG), _ten(dU), _ten(H), on.stream),
                "forge_gated_dgrad")
     return dG, dU, H
 
@@ -630,7 +636,7 @@ def dgrad_group(dYs, Ws, dX: Optional[torch.Tensor] = None, stream=None) -> torc
         w_a = (ForgeTensor * n)(*[_ten(t) for t in Ws])
         need = _lib.forge_linear_dgrad_group_workspace(*dX.shape, sum(w.shape[0] for w in Ws), _DT.get(dX.dtype, -1))
         ws = on.empty((need,), torch.uint8) if need else None
-        _check(_lib.forge_linear_dgrad_group_split(n, dy_a, w_a, _ref(_ten(dX)), _ptr(ws), need, on.stream),
+        _check(_lib.forge_linear_dgrad_group_split(n, dy_a, w_a, _ten(dX), _ptr(ws), need, on.stream),
                "forge_linear_dgrad_group_split")
     return dX
 
@@ -664,7 +670,7 @@ def linear_cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
         lse, total = on.empty((T,), torch.float32), on.empty((3,), torch.float32)
         need = _lib.forge_linear_xent_workspace(T, X.shape[1], W.shape[0], _DT.get(W.dtype, -1), 0, 0)
         ws = on.empty((need,), torch.uint8)
-        _check(_lib.forge_linear_xent_forward(_ref(_ten(X)), _ref(_ten(W)), _ptr(targets), int(ignore_index),
+        _check(_lib.forge_linear_xent_forward(_ten(X), _ten(W), _ptr(targets), int(ignore_index),
                                               _ptr(loss), _ptr(lse), total.data_ptr(), _ptr(ws), need, on.stream),
                "forge_linear_xent_forward")
     return (loss if reduction == "none" else total[2 if reduction == "mean" else 0]), lse, total
@@ -696,9 +702,9 @@ def linear_cross_entropy_backward(X: torch.Tensor, W: torch.Tensor, targets: tor
         need, ws, tot = _xent_grad_args(on, X, W, targets, lse, dloss, reduction, total, piece)
         dX = on.empty(X.shape, X.dtype) if want_dx else None
         dW = on.empty(W.shape, W.dtype) if want_dw else None
-        _check(_lib.forge_linear_xent_backward(_ref(_ten(X)), _ref(_ten(W)), _ptr(targets), int(ignore_index),
+        _check(_lib.forge_linear_xent_backward(_ten(X), _ten(W), _ptr(targets), int(ignore_index),
                                                _ptr(lse), _ptr(dloss), int(reduction == "none"), _ptr(tot),
-                                               _ref(_ten(dX)), _ref(_ten(dW)), int(piece), _ptr(ws), need,
+                                               _ten(dX), _ten(dW), int(piece), _ptr(ws), need,
                                                on.stream), "forge_linear_xent_backward")
     return dX, dW
 
@@ -717,10 +723,10 @@ def linear_cross_entropy_step(X: torch.Tensor, W: torch.Tensor, m: Optional[torc
     with _On(stream, X, W, m, v, targets, lse, dloss, m_scale, v_scale, total) as on:
         need, ws, tot = _xent_grad_args(on, X, W, targets, lse, dloss, reduction, total, piece)
         dX = on.empty(X.shape, X.dtype) if want_dx else None
-        _check(_lib.forge_linear_xent_step(_ref(_ten(X)), _ref(_ten(W)), _ref(describe(m, m_scale, code=code)),
+        _check(_lib.forge_linear_xent_step(_ten(X), _ten(W), _ref(describe(m, m_scale, code=code)),
                                            _ref(describe(v, v_scale, code=code)), OPT_ID[opt], ctypes.byref(h),
                                            int(step), seed & (2 ** 64 - 1), _ptr(targets), int(ignore_index),
                                            _ptr(lse), _ptr(dloss), int(reduction == "none"), _ptr(tot),
-                                           _ref(_ten(dX)), int(piece), _ptr(ws), need, on.stream),
+                                           _ten(dX), int(piece), _ptr(ws), need, on.stream),
                "forge_linear_xent_step")
     return dX
