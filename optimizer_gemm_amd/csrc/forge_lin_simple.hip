@@ -242,6 +242,20 @@ hipError_t pick(int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
   return hipErrorInvalidValue;
 }
 
+// Whether the kernel for a few tokens takes a forward product. It reads the tokens once per 16
+// rows of W, past the first-level cache's rate as they grow in number, where the tiles read
+// them once per 64: above 16 tokens it keeps the layers with tiles for a quarter of the chip at
+// most (32 x 14336 -> 4096: 40 us against 47; 32 x 8192 -> 8192: 45 against 30), above 4 also those
+// that fill more than two rounds or less than half of one (16 x 4096 -> 14336: 32 against 22; 16 x
+// 4096 -> 4096: 11 against 17; 4 x 4096 -> 40000: 63 against 87).
+bool few_tokens(int epi, const LinArgs& g) {
+  // (a grid of fewer than 2^32 threads)
+  if (g.N > kSkinny || g.M >= (1 << 26)) return false;
+  const int64_t tiles = ((epi == L_GATED ? 2 : 1) * (int64_t)g.M + 63) / 64, cus = g_num_cus();
+  if (g.N > 16) return 4 * tiles <= cus;
+  return g.N <= 4 || 2 * tiles <= cus || tiles > 2 * cus;
+}
+
 // tiles of 64x64: the larger kernels count theirs in 32 bits
 bool few_tiles(const LinArgs& g) {
   return ((int64_t)g.M + S_B) / S_B * (((int64_t)g.N + S_B) / S_B) < ((int64_t)1 << 30);
@@ -255,8 +269,7 @@ FORGE_LIN_FORMS(FORGE_EXTERN_LIN)
 
 hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
   if (!bf16) return pick<float>(epi, ta, tb, g, st);
-  // (2^30 rows of 16 make a grid of fewer than 2^32 threads only up to 2^27 rows)
-  if ((epi == L_LINEAR || epi == L_GATED) && g.N <= kSkinny && g.M < (1 << 26)) return launch_lin_skinny(epi, g, st);
+  if ((epi == L_LINEAR || epi == L_GATED) && few_tokens(epi, g)) return launch_lin_skinny(epi, g, st);
   if (!few_tiles(g)) return pick<uint16_t>(epi, ta, tb, g, st);
 #define FORGE_PICK(E, A, B) \
   if (epi == E && ta == A && tb == B) return lin_bf16<E, A, B>(g, st);

@@ -277,7 +277,7 @@ __host__ __device__ constexpr int epi_width(int M) {
 // Host-side launchers. bf16: operands in bfloat16, else float32. ta / tb: the operand's
 // slow index is k (its rows are k), else k is the fast index.
 hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st);
-// forward products (L_LINEAR, L_GATED) of at most kSkinny tokens, bf16
+// forward products (L_LINEAR, L_GATED) of at most kSkinny tokens, bf16 (launch_lin chooses)
 constexpr int kSkinny = 32;
 hipError_t launch_lin_skinny(int epi, const LinArgs& g, hipStream_t st);
 // vocabulary entries per partial result that launch_lin(L_LSE) writes for this product

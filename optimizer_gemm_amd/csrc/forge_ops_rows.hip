@@ -246,8 +246,10 @@ hipError_t act_backward(int act, const void* dY, int64_t lddy, const void* Z, in
 
 }  // namespace
 
-// Blocks of rows: enough workgroups to fill the chip several times, at least 16 rows each.
+// Blocks of rows: one for few rows, else enough workgroups to fill the chip several times, at
+// least 16 rows each.
 int act_backward_blocks(int64_t T, int64_t out) {
+  if (T <= 64) return 1;  // no join: 34 x 6416 11.8 us against 16.4; at 128 rows 18 against 16
   const int64_t cols = (out + kAbCols<bf16_t> - 1) / kAbCols<bf16_t>;
   int64_t b = cols > 0 ? (2048 + cols - 1) / cols : 1;
   const int64_t most = (T + 15) / 16;

@@ -441,3 +441,22 @@ def test_products_of_every_ring_position(stages):
     for _ in range(2):
         close("Y", forge.linear(X, W, act="silu", residual=R), *linear64(X, W, None, "silu", R)[:2])
     close("dX", forge.dgrad_group([X], [W.t().contiguous()]), *mm64(X, W.t().contiguous()))
+
+
+@pytest.mark.parametrize("o", [40, 2056, 4104, 9000, 33000])
+@pytest.mark.parametrize("t", [1, 4, 5, 16, 17, 32, 33])
+def test_few_tokens(t, o):
+    """Both sides of the choice between the kernel for a few tokens and the tiles."""
+    g = gen(t * 7 + o)
+    i = 136
+    X, W, W2 = rnd(g, t, i), rnd(g, o, i, std=i ** -0.5), rnd(g, o, i, std=i ** -0.5)
+    b, R = rnd(g, o), rnd(g, t, o)
+    Y, Z = forge.linear(pitched(X), W, bias=b, act="gelu", residual=pitched(R), save=True)
+    y, dy, z, dz = linear64(X, W, b, "gelu", R)
+    close("Y", Y, y, dy)
+    close("Z", Z, z, dz)
+    H, G, U = forge.gated(X, W, pitched(W2), act="silu", save=True)
+    h, dh, gg, dg, uu, du = gated64(X, W, W2, "silu")
+    close("H", H, h, dh)
+    close("G", G, gg, dg)
+    close("U", U, uu, du)
