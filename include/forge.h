@@ -355,7 +355,8 @@ int forge_linear_dgrad_group_split(int32_t n_layers, const forge_tensor* dY, con
  *   lse[t] = log sum_v exp(z[t, v]),  loss[t] = lse[t] - z[t, target[t]].
  * X [T, in], W [vocab, in] (vocab: any number from 1 on; W may exceed 2^31 bytes, its rows
  * less than 2^23 bytes apart), target: T int64 in
- * [0, vocab), or `ignore` for tokens that do not count (loss 0, no gradient). Any other
+ * [0, vocab), or `ignore` for tokens that do not count (loss 0, no gradient, whatever their
+ * logits are; but dW adds 0 times their rows of X, which have to be finite). Any other
  * target makes that token's loss and gradients NaN. loss (or NULL) and lse: T floats;
  * total: 3 floats, {sum of the losses, tokens counted, their mean (NaN for none)}.
  * Workspace: forge_linear_xent_workspace(T, in, vocab, dtype, 0, 0) bytes, else

@@ -658,7 +658,8 @@ def linear_cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
                          reduction: str = "mean", stream=None):
     """Softmax cross entropy of the logits X W^T against `targets`, the logits never stored
     (forge_linear_xent_forward). X [T, in], W [vocab, in]; targets: T int64 in [0, vocab) or
-    ignore_index (another value makes the loss NaN). Returns (loss, lse, total): the loss by
+    ignore_index (another value makes the loss NaN; rows of X whose target is ignored
+    reach no other token, but dW takes 0 times them: they are finite). Returns (loss, lse, total): the loss by
     `reduction` ("mean" over the tokens that count, "sum", or "none": one per token, 0 where
     ignored), each token's log sum of exponentials, and total = (sum of the losses, tokens
     counted, mean); linear_cross_entropy_backward takes the last two."""

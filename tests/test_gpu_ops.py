@@ -460,3 +460,23 @@ def test_few_tokens(t, o):
     close("H", H, h, dh)
     close("G", G, gg, dg)
     close("U", U, uu, du)
+
+
+@pytest.mark.parametrize("t,i,v", [(24, 8192, 140003), (70000, 8192, 264)])
+def test_cross_entropy_past_32_bit_offsets(t, i, v):
+    """Weights and their gradient of more than 2^31 bytes; float32 sums of dX of more."""
+    X, W, y = head(t + v, t, i, v, BF)
+    y[-1] = v - 1
+    keep = y != -100
+    n = int(keep.sum())
+    loss, lse, total = forge.linear_cross_entropy(X, W, y)
+    dX, dW = forge.linear_cross_entropy_backward(X, W, y, lse, torch.ones((), device="cuda"), total=total)
+    want, dl, want_lse, de, _, _, _ = xent64(X, W, y, -100)
+    close("lse", lse, want_lse, de, F)
+    close("mean", loss, want.sum() / n, dl.sum() / n + 2.0 ** -23 * want.sum() / n, F)
+    del want, dl, want_lse, de
+    dx, ex, dw, ew = xent_grad64(X, W, y, -100, keep.double() / n, BF)
+    close("dX", dX, dx, ex)
+    close("dW", dW, dw, ew)
+    del dx, ex, dw, ew
+    torch.cuda.empty_cache()
