@@ -275,6 +275,27 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+def _side(raw: int, device) -> torch.cuda.Stream:
+    """The stream of a raw handle (torch's wrapper takes 0 for "a new one", not for the default)."""
+    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+
+
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """A new tensor that a call writes on `stream` (None: the current one). Memory of the current
+    stream's pool may still be in use by work queued there when another stream writes it, so on
+    another stream it comes from that stream's own; the current stream, which may read it later,
+    is noted for the allocator."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    raw, current = _stream(stream), torch.cuda.current_stream(device)
+    if raw == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_side(raw, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 # ---------------------------------------------------------------------------
 # entry points
 # ---------------------------------------------------------------------------
@@ -334,7 +355,7 @@ def wgrad_step_group(X: torch.Tensor, dYs, Ws, ms, vs, opt: str = "adamw", hyper
 def dgrad(dY: torch.Tensor, W: torch.Tensor, dX: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dX = dY W (from the weights as they are now, i.e. before the step)."""
     if dX is None:
-        dX = torch.empty((dY.shape[0], W.shape[1]), dtype=W.dtype, device=W.device)
+        dX = _empty((dY.shape[0], W.shape[1]), W.dtype, W.device, stream)
     st = _lib.forge_linear_dgrad(_ref(describe(dY)), _ref(describe(W)), _ref(describe(dX)), _stream(stream))
     if st:
         raise ForgeError(st, "forge_linear_dgrad")
@@ -345,7 +366,7 @@ def wgrad(X: torch.Tensor, dY: torch.Tensor, dW: Optional[torch.Tensor] = None, 
           x_scale: Optional[torch.Tensor] = None, dy_scale: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Unfused baseline part 1: float32 dW = dY^T X written to device memory (FP8 inputs as in wgrad_step)."""
     if dW is None:
-        dW = torch.empty((dY.shape[1], X.shape[1]), dtype=torch.float32, device=X.device)
+        dW = _empty((dY.shape[1], X.shape[1]), torch.float32, X.device, stream)
     if dW.dtype != torch.float32 or dW.dim() != 2 or (dW.shape[1] > 1 and dW.stride(1) != 1) or not dW.is_cuda:
         raise ValueError("dW must be a row-major float32 device tensor")
     st = _lib.forge_linear_wgrad(_ref(describe(X, x_scale)), _ref(describe(dY, dy_scale)), dW.data_ptr(),
@@ -371,9 +392,9 @@ def optimizer_step(dW: torch.Tensor, W: torch.Tensor, m: Optional[torch.Tensor],
         raise ForgeError(st, "forge_optimizer_step")
 
 
-def _workspace(ws: Optional[torch.Tensor], W: torch.Tensor) -> torch.Tensor:
+def _workspace(ws: Optional[torch.Tensor], W: torch.Tensor, stream=None) -> torch.Tensor:
     if ws is None:
-        ws = torch.empty(tuple(W.shape), dtype=torch.float32, device=W.device)
+        ws = _empty(tuple(W.shape), torch.float32, W.device, stream)
     if ws.dtype != torch.float32 or ws.dim() != 2 or (ws.shape[1] > 1 and ws.stride(1) != 1) or not ws.is_cuda:
         raise ValueError("dW_workspace must be a row-major float32 device tensor")
     return ws
@@ -384,7 +405,7 @@ def wgrad_unfused(X, dY, W, m, v, opt="adamw", hyper=None, step=1, seed=0, m_sca
                   dy_scale=None, code: str = "linear") -> torch.Tensor:
     """The two-phase baseline in one call (forge_linear_wgrad_unfused): float32 dW into the
     workspace (allocated here if not given), then a separate optimizer pass. Returns dW."""
-    ws = _workspace(dW_workspace, W)
+    ws = _workspace(dW_workspace, W, stream)
     h = _hyper(opt, hyper)
     st = _lib.forge_linear_wgrad_unfused(_ref(describe(X, x_scale)), _ref(describe(dY, dy_scale)), _ref(describe(W)),
                                          _ref(describe(m, m_scale, code=code)), _ref(describe(v, v_scale, code=code)),
@@ -451,9 +472,13 @@ def _act(act: str) -> int:
 
 class _On:
     """The device and stream of a call: every tensor on one device, which is made current for
-    the call; the work goes to `stream`, or to that device's current stream."""
+    the call; the work goes to `stream`, or to that device's current stream. Work queued on another
+    stream before the call is the caller's to wait for, as with any kernel on a given stream;
+    the tensors' memory is safe without: what the call allocates comes from the pool of the stream
+    that writes it, and the allocator hands out no tensor of the call again before that stream (for
+    a new tensor: the current one too) is done with it."""
 
-    __slots__ = ("device", "stream", "_given", "_guard", "_index")
+    __slots__ = ("device", "stream", "_given", "_guard", "_index", "_others")
 
     def __init__(self, stream, first, *others):
         self._index = index = first.get_device()
@@ -467,24 +492,27 @@ class _On:
             raise ValueError("the stream belongs to another device than the tensors")
         self._given = stream
         self._guard = None
+        self._others = (first, *others) if stream is not None else None
 
     def __enter__(self):
         if _current_device() != self._index:
             self._guard = torch.cuda.device(self._index)
             self._guard.__enter__()
-        self.stream = _raw_stream(self._index) if self._given is None else _stream(self._given)
+        current = _raw_stream(self._index)
+        self.stream = current if self._given is None else _stream(self._given)
+        if self.stream != current:
+            side = _side(self.stream, self.device)
+            for t in self._others:
+                if t is not None:
+                    t.record_stream(side)
         return self
 
     def __exit__(self, *exc):
         return self._guard.__exit__(*exc) if self._guard is not None else None
 
     def empty(self, shape, dtype) -> torch.Tensor:
-        """A new tensor for this call. On a stream other than the current one the memory is
-        kept from being handed out again before that stream is done with it."""
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self._given is not None and self.stream != _raw_stream(self._index):
-            t.record_stream(torch.cuda.ExternalStream(self.stream))
-        return t
+        """A new tensor that this call writes."""
+        return _empty(shape, dtype, self.device, self._given)
 
 
 # torch's own short ways to the device's current stream and to the current device: a few

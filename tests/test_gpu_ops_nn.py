@@ -329,3 +329,71 @@ def test_loss_of_other_weights_is_refused():
         weight.mul_(2)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def pool_stream(t):
+    """The stream in whose pool a tensor's memory lies."""
+    at = t.data_ptr()
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= at < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's memory")
+
+
+def test_memory_of_a_call_on_another_stream():
+    """What a call on another stream allocates is that stream's memory, for every entry point: blocks
+    freed on the current stream, with work on them still queued there, are not taken."""
+    a = operands(20)
+    x, wg, wu, wd, b, w, y = a
+    s = torch.cuda.Stream()
+    one = torch.ones((), device="cuda")
+    w1 = wg.clone()
+    m, v, _, _ = forge.new_states(w1, "adamw")
+    torch.cuda.synchronize()
+    out = [forge.linear(x, wg, act="silu", save=True, stream=s), forge.gated(x, wg, wu, save=True, stream=s)]
+    H, G, U = out[-1]
+    out.append(forge.linear_act_backward(G, U, act="gelu", stream=s))
+    out.append(forge.gated_backward(H, G, U, stream=s))
+    out.append(forge.gated_dgrad(x, wd, G, U, stream=s))
+    out.append([forge.dgrad_group([G, U], [wg, wu], stream=s)])
+    loss, lse, total = forge.linear_cross_entropy(x, w, y, reduction="none", stream=s)
+    out.append((loss, lse, total))
+    out.append(forge.linear_cross_entropy_backward(x, w, y, lse, one, reduction="mean", total=total, stream=s))
+    out.append([forge.dgrad(G, wg, stream=s), forge.wgrad(x, G, stream=s)])
+    out.append([forge.wgrad_unfused(x, G, w1, m, v, stream=s)])
+    for group in out:
+        for t in group:
+            assert pool_stream(t) == s.cuda_stream
+    torch.cuda.synchronize()
+
+
+def test_calls_on_another_stream_beside_queued_work():
+    """Operators on a second stream while the current one writes, reads and frees memory of the same
+    sizes, the operands waited for: the results are the same bits."""
+    x, wg, wu, wd, b, w, y = operands(20)
+    one = torch.ones((), device="cuda")
+    s, cur = torch.cuda.Stream(), torch.cuda.current_stream()
+
+    def run(stream):
+        H, G, U = forge.gated(x, wg, wu, save=True, stream=stream)
+        z, pre = forge.linear(H, wd, bias=b, act="gelu", residual=x, save=True, stream=stream)
+        loss, lse, total = forge.linear_cross_entropy(z, w, y, stream=stream)
+        dz, dw = forge.linear_cross_entropy_backward(z, w, y, lse, one, total=total, stream=stream)
+        da, db = forge.linear_act_backward(dz, pre, act="gelu", stream=stream)
+        dG, dU, H2 = forge.gated_dgrad(da, wd, G, U, stream=stream)
+        return [H, z, loss, lse, dz, dw, da, db, dG, dU, H2, forge.dgrad_group([dG, dU], [wg, wu], stream=stream),
+                forge.dgrad(dG, wg, stream=stream), forge.wgrad(x, dG, stream=stream)]
+
+    want = run(None)
+    for _ in range(6):
+        s.wait_stream(cur)
+        busy = [torch.full_like(t, 3.0) for t in want for _ in range(2)]
+        sums = [(t.numel(), t.float().sum()) for t in busy]
+        del busy
+        got = run(s)
+        cur.wait_stream(s)
+        for w_, g_ in zip(want, got):
+            assert torch.equal(w_, g_)
+        for n, v in sums:
+            assert float(v) == 3.0 * n  # whole numbers below 2^24: exact in any order
+        del got

@@ -231,3 +231,60 @@ def test_xent_backward_refuses_distant_rows():
     far = 1 << 22
     assert bwd(ten(1, V, D, ld=far), ten(3, V, D)) == UNSUP
     assert bwd(ten(1, V, D), ten(3, V, D, ld=far)) == UNSUP
+
+
+def test_new_tensors_come_from_the_stream_that_writes_them(monkeypatch):
+    """On a stream other than the current one a call allocates from that stream's pool (memory of
+    the current stream's may be in use there), and notes the current one for the new tensor and
+    the other one for the call's tensors."""
+    import contextlib
+
+    from optimizer_gemm_amd import forge as impl
+
+    log, active = [], [11]
+
+    class FakeStream:
+        def __init__(self, raw):
+            self.cuda_stream = raw
+
+    class FakeTensor:
+        device = torch.device("cuda", 0)
+
+        def __init__(self, name):
+            self.name = name
+
+        def get_device(self):
+            return 0
+
+        def record_stream(self, s):
+            log.append((self.name, s.cuda_stream))
+
+    @contextlib.contextmanager
+    def stream(s):
+        active.append(s.cuda_stream)
+        yield
+        active.pop()
+
+    def empty(shape, dtype, device):
+        log.append(("new", "from", active[-1]))
+        return FakeTensor("new")
+
+    monkeypatch.setattr(impl.torch, "empty", empty)
+    monkeypatch.setattr(impl.torch.cuda, "current_stream", lambda d=None: FakeStream(11))
+    monkeypatch.setattr(impl.torch.cuda, "stream", stream)
+    monkeypatch.setattr(impl.torch.cuda, "ExternalStream", lambda raw, device=None: FakeStream(raw))
+    monkeypatch.setattr(impl.torch.cuda, "default_stream", lambda d=None: FakeStream(0))
+    monkeypatch.setattr(impl, "_raw_stream", lambda d: 11)
+    monkeypatch.setattr(impl, "_current_device", lambda: 0)
+    for given, want in ((22, [("x", 22), ("new", "from", 22), ("new", 11)]),
+                        (0, [("x", 0), ("new", "from", 0), ("new", 11)]),
+                        (11, [("new", "from", 11)]), (None, [("new", "from", 11)])):
+        log.clear()
+        with impl._On(given, FakeTensor("x"), None) as on:
+            on.empty((4,), torch.float32)
+            assert on.stream == (11 if given is None else given)
+        assert log == want, given
+    # the calls that came before these operators
+    log.clear()
+    impl._empty((4,), torch.float32, torch.device("cuda", 0), 22)
+    assert log == [("new", "from", 22), ("new", 11)]
