@@ -88,7 +88,8 @@ def _rows(t: torch.Tensor, cols: int, dtype: torch.dtype) -> torch.Tensor:
 
 def _update(layers, x2: torch.Tensor, dy2s) -> None:
     """The weight-gradient half of a backward pass for layers that read x2: their fused steps
-    (one launch for several), or, two-phase, their float32 gradients for step_all()."""
+    (one launch for several, which are _alike), or, two-phase, their float32 gradients for
+    step_all(). A call that is refused leaves the step counts as they were."""
     L0 = layers[0]
     if not L0.fused:
         for L, dy2 in zip(layers, dy2s):
@@ -98,19 +99,20 @@ def _update(layers, x2: torch.Tensor, dy2s) -> None:
             else:
                 L.grad32.add_(g)
         return
-    for L in layers:
-        L._step_count += 1
+    step = L0._step_count + 1
     ev = L0.timing
     if ev is not None:
         e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         e0.record()
     if len(layers) == 1:
-        forge.wgrad_step(x2, dy2s[0], L0.weight.detach(), L0.m, L0.v, L0.opt, L0.hyper, L0._step_count, L0.seed,
+        forge.wgrad_step(x2, dy2s[0], L0.weight.detach(), L0.m, L0.v, L0.opt, L0.hyper, step, L0.seed,
                          L0.m_scale, L0.v_scale, code=L0.code)
     else:
         forge.wgrad_step_group(x2, dy2s, [L.weight.detach() for L in layers], [L.m for L in layers],
-                               [L.v for L in layers], L0.opt, L0.hyper, L0._step_count, [L.seed for L in layers],
+                               [L.v for L in layers], L0.opt, L0.hyper, step, [L.seed for L in layers],
                                [L.m_scale for L in layers], [L.v_scale for L in layers], code=L0.code)
+    for L in layers:
+        L._step_count = step
     if ev is not None:
         e1.record()
         ev.append((e0, e1))
@@ -293,25 +295,31 @@ class _ForgeGroupFn(torch.autograd.Function):
         return (dx, None) + (None,) * len(layers)
 
 
+def _alike(layers) -> bool:
+    """Whether one grouped step may take the layers: the same optimizer, hyper-parameters, moment
+    format, schedule, type and step count."""
+    L0 = layers[0]
+    return not any(
+        (L.opt, L.code, L.fused, L._step_count, L.weight.dtype) != (L0.opt, L0.code, L0.fused, L0._step_count,
+                                                                     L0.weight.dtype) or
+        (L.m is None) != (L0.m is None) or (L.v is None) != (L0.v is None) or
+        (L.m is not None and L.m.dtype != L0.m.dtype) or (L.v is not None and L.v.dtype != L0.v.dtype) or
+        any(getattr(L.hyper, n) != getattr(L0.hyper, n) for n, _ in L0.hyper._fields_) for L in layers[1:])
+
+
 def grouped_linear(layers, x: torch.Tensor):
     """Y_l = X W_l^T for ForgeLinear layers that read the same input x, as one autograd node
     whose backward steps all of them in one grouped launch (the layers' outputs as a tuple).
     The layers must agree in optimizer, hyper-parameters, moment format, schedule and step
     count; the group's time is recorded on the first layer's `timing` list."""
     layers = list(layers)
-    L0 = layers[0]
     if not 1 <= len(layers) <= forge.MAX_GROUP:
         raise ValueError(f"a group holds 1..{forge.MAX_GROUP} layers")
     for L in layers:
         if L.bias is not None or L.act != "none":
             raise ValueError("grouped layers have no bias and no activation")
-    for L in layers[1:]:
-        if (L.opt, L.code, L.fused, L._step_count, L.weight.dtype) != (L0.opt, L0.code, L0.fused, L0._step_count,
-                                                                         L0.weight.dtype) or \
-                (L.m is None) != (L0.m is None) or (L.v is None) != (L0.v is None) or \
-                (L.m is not None and L.m.dtype != L0.m.dtype) or \
-                any(getattr(L.hyper, n) != getattr(L0.hyper, n) for n, _ in L0.hyper._fields_):
-            raise ValueError("grouped layers must share optimizer, hyper-parameters, states, schedule and step")
+    if not _alike(layers):
+        raise ValueError("grouped layers must share optimizer, hyper-parameters, states, schedule and step")
     return _ForgeGroupFn.apply(x, layers, *[L.weight for L in layers])
 
 
@@ -351,7 +359,11 @@ class _GatedBlockFn(torch.autograd.Function):
         dG, dU, H = forge.gated_dgrad(dy2, wd, G, U, act="silu")
         dh = forge.dgrad_group([dG, dU], [wg, wu]).reshape(ctx.h_shape) if ctx.needs_input_grad[0] else None
         _update([down], H, [dy2])
-        _update([gate, up], h2, [dG, dU])
+        if wg.dtype == torch.bfloat16 and _alike((gate, up)):
+            _update([gate, up], h2, [dG, dU])
+        else:  # the grouped step takes bf16 layers that agree
+            _update([gate], h2, [dG])
+            _update([up], h2, [dU])
         return dh, (dy.reshape(ctx.r_shape) if ctx.needs_input_grad[1] else None), None, None, None, None
 
 
@@ -364,8 +376,9 @@ class SwiGLUBlock(torch.nn.Module):
     so it sees the same weights as the forward pass. With grouped=True gate and up, which
     read the same n(x), take their fused steps in one grouped launch. With joined=True gate,
     up, activation and product are one kernel, the residual is added by the down projection,
-    and the backward pass is joined likewise (gate and up stepped in one launch); bf16 layers
-    (the grouped step takes no others), results as the separate layers' up to rounding."""
+    and the backward pass is joined likewise (gate and up stepped in one launch where they are bf16
+    and agree in optimizer, states and step count, else one after the other); results as the
+    separate layers' up to rounding."""
 
     def __init__(self, d: int, hidden: int, checkpoint: bool = False, seed: int = 0, grouped: bool = False,
                  joined: bool = False, **kw):

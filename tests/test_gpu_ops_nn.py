@@ -397,3 +397,69 @@ def test_calls_on_another_stream_beside_queued_work():
         for n, v in sums:
             assert float(v) == 3.0 * n  # whole numbers below 2^24: exact in any order
         del got
+
+
+def joined_by_hand(blk, x, dy, counts):
+    """The joined block's weights after one backward pass, its operators called one by one with the
+    layers' own step counts."""
+    gate, up, down = blk.gate, blk.up, blk.down
+    wg, wu, wd = (L.weight.detach().clone() for L in (gate, up, down))
+    xf = x.detach().float()
+    h = (xf * torch.rsqrt(xf.pow(2).mean(-1, keepdim=True) + 1e-5)).to(x.dtype)
+    H, G, U = forge.gated(h, wg, wu, save=True)
+    dG, dU, H2 = forge.gated_dgrad(dy, wd, G, U)
+    for L, w, a, d, n in ((gate, wg, h, dG, counts[0]), (up, wu, h, dU, counts[1]), (down, wd, H2, dy, counts[2])):
+        m, v = (None if t is None else t.clone() for t in (L.m, L.v))
+        forge.wgrad_step(a, d, w, m, v, L.opt, L.hyper, n, L.seed)
+    return [wg, wu, wd]
+
+
+def test_joined_block_steps_float32_layers():
+    """float32, which the grouped step does not take: every layer is stepped, by its own call."""
+    F = torch.float32
+    blk = block(True, dtype=F)
+    x, dy = rnd(7, 130, 256, dtype=F).requires_grad_(), rnd(8, 130, 256, std=1e-2, dtype=F)
+    for n in (1, 2):
+        want = joined_by_hand(blk, x, dy, (n, n, n))
+        blk(x).backward(dy)
+        for L, w in zip((blk.gate, blk.up, blk.down), want):
+            assert L.step_count == n and torch.equal(L.weight.detach(), w)
+
+
+def test_joined_block_of_layers_that_disagree():
+    """gate has taken a step alone: gate and up step with their own counts (the grouped step would
+    give up gate's)."""
+    blk = block(True)
+    x, dy = rnd(7, 130, 256), rnd(8, 130, 256, std=1e-2)
+    blk.gate(x).backward(rnd(9, 130, 640, std=1e-2))
+    want = joined_by_hand(blk, x, dy, (2, 1, 1))
+    blk(x.requires_grad_()).backward(dy)
+    assert (blk.gate.step_count, blk.up.step_count, blk.down.step_count) == (2, 1, 1)
+    for L, w in zip((blk.gate, blk.up, blk.down), want):
+        assert torch.equal(L.weight.detach(), w)
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_joined_block_in_two_phases(dtype):
+    """fused=False: backward keeps the float32 gradients of all three layers (a second pass adds to
+    them), step_all applies them."""
+    blk = block(True, dtype=dtype, fused=False)
+    x, dy = rnd(7, 130, 256, dtype=dtype).requires_grad_(), rnd(8, 130, 256, std=1e-2, dtype=dtype)
+    layers = (blk.gate, blk.up, blk.down)
+    old = [L.weight.detach().clone() for L in layers]
+    blk(x).backward(dy)
+    xf = x.detach().float()
+    h = (xf * torch.rsqrt(xf.pow(2).mean(-1, keepdim=True) + 1e-5)).to(dtype)
+    H, G, U = forge.gated(h, old[0], old[1], save=True)
+    dG, dU, H2 = forge.gated_dgrad(dy, old[2], G, U)
+    want = [forge.wgrad(h, dG), forge.wgrad(h, dU), forge.wgrad(H2, dy)]
+    for L, w, g in zip(layers, old, want):
+        assert L.step_count == 0 and torch.equal(L.weight.detach(), w) and torch.equal(L.grad32, g)
+    blk(x).backward(dy)
+    for L, g in zip(layers, want):
+        assert torch.equal(L.grad32, g + g)
+    step_all(blk)
+    for L, w, g in zip(layers, old, want):
+        m, v, _, _ = forge.new_states(w, "adamw")
+        forge.optimizer_step(g + g, w, m, v, "adamw", None, 1, L.seed)
+        assert L.step_count == 1 and L.grad32 is None and torch.equal(L.weight.detach(), w)

@@ -288,3 +288,22 @@ def test_new_tensors_come_from_the_stream_that_writes_them(monkeypatch):
     log.clear()
     impl._empty((4,), torch.float32, torch.device("cuda", 0), 22)
     assert log == [("new", "from", 22), ("new", 11)]
+
+
+def test_a_refused_step_leaves_the_step_counts(monkeypatch):
+    """Layers whose step is refused count no step."""
+    from types import SimpleNamespace
+
+    from optimizer_gemm_amd import nn as fnn
+
+    def refuse(*a, **kw):
+        raise forge.ForgeError(-5, "refused")
+
+    monkeypatch.setattr(fnn.forge, "wgrad_step", refuse)
+    monkeypatch.setattr(fnn.forge, "wgrad_step_group", refuse)
+    layers = [SimpleNamespace(fused=True, _step_count=4, timing=None, weight=torch.zeros(8, 8), m=None, v=None,
+                              m_scale=None, v_scale=None, opt="sgd", hyper=None, seed=0, code="linear") for _ in range(2)]
+    for some in (layers, layers[:1]):
+        with pytest.raises(forge.ForgeError):
+            fnn._update(some, None, [None] * len(some))
+        assert [L._step_count for L in layers] == [4, 4]
