@@ -10,7 +10,9 @@ place. The weight gradient is never materialised: backward returns None for it,
 so `weight.grad` stays None and no optimizer.step() follows.
 
 Each backward call is one optimizer step of that layer (a module used several
-times per step, such as a tied embedding, is outside what the method supports).
+times per step, such as a tied embedding, is outside what the method supports;
+layers with an epilogue, joined blocks and heads, which keep more of the forward
+pass than its input, refuse the second of two backward passes).
 
 For comparison the same module runs the usual two-phase schedule with
 fused=False: backward stores the float32 dW (the "gradient floor" every layer
@@ -118,6 +120,14 @@ def _update(layers, x2: torch.Tensor, dy2s) -> None:
         ev.append((e0, e1))
 
 
+def _check_unstepped(layers, counts) -> None:
+    """What a forward pass kept (pre-activations, projections) belongs to its weights, and so does
+    the input gradient: refuses a backward pass once they have been stepped. (Steps write through raw
+    pointers, which autograd's own check of saved tensors does not see.)"""
+    if [L._step_count for L in layers] != counts:
+        raise RuntimeError("the layer's weights were stepped after this output was computed")
+
+
 class _ForgeLinearEpiFn(torch.autograd.Function):
     """ForgeLinear with a bias, an activation or a residual: forward is one product with an
     epilogue; backward takes the gradient through the activation, then dX, then the steps."""
@@ -131,14 +141,16 @@ class _ForgeLinearEpiFn(torch.autograd.Function):
                          save=keep)
         y, z = y if keep else (y, None)
         ctx.layer, ctx.x_shape, ctx.r_shape = layer, x.shape, None if residual is None else residual.shape
-        ctx.save_for_backward(x2, z)
+        ctx.counts = [layer._step_count]
+        ctx.save_for_backward(x2, z, weight)
         return y.reshape(*x.shape[:-1], weight.shape[0])
 
     @staticmethod
     def backward(ctx, dy):
-        x2, z = ctx.saved_tensors
         layer = ctx.layer
-        w = layer.weight.detach()
+        _check_unstepped([layer], ctx.counts)
+        x2, z, weight = ctx.saved_tensors
+        w = weight.detach()
         dy2 = _rows(dy, w.shape[0], w.dtype)
         dz, db = forge.linear_act_backward(dy2, z, act=layer.act, want_bias=layer.bias is not None)
         # old W, before the update below
@@ -347,14 +359,16 @@ class _GatedBlockFn(torch.autograd.Function):
         H, G, U = forge.gated(h2, wg.detach(), wu.detach(), act="silu", save=True)
         y = forge.linear(H, wd.detach(), residual=r2)
         ctx.block, ctx.h_shape, ctx.r_shape = block, h.shape, r.shape
-        ctx.save_for_backward(h2, G, U)
+        ctx.counts = [L._step_count for L in (block.gate, block.up, block.down)]
+        ctx.save_for_backward(h2, G, U, wg, wu, wd)
         return y.reshape(r.shape)
 
     @staticmethod
     def backward(ctx, dy):
-        h2, G, U = ctx.saved_tensors
         gate, up, down = ctx.block.gate, ctx.block.up, ctx.block.down
-        wg, wu, wd = gate.weight.detach(), up.weight.detach(), down.weight.detach()
+        _check_unstepped((gate, up, down), ctx.counts)
+        h2, G, U, wg, wu, wd = ctx.saved_tensors
+        wg, wu, wd = wg.detach(), wu.detach(), wd.detach()
         dy2 = _rows(dy, wd.shape[0], wd.dtype)
         dG, dU, H = forge.gated_dgrad(dy2, wd, G, U, act="silu")
         dh = forge.dgrad_group([dG, dU], [wg, wu]).reshape(ctx.h_shape) if ctx.needs_input_grad[0] else None

@@ -463,3 +463,56 @@ def test_joined_block_in_two_phases(dtype):
         m, v, _, _ = forge.new_states(w, "adamw")
         forge.optimizer_step(g + g, w, m, v, "adamw", None, 1, L.seed)
         assert L.step_count == 1 and L.grad32 is None and torch.equal(L.weight.detach(), w)
+
+
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_output_of_other_weights_is_refused_by_the_joined_block(ckpt):
+    """Two forward passes, two backward passes: the second one's projections belong to weights that
+    the first has stepped."""
+    blk = block(True, ckpt=ckpt)
+    x, dy = rnd(7, 70, 256).requires_grad_(), rnd(8, 70, 256, std=1e-2)
+    first, second = blk(x), blk(x)
+    first.backward(dy)
+    kept = [L.weight.detach().clone() for L in (blk.gate, blk.up, blk.down)]
+    with pytest.raises(RuntimeError, match="stepped after"):
+        second.backward(dy)
+    for L, w in zip((blk.gate, blk.up, blk.down), kept):
+        assert L.step_count == 1 and torch.equal(L.weight.detach(), w)
+    blk(x).backward(dy)
+    assert blk.gate.step_count == blk.up.step_count == blk.down.step_count == 2
+
+
+@pytest.mark.parametrize("bias,act,residual", [(True, "none", False), (False, "gelu", False), (False, "none", True)])
+def test_output_of_other_weights_is_refused_by_the_linear_layer(bias, act, residual):
+    layer = ForgeLinear(64, 128, weight=rnd(1, 128, 64, std=0.1), bias=bias, act=act)
+    x, dy = rnd(2, 70, 64).requires_grad_(), rnd(3, 70, 128, std=1e-2)
+    r = rnd(4, 70, 128) if residual else None
+    first, second = layer(x, r), layer(x, r)
+    first.backward(dy)
+    w = layer.weight.detach().clone()
+    with pytest.raises(RuntimeError, match="stepped after"):
+        second.backward(dy)
+    assert layer.step_count == 1 and torch.equal(layer.weight.detach(), w)
+    layer(x, r).backward(dy)
+    assert layer.step_count == 2
+    # another writer of the weights: autograd's own check
+    third = layer(x, r)
+    with torch.no_grad():
+        layer.weight.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        third.backward(dy)
+
+
+def test_two_phase_layers_take_several_backward_passes():
+    """Two phases: the weights stay until step_all, so two micro-batches add their gradients; an
+    output from before the step is refused after it."""
+    layer = ForgeLinear(64, 128, weight=rnd(1, 128, 64, std=0.1), bias=True, act="gelu", fused=False)
+    x, dy = rnd(2, 70, 64).requires_grad_(), rnd(3, 70, 128, std=1e-2)
+    first, second, third = layer(x), layer(x), layer(x)
+    first.backward(dy)
+    one = layer.grad32.clone()
+    second.backward(dy)
+    assert torch.equal(layer.grad32, one + one)
+    step_all(layer)
+    with pytest.raises(RuntimeError, match="stepped after"):
+        third.backward(dy)
