@@ -757,8 +757,8 @@ void lin_kernel(LinArgs g) {
                 b0 = lo4(P.b[k]);
                 b1 = hi4(P.b[k]);
               }
-              epi_math<EPI>(act, x0, z0, a0, b0, y0, y1, y2);
-              epi_math<EPI>(act, x1, z1, a1, b1, v0, v1, v2);
+              epi_math<uint16_t, EPI>(act, x0, z0, a0, b0, y0, y1, y2);
+              epi_math<uint16_t, EPI>(act, x1, z1, a1, b1, v0, v1, v2);
               r0[k] = pack(y0, v0);
               r1[k] = pack(y1, v1);
               if constexpr (EPI != L_LINEAR) r2[k] = pack(y2, v2);

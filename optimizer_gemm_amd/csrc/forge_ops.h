@@ -27,32 +27,44 @@ namespace forge {
 __device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // Phi(z), the normal distribution function, and e^(-z^2/2), which its derivative needs as
-// well: erfc(x) = t (a1 + t (a2 + ... )) e^(-x^2), t = 1 / (1 + 0.3275911 x), absolute error
-// below 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26). The
-// erfc form keeps the relative accuracy of the left tail up to that absolute error; one
-// exponential serves both results.
+// well. T: the type of the results.
+// bfloat16: erfc(x) = t (a1 + t (a2 + ... )) e^(-x^2), t = 1 / (1 + 0.3275911 x) (Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26), one exponential for both results. Its
+// absolute error stays below 1.5e-7; the relative one of the left tail is 5e-4 at z = -4 and
+// 1.7e-3 at -5, below half a bfloat16 step (3.9e-3) down to -6, where Phi is 1e-9.
+// float32: the library's erfc and exponential; relative to Phi (z^2 + 1) 2^-23 from the rounding
+// of z / sqrt 2, and erfc's own ulps, all the way down the tail (the short form: 5e-5 at z = -3).
+// It costs the float32 epilogue backward pass of 8192 x 4096 93 us against 86, a product 1%.
+template <class T>
 __device__ __forceinline__ float normal_cdf_f(float z, float& gauss) {
   const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
-  gauss = __expf(-0.5f * z * z);
-  float p = fmaf(t, 1.061405429f, -1.453152027f);
-  p = fmaf(t, p, 1.421413741f);
-  p = fmaf(t, p, -0.284496736f);
-  p = fmaf(t, p, 0.254829592f);
-  const float half_erfc = 0.5f * t * p * gauss;
+  float half_erfc;
+  if constexpr (std::is_same<T, float>::value) {
+    gauss = expf(-0.5f * z * z);
+    half_erfc = 0.5f * erfcf(x);
+  } else {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+    gauss = __expf(-0.5f * z * z);
+    float p = fmaf(t, 1.061405429f, -1.453152027f);
+    p = fmaf(t, p, 1.421413741f);
+    p = fmaf(t, p, -0.284496736f);
+    p = fmaf(t, p, 0.254829592f);
+    half_erfc = 0.5f * t * p * gauss;
+  }
   return z < 0.f ? half_erfc : 1.f - half_erfc;
 }
 
 constexpr float kGeluC = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kGeluK = 0.044715f;
 
+template <class T>
 __device__ __forceinline__ float act_f(float z, int act) {
   switch (act) {
     case FORGE_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);  // NaN stays NaN
     case FORGE_ACT_SILU: return z * sigmoid_f(z);
     case FORGE_ACT_GELU: {
       float e;
-      return z * normal_cdf_f(z, e);
+      return z * normal_cdf_f<T>(z, e);
     }
     case FORGE_ACT_GELU_TANH:  // z (1 + tanh u) / 2 = z sigmoid(2u)
       return z * sigmoid_f(2.f * kGeluC * z * fmaf(kGeluK * z, z, 1.f));
@@ -60,6 +72,7 @@ __device__ __forceinline__ float act_f(float z, int act) {
   }
 }
 // value a and derivative d
+template <class T>
 __device__ __forceinline__ void act_vd(float z, int act, float& a, float& d) {
   switch (act) {
     case FORGE_ACT_RELU:
@@ -74,7 +87,7 @@ __device__ __forceinline__ void act_vd(float z, int act, float& a, float& d) {
     }
     case FORGE_ACT_GELU: {
       float e;
-      const float c = normal_cdf_f(z, e);
+      const float c = normal_cdf_f<T>(z, e);
       a = z * c;
       d = fmaf(z * 0.39894228040143268f, e, c);
       return;
@@ -173,21 +186,21 @@ __device__ __forceinline__ float epi_scale(const LinEpiArgs& e) {
 
 // The arithmetic of an epilogue on 4 neighbouring columns: x the product (x2 the second one of
 // L_GATED), a and b what it reads from in1 and in2 (zero where there is none), y0 .. y2 what it
-// writes to out .. out3.
-template <int EPI>
+// writes to out .. out3; T the type of the results.
+template <class T, int EPI>
 __device__ __forceinline__ void epi_math(int act, f32x4 x, f32x4 x2, f32x4 a, f32x4 b, f32x4& y0, f32x4& y1, f32x4& y2) {
   if constexpr (EPI == L_LINEAR) {  // x: bias added
     y1 = x;
-    y0 = f32x4{act_f(x.x, act), act_f(x.y, act), act_f(x.z, act), act_f(x.w, act)} + a;
+    y0 = f32x4{act_f<T>(x.x, act), act_f<T>(x.y, act), act_f<T>(x.z, act), act_f<T>(x.w, act)} + a;
   } else if constexpr (EPI == L_GATED) {
-    y0 = f32x4{act_f(x.x, act), act_f(x.y, act), act_f(x.z, act), act_f(x.w, act)} * x2;
+    y0 = f32x4{act_f<T>(x.x, act), act_f<T>(x.y, act), act_f<T>(x.z, act), act_f<T>(x.w, act)} * x2;
     y1 = x;
     y2 = x2;
   } else if constexpr (EPI == L_DGATE) {  // x = dH, a = G, b = U
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float v, d;
-      act_vd(a[j], act, v, d);
+      act_vd<T>(a[j], act, v, d);
       y0[j] = x[j] * (b[j] * d);
       y1[j] = x[j] * v;
       y2[j] = v * b[j];
@@ -260,7 +273,7 @@ __device__ __forceinline__ void epi_vec(const LinEpiArgs& e, int n, int m, int M
     }
     if (e.in1) a = load4(static_cast<const T*>(e.in1) + (int64_t)n * e.ld1 + m);
     if (e.in2) b = load4(static_cast<const T*>(e.in2) + (int64_t)n * e.ld2 + m);
-    epi_math<EPI>(ACT, x, x2, a, b, y0, y1, y2);
+    epi_math<T, EPI>(ACT, x, x2, a, b, y0, y1, y2);
     store4(static_cast<T*>(e.out) + (int64_t)n * e.ldo + m, y0);
     if (e.out2) store4(static_cast<T*>(e.out2) + (int64_t)n * e.ldo2 + m, y1);
     if (e.out3) store4(static_cast<T*>(e.out3) + (int64_t)n * e.ldo3 + m, y2);

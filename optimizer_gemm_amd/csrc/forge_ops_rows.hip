@@ -55,7 +55,7 @@ __global__ __launch_bounds__(AB_NT) void act_backward_kernel(int act, const T* d
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 float a, g;
-                act_vd(y[j], ACT, a, g);
+                act_vd<T>(y[j], ACT, a, g);
                 x[j] *= g;
               }
             }

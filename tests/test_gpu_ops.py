@@ -480,3 +480,35 @@ def test_cross_entropy_past_32_bit_offsets(t, i, v):
     close("dW", dW, dw, ew)
     del dx, ex, dw, ew
     torch.cuda.empty_cache()
+
+
+def test_float32_gelu_in_its_left_tail():
+    """Relative to the value itself, down to z = -12: z Phi(z) and its derivative Phi + z phi. u = 2^-24.
+    Phi = erfc(x) / 2 with x = |z| / sqrt 2 held to 2 u (its constant, its product), which moves erfc by
+    2 u (2 x^2 + 1) of itself at most; erfc and the exponential are the device library's, 16 and 3 ulps
+    at most (32 u, 6 u); the exponential's argument z^2 / 2 is held to 1 u, which moves it by
+    u z^2 / 2; up to 4 u of products and half a step of the result."""
+    U = 2.0 ** -24
+    n = 4096
+    z = torch.linspace(-12.0, -0.25, n * 8, device="cuda", dtype=F).reshape(n, 8)
+    one = torch.ones_like(z)
+    zd = z.double()
+    a, d = act64(zd, "gelu")
+    phi = 0.5 * torch.special.erfc(-zd / 2 ** 0.5)
+    pdf = torch.exp(-zd * zd / 2) / (2 * torch.pi) ** 0.5
+    rel = (2 * (zd * zd + 1) + 32 + 4 + 1) * U
+    tol_d = rel * phi + (zd * zd / 2 + 6 + 4) * U * (zd * pdf).abs() + U * d.abs()
+    ident = torch.eye(8, device="cuda", dtype=F)
+    value = forge.linear(z, ident, act="gelu").double()
+    wide = forge.linear(z, ident.repeat(16, 1), act="gelu")  # many columns: other tiles
+    dG, dU, H = forge.gated_backward(one, z, one, act="gelu")
+    dZ, _ = forge.linear_act_backward(one, z, act="gelu")
+    for name, got in (("linear", value), ("gated", dU.double()), ("H", H.double())):
+        worst = float(((got - a).abs() / (rel * a.abs())).max())
+        print(f"[ops] {name}: worst error / bound {worst:.3f}")
+        assert worst <= 1.0, name
+    assert torch.equal(wide, forge.linear(z, ident, act="gelu").repeat(1, 16))
+    for name, got in (("dZ", dZ.double()), ("dG", dG.double())):
+        worst = float(((got - d).abs() / tol_d).max())
+        print(f"[ops] {name}: worst error / bound {worst:.3f}")
+        assert worst <= 1.0, name
