@@ -95,7 +95,9 @@ __device__ __forceinline__ void act_vd(float z, int act, float& a, float& d) {
     case FORGE_ACT_GELU_TANH: {
       const float s = sigmoid_f(2.f * kGeluC * z * fmaf(kGeluK * z, z, 1.f));
       a = z * s;
-      d = fmaf(2.f * a * (1.f - s), kGeluC * fmaf(3.f * kGeluK * z, z, 1.f), s);
+      // (a (1 - s) first and the slope of u bounded: z^2 and 2 z overflow where that product is 0
+      // already, and 0 inf is NaN)
+      d = fmaf(a * (1.f - s), 2.f * kGeluC * fminf(fmaf(3.f * kGeluK * z, z, 1.f), 1e30f), s);
       return;
     }
     default:

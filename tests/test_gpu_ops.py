@@ -512,3 +512,20 @@ def test_float32_gelu_in_its_left_tail():
         worst = float(((got - d).abs() / tol_d).max())
         print(f"[ops] {name}: worst error / bound {worst:.3f}")
         assert worst <= 1.0, name
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_derivatives_of_extreme_values(dt):
+    """Far out every activation's derivative is its limit, 0 or 1, also where z^2 overflows; NaN
+    stays NaN in its own element."""
+    mags = [100.0, 1e4, 1e10, 1e19, 6e19, 1e25, 3e38]
+    z = torch.tensor(mags + [-m for m in mags] + [float("nan"), 0.0], device="cuda").to(DT[dt]).reshape(2, 8)
+    one, two = torch.ones_like(z), torch.full_like(z, 2.0)
+    lim = torch.tensor([1.0] * 7 + [0.0] * 7, device="cuda")
+    for act in forge.ACTS[1:]:
+        dZ, _ = forge.linear_act_backward(one, z, act=act)
+        dG, _, _ = forge.gated_backward(one, z, two, act=act)
+        for got, scale in ((dZ, 1.0), (dG, 2.0)):
+            got = got.float().reshape(-1)
+            assert torch.equal(got[:14], lim * scale), act
+            assert torch.isnan(got[14]) and torch.isfinite(got[15]), act
