@@ -587,13 +587,16 @@ def linear_act_backward(dY: torch.Tensor, Z: Optional[torch.Tensor] = None, act:
                         want_bias: bool = True, dZ: Optional[torch.Tensor] = None, stream=None):
     """Backward of linear's epilogue (forge_linear_act_backward): (dZ, dbias) with
     dZ = dY * act'(Z) and dbias its float32 sum over the tokens (None with want_bias=False).
-    act="none": dZ is dY itself."""
+    act="none": dZ is dY itself, or, with a tensor dZ given, a copy of it there."""
     a = _act(act)
     if act != "none" and Z is None:
         raise ValueError("the gradient through an activation needs Z")
     with _On(stream, dY, Z, dZ) as on:
         T, out = dY.shape
-        dZ = _same(on, dZ, (T, out), dY.dtype) if act != "none" else None
+        if act == "none" and dZ is dY:
+            dZ = None  # nothing to copy
+        if dZ is not None or act != "none":
+            dZ = _same(on, dZ, (T, out), dY.dtype)
         db = ws = None
         need = 0
         if want_bias:

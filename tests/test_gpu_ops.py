@@ -529,3 +529,21 @@ def test_derivatives_of_extreme_values(dt):
             got = got.float().reshape(-1)
             assert torch.equal(got[:14], lim * scale), act
             assert torch.isnan(got[14]) and torch.isfinite(got[15]), act
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [0, 1, 33, 1025])
+def test_linear_act_backward_into_a_given_tensor(t, dt):
+    """A tensor given for dZ is written and returned, also without an activation."""
+    g = gen(t)
+    dY, Z = rnd(g, t, 264, dtype=DT[dt]), rnd(g, t, 264, dtype=DT[dt], std=2.0)
+    for act in forge.ACTS:
+        want, want_db = forge.linear_act_backward(dY, Z, act=act)
+        for bias in (True, False):
+            buf = torch.full((t, 272), 7.0, device="cuda", dtype=DT[dt])
+            dZ, db = forge.linear_act_backward(dY, Z, act=act, want_bias=bias, dZ=buf[:, :264])
+            assert dZ.data_ptr() == buf.data_ptr()
+            assert torch.equal(dZ, want) and torch.all(buf[:, 264:] == 7.0)
+            assert torch.equal(db, want_db) if bias else db is None
+    same, _ = forge.linear_act_backward(dY, dZ=dY)
+    assert same is dY
