@@ -28,6 +28,7 @@ stores its logits and whose backward pass steps its weights piece by piece of th
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
@@ -120,6 +121,30 @@ def _update(layers, x2: torch.Tensor, dy2s) -> None:
         ev.append((e0, e1))
 
 
+class _NoDerivative(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, g):
+        return g.view_as(g)
+
+    @staticmethod
+    def backward(ctx, gg):
+        raise RuntimeError("the operators are differentiated once: their gradients have no derivatives")
+
+
+def _once(backward):
+    """A backward pass whose gradients are no functions for autograd. Under create_graph they come
+    out with a node that refuses to be differentiated, where without one a loss that holds them would
+    lose that part silently."""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        return tuple(None if g is None else _NoDerivative.apply(g.detach().requires_grad_()) for g in out)
+    return run
+
+
 def _check_unstepped(layers, counts) -> None:
     """What a forward pass kept (pre-activations, projections) belongs to its weights, and so does
     the input gradient: refuses a backward pass once they have been stepped. (Steps write through raw
@@ -146,6 +171,7 @@ class _ForgeLinearEpiFn(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], weight.shape[0])
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         layer = ctx.layer
         _check_unstepped([layer], ctx.counts)
@@ -364,6 +390,7 @@ class _GatedBlockFn(torch.autograd.Function):
         return y.reshape(r.shape)
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         gate, up, down = ctx.block.gate, ctx.block.up, ctx.block.down
         _check_unstepped((gate, up, down), ctx.counts)
@@ -437,6 +464,7 @@ class _LinearCrossEntropyFn(torch.autograd.Function):
         return loss.reshape(targets.shape) if reduction == "none" else loss.clone()
 
     @staticmethod
+    @_once
     def backward(ctx, dloss):
         x2, t1, lse, total, weight = ctx.saved_tensors
         ignore_index, reduction = ctx.args
@@ -463,7 +491,7 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
                          reduction: str = "mean") -> torch.Tensor:
     """Softmax cross entropy of the logits x weight^T without storing them, differentiable by x and
     weight (gradients in their types). x [..., d], targets [...] int64; reduction "mean" over the
-    tokens that are not ignore_index, "sum" or "none"."""
+    tokens that are not ignore_index, "sum" or "none". Once: a second derivative is refused."""
     return _LinearCrossEntropyFn.apply(x, weight, targets, ignore_index, reduction, None)
 
 

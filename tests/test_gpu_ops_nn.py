@@ -516,3 +516,19 @@ def test_two_phase_layers_take_several_backward_passes():
     step_all(layer)
     with pytest.raises(RuntimeError, match="stepped after"):
         third.backward(dy)
+
+
+def test_second_derivatives_are_refused():
+    """A gradient penalty on the operators' gradients is refused, not left out of the sum."""
+    x, y = rnd(2, 20, 64).requires_grad_(), torch.randint(0, 300, (20,), device="cuda")
+    W = rnd(1, 300, 64, std=0.2).requires_grad_()
+    layer = ForgeLinear(64, 128, weight=rnd(3, 128, 64, std=0.1), act="silu")
+    blk = block(True, d=64, hidden=128)
+    for out in (linear_cross_entropy(x, W, y), layer(x).float().sum(), blk(x).float().sum()):
+        g, = torch.autograd.grad(out, x, create_graph=True)
+        with pytest.raises(RuntimeError, match="differentiated once"):
+            (x.float().sum() + g.float().pow(2).sum()).backward()
+    # a first derivative with a graph around it stays possible
+    x.grad = None
+    linear_cross_entropy(x * 2, W, y).backward()
+    assert torch.isfinite(x.grad.float()).all()
