@@ -517,9 +517,10 @@ class _On:
 
 # torch's own short ways to the device's current stream and to the current device: a few
 # microseconds less per call than a Stream object and the checks around them, which a tensor on
-# the device makes needless
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
+# the device makes needless (the public ones where a build of torch lacks them)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 
 def _ten(t: Optional[torch.Tensor]):

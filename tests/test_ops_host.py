@@ -307,3 +307,25 @@ def test_a_refused_step_leaves_the_step_counts(monkeypatch):
         with pytest.raises(forge.ForgeError):
             fnn._update(some, None, [None] * len(some))
         assert [L._step_count for L in layers] == [4, 4]
+
+
+def test_without_torch_s_short_ways_to_the_stream():
+    """A torch without the two private functions: the public ones serve."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from optimizer_gemm_amd import forge
+class S: cuda_stream = 77
+torch.cuda.current_stream = lambda index=None: S
+torch.cuda.current_device = lambda: 3
+assert forge._raw_stream(0) == 77 and forge._current_device() == 3
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
