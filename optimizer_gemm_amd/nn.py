@@ -83,6 +83,12 @@ class _ForgeLinearFn(torch.autograd.Function):
         return dx, None, None
 
 
+def _differentiated(*tensors) -> bool:
+    """Whether autograd will record a node of these: without, a forward pass keeps nothing for
+    backward (inside a node's own forward the mode is off already)."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 def _rows(t: torch.Tensor, cols: int, dtype: torch.dtype) -> torch.Tensor:
     """t as contiguous rows of `cols` elements of `dtype`."""
     t = t.reshape(-1, cols)
@@ -158,10 +164,10 @@ class _ForgeLinearEpiFn(torch.autograd.Function):
     epilogue; backward takes the gradient through the activation, then dX, then the steps."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, residual, layer):
+    def forward(ctx, x, weight, bias, residual, layer, recorded):
         x2 = _rows(x, weight.shape[1], weight.dtype)
         r2 = None if residual is None else _rows(residual, weight.shape[0], weight.dtype)
-        keep = layer.act != "none"
+        keep = recorded and layer.act != "none"
         y = forge.linear(x2, weight.detach(), bias=None if bias is None else bias.detach(), act=layer.act, residual=r2,
                          save=keep)
         y, z = y if keep else (y, None)
@@ -184,7 +190,7 @@ class _ForgeLinearEpiFn(torch.autograd.Function):
         _update([layer], x2, [dz])
         if db is not None:
             layer._bias_update(db)
-        return dx, None, None, (dy.reshape(ctx.r_shape) if ctx.needs_input_grad[3] else None), None
+        return dx, None, None, (dy.reshape(ctx.r_shape) if ctx.needs_input_grad[3] else None), None, None
 
 
 class ForgeLinear(torch.nn.Module):
@@ -246,7 +252,8 @@ class ForgeLinear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         if self.bias is not None or self.act != "none" or residual is not None:
-            return _ForgeLinearEpiFn.apply(x, self.weight, self.bias, residual, self)
+            return _ForgeLinearEpiFn.apply(x, self.weight, self.bias, residual, self,
+                                           _differentiated(x, self.weight, self.bias, residual))
         return _ForgeLinearFn.apply(x, self.weight, self)
 
     def _bias_update(self, db: torch.Tensor) -> None:
@@ -380,9 +387,10 @@ class _GatedBlockFn(torch.autograd.Function):
     dh of both projections in one accumulation - all on the old weights - and then the steps."""
 
     @staticmethod
-    def forward(ctx, h, r, wg, wu, wd, block):
+    def forward(ctx, h, r, wg, wu, wd, block, recorded):
         h2, r2 = _rows(h, wg.shape[1], wg.dtype), _rows(r, wd.shape[0], wd.dtype)
-        H, G, U = forge.gated(h2, wg.detach(), wu.detach(), act="silu", save=True)
+        out = forge.gated(h2, wg.detach(), wu.detach(), act="silu", save=recorded)
+        H, G, U = out if recorded else (out, None, None)
         y = forge.linear(H, wd.detach(), residual=r2)
         ctx.block, ctx.h_shape, ctx.r_shape = block, h.shape, r.shape
         ctx.counts = [L._step_count for L in (block.gate, block.up, block.down)]
@@ -405,7 +413,7 @@ class _GatedBlockFn(torch.autograd.Function):
         else:  # the grouped step takes bf16 layers that agree
             _update([gate], h2, [dG])
             _update([up], h2, [dU])
-        return dh, (dy.reshape(ctx.r_shape) if ctx.needs_input_grad[1] else None), None, None, None, None
+        return dh, (dy.reshape(ctx.r_shape) if ctx.needs_input_grad[1] else None), None, None, None, None, None
 
 
 class SwiGLUBlock(torch.nn.Module):
@@ -437,7 +445,8 @@ class SwiGLUBlock(torch.nn.Module):
     def _body(self, x: torch.Tensor) -> torch.Tensor:
         h = _rms_norm(x)
         if self.joined:
-            return _GatedBlockFn.apply(h, x, self.gate.weight, self.up.weight, self.down.weight, self)
+            weights = (self.gate.weight, self.up.weight, self.down.weight)
+            return _GatedBlockFn.apply(h, x, *weights, self, _differentiated(h, x, *weights))
         if self.grouped:
             g, u = grouped_linear((self.gate, self.up), h)
         else:

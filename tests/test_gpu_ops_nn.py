@@ -532,3 +532,36 @@ def test_second_derivatives_are_refused():
     x.grad = None
     linear_cross_entropy(x * 2, W, y).backward()
     assert torch.isfinite(x.grad.float()).all()
+
+
+def test_evaluation_keeps_nothing_for_backward(monkeypatch):
+    """Without gradients the modules write neither pre-activations nor projections; the output is
+    the same bits."""
+    from optimizer_gemm_amd import nn as fnn
+
+    saves = []
+    for name in ("linear", "gated"):
+        real = getattr(forge, name)
+        monkeypatch.setattr(fnn.forge, name,
+                            lambda *a, _real=real, **kw: saves.append(bool(kw.get("save"))) or _real(*a, **kw))
+    x, r = rnd(2, 70, 256), rnd(3, 70, 512)
+    layer = ForgeLinear(256, 512, weight=rnd(1, 512, 256, std=0.1), bias=True, act="gelu")
+    blk = block(True)
+    for module, args, trained in ((layer, (x, r), [True]), (blk, (x,), [True, False])):
+        saves.clear()
+        want = module(*args)
+        assert saves == trained and want.requires_grad
+        for p in module.parameters():
+            p.requires_grad_(False)
+        saves.clear()
+        frozen = module(*args)
+        assert not any(saves) and torch.equal(frozen, want)
+        for p in module.parameters():
+            p.requires_grad_(True)
+        saves.clear()
+        with torch.no_grad():
+            got = module(*args)
+        assert not any(saves) and torch.equal(got, want)
+        with torch.inference_mode():
+            assert torch.equal(module(*args), want)
+    assert layer.step_count == 0
