@@ -353,8 +353,8 @@ int forge_linear_dgrad_group_split(int32_t n_layers, const forge_tensor* dY, con
 /*
  * Softmax cross entropy of a linear head, without storing the logits z = X W^T:
  *   lse[t] = log sum_v exp(z[t, v]),  loss[t] = lse[t] - z[t, target[t]].
- * X [T, in], W [vocab, in] (vocab: any number from 1 on; W may exceed 2^31 bytes, its rows
- * less than 2^23 bytes apart), target: T int64 in
+ * X [T, in], W [vocab, in] (vocab: any number from 1 on, T * vocab below 2^42; W may exceed 2^31
+ * bytes, its rows less than 2^23 bytes apart), target: T int64 in
  * [0, vocab), or `ignore` for tokens that do not count (loss 0, no gradient, whatever their
  * logits are; but dW adds 0 times their rows of X, which have to be finite). Any other
  * target makes that token's loss and gradients NaN. loss (or NULL) and lse: T floats;

@@ -378,10 +378,9 @@ void lin_kernel(LinArgs g) {
         b = __builtin_bit_cast(bf16x8, F.bk[fn]);
       mfma_acc(acc[fm][fn], a, b);
     };
-    // the MFMAs of F; the reads of G (k-step kk of the slots the addresses point to) spread
-    // over the first half of them, the loads of an operand's stage over all of them;
-    // sched_barrier keeps the order
-    constexpr int NM = C::FM * C::FN, LW = 2;  // the loads go out over the first 1 / LW of the products
+    // the MFMAs of F; the reads of G (k-step kk of the slots the addresses point to) and the loads
+    // of an operand's stage spread over the first half of them; sched_barrier keeps the order
+    constexpr int NM = C::FM * C::FN, LW = 2;  // (the loads: over the first 1 / LW)
     auto step = [&](const Frag& F, Frag& G, auto kk_c, auto&& load) FORGE_INLINE {
       static_for<0, NM>([&](auto i_c) FORGE_INLINE {
         constexpr int i = decltype(i_c)::value;

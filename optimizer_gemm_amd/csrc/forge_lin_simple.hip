@@ -1,11 +1,8 @@
-// Products with an epilogue, general form: float32 or bfloat16 operands, either index of either
-// operand fast, and the choice between this kernel and the bfloat16 ones. One kernel covers every
-// operator of forge_ops.h. It serves the float32 operands, and bfloat16 outputs of 2^30 tiles and
-// more, which the others do not count.
+// Products with an epilogue on float32 operands, either index of either operand fast, one kernel for
+// every operator of forge_ops.h; and the choice between the bfloat16 kernels.
 //
 // A workgroup of 4 waves stages BK k of both operands in LDS as rows of k (operands whose k is
-// slow are transposed on the way in), and multiplies them with v_mfma_f32_32x32x2_f32 (or
-// 32x32x16_bf16), FP32 accumulators in both cases. The next stage's global loads are in flight
+// slow are transposed on the way in), and multiplies them with v_mfma_f32_32x32x2_f32. The next stage's global loads are in flight
 // (in registers) during the current stage's products. The finished tile goes through LDS as
 // float rows of the output, so that the epilogue reads and writes whole row segments.
 // Two tiles. 64x64, a 32x32 block per wave; and 32x32, a quarter of the stage's k per wave, where
@@ -22,9 +19,9 @@ namespace {
 
 // B x B output elements, stages of BK k, LD: k per row of the staged operands. B = 64: the waves
 // are 2 x 2 of 32x32; B = 32: each wave takes a quarter of the stage's k for the whole tile.
-template <class T, int B_>
+template <int B_>
 struct STile {
-  static constexpr int B = B_, BK = B_ == 64 ? 32 : 64, VE = 16 / (int)sizeof(T), LD = BK + VE;
+  static constexpr int B = B_, BK = B_ == 64 ? 32 : 64, VE = 4, LD = BK + VE;
   static constexpr int KW = B_ == 64 ? BK : BK / 4;  // k of a wave's products per stage
   static constexpr int LDE = B + 4;
 };
@@ -35,21 +32,20 @@ constexpr int64_t kSimpleGrid = 1 << 20;
 
 // 16 bytes of an operand: KS: its rows are k (row k0 + r, columns c..), else its rows are
 // the output index (row r, k = k0 + c ..). Zero outside.
-template <class T>
-__device__ __forceinline__ u32x4 load16(const T* base, int64_t ld, int row, int rows, int col, int cols) {
+__device__ __forceinline__ u32x4 load16(const float* base, int64_t ld, int row, int rows, int col, int cols) {
   u32x4 z{0u, 0u, 0u, 0u};
   if (row < rows && col < cols) z = *reinterpret_cast<const u32x4*>(base + (int64_t)row * ld + col);
   return z;
 }
 
 // One operand's stage: B output indexes x BK k, as rows of k of pitch LD.
-template <class T, class C, bool TR>
+template <class C, bool TR>
 struct Stage {
   static constexpr int VE = C::VE, LD = C::LD, S_B = C::B, S_BK = C::BK;
   static constexpr int CH = S_B * S_BK / VE / S_NT;  // 16-byte chunks per thread
   u32x4 r[CH];
   // r0: first output index of the tile, R: how many there are
-  __device__ __forceinline__ void load(const T* p, int64_t ld, int r0, int R, int k0, int K, int tid) {
+  __device__ __forceinline__ void load(const float* p, int64_t ld, int r0, int R, int k0, int K, int tid) {
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int c = tid + j * S_NT;
@@ -64,19 +60,14 @@ struct Stage {
       }
     }
   }
-  __device__ __forceinline__ void store(T* s, int tid) const {
+  __device__ __forceinline__ void store(float* s, int tid) const {
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int c = tid + j * S_NT;
       if constexpr (TR) {
         const int kr = c / (S_B / VE), col = (c % (S_B / VE)) * VE;
-        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-          for (int i = 0; i < VE; ++i) s[(col + i) * LD + kr] = (T)(r[j][i / 2] >> (16 * (i & 1)));
-        } else {
-#pragma unroll
-          for (int i = 0; i < VE; ++i) s[(col + i) * LD + kr] = bits_f32(r[j][i]);
-        }
+        for (int i = 0; i < VE; ++i) s[(col + i) * LD + kr] = bits_f32(r[j][i]);
       } else {
         const int row = c / (S_BK / VE), kc = (c % (S_BK / VE)) * VE;
         *reinterpret_cast<u32x4*>(s + row * LD + kc) = r[j];
@@ -86,37 +77,31 @@ struct Stage {
 };
 
 // 32 x 32 products over the wave's k of a stage, from 16-byte LDS reads: lane half hi holds
-// elements 8 j + 4 hi .. of both operands' rows (float32), so a product of two k takes one from
-// each half
-template <class T, class C>
-__device__ __forceinline__ void mma32(f32x16& acc, const T* as, const T* bs, int row_a, int row_b, int k0, int hi) {
+// elements 8 j + 4 hi .. of both operands' rows, so a product of two k takes one from each half
+template <class C>
+__device__ __forceinline__ void mma32(f32x16& acc, const float* as, const float* bs, int row_a, int row_b, int k0, int hi) {
 #pragma unroll
   for (int k = 0; k < C::KW; k += 2 * C::VE) {
     const u32x4 a = *reinterpret_cast<const u32x4*>(as + row_a * C::LD + k0 + k + C::VE * hi);
     const u32x4 b = *reinterpret_cast<const u32x4*>(bs + row_b * C::LD + k0 + k + C::VE * hi);
-    if constexpr (sizeof(T) == 2) {
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0,
-                                                    0);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bits_f32(a[i]), bits_f32(b[i]), acc, 0, 0, 0);
-    }
+    for (int i = 0; i < 4; ++i)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bits_f32(a[i]), bits_f32(b[i]), acc, 0, 0, 0);
   }
 }
 
-template <class T, class C, int EPI, bool TA, bool TB>
+template <class C, int EPI, bool TA, bool TB>
 __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
   constexpr bool TWO = EPI == L_GATED;
   constexpr int S_B = C::B, S_BK = C::BK, LDE = C::LDE;
   constexpr int PARTS = S_B == 64 ? 1 : 4, ET = S_B * LDE;  // partial tiles of a product, floats of one
   static_assert(EPI != L_LSE || S_B == 64, "the cross entropy's blocks are of 64 entries");
-  constexpr int OP = S_B * C::LD * (int)sizeof(T);
+  constexpr int OP = S_B * C::LD * 4;
   constexpr int EB = (TWO ? 2 : 1) * PARTS * ET * 4, OB = (TWO ? 3 : 2) * OP;
   __shared__ __attribute__((aligned(16))) uint8_t smem[EB > OB ? EB : OB];
-  T* as = reinterpret_cast<T*>(smem);
-  T* bs = reinterpret_cast<T*>(smem + OP);
-  T* as2 = reinterpret_cast<T*>(smem + (TWO ? 2 * OP : 0));
+  float* as = reinterpret_cast<float*>(smem);
+  float* bs = reinterpret_cast<float*>(smem + OP);
+  float* as2 = reinterpret_cast<float*>(smem + (TWO ? 2 * OP : 0));
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, hi = lane >> 5;
   const int wm = PARTS > 1 ? 0 : (wave & 1) * 32, wn = PARTS > 1 ? 0 : (wave >> 1) * 32;
   const int wk = PARTS > 1 ? wave * C::KW : 0;
@@ -130,12 +115,12 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc2[i] = 0.f;
-  Stage<T, C, TA> sa, sa2;
-  Stage<T, C, TB> sb;
+  Stage<C, TA> sa, sa2;
+  Stage<C, TB> sb;
   for (int s = 0; s < g.nsrc; ++s) {
-    const T* A = static_cast<const T*>(g.A[s]);
-    const T* A2 = static_cast<const T*>(g.A[TWO ? 1 : 0]);
-    const T* B = static_cast<const T*>(g.B[s]);
+    const float* A = static_cast<const float*>(g.A[s]);
+    const float* A2 = static_cast<const float*>(g.A[TWO ? 1 : 0]);
+    const float* B = static_cast<const float*>(g.B[s]);
     const int K = g.K[s];
     auto fetch = [&](int k0) {
       sa.load(A, g.lda[s], m0, g.M, k0, K, tid);
@@ -150,8 +135,8 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
       sb.store(bs, tid);
       __syncthreads();
       if (k0 + S_BK < K) fetch(k0 + S_BK);
-      mma32<T, C>(acc, as, bs, wm + l32, wn + l32, wk, hi);
-      if constexpr (TWO) mma32<T, C>(acc2, as2, bs, wm + l32, wn + l32, wk, hi);
+      mma32<C>(acc, as, bs, wm + l32, wn + l32, wk, hi);
+      if constexpr (TWO) mma32<C>(acc2, as2, bs, wm + l32, wn + l32, wk, hi);
     }
   }
   __syncthreads();
@@ -206,40 +191,30 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
           x = x + *reinterpret_cast<const f32x4*>(E + p * ET + r * LDE + c);
           if constexpr (TWO) x2 = x2 + *reinterpret_cast<const f32x4*>(E2 + p * ET + r * LDE + c);
         }
-        epi_vec<T, EPI, decltype(act_c)::value>(g.e, n, m, g.M, x, x2, sc);
+        epi_vec<float, EPI, decltype(act_c)::value>(g.e, n, m, g.M, x, x2, sc);
       }
     });
   }
   }
 }
 
-template <class T, class C, int EPI, bool TA, bool TB>
+template <class C, int EPI, bool TA, bool TB>
 hipError_t run(const LinArgs& g, hipStream_t st) {
   const int64_t gx = (epi_width<EPI>(g.M) - g.m_off + C::B - 1) / C::B, gy = (g.N - g.n_off + C::B - 1) / C::B;
   if (gx <= 0 || gy <= 0) return hipSuccess;
   const int64_t tiles = gx * gy;
-  hipLaunchKernelGGL((lin_simple_kernel<T, C, EPI, TA, TB>), dim3((uint32_t)(tiles < kSimpleGrid ? tiles : kSimpleGrid)),
+  hipLaunchKernelGGL((lin_simple_kernel<C, EPI, TA, TB>), dim3((uint32_t)(tiles < kSimpleGrid ? tiles : kSimpleGrid)),
                      dim3(S_NT), 0, st, g);
   return hipGetLastError();
 }
 
-// float32: 32x32 tiles where the 64x64 ones are fewer than the compute units
-template <class T, int EPI, bool TA, bool TB>
-hipError_t size_up(const LinArgs& g, hipStream_t st) {
-  if constexpr (sizeof(T) == 4 && EPI != L_LSE) {
-    if (((int64_t)g.M + 63) / 64 * (((int64_t)g.N + 63) / 64) < g_num_cus())
-      return run<T, STile<T, 32>, EPI, TA, TB>(g, st);
+// 32x32 tiles where the 64x64 ones are fewer than the compute units
+template <int EPI, bool TA, bool TB>
+hipError_t lin_f32(const LinArgs& g, hipStream_t st) {
+  if constexpr (EPI != L_LSE) {
+    if (((int64_t)g.M + 63) / 64 * (((int64_t)g.N + 63) / 64) < g_num_cus()) return run<STile<32>, EPI, TA, TB>(g, st);
   }
-  return run<T, STile<T, 64>, EPI, TA, TB>(g, st);
-}
-
-template <class T>
-hipError_t pick(int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
-#define FORGE_PICK(E, A, B) \
-  if (epi == E && ta == A && tb == B) return size_up<T, E, A, B>(g, st);
-  FORGE_LIN_FORMS(FORGE_PICK)
-#undef FORGE_PICK
-  return hipErrorInvalidValue;
+  return run<STile<64>, EPI, TA, TB>(g, st);
 }
 
 // Whether the kernel for a few tokens takes a forward product. It reads the tokens once per 16
@@ -256,11 +231,6 @@ bool few_tokens(int epi, const LinArgs& g) {
   return g.N <= 4 || 2 * tiles <= cus || tiles > 2 * cus;
 }
 
-// tiles of 64x64: the larger kernels count theirs in 32 bits
-bool few_tiles(const LinArgs& g) {
-  return ((int64_t)g.M + S_B) / S_B * (((int64_t)g.N + S_B) / S_B) < ((int64_t)1 << 30);
-}
-
 }  // namespace
 
 #define FORGE_EXTERN_LIN(E, A, B) extern template hipError_t lin_bf16<E, A, B>(const LinArgs&, hipStream_t);
@@ -268,11 +238,9 @@ FORGE_LIN_FORMS(FORGE_EXTERN_LIN)
 #undef FORGE_EXTERN_LIN
 
 hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
-  if (!bf16) return pick<float>(epi, ta, tb, g, st);
-  if ((epi == L_LINEAR || epi == L_GATED) && few_tokens(epi, g)) return launch_lin_skinny(epi, g, st);
-  if (!few_tiles(g)) return pick<uint16_t>(epi, ta, tb, g, st);
+  if (bf16 && (epi == L_LINEAR || epi == L_GATED) && few_tokens(epi, g)) return launch_lin_skinny(epi, g, st);
 #define FORGE_PICK(E, A, B) \
-  if (epi == E && ta == A && tb == B) return lin_bf16<E, A, B>(g, st);
+  if (epi == E && ta == A && tb == B) return bf16 ? lin_bf16<E, A, B>(g, st) : lin_f32<E, A, B>(g, st);
   FORGE_LIN_FORMS(FORGE_PICK)
 #undef FORGE_PICK
   return hipErrorInvalidValue;
@@ -291,10 +259,7 @@ int lin_splits(int bf16, int64_t M, int64_t N, int64_t K) {
 }
 
 int lin_lse_block(int bf16, int M, int N) {
-  LinArgs g{};
-  g.M = M;
-  g.N = N;
-  if (!bf16 || !few_tiles(g)) return S_B;
+  if (!bf16) return S_B;
   switch (lin_tile<L_LSE>(M, N)) {
     case LT_BIG: return LinBig::TM;  // a wave's entries
     case LT_SMALL: return LinSmall::TM;

@@ -2,7 +2,7 @@
 // epilogue (linear forward, gated block, their gradients, softmax cross entropy of a
 // linear head). This file holds their arguments, the activations and the epilogues;
 // the kernels are in forge_lin_kernel.h (bfloat16 products), forge_lin_skinny.hip (a few tokens),
-// forge_lin_simple.hip (float32, and the choice between them) and forge_ops_rows.hip (passes
+// forge_lin_simple.hip (float32, and the choice between the bfloat16 ones) and forge_ops_rows.hip (passes
 // without a product).
 //
 // Every product here is C[m][n] = sum_k A[m][k] B[n][k] with m the output's columns
@@ -296,8 +296,6 @@ hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hip
 constexpr int kSkinny = 32;
 hipError_t launch_lin_skinny(int epi, const LinArgs& g, hipStream_t st);
 // vocabulary entries per partial result that launch_lin(L_LSE) writes for this product
-// (never fewer than kLseBlockMin)
-constexpr int kLseBlockMin = 64;
 int lin_lse_block(int bf16, int M, int N);
 
 // parts a product of k-slow A should be cut into (1: none): too few tiles to fill the chip with,
@@ -307,7 +305,7 @@ int lin_splits(int bf16, int64_t M, int64_t N, int64_t K);
 hipError_t launch_acc_join(const LinArgs& g, hipStream_t st);
 
 // dZ = dY act'(Z) and db = its column sums in float32 (partial sums of blocks of rows go to
-// ws, rows_blocks(T, out) x out floats, when there is more than one block)
+// ws, act_backward_blocks(T, out) x out floats, when there is more than one block)
 int act_backward_blocks(int64_t T, int64_t out);
 hipError_t launch_act_backward(int bf16, int act, const void* dY, int64_t lddy, const void* Z, int64_t ldz, void* dZ,
                                int64_t lddz, float* db, float* ws, int T, int out, hipStream_t st);

@@ -55,6 +55,10 @@ constexpr int64_t kPieceBytes = (int64_t)1 << 30;  // of dz, where the caller gi
 // bytes between the rows of W or dW, below this (256 of its rows are addressed by 32-bit offsets)
 constexpr int64_t kHeadPitch = (int64_t)1 << 23;
 
+// Logits of a call, below this: the pairs of the vocabulary's blocks would fill the memory (2^42
+// logits: 256 GB), and the kernels count their tiles in 32 bits.
+constexpr int64_t kMaxLogits = (int64_t)1 << 42;
+
 // W of the head: as check_io, but any number of bytes (tiles and pieces address it by 64-bit
 // offsets) and any number of rows.
 int check_head(const forge_tensor* X, const forge_tensor* W, const int64_t* target) {
@@ -65,6 +69,7 @@ int check_head(const forge_tensor* X, const forge_tensor* W, const int64_t* targ
   if ((r = check_io(W, W->dtype)) || (r = check_io(X, W->dtype))) return r;
   if (X->cols != W->cols || W->rows < 1) return FORGE_ERR_SHAPE;
   if (!fits_31(X) || W->ld * (int64_t)elem_size(W->dtype) >= kHeadPitch) return FORGE_ERR_UNSUPPORTED;
+  if (X->rows * W->rows >= kMaxLogits) return FORGE_ERR_UNSUPPORTED;
   if (!target && X->rows > 0) return FORGE_ERR_NULL;
   return ((uintptr_t)target & 7u) ? FORGE_ERR_ALIGN : FORGE_OK;
 }
@@ -421,6 +426,7 @@ int forge_linear_dgrad_group_split(int32_t n_layers, const forge_tensor* dY, con
 int64_t forge_linear_xent_workspace(int64_t T, int64_t in, int64_t vocab, int32_t dtype, int32_t backward,
                                     int64_t piece) {
   if (T < 0 || in < 0 || vocab < 1 || T >= kMaxDim || in >= kMaxDim || vocab >= kMaxDim || piece < 0) return 0;
+  if (T * vocab >= kMaxLogits) return 0;
   const int es = dtype == FORGE_BF16 ? 2 : 4;
   if (!backward) return fwd_ws(T, vocab, lin_lse_block(dtype == FORGE_BF16, (int)vocab, (int)T)).bytes;
   const int64_t p = piece_of(T, in, vocab, es, piece);

@@ -329,3 +329,19 @@ assert forge._raw_stream(0) == 77 and forge._current_device() == 3
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_xent_refuses_more_logits_than_the_memory_holds_partial_results_of():
+    T, V, D = 1 << 21, 1 << 21, 64
+    tgt, lse, tot, ws, dl = (BASE + (k << 33) for k in (4, 5, 6, 7, 8))
+    n = 1 << 60
+    for dt in (BF16, F32):
+        X, W, few = ten(0, T, D, dt), ten(1, V, D, dt), ten(0, T - 1, D, dt)
+        for back in (0, 1):
+            assert L.forge_linear_xent_workspace(T, D, V, dt, back, 0) == 0
+            assert L.forge_linear_xent_workspace(T - 1, D, V, dt, back, 0) > 0
+        assert L.forge_linear_xent_forward(ref(X), ref(W), tgt, -100, None, lse, tot, ws, n, None) == UNSUP
+        assert L.forge_linear_xent_backward(ref(X), ref(W), tgt, -100, lse, dl, 0, tot, ref(ten(2, T, D, dt)), None, 0, ws,
+                                            n, None) == UNSUP
+        # one row less: the next check answers
+        assert L.forge_linear_xent_forward(ref(few), ref(W), tgt, -100, None, lse, tot, ws, 0, None) == SCRATCH
