@@ -547,3 +547,150 @@ def test_linear_act_backward_into_a_given_tensor(t, dt):
             assert torch.equal(db, want_db) if bias else db is None
     same, _ = forge.linear_act_backward(dY, dZ=dY)
     assert same is dY
+
+
+def up8(n):
+    return (n + 7) // 8 * 8
+
+
+def exact_head(seed, t, i, v, dtype, kind):
+    """A head whose dz and gradients are exact in every order of summation. kind "targets": lse so large
+    that every probability is 0, so dz = -[target] w, any W. kind "ones": X and W live in different
+    halves of the columns, so every logit is 0, and lse = 0: dz = (1 - [target]) w for all entries.
+    X holds whole numbers up to 2, W eighths up to 2, w powers of two."""
+    g = gen(seed)
+    X = torch.randint(-2, 3, (t, i), generator=g, device="cuda").to(F)
+    W = torch.randint(-16, 17, (up8(v), i), generator=g, device="cuda").to(F) / 8
+    if kind == "ones":
+        X[:, : i // 2] = 0
+        W[:, i // 2:] = 0
+    y = torch.randint(0, v, (t,), generator=g, device="cuda")
+    if t > 2:
+        y[0], y[1] = v - 1, 0
+        y[2::5] = -100
+    lse = torch.full((t,), 1e30 if kind == "targets" else 0.0, device="cuda")
+    w = 2.0 ** -torch.randint(0, 4, (t,), generator=g, device="cuda").to(F)
+    dz = torch.zeros(t, up8(v), device="cuda", dtype=F)
+    if kind == "ones":
+        dz[:, :v] = 1.0
+    keep = y != -100
+    r = torch.nonzero(keep)[:, 0]
+    dz[r, y[r]] -= 1.0
+    dz[~keep] = 0
+    return X.to(dtype), W.to(dtype), y, lse, w, dz, keep
+
+
+HEAD_STEPS = [("bf16", o, s_) for o, s_ in
+              [("adamw", "f32"), ("adamw", "bf16"), ("adamw", "q8"), ("adamw", "q8dyn"), ("sgd", "f32"), ("lion", "bf16"),
+               ("rmsprop", "q8"), ("nadam", "f32")]] + [("f32", "adamw", "f32"), ("f32", "sgd_momentum", "f32")]
+
+
+@pytest.mark.parametrize("kind", ["targets", "ones"])
+@pytest.mark.parametrize("dt,opt,states", HEAD_STEPS)
+@pytest.mark.parametrize("t,v", [(190, 1003), (1501, 2051), (1, 13), (0, 264)])
+def test_head_step_of_exact_gradients(t, v, dt, opt, states, kind):
+    """Every piece of the head's step against wgrad_step of the whole W on a dz formed here, bit for
+    bit: weights with stochastic rounding, moments, scales, from moments that are all different, at a
+    step that is not the first; and dX, exact too, of the old W."""
+    i = 128
+    X, W, y, lse, w, dz, keep = exact_head(t + v, t, i, v, DT[dt], kind)
+    g = gen(7)
+    m, vv, ms, vs = forge.new_states(W, opt, states)
+    for mom in (m, vv):
+        if mom is None:
+            continue
+        if mom.dtype in (torch.int8, torch.uint8):
+            lo = -120 if mom.dtype == torch.int8 else 0
+            mom.copy_(torch.randint(lo, 120, mom.shape, generator=g, device="cuda"))
+        else:
+            mom.copy_(torch.rand(mom.shape, generator=g, device="cuda") * 0.25)
+    for sc in (ms, vs):
+        if sc is not None:
+            sc.copy_(torch.rand(sc.shape, generator=g, device="cuda") * 0.01 + 1e-3)
+    code = "dynamic" if states == "q8dyn" else "linear"
+    hyper = {"lr": 0.05}
+    n = int(keep.sum())
+    # "none": a factor per token; "sum": one for all
+    for red, dloss in (("none", w), ("sum", torch.full((), 0.25, device="cuda"))):
+        full = (dz * (w[:, None] if red == "none" else 0.25)).to(DT[dt])
+        ref = [None if a is None else a.clone() for a in (W, m, vv, ms, vs)]
+        forge.wgrad_step(X, full, ref[0], ref[1], ref[2], opt, hyper, 5, 99, ref[3], ref[4], code=code)
+        want_dx = (full.double() @ W.double()).to(F).to(DT[dt])
+        for piece in (0, 8, 256, 520):
+            if piece == 8 and v > 1500:
+                continue
+            got = [None if a is None else a[:v].clone() for a in (W, m, vv, ms, vs)]
+            dX = forge.linear_cross_entropy_step(X, got[0], got[1], got[2], y, lse, dloss, opt, hyper, 5, 99, got[3],
+                                                 got[4], code=code, reduction=red, piece=piece)
+            assert torch.equal(dX, want_dx), (red, piece)
+            for name, a, b in zip(("W", "m", "v", "m scale", "v scale"), got, ref):
+                if a is not None:
+                    assert torch.equal(a, b[:v]), (name, red, piece)
+            assert n == 0 or not torch.equal(got[0], W[:v])
+
+
+@pytest.mark.parametrize("kind", ["targets", "ones"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t,v", [(190, 1003), (1501, 2051), (1, 13)])
+def test_head_gradients_that_are_exact(t, v, dt, kind):
+    """dX and dW in pieces of every size: the exact sums, rounded once."""
+    i = 128
+    X, W, y, lse, w, dz, keep = exact_head(t + v, t, i, v, DT[dt], kind)
+    total = torch.tensor([0.0, 128.0, 0.0], device="cuda")  # a mean over 128: a power of two
+    one = torch.ones((), device="cuda")
+    for red, dloss, f in (("none", w, w[:, None].double()), ("sum", one, 1.0), ("mean", one, 2.0 ** -7)):
+        d = dz.double() * f
+        want_x = (d @ W.double()).to(F).to(DT[dt])
+        want_w = (d.t() @ X.double()).to(F).to(DT[dt])[:v]
+        for piece in (0, 8, 256, 520):
+            if piece == 8 and v > 1500:
+                continue
+            dX, dW = forge.linear_cross_entropy_backward(X, W[:v], y, lse, dloss, reduction=red, total=total, piece=piece)
+            assert torch.equal(dX, want_x) and torch.equal(dW, want_w), (red, piece)
+
+
+@pytest.mark.parametrize("t,i,o", [(2100, 512, 29 * 128), (8445, 520, 1024)])
+def test_gated_of_a_little_more_than_a_round(t, i, o):
+    """261 and 264 tiles of 256 x 128 outputs: the tiles past the first 256 run as smaller ones, as a
+    band of columns and as a band of rows."""
+    g = gen(t)
+    X = rnd(g, t, i)
+    Wg, Wu = rnd(g, o, i, std=i ** -0.5), rnd(g, o, i, std=i ** -0.5)
+    H, G, U = forge.gated(X, Wg, Wu, act="silu", save=True)
+    h, dh, gg, dg, uu, du = gated64(X, Wg, Wu, "silu")
+    close("H", H, h, dh)
+    close("G", G, gg, dg)
+    close("U", U, uu, du)
+
+
+@pytest.mark.parametrize("t,i,o", [(2100, 512, 29 * 256), (8445, 520, 2048)])
+def test_gated_dgrad_of_a_little_more_than_a_round(t, i, o):
+    """The same for the gradient through the layer behind."""
+    g = gen(t)
+    dY, Wd = rnd(g, t, i), rnd(g, i, o, std=o ** -0.5)
+    G, U = rnd(g, t, o, std=2.0), rnd(g, t, o)
+    dG, dU, H = forge.gated_dgrad(dY, Wd, G, U, act="gelu")
+    dh, ddh = mm64(dY, Wd)
+    dg, eg, du, eu, h, eh = gated_back64(dh, ddh, G, U, "gelu")
+    close("dG", dG, dg, eg)
+    close("dU", dU, du, eu)
+    close("H", H, h, eh)
+
+
+def test_cross_entropy_sums_of_dx_past_32_bit_offsets():
+    """The float32 sums of dX over two pieces of the vocabulary take 2.3 GB: written with the first
+    piece, read with the second."""
+    t, i, v = 70000, 8192, 520
+    assert t * i * 4 > 2 ** 31
+    X, W, y, lse, w, dz, keep = exact_head(3, t, i, v, BF, "targets")
+    dX, dW = forge.linear_cross_entropy_backward(X, W, y, lse, w, reduction="none", piece=264)
+    # one term per token: -w W[target], exact
+    want = torch.zeros(t, i, device="cuda", dtype=BF)
+    want[keep] = (-w[keep, None] * W[y[keep]].float()).to(BF)
+    assert torch.equal(dX, want)
+    del want, dX
+    want_w = torch.zeros(v, i, device="cuda", dtype=torch.float64)
+    want_w.index_add_(0, y[keep], -w[keep, None].double() * X[keep].double())
+    assert torch.equal(dW, want_w.to(F).to(BF))
+    del want_w, X, dW
+    torch.cuda.empty_cache()
