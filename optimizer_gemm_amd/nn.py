@@ -29,6 +29,7 @@ stores its logits and whose backward pass steps its weights piece by piece of th
 from __future__ import annotations
 
 import functools
+import math
 from typing import Optional
 
 import torch
@@ -91,6 +92,8 @@ def _differentiated(*tensors) -> bool:
 
 def _rows(t: torch.Tensor, cols: int, dtype: torch.dtype) -> torch.Tensor:
     """t as contiguous rows of `cols` elements of `dtype`."""
+    if t.dim() == 0 or t.shape[-1] != cols:
+        raise ValueError(f"rows of {cols} elements wanted, not a tensor of shape {tuple(t.shape)}")
     t = t.reshape(-1, cols)
     return t if t.is_contiguous() and t.dtype == dtype else t.to(dtype).contiguous()
 
@@ -125,6 +128,17 @@ def _update(layers, x2: torch.Tensor, dy2s) -> None:
     if ev is not None:
         e1.record()
         ev.append((e0, e1))
+
+
+def _same_rows(what: str, lead, x_lead) -> None:
+    """Leading dimensions of two tensors that are taken row by row: the same rows in the same order
+    (dimensions of 1 and a flat list of rows count as the same)."""
+    if len(lead) == 1 or len(x_lead) == 1:
+        same = math.prod(lead) == math.prod(x_lead)
+    else:
+        same = [n for n in lead if n != 1] == [n for n in x_lead if n != 1]
+    if not same:
+        raise ValueError(f"{what} of leading shape {tuple(lead)} beside an input of {tuple(x_lead)}")
 
 
 class _NoDerivative(torch.autograd.Function):
@@ -167,6 +181,8 @@ class _ForgeLinearEpiFn(torch.autograd.Function):
     def forward(ctx, x, weight, bias, residual, layer, recorded):
         x2 = _rows(x, weight.shape[1], weight.dtype)
         r2 = None if residual is None else _rows(residual, weight.shape[0], weight.dtype)
+        if residual is not None:
+            _same_rows("a residual", residual.shape[:-1], x.shape[:-1])
         keep = recorded and layer.act != "none"
         y = forge.linear(x2, weight.detach(), bias=None if bias is None else bias.detach(), act=layer.act, residual=r2,
                          save=keep)
@@ -463,6 +479,7 @@ class _LinearCrossEntropyFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, targets, ignore_index, reduction, head):
         x2 = _rows(x, weight.shape[1], weight.dtype)
+        _same_rows("targets", targets.shape, x.shape[:-1])
         t1 = targets.reshape(-1).contiguous()
         loss, lse, total = forge.linear_cross_entropy(x2, weight.detach(), t1, ignore_index=ignore_index,
                                                       reduction=reduction)

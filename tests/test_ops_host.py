@@ -345,3 +345,32 @@ def test_xent_refuses_more_logits_than_the_memory_holds_partial_results_of():
                                             n, None) == UNSUP
         # one row less: the next check answers
         assert L.forge_linear_xent_forward(ref(few), ref(W), tgt, -100, None, lse, tot, ws, 0, None) == SCRATCH
+
+
+def test_modules_refuse_rows_in_another_order():
+    """A residual or targets whose leading dimensions hold as many rows in another order, and rows of
+    another length, are refused; a flat list of rows and dimensions of 1 are the same rows."""
+    from optimizer_gemm_amd.nn import ForgeHead, ForgeLinear, linear_cross_entropy
+
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    y = lambda *s: torch.zeros(*s, dtype=torch.int64)  # noqa: E731
+    layer, head, w = ForgeLinear(16, 24, act="silu"), ForgeHead(16, 40), z(40, 16)
+    for x, r in ((z(2, 3, 16), z(3, 2, 24)), (z(2, 3, 16), z(6, 4, 24)), (z(6, 16), z(5, 24)), (z(2, 3, 16), z(24))):
+        with pytest.raises(ValueError, match="leading shape"):
+            layer(x, r)
+    for x, r in ((z(6, 16), z(3, 48)), (z(3, 32), z(6, 24)), (z(2, 3, 16), z(2, 3, 1, 12))):
+        with pytest.raises(ValueError, match="elements wanted"):
+            layer(x, r)
+    for x, t in ((z(2, 3, 16), y(3, 2)), (z(2, 3, 16), y(5)), (z(6, 16), y(2, 2))):
+        for f in (head, lambda a, b: linear_cross_entropy(a, w, b)):
+            with pytest.raises(ValueError, match="leading shape"):
+                f(x, t)
+    with pytest.raises(ValueError, match="elements wanted"):
+        linear_cross_entropy(z(3, 32), w, y(6))
+    # these get as far as the kernels, which take no CPU tensors
+    for x, r in ((z(2, 3, 16), z(2, 3, 24)), (z(2, 3, 16), z(6, 24)), (z(6, 16), z(2, 3, 24)), (z(2, 1, 3, 16), z(2, 3, 24))):
+        with pytest.raises(ValueError, match="device tensors"):
+            layer(x, r)
+    for x, t in ((z(2, 3, 16), y(2, 3)), (z(2, 3, 16), y(6)), (z(6, 16), y(2, 3)), (z(1, 6, 16), y(6, 1))):
+        with pytest.raises(ValueError, match="device tensors"):
+            head(x, t)
