@@ -62,25 +62,7 @@ class _ForgeLinearFn(torch.autograd.Function):
         dx = None
         if ctx.needs_input_grad[0]:
             dx = forge.dgrad(dy2, w.detach()).reshape(x.shape)  # old W, before the update below
-        if not layer.fused:
-            # two-phase schedule: the float32 gradient waits for step_all(); a second
-            # backward before it adds to it, as the usual gradient accumulation does
-            g = forge.wgrad(x2, dy2)
-            if layer.grad32 is None:
-                layer.grad32 = g
-            else:
-                layer.grad32.add_(g)
-            return dx, None, None
-        layer._step_count += 1
-        ev = layer.timing
-        if ev is not None:
-            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-            e0.record()
-        forge.wgrad_step(x2, dy2, w.detach(), layer.m, layer.v, layer.opt, layer.hyper, layer._step_count,
-                         layer.seed, layer.m_scale, layer.v_scale, code=layer.code)
-        if ev is not None:
-            e1.record()
-            ev.append((e0, e1))
+        _update([layer], x2, [dy2])
         return dx, None, None
 
 
@@ -98,13 +80,15 @@ def _rows(t: torch.Tensor, cols: int, dtype: torch.dtype) -> torch.Tensor:
     return t if t.is_contiguous() and t.dtype == dtype else t.to(dtype).contiguous()
 
 
-def _update(layers, x2: torch.Tensor, dy2s) -> None:
-    """The weight-gradient half of a backward pass for layers that read x2: their fused steps
-    (one launch for several, which are _alike), or, two-phase, their float32 gradients for
+def _update(layers, x2: torch.Tensor, dy2s, group: bool = False) -> None:
+    """The weight-gradient half of a backward pass: a layer's fused step on x2, or, with `group`,
+    the grouped one of layers that read x2 and are _alike; or, two-phase, the float32 gradients for
     step_all(). A call that is refused leaves the step counts as they were."""
     L0 = layers[0]
     if not L0.fused:
         for L, dy2 in zip(layers, dy2s):
+            # the float32 gradient waits for step_all(); a second backward before it adds to it, as
+            # the usual gradient accumulation does
             g = forge.wgrad(x2, dy2)
             if L.grad32 is None:
                 L.grad32 = g
@@ -116,7 +100,7 @@ def _update(layers, x2: torch.Tensor, dy2s) -> None:
     if ev is not None:
         e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         e0.record()
-    if len(layers) == 1:
+    if not group:
         forge.wgrad_step(x2, dy2s[0], L0.weight.detach(), L0.m, L0.v, L0.opt, L0.hyper, step, L0.seed,
                          L0.m_scale, L0.v_scale, code=L0.code)
     else:
@@ -332,27 +316,7 @@ class _ForgeGroupFn(torch.autograd.Function):
             for w, dy2 in zip(ws[1:], dy2s[1:]):
                 dx.add_(forge.dgrad(dy2, w))
             dx = dx.reshape(x.shape)
-        L0 = layers[0]
-        if not L0.fused:
-            for L, dy2 in zip(layers, dy2s):
-                g = forge.wgrad(x2, dy2)
-                if L.grad32 is None:
-                    L.grad32 = g
-                else:
-                    L.grad32.add_(g)
-            return (dx, None) + (None,) * len(layers)
-        for L in layers:
-            L._step_count += 1
-        ev = L0.timing
-        if ev is not None:
-            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-            e0.record()
-        forge.wgrad_step_group(x2, dy2s, ws, [L.m for L in layers], [L.v for L in layers], L0.opt, L0.hyper,
-                               L0._step_count, [L.seed for L in layers], [L.m_scale for L in layers],
-                               [L.v_scale for L in layers], code=L0.code)
-        if ev is not None:
-            e1.record()
-            ev.append((e0, e1))
+        _update(layers, x2, dy2s, group=True)
         return (dx, None) + (None,) * len(layers)
 
 
@@ -425,7 +389,7 @@ class _GatedBlockFn(torch.autograd.Function):
         dh = forge.dgrad_group([dG, dU], [wg, wu]).reshape(ctx.h_shape) if ctx.needs_input_grad[0] else None
         _update([down], H, [dy2])
         if wg.dtype == torch.bfloat16 and _alike((gate, up)):
-            _update([gate, up], h2, [dG, dU])
+            _update([gate, up], h2, [dG, dU], group=True)
         else:  # the grouped step takes bf16 layers that agree
             _update([gate], h2, [dG])
             _update([up], h2, [dU])
@@ -505,11 +469,11 @@ class _LinearCrossEntropyFn(torch.autograd.Function):
             if head._step_count != ctx.step:
                 # lse belongs to the weights of the forward pass
                 raise RuntimeError("the head's weights were stepped after this loss was computed")
-            head._step_count += 1
             dx, dw = forge.linear_cross_entropy_step(x2, w, head.m, head.v, t1, lse, g, head.opt, head.hyper,
-                                                     head._step_count, head.seed, head.m_scale, head.v_scale,
+                                                     head._step_count + 1, head.seed, head.m_scale, head.v_scale,
                                                      code=head.code, ignore_index=ignore_index, reduction=reduction,
                                                      total=total, want_dx=ctx.needs_input_grad[0], piece=head.piece), None
+            head._step_count += 1
         return (None if dx is None else dx.reshape(ctx.x_shape)), dw, None, None, None, None
 
 

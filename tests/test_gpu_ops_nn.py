@@ -565,3 +565,13 @@ def test_evaluation_keeps_nothing_for_backward(monkeypatch):
         with torch.inference_mode():
             assert torch.equal(module(*args), want)
     assert layer.step_count == 0
+
+
+def test_a_refused_head_step_counts_nothing():
+    """float32 steps of a head whose piece is no multiple of 8 are refused: weights and count stay."""
+    head = ForgeHead(64, 200, dtype=torch.float32, device="cuda", piece=12)
+    x = rnd(1, 20, 64, dtype=torch.float32).requires_grad_()
+    w = head.weight.detach().clone()
+    with pytest.raises(forge.ForgeError):
+        head(x, torch.randint(0, 200, (20,), device="cuda")).backward()
+    assert head.step_count == 0 and torch.equal(head.weight.detach(), w)

@@ -305,7 +305,7 @@ def test_a_refused_step_leaves_the_step_counts(monkeypatch):
                               m_scale=None, v_scale=None, opt="sgd", hyper=None, seed=0, code="linear") for _ in range(2)]
     for some in (layers, layers[:1]):
         with pytest.raises(forge.ForgeError):
-            fnn._update(some, None, [None] * len(some))
+            fnn._update(some, None, [None] * len(some), group=len(some) > 1)
         assert [L._step_count for L in layers] == [4, 4]
 
 
