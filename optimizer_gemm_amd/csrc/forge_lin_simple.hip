@@ -11,7 +11,7 @@
 // against 26.0; 512 x 1024 -> 1024: 18.3 against 34.3).
 // Bound: a small product by its chain of stages, about 1 us each, and the launch (512 x 256 ->
 // 256: 10.0 us, 6.0 of them the kernel); a large one by the FP32 matrix rate and LDS staging
-// (4096 x 1024 -> 4096: 100 TFLOP/s of the part's 154).
+// (4096 x 1024 -> 4096: 107 TFLOP/s of the part's 154).
 #include "forge_lin_kernel.h"
 
 namespace forge {

@@ -124,7 +124,11 @@ __device__ __forceinline__ void store4(float* p, f32x4 x) { *reinterpret_cast<f3
 // ---------------------------------------------------------------------------
 // arguments
 // ---------------------------------------------------------------------------
-// Epilogues of the products.
+// Epilogues of the products. Outputs are rounded to the operands' type once. dG and dU (L_DGATE) and dz
+// (L_DLOGIT) are rounded before the products that follow them: those run on the matrix cores in the
+// operands' type, and the fused steps take dG, dU and dz as they are. For bf16 that is half a step
+// (2^-9 to 2^-8) of each element, independent over the sum: the relative error of dX and dW is 0.0023
+// and 0.0019 where float32 intermediates would leave the outputs' own 0.0017.
 enum LinEpi {
   L_LINEAR = 0,  // out = act(x + bias) + in1; out2 = x + bias (the pre-activation), if asked for
   L_GATED = 1,   // two products g, u: out = act(g) u; out2 = g, out3 = u, if asked for

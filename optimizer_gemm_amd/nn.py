@@ -489,8 +489,10 @@ class ForgeHead(torch.nn.Module):
     """Linear head with softmax cross entropy: forward(x, targets) is the loss, its logits never
     stored; backward computes dX and steps the weights [vocab, d] piece by piece of the
     vocabulary, the gradient never stored either. Arguments as ForgeLinear's; `piece` the
-    vocabulary entries per piece (0: the library's choice). Each backward call is one step, of a
-    loss computed with the weights as they are: a loss from before another one's step is refused."""
+    vocabulary entries per piece (0: the library's choice). The step takes weights and moments
+    of less than 2^31 bytes each (131072 x 4096 in bf16, with bf16 or 8-bit moments). Each backward
+    call is one step, of a loss computed with the weights as they are: a loss from before another
+    one's step is refused."""
 
     def __init__(self, d: int, vocab: int, opt: str = "adamw", hyper: Optional[dict] = None, states: str = "f32",
                  dtype: torch.dtype = torch.bfloat16, device=None, seed: int = 0,
