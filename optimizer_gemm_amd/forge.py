@@ -275,9 +275,12 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
-def _side(raw: int, device) -> torch.cuda.Stream:
-    """The stream of a raw handle (torch's wrapper takes 0 for "a new one", not for the default)."""
-    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+def _side(stream, device) -> torch.cuda.Stream:
+    """A given stream as torch's object (whose wrapper of a raw handle takes 0 for "a new one", not
+    for the default stream)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
 
 
 def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
@@ -287,10 +290,10 @@ def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Ten
     is noted for the allocator."""
     if stream is None or device.type != "cuda":
         return torch.empty(shape, dtype=dtype, device=device)
-    raw, current = _stream(stream), torch.cuda.current_stream(device)
-    if raw == current.cuda_stream:
+    current = torch.cuda.current_stream(device)
+    if _stream(stream) == current.cuda_stream:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(_side(raw, device)):
+    with torch.cuda.stream(_side(stream, device)):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(current)
     return t
@@ -478,7 +481,7 @@ class _On:
     that writes it, and the allocator hands out no tensor of the call again before that stream (for
     a new tensor: the current one too) is done with it."""
 
-    __slots__ = ("device", "stream", "_given", "_guard", "_index", "_others")
+    __slots__ = ("device", "stream", "_given", "_guard", "_index", "_others", "_current")
 
     def __init__(self, stream, first, *others):
         self._index = index = first.get_device()
@@ -491,20 +494,23 @@ class _On:
         if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device != self.device:
             raise ValueError("the stream belongs to another device than the tensors")
         self._given = stream
-        self._guard = None
+        self._guard = self._current = None
         self._others = (first, *others) if stream is not None else None
 
     def __enter__(self):
-        if _current_device() != self._index:
-            self._guard = torch.cuda.device(self._index)
-            self._guard.__enter__()
-        current = _raw_stream(self._index)
-        self.stream = current if self._given is None else _stream(self._given)
-        if self.stream != current:
-            side = _side(self.stream, self.device)
+        given = None if self._given is None else _stream(self._given)
+        if given is not None and given != _raw_stream(self._index):
+            # one switch of device and stream for all that the call allocates
+            side, self._current = _side(self._given, self.device), torch.cuda.current_stream(self.device)
             for t in self._others:
                 if t is not None:
                     t.record_stream(side)
+            self._guard = torch.cuda.stream(side)
+        elif _current_device() != self._index:
+            self._guard = torch.cuda.device(self._index)
+        if self._guard is not None:
+            self._guard.__enter__()
+        self.stream = _raw_stream(self._index) if given is None else given
         return self
 
     def __exit__(self, *exc):
@@ -512,7 +518,10 @@ class _On:
 
     def empty(self, shape, dtype) -> torch.Tensor:
         """A new tensor that this call writes."""
-        return _empty(shape, dtype, self.device, self._given)
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self._current is not None:
+            t.record_stream(self._current)
+        return t
 
 
 # torch's own short ways to the device's current stream and to the current device: a few
