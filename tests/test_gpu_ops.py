@@ -694,3 +694,166 @@ def test_cross_entropy_sums_of_dx_past_32_bit_offsets():
     assert torch.equal(dW, want_w.to(F).to(BF))
     del want_w, X, dW
     torch.cuda.empty_cache()
+
+
+def c_tensor(t):
+    import ctypes
+    return ctypes.byref(forge.forge._ten(t))
+
+
+def test_dgrad_group_without_a_workspace():
+    """The C call that takes no workspace: the same product with a tile's whole sum in one workgroup."""
+    g = gen(4)
+    t, i, outs = 15, 512, (6568, 40, 6568)
+    dYs, Ws = [rnd(g, t, o) for o in outs], [rnd(g, o, i, std=0.01) for o in outs]
+    dX = torch.full((t, i), float("nan"), device="cuda", dtype=BF)
+    A = forge.forge.ForgeTensor * len(outs)
+    stream = torch.cuda.current_stream().cuda_stream
+    st = forge.lib().forge_linear_dgrad_group(len(outs), A(*[forge.forge._ten(d) for d in dYs]),
+                                              A(*[forge.forge._ten(w) for w in Ws]), c_tensor(dX), stream)
+    assert st == 0
+    want, bound = 0, 0
+    for d, w in zip(dYs, Ws):
+        x, e = mm64(d, w)
+        want, bound = want + x, bound + len(outs) * e
+    close("dX", dX, want, bound)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_factors_per_token_of_a_mean(dt, piece):
+    """The C calls with a factor per token and a total: every factor is divided by the count. Outputs with
+    rows of their own pitch."""
+    import ctypes
+    t, i, v = 190, 128, 1003
+    X, W, y, lse, w, dz, keep = exact_head(t, t, i, v, DT[dt], "targets")
+    W = W[:v].contiguous()
+    total = torch.tensor([0.0, 128.0, 0.0], device="cuda")
+    lib, stream = forge.lib(), torch.cuda.current_stream().cuda_stream
+    f = (dz.double() * w[:, None].double() / 128)[:, :v]
+    want_x, want_w = (f @ W.double()).to(F).to(DT[dt]), (f.t() @ X.double()).to(F).to(DT[dt])
+    big_x = torch.full((t, i + 16), 7.0, device="cuda", dtype=DT[dt])
+    big_w = torch.full((v, i + 16), 7.0, device="cuda", dtype=DT[dt])
+    need = lib.forge_linear_xent_workspace(t, i, v, forge.forge._DT[DT[dt]], 1, piece)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    st = lib.forge_linear_xent_backward(c_tensor(X), c_tensor(W), y.data_ptr(), -100, lse.data_ptr(), w.data_ptr(), 1,
+                                        total.data_ptr(), c_tensor(big_x[:, :i]), c_tensor(big_w[:, :i]), piece,
+                                        ws.data_ptr(), need, stream)
+    assert st == 0
+    assert torch.equal(big_x[:, :i], want_x) and torch.equal(big_w[:, :i], want_w)
+    assert torch.all(big_x[:, i:] == 7.0) and torch.all(big_w[:, i:] == 7.0)
+    h = forge.make_hyper("sgd", lr=0.5, stochastic_round=0)
+    w1 = W.clone()
+    st = lib.forge_linear_xent_step(c_tensor(X), c_tensor(w1), None, None, forge.forge.OPT_ID["sgd"], ctypes.byref(h), 1, 0,
+                                    y.data_ptr(), -100, lse.data_ptr(), w.data_ptr(), 1, total.data_ptr(),
+                                    c_tensor(big_x[:, :i]), piece, ws.data_ptr(), need, stream)
+    assert st == 0
+    # sums and products by powers of two are exact: W - lr dW in float32, rounded once
+    assert torch.equal(w1, (W.double() - 0.5 * (f.t() @ X.double())).to(F).to(DT[dt]))
+    assert torch.equal(big_x[:, :i], want_x)
+
+
+@pytest.mark.parametrize("piece", [0, 256])
+def test_head_step_of_pitched_tensors(piece):
+    """W and the moments as views with wider rows, X too: the same bits, the padding untouched."""
+    t, i, v = 190, 128, 1003
+    X, W, y, lse, w, dz, keep = exact_head(5, t, i, v, BF, "targets")
+    W = W[:v].contiguous()
+    g = gen(3)
+    m, vv = torch.rand(v, i, generator=g, device="cuda"), torch.rand(v, i, generator=g, device="cuda")
+    want = [a.clone() for a in (W, m, vv)]
+    dX = forge.linear_cross_entropy_step(X, *want, y, lse, w, "adamw", {"lr": 0.05}, 3, 11, reduction="none", piece=piece)
+    bigs = []
+    for a, extra in ((W, 40), (m, 8), (vv, 24)):
+        big = torch.full((v, i + extra), 7.0, device="cuda", dtype=a.dtype)
+        big[:, :i] = a
+        bigs.append(big)
+    got = forge.linear_cross_entropy_step(pitched(X), *[b[:, :i] for b in bigs], y, lse, w, "adamw", {"lr": 0.05}, 3, 11,
+                                          reduction="none", piece=piece)
+    assert torch.equal(got, dX)
+    for a, b in zip(want, bigs):
+        assert torch.equal(b[:, :i], a) and torch.all(b[:, i:] == 7.0)
+
+
+def test_head_of_distant_rows():
+    """Rows of W 4 MB apart: a piece of the vocabulary holds fewer of them, in the documented workspace."""
+    t, i, v = 190, 128, 1500
+    X, W, y, lse, w, dz, keep = exact_head(6, t, i, v, BF, "targets")
+    big = torch.empty(v, 1 << 21, device="cuda", dtype=BF)
+    far = big[:, :i]
+    far.copy_(W[:v])
+    want = forge.linear_cross_entropy_backward(X, W[:v], y, lse, w, reduction="none")
+    got = forge.linear_cross_entropy_backward(X, far, y, lse, w, reduction="none")
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    a, b = forge.linear_cross_entropy(X, W[:v], y), forge.linear_cross_entropy(X, far, y)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    del big, far
+    torch.cuda.empty_cache()
+
+
+def test_pieces_in_a_graph():
+    """Gradients and steps over several pieces of the vocabulary, captured and replayed with eager work
+    between the replays."""
+    t, i, v = 190, 128, 1003
+    X, W, y, lse, w, dz, keep = exact_head(8, t, i, v, BF, "targets")
+    W = W[:v].contiguous()
+    live, eager = W.clone(), W.clone()
+    sl, se = forge.new_states(W, "adamw")[:2], forge.new_states(W, "adamw")[:2]
+
+    def both(wt, st):
+        out = forge.linear_cross_entropy_backward(X, wt, y, lse, w, reduction="none", piece=256)
+        return [*out, forge.linear_cross_entropy_step(X, wt, *st, y, lse, w, "adamw", {"lr": 0.05}, 2, 11,
+                                                      reduction="none", piece=256)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(live, sl)
+    torch.cuda.synchronize()
+    live.copy_(W)
+    for s in sl:
+        s.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both(live, sl)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for o in out:
+            o.zero_()
+        graph.replay()
+        want = both(eager, se)
+        torch.cuda.synchronize()
+        for a, b in zip(out + [live, *sl], want + [eager, *se]):
+            assert torch.equal(a, b)
+
+
+def test_calls_of_two_threads():
+    """Two host threads, a stream each: the same bits as one after the other."""
+    import threading
+    t, i, v = 190, 128, 1003
+    cases = [exact_head(k, t, i, v, BF, "targets") for k in (1, 2)]
+    G, U = rnd(gen(1), t, 264), rnd(gen(2), t, 264)
+
+    def work(c):
+        X, W, y, lse, w, dz, keep = c
+        out = [forge.linear(X, W, act="gelu"), *forge.gated(X, W, W, save=True), *forge.gated_backward(G, U, G)]
+        return out + list(forge.linear_cross_entropy_backward(X, W[:v], y, lse, w, reduction="none", piece=256))
+
+    want = [work(c) for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def run(k):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got = work(cases[k])
+                s.synchronize()
+                bad.extend(k for a, b in zip(got, want[k]) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in (0, 1)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not bad
