@@ -759,7 +759,8 @@ def linear_cross_entropy_step(X: torch.Tensor, W: torch.Tensor, m: Optional[torc
                               piece: int = 0, stream=None) -> Optional[torch.Tensor]:
     """linear_cross_entropy_backward with the head's fused optimizer step in the place of dW
     (forge_linear_xent_step): W, m, v (and scales) updated in place piece by piece; returns
-    dX (from the old W) or None. Optimizer arguments as in wgrad_step."""
+    dX (from the old W) or None. Optimizer arguments as in wgrad_step; W, m and v of less than
+    2^31 bytes each."""
     _reduction(reduction)
     h = _hyper(opt, hyper)
     with _On(stream, X, W, m, v, targets, lse, dloss, m_scale, v_scale, total) as on:
