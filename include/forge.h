@@ -71,6 +71,8 @@ typedef enum {
  *     max sqrt(v)/255 (v);
  *   - FORGE_I8_DYN / FORGE_U8_DYN moments: the same layout, the scale being the
  *     block's absmax of m (or max of v);
+ *   - FORGE_I8 operands of products (forge_linear_q8 and its kin): one float32 per row, the factor of its
+ *     codes;
  *   - FORGE_E4M3 / FORGE_E5M2 inputs: one float32 in device memory, the tensor's
  *     dequantisation scale (element value = decoded code * scale[0]). */
 typedef struct {
@@ -398,6 +400,107 @@ int forge_linear_xent_step(const forge_tensor* X, forge_tensor* W, forge_tensor*
                            int64_t ignore, const float* lse, const float* dloss, int32_t per_token,
                            const float* total, forge_tensor* dX, int64_t piece, void* workspace,
                            int64_t workspace_bytes, forge_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Layers of experts: the linear layers above, `experts` of them stacked, each applied to the tokens that a
+ * router sends to it. A route is a pair (token t, slot j) with an expert idx[t, j]; the routes, ordered by
+ * expert, are the rows of the products: expert x owns rows offsets[x] .. offsets[x + 1] - 1, any number of
+ * them, and the x-th of the stacked matrices. The operators' conventions above hold; in addition:
+ *   - 1 <= experts <= FORGE_MAX_EXPERTS, else FORGE_ERR_SHAPE.
+ *   - A stack W [experts * out, in] is one tensor (its rows a multiple of `experts`, FORGE_ERR_SHAPE); one
+ *     expert's part spans less than 2^31 bytes, the whole any number.
+ *   - offsets: experts + 1 int64 in device memory, ascending, within 0 .. rows. The sizes are read on the
+ *     device, so no call waits for them. Other values reach no memory outside the tensors (they are held to
+ *     that range and order), but the results are then unspecified.
+ *   - Rows in front of offsets[0] and from offsets[experts] on belong to no expert: they are not read, and those of
+ *     a result are left as they were.
+ * ---------------------------------------------------------------------------
+ */
+#define FORGE_MAX_EXPERTS 1024
+
+/*
+ * The order of the routes: a stable sort by expert. idx: T * k int64, row by row; a value outside [0, experts)
+ * (-1, say) drops the route. offsets as above (offsets[0] = 0, offsets[experts] = the routes kept);
+ * pos: T * k int32, the row of each route, -1 for a dropped one. T * k < 2^30, else
+ * FORGE_ERR_UNSUPPORTED. Workspace: forge_expert_plan_workspace(T, k, experts) bytes (0 for a few).
+ */
+int64_t forge_expert_plan_workspace(int64_t T, int64_t k, int32_t experts);
+int forge_expert_plan(const int64_t* idx, int64_t T, int64_t k, int32_t experts, int64_t* offsets, int32_t* pos,
+                      void* workspace, int64_t workspace_bytes, forge_stream_t stream);
+
+/*
+ * Rows to their experts: Xp[pos[t, j]] = X[t]. X [T, cols] in FORGE_F32, FORGE_BF16, or FORGE_I8 with a factor
+ * for each row in `scale` (T floats; cols and ld multiples of 16), which goes along into Xp's. Xp [rows, cols]; a
+ * place outside 0 .. rows - 1 is skipped, rows that no route has are left as they were; routes have different
+ * places. T < 2^26, else FORGE_ERR_UNSUPPORTED. Its gradient is forge_expert_combine without weights.
+ */
+int forge_expert_dispatch(const forge_tensor* X, const int32_t* pos, int64_t k, forge_tensor* Xp, forge_stream_t stream);
+
+/*
+ * And back: Y[t] = sum over j of weights[t, j] Yp[pos[t, j]] + R[t], in FP32 in the order of the slots, rounded
+ * once; dropped routes add nothing. weights: T * k floats, or NULL for ones; R [T, cols] or NULL. T < 2^26.
+ * Backward: dYp[pos[t, j]] = weights[t, j] dY[t], and dweights[t, j] = the product of dY[t] and Yp[pos[t, j]]
+ * (0 for a dropped route). Either may be NULL; Yp may be NULL without dweights. The residual's gradient is dY.
+ */
+int forge_expert_combine(const forge_tensor* Yp, const int32_t* pos, int64_t k, const float* weights,
+                         const forge_tensor* R, forge_tensor* Y, forge_stream_t stream);
+int forge_expert_combine_backward(const forge_tensor* dY, const forge_tensor* Yp, const int32_t* pos, int64_t k,
+                                  const float* weights, forge_tensor* dYp, float* dweights, forge_stream_t stream);
+
+/*
+ * The products, row by row those of forge_linear_forward (without bias and residual), forge_gated_forward,
+ * forge_gated_dgrad and forge_linear_dgrad_group with the row's expert's matrices: X, dY, G, U and the
+ * results have one row per route, W, Wg, Wu [experts * out, in], Wd [experts * out, hid].
+ */
+int forge_expert_linear(const forge_tensor* X, const forge_tensor* W, int32_t experts, const int64_t* offsets,
+                        int32_t act, forge_tensor* Y, forge_tensor* Z, forge_stream_t stream);
+int forge_expert_gated(const forge_tensor* X, const forge_tensor* Wg, const forge_tensor* Wu, int32_t experts,
+                       const int64_t* offsets, int32_t act, forge_tensor* H, forge_tensor* G, forge_tensor* U,
+                       forge_stream_t stream);
+int forge_expert_gated_dgrad(const forge_tensor* dY, const forge_tensor* Wd, const forge_tensor* G,
+                             const forge_tensor* U, int32_t experts, const int64_t* offsets, int32_t act,
+                             forge_tensor* dG, forge_tensor* dU, forge_tensor* H, forge_stream_t stream);
+int forge_expert_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,
+                             const int64_t* offsets, forge_tensor* dX, forge_stream_t stream);
+
+/*
+ * The stack's weight gradient dW = dY^T X over each expert's rows, stored as float32 [experts * out, in] (row
+ * pitch ld_dw, a multiple of 4), and the fused step of forge_linear_wgrad_step on it, never stored, all experts in
+ * one launch: the weights, moments and random streams are those of one layer W [experts * out, in]
+ * (fewer than 2^32 weights), and every expert's weights take the step, without rows with a gradient of zero.
+ * FP8 operands: FORGE_ERR_UNSUPPORTED.
+ */
+int forge_expert_wgrad(const forge_tensor* X, const forge_tensor* dY, int32_t experts, const int64_t* offsets,
+                       float* dW, int64_t ld_dw, forge_stream_t stream);
+int forge_expert_wgrad_step(const forge_tensor* X, const forge_tensor* dY, forge_tensor* W, forge_tensor* m,
+                            forge_tensor* v, int32_t experts, const int64_t* offsets, int32_t opt,
+                            const forge_hyper* hyper, int64_t step, uint64_t seed, forge_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Products of 8-bit integers, for serving. Q FORGE_I8 [rows, cols] with a factor for each row in `scale`
+ * (rows floats; cols and ld multiples of 16, else FORGE_ERR_ALIGN) stands for the values Q[r, c] scale[r]:
+ * tokens have theirs, weights one for each output channel (16-byte aligned). Sums of products are exact in 32-bit integers
+ * (in < 2^17, else FORGE_ERR_UNSUPPORTED), the epilogue is in FP32, results are FORGE_BF16.
+ * ---------------------------------------------------------------------------
+ *
+ * Rows to 8 bits: scale = max |x| / 127 (float32), Q = x / scale to the nearest whole number, ties to even. A
+ * row of zeros has scale 0; one that holds an infinity or NaN has scale NaN and codes 0. X FORGE_F32 or
+ * FORGE_BF16, cols a multiple of 16; Q and its scale are written. rows < 2^26, else FORGE_ERR_UNSUPPORTED.
+ */
+int forge_quantize_rows(const forge_tensor* X, forge_tensor* Q, forge_stream_t stream);
+
+/* Y = act(X W^T + bias) + R and H = act(X Wg^T) * (X Wu^T), as above; R bfloat16, bias bfloat16 or float32. And the
+ * same grouped by expert, without bias and residual. */
+int forge_linear_q8(const forge_tensor* X, const forge_tensor* W, const forge_tensor* bias, int32_t act,
+                    const forge_tensor* R, forge_tensor* Y, forge_stream_t stream);
+int forge_gated_q8(const forge_tensor* X, const forge_tensor* Wg, const forge_tensor* Wu, int32_t act, forge_tensor* H,
+                   forge_stream_t stream);
+int forge_expert_linear_q8(const forge_tensor* X, const forge_tensor* W, int32_t experts, const int64_t* offsets,
+                           int32_t act, forge_tensor* Y, forge_stream_t stream);
+int forge_expert_gated_q8(const forge_tensor* X, const forge_tensor* Wg, const forge_tensor* Wu, int32_t experts,
+                          const int64_t* offsets, int32_t act, forge_tensor* H, forge_stream_t stream);
 
 /* Host-only helpers (no GPU work). */
 

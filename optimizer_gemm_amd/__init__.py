@@ -10,4 +10,7 @@ from .forge import (  # noqa: F401
     dyn_value, dyn_encode, mfma_peak,
     ACTS, linear, linear_act_backward, gated, gated_backward, gated_dgrad, dgrad_group, linear_cross_entropy,
     linear_cross_entropy_backward, linear_cross_entropy_step,
+    MAX_EXPERTS, expert_plan, expert_dispatch, expert_combine, expert_combine_backward, expert_linear, expert_gated,
+    expert_gated_dgrad, expert_dgrad_group, expert_wgrad, expert_wgrad_step,
+    quantize_rows, linear_q8, gated_q8, expert_linear_q8, expert_gated_q8,
 )

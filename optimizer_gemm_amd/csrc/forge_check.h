@@ -187,5 +187,39 @@ OptArgs make_args(forge_tensor* W, forge_tensor* m, forge_tensor* v, int opt, co
   return a;
 }
 
+// ---- the operators' checks ----
+// Operand type of a call: every tensor given must have it.
+int op_dtype(const forge_tensor* t) {
+  if (!t) return FORGE_ERR_NULL;
+  if (is_fp8(t->dtype)) return FORGE_ERR_UNSUPPORTED;
+  return t->dtype == FORGE_F32 || t->dtype == FORGE_BF16 ? FORGE_OK : FORGE_ERR_DTYPE;
+}
+
+// A dense operand or result of the given size.
+int check_mat(const forge_tensor* t, int dtype, int64_t rows, int64_t cols) {
+  int r = check_io(t, dtype);
+  if (r) return r;
+  if (t->rows != rows || t->cols != cols) return FORGE_ERR_SHAPE;
+  return fits_31(t) ? FORGE_OK : FORGE_ERR_UNSUPPORTED;
+}
+
+bool act_ok(int act) { return act >= FORGE_ACT_NONE && act <= FORGE_ACT_GELU_TANH; }
+
+int hip_status(hipError_t e) { return e == hipSuccess ? FORGE_OK : FORGE_ERR_HIP; }
+
+// Plain memory as a tensor, for the overlap checks.
+forge_tensor flat(const void* p, int64_t bytes) {
+  return forge_tensor{const_cast<void*>(p), FORGE_I8, 0, p && bytes > 0 ? 1 : 0, bytes, bytes, nullptr};
+}
+
+int check_workspace(const void* ws, int64_t have, int64_t need) {
+  if (need == 0) return FORGE_OK;
+  if (have < need) return FORGE_ERR_SCRATCH;
+  if (!ws) return FORGE_ERR_NULL;
+  return ((uintptr_t)ws & 15u) ? FORGE_ERR_ALIGN : FORGE_OK;
+}
+
+int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
 }  // namespace
 }  // namespace forge

@@ -13,6 +13,14 @@ FORGE_EXTERN_BF16(FORGE_RMSPROP)
 FORGE_EXTERN_BF16(FORGE_ADAGRAD)
 FORGE_EXTERN_BF16(FORGE_NADAM)
 FORGE_EXTERN_BF16(FORGE_RADAM)
+FORGE_EXTERN_EXPERT(FORGE_ADAMW)
+FORGE_EXTERN_EXPERT(FORGE_SGD)
+FORGE_EXTERN_EXPERT(FORGE_SGD_MOMENTUM)
+FORGE_EXTERN_EXPERT(FORGE_LION)
+FORGE_EXTERN_EXPERT(FORGE_RMSPROP)
+FORGE_EXTERN_EXPERT(FORGE_ADAGRAD)
+FORGE_EXTERN_EXPERT(FORGE_NADAM)
+FORGE_EXTERN_EXPERT(FORGE_RADAM)
 #define FORGE_EXTERN_F8_ALL(FB)             \
   FORGE_EXTERN_F8(FORGE_ADAMW, FB)          \
   FORGE_EXTERN_F8(FORGE_SGD, FB)            \
@@ -127,6 +135,49 @@ hipError_t launch_wgrad_store_bf16(const void* X, const void* dY, const GemmDims
   OptArgs a{};
   return g_pick<WgradBig, WgradSmall, WgradSplit, WgradBand, WgradTiny>(
       g, [&](auto c, const GArgs& gc) { return g_launch<decltype(c), G_EPI_STORE, FORGE_SGD, ST_F32, false>(gc, a, st); });
+}
+
+// Stacked layers: d.T rows of the common operands, d.out and d.in of one layer.
+static GArgs expert_args(const void* X, const void* dY, const GemmDims& d, const int64_t* offsets, int experts) {
+  GArgs g{};
+  g.A = X;
+  g.B = dY;
+  g.lda = d.ldx;
+  g.ldb = d.lddy;
+  g.M = d.in;
+  g.N = d.out;
+  g.K = d.T;
+  g.offsets = offsets;
+  g.experts = experts;
+  return g;
+}
+
+hipError_t launch_wgrad_fused_expert_bf16(int sf, int opt, int sr, const void* X, const void* dY, const GemmDims& d,
+                                          const int64_t* offsets, int experts, const OptArgs& a, hipStream_t st) {
+  const GArgs g = expert_args(X, dY, d, offsets, experts);
+  switch (opt) {
+    case FORGE_ADAMW: return wgrad_fused_expert_opt<FORGE_ADAMW>(sf, sr, g, a, st);
+    case FORGE_SGD: return wgrad_fused_expert_opt<FORGE_SGD>(sf, sr, g, a, st);
+    case FORGE_SGD_MOMENTUM: return wgrad_fused_expert_opt<FORGE_SGD_MOMENTUM>(sf, sr, g, a, st);
+    case FORGE_LION: return wgrad_fused_expert_opt<FORGE_LION>(sf, sr, g, a, st);
+    case FORGE_RMSPROP: return wgrad_fused_expert_opt<FORGE_RMSPROP>(sf, sr, g, a, st);
+    case FORGE_ADAGRAD: return wgrad_fused_expert_opt<FORGE_ADAGRAD>(sf, sr, g, a, st);
+    case FORGE_NADAM: return wgrad_fused_expert_opt<FORGE_NADAM>(sf, sr, g, a, st);
+    case FORGE_RADAM: return wgrad_fused_expert_opt<FORGE_RADAM>(sf, sr, g, a, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_wgrad_store_expert_bf16(const void* X, const void* dY, const GemmDims& d, const int64_t* offsets,
+                                          int experts, float* dW, int64_t ld_dw, hipStream_t st) {
+  GArgs g = expert_args(X, dY, d, offsets, experts);
+  g.out = dW;
+  g.ldo = ld_dw;
+  g.out_bytes = extent(d.out, d.in, ld_dw, 4);
+  OptArgs a{};
+  return g_pick_expert(g, [&](auto c) {
+    return g_launch<decltype(c), G_EPI_STORE, FORGE_SGD, ST_F32, false, true>(g, a, st);
+  });
 }
 
 template <int FB>

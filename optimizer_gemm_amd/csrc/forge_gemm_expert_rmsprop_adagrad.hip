@@ -1,0 +1,6 @@
+// Fused steps of stacked layers (experts), bfloat16.
+#include "forge_gemm_kernel.h"
+namespace forge {
+FORGE_INST_EXPERT(FORGE_RMSPROP)
+FORGE_INST_EXPERT(FORGE_ADAGRAD)
+}  // namespace forge

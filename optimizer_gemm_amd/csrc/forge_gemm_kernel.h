@@ -190,6 +190,10 @@ struct GArgs {
   // Origin of this launch's tiles in C: the launch covers rows [m_off, M) and columns
   // [n_off, N); all addressing (and the weight element index of the RNG) stays absolute.
   int32_t m_off, n_off;
+  // Stacked layers (experts): layer x has rows offsets[x] .. offsets[x + 1] - 1 of A and B as its k, and the
+  // x-th of the stacked outputs; a_bytes, b_bytes and out_bytes go unused or are one layer's
+  const int64_t* offsets;
+  int32_t experts;
 };
 
 // A grouped fused step: up to kMaxGroup layers that share the A operand (X) and the
@@ -305,15 +309,16 @@ __device__ __forceinline__ void issue_prio() {
 // Persistent tile order: tile ids a workgroup takes are blockIdx.x + r*gridDim.x.
 // Workgroups are dealt to the 8 XCDs round-robin, so within a full round the ids of
 // one XCD are made contiguous, and contiguous ids walk GROUP tile-rows at a time.
-__device__ __forceinline__ void g_tile(int tile, int ntm, int ntn, int& tm, int& tn) {
+__device__ __forceinline__ int g_order(int tile, int ntiles) {
   const int G = gridDim.x;
-  const int ntiles = ntm * ntn;
-  int L = tile;
   const int round0 = (tile / G) * G;
   if ((G & 7) == 0 && round0 + G <= ntiles) {
     const int w = tile - round0;
-    L = round0 + (w & 7) * (G >> 3) + (w >> 3);
+    return round0 + (w & 7) * (G >> 3) + (w >> 3);
   }
+  return tile;
+}
+__device__ __forceinline__ void g_place(int L, int ntm, int ntn, int& tm, int& tn) {
   constexpr int GROUP = 4;
   const int per = GROUP * ntn;
   const int g = L / per;
@@ -322,6 +327,9 @@ __device__ __forceinline__ void g_tile(int tile, int ntm, int ntn, int& tm, int&
   const int r = L - g * per;
   tm = first + r % gs;
   tn = r / gs;
+}
+__device__ __forceinline__ void g_tile(int tile, int ntm, int ntn, int& tm, int& tn) {
+  g_place(g_order(tile, ntm * ntn), ntm, ntn, tm, tn);
 }
 
 // Epilogue memory access through buffer resources (32-bit offsets; an out-of-range
@@ -349,9 +357,11 @@ __device__ __forceinline__ EpiRes epi_res(const OptArgs& a) {
 }
 
 // SF: moment storage format (StateFmt: float32, INT8 block-64, or bfloat16).
-template <class C, int EPI, int OPT, int SF, bool SR>
+// EXP: stacked layers whose k ranges are rows of common operands (GArgs::offsets), in one launch.
+template <class C, int EPI, int OPT, int SF, bool SR, bool EXP = false>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::OCC, C::OCC)))
 void gemm_kernel(GArgs g, OptArgs a, GroupArgs gr) {
+  static_assert(!EXP || (C::B_TR && !C::F8), "stacked layers: rows of A and B are k, bfloat16");
   // Q8: INT8 codes with block scales, linear (ST_Q8) or the dynamic code (ST_Q8D)
   constexpr bool Q8D = SF == ST_Q8D, Q8 = SF == ST_Q8 || Q8D, B16S = SF == ST_BF16;
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::SMEM_BYTES];
@@ -371,17 +381,17 @@ void gemm_kernel(GArgs g, OptArgs a, GroupArgs gr) {
   const int wave_m0 = wm * C::TM, wave_n0 = wn * C::TN;
   const int l32 = lane & 31, hi = lane >> 5;
 
-  const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.A, g.a_bytes);
+  __amdgpu_buffer_rsrc_t rA = make_rsrc(g.A, EXP ? 0u : g.a_bytes);
   // FP8 operands: the gradient is the product of the two dequantisation scales times
   // the sum of code products (B's scale is the tile's layer's, in a grouped launch)
   const float a_sc = C::F8 ? g.a_scale[0] : 1.f;
 
   const int ntm = g_ntm<C>(g), ntn = g_ntn<C>(g);
-  const int ntiles = ntm * ntn;
-  const int nst = (g.K + C::BK - 1) / C::BK;
+  const int ntiles = ntm * ntn * (EXP ? g.experts : 1);
+  int gt_K = g.K, nst = (g.K + C::BK - 1) / C::BK;
   // Stages are issued in groups of the ring size; stages past the last one, like rows
   // past the last token, load through out-of-range offsets and so hold zeros.
-  const int nstr = ((nst + C::NSTAGE - 1) / C::NSTAGE) * C::NSTAGE;
+  int nstr = ((nst + C::NSTAGE - 1) / C::NSTAGE) * C::NSTAGE;
   constexpr int LPS = C::PA + C::PB;                                     // loads per stage and wave
   constexpr int NRA = C::RA * C::FM, NRB = C::B_TR ? C::RA * C::FN : C::FN;
   constexpr int NR = NRA + NRB;                                           // LDS reads per k-step and wave
@@ -394,8 +404,14 @@ void gemm_kernel(GArgs g, OptArgs a, GroupArgs gr) {
   const int kr0 = ks * C::KPW * C::KSTEP;  // first k row of this wave in a stage
 
   for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-    int tm, tn;
-    g_tile(tile, ntm, ntn, tm, tn);
+    int tm, tn, ex = 0;
+    if constexpr (EXP) {
+      const int L = g_order(tile, ntiles);
+      ex = L / (ntm * ntn);
+      g_place(L - ex * (ntm * ntn), ntm, ntn, tm, tn);
+    } else {
+      g_tile(tile, ntm, ntn, tm, tn);
+    }
     // the tile's layer (a grouped launch): its B operand, rows and pitch, and the
     // epilogue's tensors and random stream; chosen with uniform selects
     const void* t_B = g.B;
@@ -404,7 +420,31 @@ void gemm_kernel(GArgs g, OptArgs a, GroupArgs gr) {
     int64_t gt_ldb = g.ldb;
     int gt_N = g.N;
     OptArgs at = a;
-    if (gr.count > 0) {
+    if constexpr (EXP) {
+      // the layer's rows, held to those of the operands whatever the offsets are; its weights and their
+      // place in the random stream of the whole stack (counter ex out in + index, linear in the counter)
+      const int64_t t0 = g.offsets[ex], t1 = g.offsets[ex + 1];
+      const int r0 = (int)(t0 < 0 ? 0 : t0 > g.K ? g.K : t0), r1 = (int)(t1 < r0 ? r0 : t1 > g.K ? g.K : t1);
+      gt_K = r1 - r0;
+      nst = (gt_K + C::BK - 1) / C::BK;
+      nstr = ((nst + C::NSTAGE - 1) / C::NSTAGE) * C::NSTAGE;
+      rA = make_rsrc(static_cast<const char*>(g.A) + (int64_t)r0 * g.lda * C::EB,
+                     gt_K > 0 ? (uint32_t)(((int64_t)(gt_K - 1) * g.lda + g.M) * C::EB) : 0u);
+      t_B = static_cast<const char*>(g.B) + (int64_t)r0 * g.ldb * C::EB;
+      t_b_bytes = gt_K > 0 ? (uint32_t)(((int64_t)(gt_K - 1) * g.ldb + g.N) * C::EB) : 0u;
+      if constexpr (EPI == G_EPI_OPT) {
+        constexpr int es = Q8 ? 1 : B16S ? 2 : 4;
+        const int64_t row = (int64_t)ex * g.N;
+        at.W = static_cast<char*>(a.W) + row * a.ldw * 2;
+        at.m = static_cast<char*>(a.m) + row * a.ldm * es;
+        at.v = static_cast<char*>(a.v) + row * a.ldv * es;
+        at.m_scale = a.m_scale + row * (a.in >> 6);
+        at.v_scale = a.v_scale + row * (a.in >> 6);
+        at.out = g.N;
+        at.rng_base = a.rng_base + 0x9E3779B97F4A7C15ull * ((uint64_t)row * (uint64_t)a.in);
+      }
+    }
+    if (!EXP && gr.count > 0) {
       int tn0 = 0;
 #pragma unroll
       for (int j = 0; j < kMaxGroup; ++j) {
@@ -506,13 +546,13 @@ void gemm_kernel(GArgs g, OptArgs a, GroupArgs gr) {
       const int k0 = s * C::BK;
 #pragma unroll
       for (int j = 0; j < C::PA; ++j) {
-        const uint32_t off = (k0 + a_row0 + j * A_RSTEP < g.K) ? a_base0 + (uint32_t)s * a_stageb + (uint32_t)j * a_rowb : kOOB;
+        const uint32_t off = (k0 + a_row0 + j * A_RSTEP < gt_K) ? a_base0 + (uint32_t)s * a_stageb + (uint32_t)j * a_rowb : kOOB;
         dma16(rA, smem + C::a_base(buf) + (j * C::NT + wave_u * 64) * 16, off);
       }
 #pragma unroll
       for (int j = 0; j < C::PB; ++j) {
         const int kb = C::B_TR ? k0 + b_row0 + j * B_RSTEP : k0 + b_colb / C::EB;
-        const uint32_t off = (kb < g.K) ? b_base0 + (uint32_t)s * b_stageb + (uint32_t)j * b_rowb : kOOB;
+        const uint32_t off = (kb < gt_K) ? b_base0 + (uint32_t)s * b_stageb + (uint32_t)j * b_rowb : kOOB;
         dma16(rB, smem + C::b_base(buf) + (j * C::NT + wave_u * 64) * 16, off);
       }
     };
@@ -888,7 +928,8 @@ void gemm_kernel(GArgs g, OptArgs a, GroupArgs gr) {
       constexpr int NTHR = decltype(nthr_c)::value;
       static_assert(VPRc % 16 == 0, "an INT8 block of 64 must be 16 adjacent lanes");
       if constexpr (EPI == G_EPI_STORE || EPI == G_EPI_DX) {
-        const __amdgpu_buffer_rsrc_t rO = make_rsrc(g.out, g.out_bytes);
+        const __amdgpu_buffer_rsrc_t rO =
+            make_rsrc(static_cast<const char*>(g.out) + (EXP ? (int64_t)ex * g.N * g.ldo * 4 : 0), g.out_bytes);
 #pragma unroll
         for (int k = 0; k < NVc; ++k) {
           const int vi = t + k * NTHR, row = vi / VPRc, col = (vi % VPRc) * 4;
@@ -1142,7 +1183,7 @@ static int g_num_cus() {
   return n;
 }
 
-template <class C, int EPI, int OPT, int SF, bool SR>
+template <class C, int EPI, int OPT, int SF, bool SR, bool EXP = false>
 static hipError_t g_launch(const GArgs& g0, const OptArgs& a, hipStream_t st, const GroupArgs* grp = nullptr) {
   GArgs g = g0;
   GroupArgs gr{};
@@ -1157,11 +1198,11 @@ static hipError_t g_launch(const GArgs& g0, const OptArgs& a, hipStream_t st, co
     g.n_off = 0;
     g.N = tn * C::BN;
   }
-  const int ntiles = g_ntm<C>(g) * g_ntn<C>(g);
+  const int ntiles = g_ntm<C>(g) * g_ntn<C>(g) * (EXP ? g.experts : 1);
   if (ntiles == 0) return hipSuccess;
   const int resident = C::OCC * 4 / C::NW * g_num_cus();  // OCC waves on each of 4 SIMDs
   const int grid = ntiles < resident ? ntiles : resident;
-  hipLaunchKernelGGL((gemm_kernel<C, EPI, OPT, SF, SR>), dim3(grid), dim3(C::NT), 0, st, g, a, gr);
+  hipLaunchKernelGGL((gemm_kernel<C, EPI, OPT, SF, SR, EXP>), dim3(grid), dim3(C::NT), 0, st, g, a, gr);
   return hipGetLastError();
 }
 
@@ -1220,22 +1261,22 @@ static uint32_t extent(int64_t rows, int64_t cols, int64_t ld, int64_t es) {
 
 // Fused step for one optimizer on bf16 / fp32 operands (instantiated per optimizer
 // in the forge_gemm_bf16_*.hip sources).
-template <class C, int OPT>
+template <class C, int OPT, bool EXP = false>
 static hipError_t g_launch_opt(int sf, int sr, const GArgs& g, const OptArgs& a, hipStream_t st,
                                const GroupArgs* gr = nullptr) {
   switch (sf) {
     case ST_Q8:
-      return sr ? g_launch<C, G_EPI_OPT, OPT, ST_Q8, true>(g, a, st, gr)
-                : g_launch<C, G_EPI_OPT, OPT, ST_Q8, false>(g, a, st, gr);
+      return sr ? g_launch<C, G_EPI_OPT, OPT, ST_Q8, true, EXP>(g, a, st, gr)
+                : g_launch<C, G_EPI_OPT, OPT, ST_Q8, false, EXP>(g, a, st, gr);
     case ST_Q8D:
-      return sr ? g_launch<C, G_EPI_OPT, OPT, ST_Q8D, true>(g, a, st, gr)
-                : g_launch<C, G_EPI_OPT, OPT, ST_Q8D, false>(g, a, st, gr);
+      return sr ? g_launch<C, G_EPI_OPT, OPT, ST_Q8D, true, EXP>(g, a, st, gr)
+                : g_launch<C, G_EPI_OPT, OPT, ST_Q8D, false, EXP>(g, a, st, gr);
     case ST_BF16:
-      return sr ? g_launch<C, G_EPI_OPT, OPT, ST_BF16, true>(g, a, st, gr)
-                : g_launch<C, G_EPI_OPT, OPT, ST_BF16, false>(g, a, st, gr);
+      return sr ? g_launch<C, G_EPI_OPT, OPT, ST_BF16, true, EXP>(g, a, st, gr)
+                : g_launch<C, G_EPI_OPT, OPT, ST_BF16, false, EXP>(g, a, st, gr);
     default:
-      return sr ? g_launch<C, G_EPI_OPT, OPT, ST_F32, true>(g, a, st, gr)
-                : g_launch<C, G_EPI_OPT, OPT, ST_F32, false>(g, a, st, gr);
+      return sr ? g_launch<C, G_EPI_OPT, OPT, ST_F32, true, EXP>(g, a, st, gr)
+                : g_launch<C, G_EPI_OPT, OPT, ST_F32, false, EXP>(g, a, st, gr);
   }
 }
 
@@ -1301,6 +1342,18 @@ hipError_t wgrad_fused_bf16_opt(int sf, int sr, const GArgs& g, const OptArgs& a
       g, [&](auto c, const GArgs& gc) { return g_launch_opt<decltype(c), OPT>(sf, sr, gc, a, st); });
 }
 
+// The tiles of stacked layers: 256x256 for more than half a round of them, else 128x128.
+template <class F>
+static hipError_t g_pick_expert(const GArgs& g, F&& f) {
+  if (2 * (int64_t)g_tiles<WgradBig>(g) * g.experts > g_num_cus()) return f(WgradBig{});
+  return f(WgradSmall{});
+}
+
+template <int OPT>
+hipError_t wgrad_fused_expert_opt(int sf, int sr, const GArgs& g, const OptArgs& a, hipStream_t st) {
+  return g_pick_expert(g, [&](auto c) { return g_launch_opt<decltype(c), OPT, true>(sf, sr, g, a, st); });
+}
+
 // FP8 operands, dY in format FB (0 = E4M3, 1 = E5M2): the fused step of one
 // optimizer, and the float32 dW store (instantiated in forge_gemm_f8_*.hip).
 template <class C, int OPT>
@@ -1337,6 +1390,10 @@ hipError_t wgrad_store_f8(const GArgs& g, hipStream_t st) {
 #define FORGE_INST_BF16(OPT)                                                                     \
   template hipError_t wgrad_fused_bf16_opt<OPT>(int, int, const GArgs&, const OptArgs&, hipStream_t); \
   template hipError_t wgrad_fused_bf16_group_opt<OPT>(int, int, const GArgs&, const OptArgs&, const GroupArgs&, hipStream_t);
+#define FORGE_EXTERN_EXPERT(OPT) \
+  extern template hipError_t wgrad_fused_expert_opt<OPT>(int, int, const GArgs&, const OptArgs&, hipStream_t);
+#define FORGE_INST_EXPERT(OPT) \
+  template hipError_t wgrad_fused_expert_opt<OPT>(int, int, const GArgs&, const OptArgs&, hipStream_t);
 #define FORGE_EXTERN_F8(OPT, FB)                                                                          \
   extern template hipError_t wgrad_fused_f8_opt<OPT, FB>(int, int, const GArgs&, const OptArgs&, hipStream_t); \
   extern template hipError_t wgrad_fused_f8_group_opt<OPT, FB>(int, int, const GArgs&, const OptArgs&,         \

@@ -402,6 +402,18 @@ hipError_t launch_optimizer(int w_bf16, int state_fmt, int opt, int sr, const fl
                             const OptArgs& a, hipStream_t stream);
 hipError_t launch_dgrad(int io_bf16, const void* dY, int64_t lddy, const void* W, int64_t ldw, void* dX,
                         int64_t lddx, int32_t T, int32_t out, int32_t in, hipStream_t stream);
+// Stacked layers (experts): layer x has rows offsets[x] .. offsets[x + 1] - 1 of the d.T rows of X and dY, d.out
+// and d.in are one layer's, a's tensors and random stream the whole stack's.
+hipError_t launch_wgrad_fused_expert(int io_bf16, int state_fmt, int opt, int sr, const void* X, const void* dY,
+                                     const GemmDims& d, const int64_t* offsets, int experts, const OptArgs& a,
+                                     hipStream_t stream);
+hipError_t launch_wgrad_store_expert(int io_bf16, const void* X, const void* dY, const GemmDims& d,
+                                     const int64_t* offsets, int experts, float* dW, int64_t ld_dw, hipStream_t stream);
+hipError_t launch_wgrad_fused_expert_bf16(int state_fmt, int opt, int sr, const void* X, const void* dY,
+                                          const GemmDims& d, const int64_t* offsets, int experts, const OptArgs& a,
+                                          hipStream_t stream);
+hipError_t launch_wgrad_store_expert_bf16(const void* X, const void* dY, const GemmDims& d, const int64_t* offsets,
+                                          int experts, float* dW, int64_t ld_dw, hipStream_t stream);
 // bfloat16 / FP8 kernels (forge_gemm.hip, forge_gemm_kernel.h)
 hipError_t launch_wgrad_fused_bf16(int state_fmt, int opt, int sr, const void* X, const void* dY, const GemmDims& d,
                                    const OptArgs& a, hipStream_t stream);

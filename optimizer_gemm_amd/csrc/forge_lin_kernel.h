@@ -102,6 +102,11 @@ __device__ __forceinline__ void dma16s(__amdgpu_buffer_rsrc_t r, uint8_t* dst, u
 __device__ __forceinline__ void mfma_acc(f32x4& c, bf16x8 a, bf16x8 b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
+// the same on 8-bit integers: a fragment's 16 bytes hold 16 k where bfloat16 has 8 (both operands in the
+// same order), c holds 32-bit integers
+__device__ __forceinline__ void mfma_acc_q8(f32x4& c, u32x4 a, u32x4 b) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
 __device__ __forceinline__ void mfma_drain() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // The kernel's argument where it lies (its only one, at the start of the argument segment): its
@@ -114,9 +119,11 @@ __device__ __forceinline__ LinArgsPtr lin_args() { return (LinArgsPtr)__builtin_
 // inlined would put them into scratch memory
 #define FORGE_INLINE __attribute__((always_inline))
 
-template <class C, int EPI, bool TA, bool TB>
+template <class C, int EPI, bool TA, bool TB, int MODE>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::OCC, C::OCC)))
 void lin_kernel(LinArgs g) {
+  constexpr bool EXP = (MODE & LM_EXPERT) != 0, Q8 = (MODE & LM_Q8) != 0;
+  static_assert(!Q8 || (!TA && !TB && (EPI == L_LINEAR || EPI == L_GATED)), "8-bit operands: forward products");
   using OA = LOper<C, C::BM, TA>;
   using OB = LOper<C, C::BN, TB>;
   constexpr bool TWO = EPI == L_GATED;              // A: BM / 2 rows of gate, then BM / 2 of up
@@ -133,7 +140,9 @@ void lin_kernel(LinArgs g) {
   uint8_t* const ring = smem + grp * 5 * C::SLOT;
   const uint32_t lds0 = lds_addr(smem) + (uint32_t)(grp * 5 * C::SLOT);
   const int ntm = (epi_width<EPI>(g.M) - g.m_off + OM - 1) / OM, ntn = (g.N - g.n_off + C::BN - 1) / C::BN;
-  const int ntiles = ntm * ntn * (EPI == L_ACC && TA && !TB ? g.splits : 1);
+  ExpertRows<C::BN> xr{g.offsets, g.experts, g.N, -1, 0, 0, 0};
+  int ntiles = ntm * ntn * (EPI == L_ACC && TA && !TB && !EXP ? g.splits : 1);
+  if constexpr (EXP) ntiles = ntm * xr.total();
   const LinArgsPtr ga = lin_args();
   const int nsrc = MULTI ? ga->nsrc : 1;
   int nst = (g.K[0] + C::BK - 1) / C::BK;
@@ -141,7 +150,7 @@ void lin_kernel(LinArgs g) {
     for (int s = 1; s < nsrc; ++s) nst += (ga->K[s] + C::BK - 1) / C::BK;
   }
   // SPLIT: g.splits workgroups share a tile's k range, each writing its part of the sums
-  constexpr bool SPLIT = MULTI;
+  constexpr bool SPLIT = MULTI && !EXP;
   const int splits = SPLIT ? g.splits : 1;
   const int mine = (nst + C::KS * splits - 1) / (C::KS * splits);  // stages of a group
 
@@ -154,6 +163,7 @@ void lin_kernel(LinArgs g) {
   __amdgpu_buffer_rsrc_t rA, rA2, rB;
   uint32_t av[PA], bv[PB];     // this thread's offsets in a stage
   int lm0 = 0, ln0 = 0, lsp = 0;  // the tile that is being loaded, its part of the k range
+  int lx = 0, lend = g.N;         // its expert, the end of that expert's rows
   // offsets of the loads from a panel whose first output index is the tile's (lim of them exist)
   auto ext = [&](bool tr, int64_t ld, int64_t lim, int64_t rows, int K) FORGE_INLINE -> uint32_t {
     if (K <= 0 || lim <= 0) return 0u;
@@ -169,10 +179,12 @@ void lin_kernel(LinArgs g) {
     fa_K = (MULTI ? ga->K[s] : g.K[0]);
     fa_k = 0;
     fa_kb = TA ? (uint32_t)(ld * 2) : 2u;
-    rA = make_rsrc(static_cast<const char*>((MULTI ? ga->A[s] : g.A[0])) + (TA ? (int64_t)lm0 : (int64_t)lm0 * ld) * 2,
+    // rows of the stacked matrices in front of the tile's expert
+    const int64_t xrow = EXP ? (int64_t)lx * (TA ? fa_K : g.M) : 0;
+    rA = make_rsrc(static_cast<const char*>((MULTI ? ga->A[s] : g.A[0])) + (TA ? (int64_t)lm0 + xrow * ld : (lm0 + xrow) * ld) * 2,
                    ext(TA, ld, lim, OM, fa_K));
     if constexpr (TWO)
-      rA2 = make_rsrc(static_cast<const char*>(g.A[1]) + (int64_t)lm0 * g.lda[1] * 2,
+      rA2 = make_rsrc(static_cast<const char*>(g.A[1]) + (lm0 + xrow) * g.lda[1] * 2,
                       ext(false, g.lda[1], lim, OM, fa_K));
     int t = tid;
     asm volatile("" : "+v"(t));
@@ -187,7 +199,7 @@ void lin_kernel(LinArgs g) {
   };
   auto source_b = [&](int s) FORGE_INLINE {
     const int64_t ld = (MULTI ? ga->ldb[s] : g.ldb[0]);
-    const int lim = g.N - ln0;
+    const int lim = (EXP ? lend : g.N) - ln0;
     fb_src = s;
     fb_K = (MULTI ? ga->K[s] : g.K[0]);
     fb_k = 0;
@@ -246,10 +258,19 @@ void lin_kernel(LinArgs g) {
       part = tile % splits;
       tile /= splits;
     }
-    g_tile(tile, ntm, ntn, tm, tn);
+    if constexpr (EXP) {
+      const int L = g_order(tile, ntiles);
+      int r0, t0;
+      xr.find(L / ntm, lx, r0, lend, t0);
+      g_place(L - t0 * ntm, ntm, (lend - r0 + C::BN - 1) / C::BN, tm, tn);
+      lm0 = tm * OM;
+      ln0 = r0 + tn * C::BN;
+    } else {
+      g_tile(tile, ntm, ntn, tm, tn);
+      lm0 = g.m_off + tm * OM;
+      ln0 = g.n_off + tn * C::BN;
+    }
     lsp = part;
-    lm0 = g.m_off + tm * OM;
-    ln0 = g.n_off + tn * C::BN;
     int src0 = 0, k0 = (part * C::KS + grp) * mine * C::BK;  // the group's first stage: its pair and k
     if constexpr (MULTI) {
       while (src0 + 1 < nsrc && k0 >= (ga->K[src0] + C::BK - 1) / C::BK * C::BK) {
@@ -358,6 +379,8 @@ void lin_kernel(LinArgs g) {
   if (blockIdx.x < ntiles) dma_begin(blockIdx.x);
   for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
     const int m0 = lm0, n0 = ln0, part = lsp;
+    const int n_end = EXP ? lend : g.N;
+    const int64_t sw0 = EXP ? (int64_t)lx * g.M : 0;  // 8-bit operands: the expert's first column factor
     f32x4 acc[C::FM][C::FN];
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm)
@@ -376,7 +399,10 @@ void lin_kernel(LinArgs g) {
         b = __builtin_bit_cast(bf16x8, u32x4{F.bt[fn][0].x, F.bt[fn][0].y, F.bt[fn][1].x, F.bt[fn][1].y});
       else
         b = __builtin_bit_cast(bf16x8, F.bk[fn]);
-      mfma_acc(acc[fm][fn], a, b);
+      if constexpr (Q8)
+        mfma_acc_q8(acc[fm][fn], __builtin_bit_cast(u32x4, a), __builtin_bit_cast(u32x4, b));
+      else
+        mfma_acc(acc[fm][fn], a, b);
     };
     // the MFMAs of F; the reads of G (k-step kk of the slots the addresses point to) and the loads
     // of an operand's stage spread over the first half of them; sched_barrier keeps the order
@@ -471,7 +497,11 @@ void lin_kernel(LinArgs g) {
               const int col = !TWO ? wm * C::TM + 16 * fm
                                    : (fm < C::FM / 2 ? 0 : C::BM / 2 - C::TM / 2) + wm * (C::TM / 2) + 16 * fm;
               f32x4* p = reinterpret_cast<f32x4*>(E + (wn * C::TN + 16 * fn + e_l16) * C::LDE + col + 4 * e_q);
-              *p = kg == 0 ? acc[fm][fn] : *p + acc[fm][fn];
+              if constexpr (Q8)
+                *p = kg == 0 ? acc[fm][fn]
+                             : __builtin_bit_cast(f32x4, __builtin_bit_cast(i32x4, *p) + __builtin_bit_cast(i32x4, acc[fm][fn]));
+              else
+                *p = kg == 0 ? acc[fm][fn] : *p + acc[fm][fn];
             }
         }
         __syncthreads();
@@ -504,10 +534,15 @@ void lin_kernel(LinArgs g) {
         act_dispatch<EPI>(g.e.act, [&](auto act_c) {
           for (int v = t; v < C::BN * OM / 4; v += C::NT) {
             const int row = v / (OM / 4), col = (v % (OM / 4)) * 4, n = n0 + row, m = m0 + col;
-            if (n < g.N && m < Mw) {
-              const f32x4 x = *reinterpret_cast<const f32x4*>(E + row * C::LDE + col);
+            if (n < n_end && m < Mw) {
+              f32x4 x = *reinterpret_cast<const f32x4*>(E + row * C::LDE + col);
               f32x4 x2 = x;
               if constexpr (TWO) x2 = *reinterpret_cast<const f32x4*>(E + row * C::LDE + C::BM / 2 + col);
+              if constexpr (Q8) {
+                const float sx = g.e.sx[n];
+                x = int_sums(x) * (load4(g.e.sw + sw0 + m) * sx);
+                if constexpr (TWO) x2 = int_sums(x2) * (load4(g.e.sw2 + sw0 + m) * sx);
+              }
               epi_vec<uint16_t, EPI, decltype(act_c)::value>(g.e, n, m, g.M, x, x2, sc,
                                                              SPLIT ? (int64_t)part * g.N * g.e.ldacc : 0);
             }
@@ -598,7 +633,7 @@ void lin_kernel(LinArgs g) {
       const int e_row = e_lane / VPR, e_col = e_lane % VPR;
       constexpr int RS = 64 / VPR;
       // what the epilogue reads and writes, from this wave's first row on
-      const int rows = g.N - nw < C::TN ? g.N - nw : C::TN;
+      const int rows = n_end - nw < C::TN ? n_end - nw : C::TN;
       auto res = [&](const void* p, int64_t ld, int es) FORGE_INLINE -> __amdgpu_buffer_rsrc_t {
         return make_rsrc(static_cast<const char*>(p) + (int64_t)nw * ld * es,
                          rows > 0 ? (uint32_t)(((int64_t)(rows - 1) * ld + Mw) * es) : 0u);
@@ -615,6 +650,8 @@ void lin_kernel(LinArgs g) {
       // loaded two blocks ahead.
       struct Pre {
         u32x4 a[NV], b[NV];
+        float sx[NV];     // 8-bit operands: the rows' factors, the columns' (of both products)
+        f32x4 sw[4];
       };
       auto get = [&](u32x4 (&x)[NV], const void* p, int64_t ld, int es, int at, int blk) FORGE_INLINE {
         uint32_t o[NV];
@@ -624,6 +661,21 @@ void lin_kernel(LinArgs g) {
         for (int k = 0; k < NV; ++k) x[k] = __builtin_amdgcn_raw_buffer_load_b128(r, o[k], at, 0);
       };
       auto load = [&](Pre& P, int blk) FORGE_INLINE {
+        if constexpr (Q8) {
+          // rows and columns past the end: the last row's, the first column's
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            const int n = nw + 32 * (blk / CH) + e_row + k * RS;
+            P.sx[k] = e.sx[n < n_end ? n : n_end - 1];
+          }
+          const int m = mw + OWB * (blk % CH) + 8 * e_col, mc = m < Mw ? m : 0;
+          P.sw[0] = load4(e.sw + sw0 + mc);
+          P.sw[1] = load4(e.sw + sw0 + mc + 4);
+          if constexpr (TWO) {
+            P.sw[2] = load4(e.sw2 + sw0 + mc);
+            P.sw[3] = load4(e.sw2 + sw0 + mc + 4);
+          }
+        }
         if constexpr (EPI == L_LINEAR) {
           if (e.in1) get(P.a, e.in1, e.ld1, 2, 0, blk);
         } else if constexpr (EPI == L_DGATE) {
@@ -743,6 +795,14 @@ void lin_kernel(LinArgs g) {
                 z0 = chunk(k, 8 + 2 * e_col);
                 z1 = chunk(k, 8 + 2 * e_col + 1);
               }
+              if constexpr (Q8) {
+                x0 = int_sums(x0) * (P.sw[0] * P.sx[k]);
+                x1 = int_sums(x1) * (P.sw[1] * P.sx[k]);
+                if constexpr (TWO) {
+                  z0 = int_sums(z0) * (P.sw[2] * P.sx[k]);
+                  z1 = int_sums(z1) * (P.sw[3] * P.sx[k]);
+                }
+              }
               if constexpr (EPI == L_LINEAR) {
                 x0 = x0 + bias0;
                 x1 = x1 + bias1;
@@ -806,14 +866,18 @@ using LinSmall = LTile<128, 2, false>;
 using LinSplit = LTile<128, 2, false, 2>;
 using LinTiny = LTile<64, 4, false, 4>;
 
-template <class C, int EPI, bool TA, bool TB>
+template <class C, int EPI, bool TA, bool TB, int MODE = 0>
 hipError_t lin_run(const LinArgs& g, hipStream_t st) {
   constexpr int OM = EPI == L_GATED ? C::BM / 2 : C::BM;
-  const int64_t ntm = (epi_width<EPI>(g.M) - g.m_off + OM - 1) / OM, ntn = (g.N - g.n_off + C::BN - 1) / C::BN;
-  const int64_t tiles = ntm * ntn * (EPI == L_ACC && TA && !TB ? g.splits : 1);
+  constexpr bool EXP = (MODE & LM_EXPERT) != 0;
+  const int64_t ntm = (epi_width<EPI>(g.M) - g.m_off + OM - 1) / OM;
+  // (grouped by expert: as many as there can be, each expert's last one partly full)
+  const int64_t ntn = EXP ? (g.N + C::BN - 1) / C::BN + (g.experts < g.N ? g.experts : g.N)
+                          : (g.N - g.n_off + C::BN - 1) / C::BN;
+  const int64_t tiles = ntm * ntn * (EPI == L_ACC && TA && !TB && !EXP ? g.splits : 1);
   if (tiles <= 0) return hipSuccess;
   const int64_t resident = (int64_t)(C::OCC * 4 / C::NW) * g_num_cus();
-  hipLaunchKernelGGL((lin_kernel<C, EPI, TA, TB>), dim3((uint32_t)(tiles < resident ? tiles : resident)), dim3(C::NT), 0,
+  hipLaunchKernelGGL((lin_kernel<C, EPI, TA, TB, MODE>), dim3((uint32_t)(tiles < resident ? tiles : resident)), dim3(C::NT), 0,
                      st, g);
   return hipGetLastError();
 }
@@ -885,6 +949,22 @@ hipError_t lin_bf16(const LinArgs& g, hipStream_t st) {
     case LT_SPLIT: return lin_run<LinSplit, EPI, TA, TB>(g, st);
     default: return lin_run<LinTiny, EPI, TA, TB>(g, st);
   }
+}
+
+// Products grouped by expert: the tiles as far as they can be told without the experts' sizes, which are
+// in device memory.
+template <int EPI, bool TA, int MODE>
+hipError_t lin_expert(const LinArgs& g, hipStream_t st) {
+  const int64_t cus = g_num_cus(), w = EPI == L_GATED ? 2 * (int64_t)g.M : g.M;
+  const int64_t used = g.experts < g.N ? g.experts : g.N, each = g.N / used;
+  auto tiles = [&](int64_t b) { return (w + b - 1) / b * used * ((each + b - 1) / b); };
+  if (each >= 128 && 2 * tiles(256) > cus) return lin_run<LinBig, EPI, TA, false, MODE>(g, st);
+  // (the gated gradient's epilogue and the experts' rows need more registers than two workgroups per unit leave)
+  if constexpr (EPI != L_DGATE) {
+    if (each >= 48 && tiles(128) > cus) return lin_run<LinSmall, EPI, TA, false, MODE>(g, st);
+  }
+  if (each >= 48) return lin_run<LinSplit, EPI, TA, false, MODE>(g, st);
+  return lin_run<LinTiny, EPI, TA, false, MODE>(g, st);
 }
 
 #define FORGE_LIN_FORMS(X)                                                                                  \

@@ -90,7 +90,7 @@ __device__ __forceinline__ void mma32(f32x16& acc, const float* as, const float*
   }
 }
 
-template <class C, int EPI, bool TA, bool TB>
+template <class C, int EPI, bool TA, bool TB, bool EXP>
 __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
   constexpr bool TWO = EPI == L_GATED;
   constexpr int S_B = C::B, S_BK = C::BK, LDE = C::LDE;
@@ -108,8 +108,16 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
   const float sc = (EPI == L_ACC || EPI == L_DLOGIT) ? epi_scale(g.e) : 1.f;
 
   const int tiles_m = (epi_width<EPI>(g.M) - g.m_off + S_B - 1) / S_B, tiles_n = (g.N - g.n_off + S_B - 1) / S_B;
-  for (int64_t tile = blockIdx.x; tile < (int64_t)tiles_m * tiles_n; tile += gridDim.x) {
-  const int m0 = g.m_off + (int)(tile % tiles_m) * S_B, n0 = g.n_off + (int)(tile / tiles_m) * S_B;
+  ExpertRows<S_B> xr{g.offsets, g.experts, g.N, -1, 0, 0, 0};
+  const int64_t ntiles = EXP ? (int64_t)tiles_m * xr.total() : (int64_t)tiles_m * tiles_n;
+  for (int64_t tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
+  int tn = (int)(tile / tiles_m), ex = 0, r0 = g.n_off, n_end = g.N;
+  if constexpr (EXP) {
+    int t0;
+    xr.find(tn, ex, r0, n_end, t0);
+    tn -= t0;
+  }
+  const int m0 = g.m_off + (int)(tile % tiles_m) * S_B, n0 = r0 + tn * S_B;
   f32x16 acc, acc2;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
@@ -122,10 +130,15 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
     const float* A2 = static_cast<const float*>(g.A[TWO ? 1 : 0]);
     const float* B = static_cast<const float*>(g.B[s]);
     const int K = g.K[s];
+    if constexpr (EXP) {  // the expert's matrices
+      const int64_t xrow = (int64_t)ex * (TA ? K : g.M);
+      A += xrow * g.lda[s];
+      if constexpr (TWO) A2 += xrow * g.lda[1];
+    }
     auto fetch = [&](int k0) {
       sa.load(A, g.lda[s], m0, g.M, k0, K, tid);
       if constexpr (TWO) sa2.load(A2, g.lda[1], m0, g.M, k0, K, tid);
-      sb.load(B, g.ldb[s], n0, g.N, k0, K, tid);
+      sb.load(B, g.ldb[s], n0, n_end, k0, K, tid);
     };
     if (K > 0) fetch(0);
     for (int k0 = 0; k0 < K; k0 += S_BK) {
@@ -183,7 +196,7 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
       for (int j = 0; j < S_B * S_B / 4 / S_NT; ++j) {
         const int v = tid + j * S_NT, r = v / (S_B / 4), c = (v % (S_B / 4)) * 4;
         const int n = n0 + r, m = m0 + c;
-        if (n >= g.N || m >= Mw) continue;
+        if (n >= n_end || m >= Mw) continue;
         f32x4 x = *reinterpret_cast<const f32x4*>(E + r * LDE + c), x2 = x;
         if constexpr (TWO) x2 = *reinterpret_cast<const f32x4*>(E2 + r * LDE + c);
 #pragma unroll
@@ -198,12 +211,13 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
   }
 }
 
-template <class C, int EPI, bool TA, bool TB>
+template <class C, int EPI, bool TA, bool TB, bool EXP = false>
 hipError_t run(const LinArgs& g, hipStream_t st) {
-  const int64_t gx = (epi_width<EPI>(g.M) - g.m_off + C::B - 1) / C::B, gy = (g.N - g.n_off + C::B - 1) / C::B;
+  const int64_t gx = (epi_width<EPI>(g.M) - g.m_off + C::B - 1) / C::B;
+  const int64_t gy = EXP ? (g.N + C::B - 1) / C::B + (g.experts < g.N ? g.experts : g.N) : (g.N - g.n_off + C::B - 1) / C::B;
   if (gx <= 0 || gy <= 0) return hipSuccess;
   const int64_t tiles = gx * gy;
-  hipLaunchKernelGGL((lin_simple_kernel<C, EPI, TA, TB>), dim3((uint32_t)(tiles < kSimpleGrid ? tiles : kSimpleGrid)),
+  hipLaunchKernelGGL((lin_simple_kernel<C, EPI, TA, TB, EXP>), dim3((uint32_t)(tiles < kSimpleGrid ? tiles : kSimpleGrid)),
                      dim3(S_NT), 0, st, g);
   return hipGetLastError();
 }
@@ -217,12 +231,26 @@ hipError_t lin_f32(const LinArgs& g, hipStream_t st) {
   return run<STile<64>, EPI, TA, TB>(g, st);
 }
 
+namespace {
+
+// grouped by expert, by the same rule on the tiles as far as they can be told
+template <int EPI, bool TA>
+hipError_t lin_f32_expert(const LinArgs& g, hipStream_t st) {
+  const int64_t used = g.experts < g.N ? g.experts : g.N, each = (g.N + used - 1) / used;
+  if (((int64_t)g.M + 63) / 64 * used * ((each + 63) / 64) < g_num_cus()) return run<STile<32>, EPI, TA, false, true>(g, st);
+  return run<STile<64>, EPI, TA, false, true>(g, st);
+}
+
+}  // namespace
+
 // Whether the kernel for a few tokens takes a forward product. It reads the tokens once per 16
 // rows of W, past the first-level cache's rate as they grow in number, where the tiles read
 // them once per 64: above 16 tokens it keeps the layers with tiles for a quarter of the chip at
 // most (32 x 14336 -> 4096: 40 us against 47; 32 x 8192 -> 8192: 45 against 30), above 4 also those
 // that fill more than two rounds or less than half of one (16 x 4096 -> 14336: 32 against 22; 16 x
 // 4096 -> 4096: 11 against 17; 4 x 4096 -> 40000: 63 against 87).
+}  // namespace
+
 bool few_tokens(int epi, const LinArgs& g) {
   // (a grid of fewer than 2^32 threads)
   if (g.N > kSkinny || g.M >= (1 << 26)) return false;
@@ -231,17 +259,29 @@ bool few_tokens(int epi, const LinArgs& g) {
   return g.N <= 4 || 2 * tiles <= cus || tiles > 2 * cus;
 }
 
-}  // namespace
-
 #define FORGE_EXTERN_LIN(E, A, B) extern template hipError_t lin_bf16<E, A, B>(const LinArgs&, hipStream_t);
 FORGE_LIN_FORMS(FORGE_EXTERN_LIN)
 #undef FORGE_EXTERN_LIN
 
 hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st) {
-  if (bf16 && (epi == L_LINEAR || epi == L_GATED) && few_tokens(epi, g)) return launch_lin_skinny(epi, g, st);
+  if (bf16 && (epi == L_LINEAR || epi == L_GATED) && few_tokens(epi, g)) return launch_lin_skinny(0, epi, g, st);
 #define FORGE_PICK(E, A, B) \
   if (epi == E && ta == A && tb == B) return bf16 ? lin_bf16<E, A, B>(g, st) : lin_f32<E, A, B>(g, st);
   FORGE_LIN_FORMS(FORGE_PICK)
+#undef FORGE_PICK
+  return hipErrorInvalidValue;
+}
+
+#define FORGE_LIN_EXPERT_FORMS(X) X(L_LINEAR, false) X(L_GATED, false) X(L_DGATE, true) X(L_ACC, true)
+#define FORGE_EXTERN_EXP(E, A) extern template hipError_t lin_expert<E, A, LM_EXPERT>(const LinArgs&, hipStream_t);
+FORGE_LIN_EXPERT_FORMS(FORGE_EXTERN_EXP)
+#undef FORGE_EXTERN_EXP
+
+hipError_t launch_lin_expert(int bf16, int epi, const LinArgs& g, hipStream_t st) {
+  if (bf16 && (epi == L_LINEAR || epi == L_GATED) && few_rows(g)) return launch_lin_skinny(LM_EXPERT, epi, g, st);
+#define FORGE_PICK(E, A) \
+  if (epi == E) return bf16 ? lin_expert<E, A, LM_EXPERT>(g, st) : lin_f32_expert<E, A>(g, st);
+  FORGE_LIN_EXPERT_FORMS(FORGE_PICK)
 #undef FORGE_PICK
   return hipErrorInvalidValue;
 }

@@ -165,6 +165,11 @@ struct LinEpiArgs {
   float* part;          // L_LSE: [blocks of the vocabulary][tokens][2]: maximum, sum of exponentials
   int64_t part_ld;      // tokens
   float* tlogit;        // L_LSE: logit of each token's target
+  // 8-bit operands: factors of the integer sums, one per token, one per output column (sw2: those
+  // of L_GATED's second product)
+  const float* sx;
+  const float* sw;
+  const float* sw2;
 };
 
 constexpr int kMaxSrc = FORGE_MAX_GROUP;
@@ -180,8 +185,102 @@ struct LinArgs {
   // L_ACC with k-slow A, bf16: parts that share a tile's k range, each with float32 sums of its
   // own, N x ldacc apart from e.acc on (acc_write; added by launch_acc_join)
   int32_t splits;
+  // Products grouped by expert: expert x owns rows offsets[x] .. offsets[x + 1] - 1 of the N rows of
+  // B and of the output, and the x-th of the stacked matrices A
+  int32_t experts;
+  const int64_t* offsets;
   LinEpiArgs e;
 };
+
+// One pair of operands of a product.
+inline void set_pair(LinArgs& g, int s, const void* A, int64_t lda, const void* B, int64_t ldb, int64_t K) {
+  g.A[s] = A;
+  g.lda[s] = lda;
+  g.B[s] = B;
+  g.ldb[s] = ldb;
+  g.K[s] = (int32_t)K;
+}
+
+// Forms of a product's kernel.
+enum LinMode {
+  LM_EXPERT = 1,  // grouped by expert
+  LM_Q8 = 2,      // operands of 8-bit integers (LinArgs' K and pitches count pairs of them), bfloat16 output
+};
+
+// The rows of a product's experts, spread over the lanes of a wave (64 experts at a time): lane i
+// holds those of expert base + i. The offsets come from device memory, so they are held to 0 .. N and to
+// ascending order here: no value of theirs leads outside the operands.
+template <int BN>
+struct ExpertRows {
+  const int64_t* off;
+  int experts, rows;  // how many, all rows of the operand
+  int base, r0, r1, upto;  // upto: tiles of BN rows of the experts base .. base + lane
+  __device__ __forceinline__ void load(int first) {
+    const int lane = static_cast<int>(threadIdx.x) & 63, x = first + lane;
+    base = first;
+    const bool in = x < experts;
+    const int64_t a = in ? off[x] : 0, b = in ? off[x + 1] : 0;
+    r0 = (int)(a < 0 ? 0 : a > rows ? rows : a);
+    r1 = (int)(b < r0 ? r0 : b > rows ? rows : b);
+    upto = (r1 - r0 + BN - 1) / BN;
+#pragma unroll
+    for (int h = 1; h < 64; h <<= 1) {
+      const int other = __shfl_up(upto, h);
+      if (lane >= h) upto += other;
+    }
+  }
+  // tiles of rows of all experts; afterwards the first 64 are loaded
+  __device__ __forceinline__ int total() {
+    int n = 0;
+    for (int first = (experts - 1) / 64 * 64; first >= 0; first -= 64) {
+      load(first);
+      n += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return n;
+  }
+  // the expert of row tile q, its first row and its end, its first row tile
+  __device__ __forceinline__ void find(int q, int& x, int& first_row, int& end_row, int& first_tile) {
+    int before = 0;
+    if (base != 0) load(0);
+    while (true) {
+      const int here = __builtin_amdgcn_readlane(upto, 63);
+      if (q < before + here || base + 64 >= experts) break;
+      before += here;
+      load(base + 64);
+    }
+    const uint64_t hit = __ballot(q - before < upto);
+    const int lane = hit ? __builtin_ctzll(hit) : 0;
+    x = base + lane;
+    first_row = __builtin_amdgcn_readlane(r0, lane);
+    end_row = __builtin_amdgcn_readlane(r1, lane);
+    first_tile = before + __builtin_amdgcn_readlane(upto, lane) - (end_row - first_row + BN - 1) / BN;
+  }
+  // the q-th expert that has rows; false: there is none
+  __device__ __forceinline__ bool find_used(int q, int& x, int& first_row, int& end_row) {
+    for (int first = 0; first < experts; first += 64) {
+      load(first);
+      uint64_t used = __ballot(r1 > r0);
+      const int n = __popcll(used);
+      if (q < n) {
+        for (; q > 0; --q) used &= used - 1;
+        const int lane = __builtin_ctzll(used);
+        x = first + lane;
+        first_row = __builtin_amdgcn_readlane(r0, lane);
+        end_row = __builtin_amdgcn_readlane(r1, lane);
+        return true;
+      }
+      q -= n;
+    }
+    return false;
+  }
+};
+
+// the integer sums of 8-bit operands as floats: exact below 2^24, else rounded once (2^-24, where the
+// bfloat16 result is rounded to 2^-8)
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f32x4 int_sums(f32x4 bits) {
+  return __builtin_convertvector(__builtin_bit_cast(i32x4, bits), f32x4);
+}
 
 // the factor of L_ACC / L_DLOGIT
 __device__ __forceinline__ float epi_scale(const LinEpiArgs& e) {
@@ -296,9 +395,20 @@ __host__ __device__ constexpr int epi_width(int M) {
 // Host-side launchers. bf16: operands in bfloat16, else float32. ta / tb: the operand's
 // slow index is k (its rows are k), else k is the fast index.
 hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st);
-// forward products (L_LINEAR, L_GATED) of at most kSkinny tokens, bf16 (launch_lin chooses)
+// products grouped by expert (g.offsets, g.experts); forward products of 8-bit operands, grouped where
+// g.experts > 0
+hipError_t launch_lin_expert(int bf16, int epi, const LinArgs& g, hipStream_t st);
+hipError_t launch_lin_q8(int epi, const LinArgs& g, hipStream_t st);
+// forward products (L_LINEAR, L_GATED) of at most kSkinny tokens, bf16 (launch_lin chooses); mode: LinMode,
+// grouped by expert any number
 constexpr int kSkinny = 32;
-hipError_t launch_lin_skinny(int epi, const LinArgs& g, hipStream_t st);
+hipError_t launch_lin_skinny(int mode, int epi, const LinArgs& g, hipStream_t st);
+// whether a forward product of so few tokens (rows of an expert) is one for launch_lin_skinny
+bool few_tokens(int epi, const LinArgs& g);
+inline bool few_rows(const LinArgs& g) {
+  const int64_t used = g.experts < g.N ? g.experts : g.N;
+  return g.N <= 16 * used && g.M < (1 << 26);  // (a grid of fewer than 2^32 threads)
+}
 // vocabulary entries per partial result that launch_lin(L_LSE) writes for this product
 int lin_lse_block(int bf16, int M, int N);
 
@@ -316,6 +426,35 @@ hipError_t launch_act_backward(int bf16, int act, const void* dY, int64_t lddy, 
 // dG, dU and (if H) H from dH, G, U
 hipError_t launch_gated_backward(int bf16, const void* dH, int64_t lddh, const LinEpiArgs& e, int T, int hid,
                                  hipStream_t st);
+// ---- experts (forge_expert.hip) ----
+// blocks of routes that a plan of n routes takes (one: no workspace), routes of each
+int64_t expert_plan_blocks(int64_t n, int64_t* per);
+// counts: blocks x experts integers of workspace
+hipError_t launch_expert_plan(const int64_t* idx, int64_t n, int experts, int64_t* offsets, int* pos, int* counts,
+                              hipStream_t st);
+// rows of `chunks` 16-byte pieces; places: rows of Y; sx, sy: factors that go along, or NULL
+hipError_t launch_expert_dispatch(const void* X, int64_t ldx_bytes, const int* pos, int k, int64_t T, int64_t places,
+                                  void* Y, int64_t ldy_bytes, int chunks, const float* sx, float* sy, hipStream_t st);
+struct CombineArgs {
+  const void* Yp;  // [places, cols]; may be NULL in the backward pass without dw
+  int64_t ldp, places;
+  const int* pos;  // [tokens, k]
+  const float* w;  // [tokens, k], or NULL for ones
+  int k;
+  const void* R;   // residual or NULL
+  int64_t ldr;
+  void* Y;         // result; in the backward pass its gradient
+  int64_t ldy, tokens;
+  int cols;
+  void* dYp;       // backward: either may be NULL
+  int64_t lddp;
+  float* dw;
+};
+hipError_t launch_expert_combine(int bf16, const CombineArgs& a, hipStream_t st);
+hipError_t launch_expert_combine_backward(int bf16, const CombineArgs& a, hipStream_t st);
+hipError_t launch_quantize_rows(int bf16, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, int64_t rows,
+                                int cols, hipStream_t st);
+
 // joins the partial maxima and sums of nblk vocabulary blocks: lse, the per-token loss, and
 // total = {sum of the losses, tokens counted, mean}; tsum: 2 * lse_join_groups(T) doubles
 int lse_join_groups(int64_t T);

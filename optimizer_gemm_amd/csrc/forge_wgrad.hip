@@ -63,10 +63,11 @@ struct Smem {
 // ---------------------------------------------------------------------------
 // The kernel.
 // ---------------------------------------------------------------------------
-template <class C, int EPI, int OPT>
+// EXP: stacked layers, blockIdx.y counts them: layer x has rows offsets[x] .. offsets[x + 1] - 1 of X and dY.
+template <class C, int EPI, int OPT, bool EXP>
 __global__ __launch_bounds__(C::NT) void wgrad_f32_kernel(const void* __restrict__ Xp, const void* __restrict__ dYp,
                                                           GemmDims d, OptArgs a, float* __restrict__ dW,
-                                                          int64_t ld_dw) {
+                                                          int64_t ld_dw, const int64_t* __restrict__ offsets) {
   using S = Smem<C>;
   __shared__ __attribute__((aligned(16))) char smem[S::BYTES];
 
@@ -79,6 +80,21 @@ __global__ __launch_bounds__(C::NT) void wgrad_f32_kernel(const void* __restrict
   const int wave_m0 = wm * C::TM, wave_n0 = wn * C::TN;
   const int g16 = lane >> 4, l16 = lane & 15;
 
+  if constexpr (EXP) {
+    // held to the operands' rows whatever the offsets are
+    const int64_t t0 = offsets[blockIdx.y], t1 = offsets[blockIdx.y + 1], row = (int64_t)blockIdx.y * d.out;
+    const int r0 = (int)(t0 < 0 ? 0 : t0 > d.T ? d.T : t0), r1 = (int)(t1 < r0 ? r0 : t1 > d.T ? d.T : t1);
+    Xp = static_cast<const float*>(Xp) + (int64_t)r0 * d.ldx;
+    dYp = static_cast<const float*>(dYp) + (int64_t)r0 * d.lddy;
+    d.T = r1 - r0;
+    if constexpr (EPI == EPI_STORE) {
+      dW += row * ld_dw;
+    } else {
+      a.W = static_cast<float*>(a.W) + row * a.ldw;
+      a.m = static_cast<float*>(a.m) + row * a.ldm;
+      a.v = static_cast<float*>(a.v) + row * a.ldv;
+    }
+  }
   const int tiles_o = (d.out + C::BN - 1) / C::BN;
   const int tiles_i = (d.in + C::BM - 1) / C::BM;
   int bo, bi;
@@ -245,28 +261,46 @@ using CfgF32 = TileCfg<64, 64, 16, 2, 2, 2>;  // 8 waves: 2x2 wave tiles of 32x3
 
 template <int EPI, int OPT>
 static hipError_t launch_f32(const void* X, const void* dY, const GemmDims& d, const OptArgs& a, float* dW,
-                             int64_t ld_dw, hipStream_t stream) {
+                             int64_t ld_dw, hipStream_t stream, const int64_t* offsets = nullptr, int experts = 1) {
   using C = CfgF32;
   const int tiles = ((d.out + C::BN - 1) / C::BN) * ((d.in + C::BM - 1) / C::BM);
   if (tiles == 0) return hipSuccess;
-  hipLaunchKernelGGL((wgrad_f32_kernel<C, EPI, OPT>), dim3(tiles), dim3(C::NT), 0, stream, X, dY, d, a, dW, ld_dw);
+  if (offsets)
+    hipLaunchKernelGGL((wgrad_f32_kernel<C, EPI, OPT, true>), dim3(tiles, experts), dim3(C::NT), 0, stream, X, dY, d, a, dW,
+                       ld_dw, offsets);
+  else
+    hipLaunchKernelGGL((wgrad_f32_kernel<C, EPI, OPT, false>), dim3(tiles), dim3(C::NT), 0, stream, X, dY, d, a, dW, ld_dw,
+                       offsets);
   return hipGetLastError();
+}
+
+static hipError_t fused_f32(int opt, const void* X, const void* dY, const GemmDims& d, const OptArgs& a,
+                            hipStream_t stream, const int64_t* offsets = nullptr, int experts = 1) {
+  switch (opt) {
+    case FORGE_ADAMW: return launch_f32<EPI_OPT, FORGE_ADAMW>(X, dY, d, a, nullptr, 0, stream, offsets, experts);
+    case FORGE_SGD: return launch_f32<EPI_OPT, FORGE_SGD>(X, dY, d, a, nullptr, 0, stream, offsets, experts);
+    case FORGE_SGD_MOMENTUM:
+      return launch_f32<EPI_OPT, FORGE_SGD_MOMENTUM>(X, dY, d, a, nullptr, 0, stream, offsets, experts);
+    case FORGE_LION: return launch_f32<EPI_OPT, FORGE_LION>(X, dY, d, a, nullptr, 0, stream, offsets, experts);
+    case FORGE_RMSPROP: return launch_f32<EPI_OPT, FORGE_RMSPROP>(X, dY, d, a, nullptr, 0, stream, offsets, experts);
+    case FORGE_ADAGRAD: return launch_f32<EPI_OPT, FORGE_ADAGRAD>(X, dY, d, a, nullptr, 0, stream, offsets, experts);
+    case FORGE_NADAM: return launch_f32<EPI_OPT, FORGE_NADAM>(X, dY, d, a, nullptr, 0, stream, offsets, experts);
+    case FORGE_RADAM: return launch_f32<EPI_OPT, FORGE_RADAM>(X, dY, d, a, nullptr, 0, stream, offsets, experts);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 hipError_t launch_wgrad_fused(int io_bf16, int state_fmt, int opt, int sr, const void* X, const void* dY,
                               const GemmDims& d, const OptArgs& a, hipStream_t stream) {
   if (io_bf16) return launch_wgrad_fused_bf16(state_fmt, opt, sr, X, dY, d, a, stream);
-  switch (opt) {
-    case FORGE_ADAMW: return launch_f32<EPI_OPT, FORGE_ADAMW>(X, dY, d, a, nullptr, 0, stream);
-    case FORGE_SGD: return launch_f32<EPI_OPT, FORGE_SGD>(X, dY, d, a, nullptr, 0, stream);
-    case FORGE_SGD_MOMENTUM: return launch_f32<EPI_OPT, FORGE_SGD_MOMENTUM>(X, dY, d, a, nullptr, 0, stream);
-    case FORGE_LION: return launch_f32<EPI_OPT, FORGE_LION>(X, dY, d, a, nullptr, 0, stream);
-    case FORGE_RMSPROP: return launch_f32<EPI_OPT, FORGE_RMSPROP>(X, dY, d, a, nullptr, 0, stream);
-    case FORGE_ADAGRAD: return launch_f32<EPI_OPT, FORGE_ADAGRAD>(X, dY, d, a, nullptr, 0, stream);
-    case FORGE_NADAM: return launch_f32<EPI_OPT, FORGE_NADAM>(X, dY, d, a, nullptr, 0, stream);
-    case FORGE_RADAM: return launch_f32<EPI_OPT, FORGE_RADAM>(X, dY, d, a, nullptr, 0, stream);
-    default: return hipErrorInvalidValue;
-  }
+  return fused_f32(opt, X, dY, d, a, stream);
+}
+
+hipError_t launch_wgrad_fused_expert(int io_bf16, int state_fmt, int opt, int sr, const void* X, const void* dY,
+                                     const GemmDims& d, const int64_t* offsets, int experts, const OptArgs& a,
+                                     hipStream_t stream) {
+  if (io_bf16) return launch_wgrad_fused_expert_bf16(state_fmt, opt, sr, X, dY, d, offsets, experts, a, stream);
+  return fused_f32(opt, X, dY, d, a, stream, offsets, experts);
 }
 
 hipError_t launch_wgrad_store(int io_bf16, const void* X, const void* dY, const GemmDims& d, float* dW,
@@ -274,6 +308,13 @@ hipError_t launch_wgrad_store(int io_bf16, const void* X, const void* dY, const 
   if (io_bf16) return launch_wgrad_store_bf16(X, dY, d, dW, ld_dw, stream);
   OptArgs a{};
   return launch_f32<EPI_STORE, FORGE_SGD>(X, dY, d, a, dW, ld_dw, stream);
+}
+
+hipError_t launch_wgrad_store_expert(int io_bf16, const void* X, const void* dY, const GemmDims& d,
+                                     const int64_t* offsets, int experts, float* dW, int64_t ld_dw, hipStream_t stream) {
+  if (io_bf16) return launch_wgrad_store_expert_bf16(X, dY, d, offsets, experts, dW, ld_dw, stream);
+  OptArgs a{};
+  return launch_f32<EPI_STORE, FORGE_SGD>(X, dY, d, a, dW, ld_dw, stream, offsets, experts);
 }
 
 }  // namespace forge

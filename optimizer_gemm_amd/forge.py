@@ -115,6 +115,37 @@ def _load() -> ctypes.CDLL:
                                    [ctypes.c_void_p] * 2 + [ctypes.c_int32, ctypes.c_void_p, P(ForgeTensor),
                                                             ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
                                                             ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_plan_workspace": ([ctypes.c_int64] * 2 + [ctypes.c_int32], ctypes.c_int64),
+        "forge_expert_plan": ([ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32] + [ctypes.c_void_p] * 3 +
+                              [ctypes.c_int64, ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_dispatch": ([P(ForgeTensor), ctypes.c_void_p, ctypes.c_int64, P(ForgeTensor), ctypes.c_void_p],
+                                  ctypes.c_int),
+        "forge_expert_combine": ([P(ForgeTensor), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p] +
+                                 [P(ForgeTensor)] * 2 + [ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_combine_backward": ([P(ForgeTensor)] * 2 + [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                                                  P(ForgeTensor), ctypes.c_void_p, ctypes.c_void_p],
+                                          ctypes.c_int),
+        "forge_expert_linear": ([P(ForgeTensor)] * 2 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32] +
+                                [P(ForgeTensor)] * 2 + [ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_gated": ([P(ForgeTensor)] * 3 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32] +
+                               [P(ForgeTensor)] * 3 + [ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_gated_dgrad": ([P(ForgeTensor)] * 4 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32] +
+                                     [P(ForgeTensor)] * 3 + [ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_dgrad_group": ([ctypes.c_int32] + [P(ForgeTensor)] * 2 +
+                                     [ctypes.c_int32, ctypes.c_void_p, P(ForgeTensor), ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_wgrad": ([P(ForgeTensor)] * 2 + [ctypes.c_int32] + [ctypes.c_void_p] * 2 +
+                               [ctypes.c_int64, ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_wgrad_step": ([P(ForgeTensor)] * 5 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                                            P(ForgeHyper), ctypes.c_int64, ctypes.c_uint64,
+                                                            ctypes.c_void_p], ctypes.c_int),
+        "forge_quantize_rows": ([P(ForgeTensor)] * 2 + [ctypes.c_void_p], ctypes.c_int),
+        "forge_linear_q8": ([P(ForgeTensor)] * 3 + [ctypes.c_int32] + [P(ForgeTensor)] * 2 + [ctypes.c_void_p],
+                            ctypes.c_int),
+        "forge_gated_q8": ([P(ForgeTensor)] * 3 + [ctypes.c_int32, P(ForgeTensor), ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_linear_q8": ([P(ForgeTensor)] * 2 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                                           P(ForgeTensor), ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_gated_q8": ([P(ForgeTensor)] * 3 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                                          P(ForgeTensor), ctypes.c_void_p], ctypes.c_int),
     }
     for name, (argt, rest) in sigs.items():
         fn = getattr(lib, name)
@@ -434,29 +465,23 @@ def wgrad_unfused_noalloc(X, dY, W, m, v, opt="adamw", hyper=None, step=1, seed=
 
 def new_states(W: torch.Tensor, opt: str = "adamw", fmt: str = "f32"):
     """Zero moment slots for `opt` in format f32, bf16, q8 (linear codes) or q8dyn (dynamic
-    codes; pass code="dynamic" to the step): returns (m, v, m_scale, v_scale)."""
+    codes; pass code="dynamic" to the step): returns (m, v, m_scale, v_scale), the moments of W's shape (a layer's
+    [out, in], a stack's [experts, out, in])."""
     use_m, use_v = SLOTS[opt]
-    rows, cols = W.shape
     m = v = ms = vs = None
-    if fmt == "f32":
-        if use_m:
-            m = torch.zeros((rows, cols), dtype=torch.float32, device=W.device)
-        if use_v:
-            v = torch.zeros((rows, cols), dtype=torch.float32, device=W.device)
-    elif fmt == "bf16":
-        if use_m:
-            m = torch.zeros((rows, cols), dtype=torch.bfloat16, device=W.device)
-        if use_v:
-            v = torch.zeros((rows, cols), dtype=torch.bfloat16, device=W.device)
-    elif fmt in ("q8", "q8dyn"):
-        if use_m:
-            m = torch.zeros((rows, cols), dtype=torch.int8, device=W.device)
-            ms = torch.zeros((rows, cols // 64), dtype=torch.float32, device=W.device)
-        if use_v:
-            v = torch.zeros((rows, cols), dtype=torch.uint8, device=W.device)
-            vs = torch.zeros((rows, cols // 64), dtype=torch.float32, device=W.device)
-    else:
+    if fmt not in ("f32", "bf16", "q8", "q8dyn"):
         raise ValueError(fmt)
+    q8 = fmt in ("q8", "q8dyn")
+
+    def zeros(dtype, shape):
+        return torch.zeros(shape, dtype=dtype, device=W.device)
+
+    blocks = (*W.shape[:-1], W.shape[-1] // 64)
+    dtype = torch.bfloat16 if fmt == "bf16" else torch.float32
+    if use_m:
+        m, ms = zeros(torch.int8 if q8 else dtype, W.shape), zeros(torch.float32, blocks) if q8 else None
+    if use_v:
+        v, vs = zeros(torch.uint8 if q8 else dtype, W.shape), zeros(torch.float32, blocks) if q8 else None
     return m, v, ms, vs
 
 
@@ -773,3 +798,319 @@ def linear_cross_entropy_step(X: torch.Tensor, W: torch.Tensor, m: Optional[torc
                                            _ten(dX), int(piece), _ptr(ws), need, on.stream),
                "forge_linear_xent_step")
     return dX
+
+
+# ---------------------------------------------------------------------------
+# layers of experts
+# ---------------------------------------------------------------------------
+MAX_EXPERTS = 1024
+
+
+def _stack(W: Optional[torch.Tensor]):
+    """_ten() of stacked matrices [experts, out, in] as one tensor of experts * out rows"""
+    if W is None:
+        return None
+    if W.dim() != 3:
+        raise ValueError("stacked matrices [experts, out, in] wanted")
+    e, rows, cols = W.shape
+    dt = _DT.get(W.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {W.dtype}")
+    if W.numel() == 0:
+        return ForgeTensor(None, dt, 0, e * rows, cols, cols)
+    s0, s1, s2 = W.stride()
+    if s2 != 1 and cols > 1:
+        raise ValueError("rows must be contiguous (stride(2) == 1)")
+    ld = s1 if rows > 1 else (s0 if e > 1 else cols)
+    if e > 1 and s0 != rows * ld:
+        raise ValueError("the rows of a stack follow one another in one pitch (stride(0) == out * stride(1))")
+    return ForgeTensor(W.data_ptr(), dt, 0, e * rows, cols, ld)
+
+
+def _experts(W: torch.Tensor, offsets: torch.Tensor, *others) -> int:
+    e = W.shape[0]
+    if W.dim() != 3 or any(w.dim() != 3 or w.shape[0] != e for w in others):
+        raise ValueError("stacked matrices [experts, out, in] of the same experts wanted")
+    _vec(offsets, e + 1, torch.int64, "offsets")
+    return e
+
+
+def _places(pos: torch.Tensor) -> int:
+    if pos.dim() != 2 or pos.dtype != torch.int32 or not pos.is_contiguous():
+        raise ValueError("pos: a contiguous [T, k] int32 tensor, as expert_plan returned it, wanted")
+    if pos.shape[1] < 1:
+        raise ValueError("a token has one route at least")
+    return pos.shape[1]
+
+
+def _factors(weights: Optional[torch.Tensor], pos: torch.Tensor) -> None:
+    if weights is not None and (weights.shape != pos.shape or weights.dtype != torch.float32 or not weights.is_contiguous()):
+        raise ValueError("weights: a contiguous float32 tensor of pos's shape wanted")
+
+
+def expert_plan(idx: torch.Tensor, experts: int, stream=None):
+    """The routes of a router ordered by expert (forge_expert_plan): idx [T, k] int64, the experts of each
+    token; a value outside [0, experts) drops the route. Returns (offsets, pos): expert x owns rows
+    offsets[x] .. offsets[x + 1] - 1 (int64, experts + 1 of them), pos [T, k] int32 is each route's row, -1
+    for a dropped one. Routes of an expert keep the tokens' order. Both stay on the device: no call waits for them."""
+    if idx.dim() != 2 or idx.dtype != torch.int64 or not idx.is_contiguous():
+        raise ValueError("idx: a contiguous [T, k] int64 tensor wanted")
+    if idx.shape[1] < 1:
+        raise ValueError("a token has one route at least")
+    if not 1 <= experts <= MAX_EXPERTS:
+        raise ValueError(f"1..{MAX_EXPERTS} experts")
+    with _On(stream, idx) as on:
+        T, k = idx.shape
+        offsets, pos = on.empty((experts + 1,), torch.int64), on.empty((T, k), torch.int32)
+        need = _lib.forge_expert_plan_workspace(T, k, experts)
+        ws = on.empty((need,), torch.uint8) if need else None
+        _check(_lib.forge_expert_plan(_ptr(idx), T, k, experts, offsets.data_ptr(), _ptr(pos), _ptr(ws), need, on.stream),
+               "forge_expert_plan")
+    return offsets, pos
+
+
+def expert_dispatch(X: torch.Tensor, pos: torch.Tensor, scale: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, stream=None):
+    """Rows to their experts, Xp[pos[t, j]] = X[t] (forge_expert_dispatch): X [T, cols] float32, bfloat16, or
+    int8 with its rows' factors `scale` (T float32), which go along: returns Xp [T * k, cols], with them
+    (Xp, factors). Rows that no route has (those of dropped ones, at the end) are not written. Its gradient is
+    expert_combine(dXp, pos)."""
+    k = _places(pos)
+    if (X.dtype == torch.int8) != (scale is not None):
+        raise ValueError("int8 rows come with their factors, others without")
+    with _On(stream, X, pos, scale, out) as on:
+        if X.shape[0] != pos.shape[0]:
+            raise ValueError("pos has the routes of another number of tokens")
+        Xp = _same(on, out, (pos.numel(), X.shape[1]), X.dtype)
+        x, y, sp = _ten(X), _ten(Xp), None
+        if scale is not None:
+            _vec(scale, X.shape[0], torch.float32, "scale")
+            sp = on.empty((Xp.shape[0],), torch.float32)
+            x.scale, y.scale = _ptr(scale), _ptr(sp)
+        _check(_lib.forge_expert_dispatch(x, _ptr(pos), k, y, on.stream), "forge_expert_dispatch")
+    return Xp if scale is None else (Xp, sp)
+
+
+def expert_combine(Yp: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The experts' results back to their tokens, Y[t] = sum_j weights[t, j] Yp[pos[t, j]] + residual[t], dropped
+    routes left out (forge_expert_combine); weights float32 or None for ones."""
+    k = _places(pos)
+    _factors(weights, pos)
+    with _On(stream, Yp, pos, weights, residual, out) as on:
+        Y = _same(on, out, (pos.shape[0], Yp.shape[1]), Yp.dtype)
+        if Y.shape[0] != pos.shape[0]:
+            raise ValueError("pos has the routes of another number of tokens")
+        _check(_lib.forge_expert_combine(_ten(Yp), _ptr(pos), k, _ptr(weights), _ten(residual), _ten(Y), on.stream),
+               "forge_expert_combine")
+    return Y
+
+
+def expert_combine_backward(dY: torch.Tensor, Yp: Optional[torch.Tensor], pos: torch.Tensor,
+                            weights: Optional[torch.Tensor] = None, want_dweights: bool = True, stream=None):
+    """Backward of expert_combine (forge_expert_combine_backward): (dYp, dweights), dYp[pos[t, j]] = weights[t, j]
+    dY[t] (rows that no route has are not written), dweights[t, j] = <dY[t], Yp[pos[t, j]]> in float32 (0 for a
+    dropped route; None with want_dweights=False, where Yp may be None)."""
+    k = _places(pos)
+    _factors(weights, pos)
+    if want_dweights and Yp is None:
+        raise ValueError("the weights' gradient needs Yp")
+    with _On(stream, dY, Yp, pos, weights) as on:
+        if dY.shape[0] != pos.shape[0]:
+            raise ValueError("pos has the routes of another number of tokens")
+        rows = pos.numel() if Yp is None else Yp.shape[0]
+        dYp = on.empty((rows, dY.shape[1]), dY.dtype)
+        dw = on.empty(pos.shape, torch.float32) if want_dweights else None
+        _check(_lib.forge_expert_combine_backward(_ten(dY), _ten(Yp) if want_dweights else None, _ptr(pos), k, _ptr(weights),
+                                                  _ten(dYp), _ptr(dw), on.stream), "forge_expert_combine_backward")
+    return dYp, dw
+
+
+def expert_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, act: str = "none", save: bool = False,
+                  out: Optional[torch.Tensor] = None, stream=None):
+    """Y[r] = act(X[r] W[x]^T) for the rows r of each expert x (forge_expert_linear): X [R, in] in expert_plan's
+    order, W [experts, out, in], offsets as expert_plan returned them. Rows behind offsets[-1] are
+    neither read nor written. With save=True returns (Y, Z), Z the pre-activation."""
+    a = _act(act)
+    with _On(stream, X, W, offsets, out) as on:
+        e = _experts(W, offsets)
+        shape = (X.shape[0], W.shape[1])
+        Y = _same(on, out, shape, W.dtype)
+        Z = on.empty(shape, W.dtype) if save else None
+        _check(_lib.forge_expert_linear(_ten(X), _stack(W), e, offsets.data_ptr(), a, _ten(Y), _ten(Z), on.stream),
+               "forge_expert_linear")
+    return (Y, Z) if save else Y
+
+
+def expert_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, offsets: torch.Tensor, act: str = "silu",
+                 save: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """gated() with each row's expert's matrices (forge_expert_gated): Wg, Wu [experts, hidden, in], rows and
+    offsets as in expert_linear. With save=True returns (H, G, U)."""
+    a = _act(act)
+    with _On(stream, X, Wg, Wu, offsets, out) as on:
+        e = _experts(Wg, offsets, Wu)
+        shape = (X.shape[0], Wg.shape[1])
+        H = _same(on, out, shape, Wg.dtype)
+        G, U = (on.empty(shape, Wg.dtype), on.empty(shape, Wg.dtype)) if save else (None, None)
+        _check(_lib.forge_expert_gated(_ten(X), _stack(Wg), _stack(Wu), e, offsets.data_ptr(), a, _ten(H), _ten(G), _ten(U),
+                                       on.stream), "forge_expert_gated")
+    return (H, G, U) if save else H
+
+
+def expert_gated_dgrad(dY: torch.Tensor, Wd: torch.Tensor, G: torch.Tensor, U: torch.Tensor, offsets: torch.Tensor,
+                       act: str = "silu", want_h: bool = True, stream=None):
+    """gated_dgrad() with each row's expert's matrix (forge_expert_gated_dgrad): Wd [experts, out, hidden];
+    (dG, dU, H)."""
+    a = _act(act)
+    with _On(stream, dY, Wd, G, U, offsets) as on:
+        e = _experts(Wd, offsets)
+        shape = (dY.shape[0], Wd.shape[2])
+        dG, dU = on.empty(shape, Wd.dtype), on.empty(shape, Wd.dtype)
+        H = on.empty(shape, Wd.dtype) if want_h else None
+        _check(_lib.forge_expert_gated_dgrad(_ten(dY), _stack(Wd), _ten(G), _ten(U), e, offsets.data_ptr(), a, _ten(dG),
+                                             _ten(dU), _ten(H), on.stream), "forge_expert_gated_dgrad")
+    return dG, dU, H
+
+
+def expert_dgrad_group(dYs, Ws, offsets: torch.Tensor, dX: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dX[r] = sum_l dYs[l][r] Ws[l][x] for the rows r of each expert x (forge_expert_dgrad_group): Ws[l]
+    [experts, out_l, in]; from the weights as they are now, before their step."""
+    n = len(Ws)
+    if len(dYs) != n or not 1 <= n <= MAX_GROUP:
+        raise ValueError(f"a group holds 1..{MAX_GROUP} layers, each with its dY and W")
+    with _On(stream, *dYs, *Ws, offsets, dX) as on:
+        e = _experts(Ws[0], offsets, *Ws[1:])
+        dX = _same(on, dX, (dYs[0].shape[0], Ws[0].shape[2]), Ws[0].dtype)
+        dy_a, w_a = (ForgeTensor * n)(*[_ten(t) for t in dYs]), (ForgeTensor * n)(*[_stack(t) for t in Ws])
+        _check(_lib.forge_expert_dgrad_group(n, dy_a, w_a, e, offsets.data_ptr(), _ten(dX), on.stream),
+               "forge_expert_dgrad_group")
+    return dX
+
+
+def expert_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor, dW: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """The stack's gradient dW[x] = dY^T X over each expert's rows, float32 [experts, out, in]
+    (forge_expert_wgrad): the two-phase schedule's first half (optimizer_step on the stack as one
+    [experts * out, in] layer is its second)."""
+    with _On(stream, X, dY, offsets, dW) as on:
+        e = offsets.numel() - 1
+        _vec(offsets, e + 1, torch.int64, "offsets")
+        dW = _same(on, dW, (e, dY.shape[1], X.shape[1]), torch.float32)
+        t = _stack(dW)
+        if t.dtype != F32 or tuple(dW.shape) != (e, dY.shape[1], X.shape[1]):
+            raise ValueError("dW: float32 [experts, out, in] wanted")
+        _check(_lib.forge_expert_wgrad(_ten(X), _ten(dY), e, offsets.data_ptr(), t.data, t.ld, on.stream),
+               "forge_expert_wgrad")
+    return dW
+
+
+def expert_wgrad_step(X: torch.Tensor, dY: torch.Tensor, W: torch.Tensor, m: Optional[torch.Tensor],
+                      v: Optional[torch.Tensor], offsets: torch.Tensor, opt: str = "adamw", hyper=None, step: int = 1,
+                      seed: int = 0, m_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                      code: str = "linear", stream=None) -> None:
+    """wgrad_step() of every expert of a stack in one launch (forge_expert_wgrad_step): X [R, in], dY [R, out] in
+    expert_plan's order, W [experts, out, in]; m and v of W's shape, block scales
+    [experts, out, in / 64], as new_states(W) makes them. The step is that of the stack as one [experts * out, in] layer:
+    same element indices and random streams. Experts without rows step on a gradient of zero."""
+    h = _hyper(opt, hyper)
+    with _On(stream, X, dY, W, m, v, offsets, m_scale, v_scale) as on:
+        e = _experts(W, offsets)
+
+        def state(t, scale):
+            if t is None:
+                return None
+            if tuple(t.shape) != tuple(W.shape):
+                raise ValueError("moments have the weights' shape")
+            d = _stack(t)
+            if scale is not None:
+                if scale.dtype != torch.float32 or not scale.is_contiguous() or \
+                        tuple(scale.shape) != (e, W.shape[1], W.shape[2] // 64):
+                    raise ValueError("block scale shape must be [experts, out, in / 64]")
+                d.scale = _ptr(scale)
+            if code not in ("linear", "dynamic"):
+                raise ValueError(f"unknown moment code {code!r}")
+            if code == "dynamic" and d.dtype in (I8, U8):
+                d.dtype = I8_DYN if d.dtype == I8 else U8_DYN
+            return _ref(d)
+
+        _check(_lib.forge_expert_wgrad_step(_ten(X), _ten(dY), _stack(W), state(m, m_scale), state(v, v_scale), e,
+                                            offsets.data_ptr(), OPT_ID[opt], ctypes.byref(h), int(step),
+                                            seed & (2 ** 64 - 1), on.stream), "forge_expert_wgrad_step")
+
+
+# ---------------------------------------------------------------------------
+# products of 8-bit integers
+# ---------------------------------------------------------------------------
+def _codes(t: torch.Tensor, scale: torch.Tensor, what: str):
+    """_ten() or _stack() of int8 rows with a factor each"""
+    if t.dtype != torch.int8:
+        raise ValueError(f"{what}: int8 codes wanted")
+    d = _ten(t) if t.dim() == 2 else _stack(t)
+    _vec(scale, d.rows, torch.float32, f"factors of {what}")
+    d.scale = _ptr(scale)
+    return d
+
+
+def quantize_rows(X: torch.Tensor, stream=None):
+    """Rows to 8 bits (forge_quantize_rows): X [rows, cols] float32 or bfloat16, cols a multiple of 16; returns (Q, scale),
+    int8 codes and one float32 factor per row, scale = max |x| / 127 and Q = x / scale to the nearest. A
+    row of zeros has scale 0; one with an infinity or NaN has scale NaN, and so NaN for its products. Weights
+    are quantised the same way, one factor per output channel: a stack [experts, out, in] as its rows
+    W.reshape(-1, in)."""
+    with _On(stream, X) as on:
+        Q, scale = on.empty(X.shape, torch.int8), on.empty((X.shape[0],), torch.float32)
+        q = _ten(Q)
+        q.scale = _ptr(scale)
+        _check(_lib.forge_quantize_rows(_ten(X), q, on.stream), "forge_quantize_rows")
+    return Q, scale
+
+
+def linear_q8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
+              bias: Optional[torch.Tensor] = None, act: str = "none", residual: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """linear() of 8-bit integers (forge_linear_q8): X [T, in] and W [out, in] int8 with a factor for each row (token,
+    output channel), as quantize_rows makes them; the sums are exact, the epilogue float32, Y bfloat16."""
+    a = _act(act)
+    with _On(stream, X, x_scale, W, w_scale, bias, residual, out) as on:
+        Y = _same(on, out, (X.shape[0], W.shape[0]), torch.bfloat16)
+        _check(_lib.forge_linear_q8(_codes(X, x_scale, "X"), _codes(W, w_scale, "W"), _row(bias), a, _ten(residual), _ten(Y),
+                                    on.stream), "forge_linear_q8")
+    return Y
+
+
+def gated_q8(X: torch.Tensor, x_scale: torch.Tensor, Wg: torch.Tensor, wg_scale: torch.Tensor, Wu: torch.Tensor,
+             wu_scale: torch.Tensor, act: str = "silu", out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """gated() of 8-bit integers (forge_gated_q8), operands as in linear_q8; H bfloat16."""
+    a = _act(act)
+    with _On(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, out) as on:
+        H = _same(on, out, (X.shape[0], Wg.shape[0]), torch.bfloat16)
+        _check(_lib.forge_gated_q8(_codes(X, x_scale, "X"), _codes(Wg, wg_scale, "Wg"), _codes(Wu, wu_scale, "Wu"), a, _ten(H),
+                                   on.stream), "forge_gated_q8")
+    return H
+
+
+def expert_linear_q8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
+                     offsets: torch.Tensor, act: str = "none", out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """expert_linear() of 8-bit integers (forge_expert_linear_q8): W [experts, out, in] int8 with experts * out
+    factors, X and its factors as expert_dispatch(Q, pos, scale) returned them; Y bfloat16."""
+    a = _act(act)
+    with _On(stream, X, x_scale, W, w_scale, offsets, out) as on:
+        e = _experts(W, offsets)
+        Y = _same(on, out, (X.shape[0], W.shape[1]), torch.bfloat16)
+        _check(_lib.forge_expert_linear_q8(_codes(X, x_scale, "X"), _codes(W, w_scale, "W"), e, offsets.data_ptr(), a, _ten(Y),
+                                           on.stream), "forge_expert_linear_q8")
+    return Y
+
+
+def expert_gated_q8(X: torch.Tensor, x_scale: torch.Tensor, Wg: torch.Tensor, wg_scale: torch.Tensor, Wu: torch.Tensor,
+                    wu_scale: torch.Tensor, offsets: torch.Tensor, act: str = "silu", out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """expert_gated() of 8-bit integers (forge_expert_gated_q8), operands as in expert_linear_q8; H bfloat16."""
+    a = _act(act)
+    with _On(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, offsets, out) as on:
+        e = _experts(Wg, offsets, Wu)
+        H = _same(on, out, (X.shape[0], Wg.shape[1]), torch.bfloat16)
+        _check(_lib.forge_expert_gated_q8(_codes(X, x_scale, "X"), _codes(Wg, wg_scale, "Wg"), _codes(Wu, wu_scale, "Wu"), e,
+                                          offsets.data_ptr(), a, _ten(H), on.stream), "forge_expert_gated_q8")
+    return H

@@ -1,0 +1,241 @@
+"""Host checks of the layers of experts and of the 8-bit products, on the CPU: every refusal the C ABI documents is
+returned before anything is enqueued (the descriptors hold made-up addresses), workspace sizes, and the Python layer's own
+argument checks."""
+import ctypes
+
+import pytest
+import torch
+
+import optimizer_gemm_amd as forge
+from optimizer_gemm_amd.forge import BF16, E4M3, F32, I8, ForgeTensor, make_hyper
+
+NULL, SHAPE, DTYPE, ALIGN, UNSUP, HYPER, ALIAS, SCRATCH = -1, -2, -3, -4, -5, -6, -8, -9
+L = forge.lib()
+BASE = 1 << 40
+OFF = BASE + (40 << 34)
+
+
+def ten(k, rows, cols, dt=BF16, ld=None, off=0, scale=None):
+    """descriptor number k, far from the others'"""
+    return ForgeTensor(BASE + (k << 34) + off, dt, 0, rows, cols, cols if ld is None else ld, scale)
+
+
+def q8(k, rows, cols, ld=None, scale=True, off=0):
+    return ten(k, rows, cols, I8, ld, off, BASE + (k << 34) + (1 << 33) if scale is True else scale)
+
+
+def ref(t):
+    return ctypes.byref(t) if t is not None else None
+
+
+def test_plan_refusals():
+    idx, offs, pos, ws = BASE, BASE + (1 << 34), BASE + (2 << 34), BASE + (3 << 34)
+    need = L.forge_expert_plan_workspace(5000, 2, 16)
+    assert need == 10 * 16 * 4 and L.forge_expert_plan_workspace(512, 2, 16) == 0
+    assert L.forge_expert_plan_workspace(0, 2, 16) == 0 and L.forge_expert_plan_workspace(5000, 2, 0) == 0
+    assert L.forge_expert_plan_workspace(1 << 20, 8, 1024) <= 512 * 1024 * 4  # the blocks grow, not their number
+
+    def call(idx=idx, T=5000, k=2, e=16, offs=offs, pos=pos, ws=ws, n=need):
+        return L.forge_expert_plan(idx, T, k, e, offs, pos, ws, n, None)
+
+    assert call(e=0) == SHAPE and call(e=1025) == SHAPE and call(T=-1) == SHAPE and call(k=0) == SHAPE
+    assert call(idx=None) == NULL and call(offs=None) == NULL and call(pos=None) == NULL and call(ws=None) == NULL
+    assert call(idx=idx + 4) == ALIGN and call(offs=offs + 4) == ALIGN and call(pos=pos + 2) == ALIGN and call(ws=ws + 8) == ALIGN
+    assert call(n=need - 1) == SCRATCH
+    assert call(T=1 << 30) == UNSUP and call(T=1 << 25, k=32) == UNSUP and call(T=1 << 29, k=1 << 29) == UNSUP
+    assert call(pos=idx + 8) == ALIAS and call(offs=idx) == ALIAS and call(ws=pos) == ALIAS
+
+
+def test_dispatch_refusals():
+    def call(X=None, pos=BASE + (9 << 34), k=2, Y=None):
+        return L.forge_expert_dispatch(ref(X or ten(0, 16, 64)), pos, k, ref(Y or ten(1, 32, 64)), None)
+
+    assert L.forge_expert_dispatch(None, BASE, 2, ref(ten(1, 32, 64)), None) == NULL
+    assert call(pos=None) == NULL and call(pos=BASE + 2) == ALIGN and call(k=0) == SHAPE
+    assert call(Y=ten(1, 32, 72)) == SHAPE and call(Y=ten(1, 32, 64, F32)) == DTYPE and call(X=ten(0, 16, 64, E4M3)) == UNSUP
+    assert call(X=ten(0, 16, 60)) == ALIGN and call(X=ten(0, 16, 64, 3)) == DTYPE
+    assert call(Y=ten(0, 32, 64, off=64)) == ALIAS and call(pos=BASE + (1 << 34)) == ALIAS
+    assert call(X=ten(0, 1 << 26, 8), Y=ten(1, 16, 8)) == UNSUP
+    assert call(X=q8(0, 16, 64)) == DTYPE
+    assert call(X=q8(0, 16, 64), Y=q8(1, 32, 64, scale=None)) == NULL
+    assert call(X=q8(0, 16, 72), Y=q8(1, 32, 72)) == ALIGN
+    assert call(X=q8(0, 16, 64), Y=q8(1, 32, 64, scale=BASE + (1 << 33))) == ALIAS
+
+
+def test_combine_refusals():
+    P, W = BASE + (9 << 34), BASE + (10 << 34)
+
+    def call(Yp=None, pos=P, k=2, w=W, R=None, Y=None):
+        return L.forge_expert_combine(ref(Yp or ten(0, 32, 64)), pos, k, w, ref(R), ref(Y or ten(1, 16, 64)), None)
+
+    assert call(pos=None) == NULL and call(pos=P + 1) == ALIGN and call(w=W + 2) == ALIGN and call(k=0) == SHAPE
+    assert call(Yp=ten(0, 32, 72)) == SHAPE and call(R=ten(2, 16, 72)) == SHAPE and call(R=ten(2, 15, 64)) == SHAPE
+    assert call(Yp=ten(0, 32, 64, F32)) == DTYPE and call(R=ten(2, 16, 64, F32)) == DTYPE
+    assert call(Y=ten(0, 16, 64)) == ALIAS and call(R=ten(1, 16, 64)) == ALIAS and call(w=BASE + (1 << 34)) == ALIAS
+
+    def back(dY=None, Yp=0, pos=P, k=2, w=W, dYp=0, dw=BASE + (11 << 34)):
+        Yp = ten(0, 32, 64) if Yp == 0 else Yp
+        dYp = ten(3, 32, 64) if dYp == 0 else dYp
+        return L.forge_expert_combine_backward(ref(dY or ten(1, 16, 64)), ref(Yp), pos, k, w, ref(dYp), dw, None)
+
+    assert back(Yp=None) == NULL and back(pos=None) == NULL
+    assert back(dYp=ten(3, 31, 64)) == SHAPE and back(dYp=ten(3, 32, 72)) == SHAPE
+    assert back(dw=BASE + (11 << 34) + 2) == ALIGN and back(dYp=ten(3, 32, 64, F32)) == DTYPE
+    assert back(dYp=ten(1, 32, 64)) == ALIAS and back(dw=W) == ALIAS and back(dw=BASE + (3 << 34)) == ALIAS
+
+
+def test_product_refusals():
+    def lin(X=None, W=None, e=4, off=OFF, act=0, Y=None, Z=None):
+        return L.forge_expert_linear(ref(X or ten(0, 16, 64)), ref(W or ten(1, 128, 64)), e, off, act,
+                                     ref(Y or ten(2, 16, 32)), ref(Z), None)
+
+    assert lin(e=0) == SHAPE and lin(e=1025) == SHAPE and lin(e=3) == SHAPE and lin(off=None) == NULL
+    assert lin(off=OFF + 4) == ALIGN and lin(act=5) == UNSUP and lin(X=ten(0, 16, 72)) == SHAPE
+    assert lin(X=ten(0, 16, 64, F32)) == DTYPE and lin(X=ten(0, 16, 64, E4M3), W=ten(1, 128, 64, E4M3)) == UNSUP
+    assert lin(Y=ten(2, 16, 40)) == SHAPE and lin(Y=ten(2, 15, 32)) == SHAPE and lin(Z=ten(3, 16, 40)) == SHAPE
+    assert lin(Y=ten(0, 16, 32)) == ALIAS and lin(Z=ten(2, 16, 32)) == ALIAS
+    assert lin(off=BASE + (2 << 34)) == ALIAS
+    # one expert's part past 2^31 bytes is refused, the whole stack's is not (here: refused for its alignment only)
+    assert lin(X=ten(0, 16, 65536), W=ten(1, 4 * 16384, 65536)) == UNSUP
+    assert lin(X=ten(0, 1 << 24, 64), Y=ten(2, 1 << 24, 32)) == UNSUP
+    assert lin(W=ten(1, 144, 64), Y=ten(2, 16, 36)) == ALIGN
+
+    def gat(Wu=None, G=None, U=None, H=None, e=4, off=OFF):
+        return L.forge_expert_gated(ref(ten(0, 16, 64)), ref(ten(1, 128, 64)), ref(Wu or ten(2, 128, 64)), e, off, 2,
+                                    ref(H or ten(3, 16, 32)), ref(G), ref(U), None)
+
+    assert gat(G=ten(4, 16, 32)) == NULL and gat(Wu=ten(2, 132, 64)) == SHAPE and gat(Wu=ten(2, 128, 56)) == SHAPE
+    assert gat(e=5) == SHAPE and gat(off=None) == NULL and gat(H=ten(1, 16, 32)) == ALIAS
+    assert gat(G=ten(4, 16, 32), U=ten(4, 16, 32)) == ALIAS
+
+    def gd(dY=None, Wd=None, G=None, dG=None, H=None, e=4, off=OFF):
+        return L.forge_expert_gated_dgrad(ref(dY or ten(0, 16, 64)), ref(Wd or ten(1, 256, 32)), ref(G or ten(2, 16, 32)),
+                                          ref(ten(3, 16, 32)), e, off, 2, ref(dG or ten(4, 16, 32)), ref(ten(5, 16, 32)), ref(H),
+                                          None)
+
+    assert gd(dY=ten(0, 16, 72)) == SHAPE and gd(G=ten(2, 16, 40)) == SHAPE and gd(e=0) == SHAPE and gd(off=None) == NULL
+    assert gd(dG=ten(2, 16, 32)) == ALIAS and gd(H=ten(5, 16, 32)) == ALIAS and gd(Wd=ten(1, 256, 32, F32)) == DTYPE
+
+    def dg(n=2, e=4, off=OFF, dX=None, W1=None):
+        dy = (ForgeTensor * 2)(ten(0, 16, 32), ten(1, 16, 40))
+        w = (ForgeTensor * 2)(ten(2, 128, 64), W1 or ten(3, 160, 64))
+        return L.forge_expert_dgrad_group(n, dy, w, e, off, ref(dX or ten(4, 16, 64)), None)
+
+    assert dg(n=0) == SHAPE and dg(n=5) == SHAPE and dg(e=3) == SHAPE and dg(off=None) == NULL
+    assert dg(W1=ten(3, 160, 72)) == SHAPE and dg(dX=ten(4, 16, 72)) == SHAPE and dg(dX=ten(1, 16, 64)) == ALIAS
+
+
+def test_step_refusals():
+    h = make_hyper("adamw")
+
+    def step(X=None, dY=None, W=None, m=None, v=None, e=4, off=OFF, opt=0, h=h, t=1):
+        return L.forge_expert_wgrad_step(ref(X or ten(0, 16, 64)), ref(dY or ten(1, 16, 32)), ref(W or ten(2, 128, 64)),
+                                         ref(m or ten(3, 128, 64, F32)), ref(v or ten(4, 128, 64, F32)), e, off, opt, ref(h), t,
+                                         1, None)
+
+    assert step(t=0) == HYPER and step(opt=8) == HYPER and step(e=0) == SHAPE and step(e=3) == SHAPE and step(off=None) == NULL
+    assert step(X=ten(0, 15, 64)) == SHAPE and step(dY=ten(1, 16, 40)) == SHAPE and step(W=ten(2, 128, 72)) == SHAPE
+    assert step(X=ten(0, 16, 64, E4M3)) == UNSUP and step(X=ten(0, 16, 64, F32)) == DTYPE and step(m=ten(3, 120, 64, F32)) == SHAPE
+    assert step(m=ten(3, 128, 64, BF16)) == DTYPE                   # m and v in two formats
+    assert step(m=ten(3, 128, 64, I8), v=ten(4, 128, 64, 3)) == NULL  # codes without scales
+    assert step(v=ten(3, 128, 64, F32)) == ALIAS and step(m=ten(0, 128, 64, F32)) == ALIAS
+    assert step(X=ten(0, 16, 8192), dY=ten(1, 16, 131072), W=ten(2, 4 * 131072, 8192), m=ten(3, 4 * 131072, 8192, F32),
+                v=ten(4, 4 * 131072, 8192, F32)) == UNSUP           # 2^32 weights
+    assert step(X=ten(0, 16, 8192), dY=ten(1, 16, 65536), W=ten(2, 4 * 65536, 8192), m=ten(3, 4 * 65536, 8192, F32),
+                v=ten(4, 4 * 65536, 8192, F32)) == UNSUP            # an expert's moments past 2^31 bytes
+
+    def wg(X=None, dY=None, e=4, off=OFF, dW=BASE + (5 << 34), ld=64):
+        return L.forge_expert_wgrad(ref(X or ten(0, 16, 64)), ref(dY or ten(1, 16, 32)), e, off, dW, ld, None)
+
+    assert wg(dW=None) == NULL and wg(off=None) == NULL and wg(e=0) == SHAPE and wg(ld=60) == SHAPE and wg(ld=66) == ALIGN
+    assert wg(dW=BASE + 8) == ALIGN and wg(X=ten(0, 16, 64, E4M3)) == UNSUP and wg(dY=ten(1, 17, 32)) == SHAPE
+    assert wg(dW=BASE) == ALIAS
+
+
+def test_q8_refusals():
+    def quant(X=None, Q=None):
+        return L.forge_quantize_rows(ref(X or ten(0, 16, 64)), ref(Q or q8(1, 16, 64)), None)
+
+    assert quant(X=ten(0, 16, 64, I8)) == DTYPE and quant(X=ten(0, 16, 64, E4M3)) == UNSUP and quant(Q=ten(1, 16, 64)) == DTYPE
+    assert quant(Q=q8(1, 16, 64, scale=None)) == NULL and quant(Q=q8(1, 15, 64)) == SHAPE
+    assert quant(X=ten(0, 16, 72), Q=q8(1, 16, 72)) == ALIGN and quant(Q=q8(1, 16, 64, ld=72)) == ALIGN
+    assert quant(Q=q8(1, 16, 64, scale=BASE)) == ALIAS and quant(Q=q8(0, 16, 64)) == ALIAS
+    assert quant(X=ten(0, 1 << 26, 16), Q=q8(1, 1 << 26, 16)) == UNSUP
+
+    def lin(X=None, W=None, b=None, act=0, R=None, Y=None):
+        return L.forge_linear_q8(ref(X or q8(0, 16, 64)), ref(W or q8(1, 32, 64)), ref(b), act, ref(R), ref(Y or ten(2, 16, 32)),
+                                 None)
+
+    assert lin(act=5) == UNSUP and lin(X=ten(0, 16, 64)) == DTYPE and lin(W=ten(1, 32, 64)) == DTYPE
+    assert lin(X=q8(0, 16, 64, scale=None)) == NULL and lin(W=q8(1, 32, 64, scale=BASE + 4)) == ALIGN
+    assert lin(X=q8(0, 16, 80)) == SHAPE and lin(Y=ten(2, 16, 40)) == SHAPE and lin(Y=ten(2, 16, 32, F32)) == DTYPE
+    assert lin(X=q8(0, 16, 72), W=q8(1, 32, 72)) == ALIGN and lin(W=q8(1, 36, 64), Y=ten(2, 16, 36)) == ALIGN
+    assert lin(b=ten(3, 1, 40)) == SHAPE and lin(R=ten(3, 16, 32, F32)) == DTYPE and lin(R=ten(2, 16, 32)) == ALIAS
+    assert lin(X=q8(0, 16, 1 << 17), W=q8(1, 32, 1 << 17)) == UNSUP  # 32-bit sums
+    assert lin(Y=ten(2, 16, 32, off=0), X=q8(0, 16, 64, scale=BASE + (2 << 34))) == ALIAS
+
+    def gat(Wu=None, H=None):
+        return L.forge_gated_q8(ref(q8(0, 16, 64)), ref(q8(1, 32, 64)), ref(Wu), 2, ref(H or ten(3, 16, 32)), None)
+
+    assert gat() == NULL and gat(Wu=q8(2, 40, 64)) == SHAPE and gat(Wu=ten(2, 32, 64)) == DTYPE
+    assert gat(Wu=q8(2, 32, 64), H=ten(2, 16, 32)) == ALIAS
+
+    def ex(W=None, e=4, off=OFF, Y=None):
+        return L.forge_expert_linear_q8(ref(q8(0, 16, 64)), ref(W or q8(1, 128, 64)), e, off, 0, ref(Y or ten(3, 16, 32)), None)
+
+    assert ex(off=None) == NULL and ex(e=0) == SHAPE and ex(e=3) == SHAPE and ex(off=OFF + 4) == ALIGN
+    assert ex(Y=ten(3, 16, 128)) == SHAPE
+    assert L.forge_expert_gated_q8(ref(q8(0, 16, 64)), ref(q8(1, 128, 64)), None, 4, OFF, 0, ref(ten(3, 16, 32)), None) == NULL
+
+
+def test_python_checks():
+    i64 = torch.zeros(4, 2, dtype=torch.int64)
+    pos = torch.zeros(4, 2, dtype=torch.int32)
+    X = torch.zeros(4, 16, dtype=torch.bfloat16)
+    W = torch.zeros(3, 8, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="int64"):
+        forge.expert_plan(i64.int(), 4)
+    with pytest.raises(ValueError, match="experts"):
+        forge.expert_plan(i64, 1025)
+    with pytest.raises(ValueError, match="one route"):
+        forge.expert_plan(i64[:, :0].contiguous(), 4)
+    with pytest.raises(ValueError, match="device tensors"):
+        forge.expert_plan(i64, 4)
+    with pytest.raises(ValueError, match="int32"):
+        forge.expert_dispatch(X, i64)
+    with pytest.raises(ValueError, match="factors"):
+        forge.expert_dispatch(X, pos, scale=torch.zeros(4))
+    with pytest.raises(ValueError, match="factors"):
+        forge.expert_dispatch(X.to(torch.int8), pos)
+    with pytest.raises(ValueError, match="float32 tensor of pos's shape"):
+        forge.expert_combine(X, pos, torch.zeros(4, 3))
+    with pytest.raises(ValueError, match="needs Yp"):
+        forge.expert_combine_backward(X, None, pos)
+    with pytest.raises(ValueError, match="unknown activation"):
+        forge.expert_linear(X, W, torch.zeros(4, dtype=torch.int64), act="tanh")
+    with pytest.raises(ValueError, match="a group holds"):
+        forge.expert_dgrad_group([X], [W, W], torch.zeros(4, dtype=torch.int64))
+    from optimizer_gemm_amd import forge as f
+    with pytest.raises(ValueError, match="offsets"):
+        f._experts(W, torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError, match="stacked"):
+        f._experts(X, torch.zeros(5, dtype=torch.int64))
+    with pytest.raises(ValueError, match="one pitch"):
+        f._stack(torch.zeros(3, 10, 16)[:, :8])
+    with pytest.raises(ValueError, match="contiguous"):
+        f._stack(W.transpose(1, 2))
+    # a stack of one row each: the pitch is the distance of the experts
+    d = f._stack(torch.zeros(3, 4, 16)[:, :1])
+    assert (d.rows, d.cols, d.ld) == (3, 16, 64)
+    d = f._stack(torch.zeros(3, 8, 32)[:, :, :16])
+    assert (d.rows, d.cols, d.ld) == (24, 16, 32)
+
+
+def test_states_of_a_stack():
+    W = torch.zeros(3, 8, 128, dtype=torch.bfloat16)
+    m, v, ms, vs = forge.new_states(W, "adamw", "q8")
+    assert m.shape == v.shape == W.shape and ms.shape == vs.shape == (3, 8, 2)
+    m, v, ms, vs = forge.new_states(W[0], "lion", "bf16")
+    assert m.shape == (8, 128) and m.dtype == torch.bfloat16 and v is None and ms is None
+    with pytest.raises(ValueError):
+        forge.new_states(W, "adamw", "fp4")
