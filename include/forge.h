@@ -439,7 +439,8 @@ int forge_expert_dispatch(const forge_tensor* X, const int32_t* pos, int64_t k, 
 
 /*
  * And back: Y[t] = sum over j of weights[t, j] Yp[pos[t, j]] + R[t], in FP32 in the order of the slots, rounded
- * once; dropped routes add nothing. weights: T * k floats, or NULL for ones; R [T, cols] or NULL. T < 2^26.
+ * once; dropped routes add nothing. weights: T * k floats, or NULL for ones; R [T, cols] in Y's type, or NULL. Yp may be
+ * FORGE_F32 with Y (dY, dYp) FORGE_BF16. T < 2^26.
  * Backward: dYp[pos[t, j]] = weights[t, j] dY[t], and dweights[t, j] = the product of dY[t] and Yp[pos[t, j]]
  * (0 for a dropped route). Either may be NULL; Yp may be NULL without dweights. The residual's gradient is dY.
  */
@@ -451,7 +452,9 @@ int forge_expert_combine_backward(const forge_tensor* dY, const forge_tensor* Yp
 /*
  * The products, row by row those of forge_linear_forward (without bias and residual), forge_gated_forward,
  * forge_gated_dgrad and forge_linear_dgrad_group with the row's expert's matrices: X, dY, G, U and the
- * results have one row per route, W, Wg, Wu [experts * out, in], Wd [experts * out, hid].
+ * results have one row per route, W, Wg, Wu [experts * out, in], Wd [experts * out, hid]. Y of bfloat16 operands may
+ * be FORGE_F32 (the sums unrounded, for forge_expert_combine to weight and add), with FORGE_ACT_NONE and without Z, else
+ * FORGE_ERR_UNSUPPORTED.
  */
 int forge_expert_linear(const forge_tensor* X, const forge_tensor* W, int32_t experts, const int64_t* offsets,
                         int32_t act, forge_tensor* Y, forge_tensor* Z, forge_stream_t stream);
@@ -492,7 +495,7 @@ int forge_expert_wgrad_step(const forge_tensor* X, const forge_tensor* dY, forge
 int forge_quantize_rows(const forge_tensor* X, forge_tensor* Q, forge_stream_t stream);
 
 /* Y = act(X W^T + bias) + R and H = act(X Wg^T) * (X Wu^T), as above; R bfloat16, bias bfloat16 or float32. And the
- * same grouped by expert, without bias and residual. */
+ * same grouped by expert, without bias and residual; Y of the linear one may be FORGE_F32 as in forge_expert_linear. */
 int forge_linear_q8(const forge_tensor* X, const forge_tensor* W, const forge_tensor* bias, int32_t act,
                     const forge_tensor* R, forge_tensor* Y, forge_stream_t stream);
 int forge_gated_q8(const forge_tensor* X, const forge_tensor* Wg, const forge_tensor* Wu, int32_t act, forge_tensor* H,

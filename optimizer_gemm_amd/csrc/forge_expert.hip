@@ -55,9 +55,10 @@ __global__ __launch_bounds__(PL_NT) void plan_place_kernel(const int64_t* idx, i
       if (gridDim.x == 1) {
         all = at[e];
       } else {
+#pragma unroll 16
         for (int b = 0; b < (int)gridDim.x; ++b) {
           const int c = counts[(int64_t)b * experts + e];
-          if (b < (int)blockIdx.x) mine += c;
+          mine += b < (int)blockIdx.x ? c : 0;
           all += c;
         }
       }
@@ -148,8 +149,10 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const char* X, int64_t ld
 }
 
 // ---- and back: Y[t] = sum_j w[t][j] Yp[pos[t][j]] + R[t] ----------------------
-// 16 bytes of a row per lane; the rows of up to eight routes are asked for before the first is used. Summed in
-// float32 in the order of the routes.
+// P: the type of Yp, T: that of the tokens' side (float32 sums may go with bfloat16 tokens). A lane holds the 16 bytes
+// of a P row at a time; the rows of up to eight routes are asked for before the first is used. Summed in float32 in
+// the order of the routes. 8191 tokens of 8 routes, 2048 bfloat16 columns (302 MB): 59 us,
+// 5.1 TB/s.
 template <class T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
@@ -166,52 +169,68 @@ __device__ __forceinline__ void unpack(u32x4 r, float (&x)[kVec<T>]) {
     }
   }
 }
-template <class T>
-__device__ __forceinline__ u32x4 pack(const float (&x)[kVec<T>]) {
-  u32x4 r;
-  if constexpr (sizeof(T) == 4) {
-    store4(reinterpret_cast<float*>(&r), f32x4{x[0], x[1], x[2], x[3]});
+// V neighbouring elements as floats
+template <class T, int V>
+__device__ __forceinline__ void get(const T* p, float (&x)[V]) {
+  if constexpr (V * sizeof(T) == 16) {
+    unpack<T>(*reinterpret_cast<const u32x4*>(p), x);
   } else {
-    store4(reinterpret_cast<bf16_t*>(&r), f32x4{x[0], x[1], x[2], x[3]});
-    store4(reinterpret_cast<bf16_t*>(&r) + 4, f32x4{x[4], x[5], x[6], x[7]});
+    static_assert(V == 4, "8 bytes");
+    const f32x4 y = load4(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = y[i];
   }
-  return r;
+}
+template <class T, int V>
+__device__ __forceinline__ void put(T* p, const float (&x)[V]) {
+  if constexpr (V * sizeof(T) == 16) {  // in one piece
+    u32x4 r;
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q)
+      store4(reinterpret_cast<T*>(&r) + 4 * q, f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]});
+    *reinterpret_cast<u32x4*>(p) = r;
+  } else {
+    static_assert(V == 4, "8 bytes");
+    store4(p, f32x4{x[0], x[1], x[2], x[3]});
+  }
 }
 
 constexpr int CB_K = 8;  // routes at a time
 
-template <class T, int LANES>
-__global__ __launch_bounds__(256) void combine_kernel(const T* Yp, int64_t ldp, int64_t places, const int* pos,
+template <class P, class T, int LANES>
+__global__ __launch_bounds__(256) void combine_kernel(const P* Yp, int64_t ldp, int64_t places, const int* pos,
                                                       const float* w, int k, const T* R, int64_t ldr, T* Y, int64_t ldy,
                                                       int64_t tokens, int cols) {
-  constexpr int V = kVec<T>;
-  const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  constexpr int V = kVec<P>;
+  const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / LANES);
   if (t >= tokens) return;
   const int l = threadIdx.x % LANES;
-  const int* p = pos + t * k;
+  // eight routes' rows (NULL: dropped or past the last one) and factors, the same for all lanes
+  const P* row[CB_K];
+  float f[CB_K];
+  auto routes = [&](int j0) {
+#pragma unroll
+    for (int j = 0; j < CB_K; ++j) {
+      const bool in = j0 + j < k;
+      const int64_t r = in ? pos[t * k + j0 + j] : -1;
+      row[j] = r >= 0 && r < places ? Yp + r * ldp : nullptr;
+      f[j] = in && w ? w[t * k + j0 + j] : 1.f;
+    }
+  };
+  routes(0);
   for (int c = l * V; c < cols; c += LANES * V) {
     float sum[V] = {};
     for (int j0 = 0; j0 < k; j0 += CB_K) {
+      if (k > CB_K) routes(j0);
       u32x4 v[CB_K];
-      float f[CB_K];
-      bool in[CB_K];
+#pragma unroll
+      for (int j = 0; j < CB_K; ++j)
+        if (row[j]) v[j] = *reinterpret_cast<const u32x4*>(row[j] + c);
 #pragma unroll
       for (int j = 0; j < CB_K; ++j) {
-        in[j] = false;
-        if (j0 + j < k) {
-          const int64_t row = p[j0 + j];
-          in[j] = row >= 0 && row < places;
-          if (in[j]) {
-            v[j] = *reinterpret_cast<const u32x4*>(Yp + row * ldp + c);
-            f[j] = w ? w[t * k + j0 + j] : 1.f;
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < CB_K; ++j) {
-        if (in[j]) {
+        if (row[j]) {
           float x[V];
-          unpack<T>(v[j], x);
+          unpack<P>(v[j], x);
 #pragma unroll
           for (int i = 0; i < V; ++i) sum[i] = fmaf(f[j], x[i], sum[i]);
         }
@@ -219,24 +238,24 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* Yp, int64_t ldp, 
     }
     if (R) {
       float x[V];
-      unpack<T>(*reinterpret_cast<const u32x4*>(R + t * ldr + c), x);
+      get<T, V>(R + t * ldr + c, x);
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[i] += x[i];
     }
-    *reinterpret_cast<u32x4*>(Y + t * ldy + c) = pack<T>(sum);
+    put<T, V>(Y + t * ldy + c, sum);
   }
 }
 
 // ---- its backward pass: dYp[pos] = w dY[t], dw = <dY[t], Yp[pos]> -------------
 // A token's lanes go over its row once for every eight routes; the products' sums are joined over the
 // lanes, and over a workgroup's waves where it holds one token, in a fixed order.
-template <class T, int LANES>
-__global__ __launch_bounds__(256) void combine_backward_kernel(const T* dY, int64_t lddy, const T* Yp, int64_t ldp,
+template <class P, class T, int LANES>
+__global__ __launch_bounds__(256) void combine_backward_kernel(const T* dY, int64_t lddy, const P* Yp, int64_t ldp,
                                                                int64_t places, const int* pos, const float* w, int k,
                                                                T* dYp, int64_t lddp, float* dw, int64_t tokens, int cols) {
-  constexpr int V = kVec<T>;
+  constexpr int V = kVec<P>;
   __shared__ float part[4][CB_K];
-  const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / LANES);
   if (t >= tokens) return;  // (a wave's or a workgroup's lanes hold one token: all of them leave)
   const int l = threadIdx.x % LANES;
   const int* p = pos + t * k;
@@ -256,7 +275,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const T* dY, int6
     }
     for (int c = l * V; c < cols; c += LANES * V) {
       float d[V];
-      unpack<T>(*reinterpret_cast<const u32x4*>(dY + t * lddy + c), d);
+      get<T, V>(dY + t * lddy + c, d);
       u32x4 v[CB_K];
       if (dw) {
 #pragma unroll
@@ -268,7 +287,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const T* dY, int6
         if (row[j] < 0) continue;
         if (dw) {
           float x[V];
-          unpack<T>(v[j], x);
+          unpack<P>(v[j], x);
 #pragma unroll
           for (int i = 0; i < V; ++i) dot[j] = fmaf(d[i], x[i], dot[j]);
         }
@@ -276,7 +295,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const T* dY, int6
           float x[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) x[i] = f[j] * d[i];
-          *reinterpret_cast<u32x4*>(dYp + row[j] * lddp + c) = pack<T>(x);
+          put<T, V>(dYp + row[j] * lddp + c, x);
         }
       }
     }
@@ -374,9 +393,13 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* X, int64_t ldx, 
 
 // workgroups of 256 lanes for `rows` rows of `lanes` lanes each
 uint32_t row_blocks(int64_t rows, int lanes) { return (uint32_t)((rows * lanes + 255) / 256); }
-// lanes of a row of so many 16-byte chunks: a wave's, or a workgroup's where a wave would go over it
-// more than twice and the rows alone do not fill the chip
-bool wide_rows(int64_t rows, int64_t chunks) { return chunks > 128 && (chunks >= 1024 || rows < 4096); }
+// Lanes of a row of so many 16-byte chunks: a wave's, or a workgroup's where a wave would go over it more than
+// twice and either that often that its loads wait for one another (8191 tokens of 8 routes, 256 chunks:
+// combination 59 us against 74), or the rows alone do not fill the chip.
+bool wide_rows(int64_t rows, int64_t chunks) { return chunks >= 256 || (chunks > 128 && rows < 4096); }
+// Of a row to quantise, which a wave holds in registers up to 512 chunks of: a workgroup's from there on or for few rows
+// (65528 rows of 256 chunks 78 us against 148).
+bool wide_quant(int64_t rows, int64_t chunks) { return chunks > 512 || (chunks > 128 && rows < 4096); }
 
 }  // namespace
 
@@ -415,42 +438,42 @@ hipError_t launch_expert_dispatch(const void* X, int64_t ldx_bytes, const int* p
   return hipGetLastError();
 }
 
-template <class T>
+template <class P, class T>
 static hipError_t combine(const CombineArgs& a, hipStream_t st) {
-  const bool wide = wide_rows(a.tokens, a.cols / kVec<T>);
   auto go = [&](auto lanes_c) {
     constexpr int L = decltype(lanes_c)::value;
-    hipLaunchKernelGGL((combine_kernel<T, L>), dim3(row_blocks(a.tokens, L)), dim3(256), 0, st, static_cast<const T*>(a.Yp),
-                       a.ldp, a.places, a.pos, a.w, a.k, static_cast<const T*>(a.R), a.ldr, static_cast<T*>(a.Y), a.ldy,
-                       a.tokens, a.cols);
+    hipLaunchKernelGGL((combine_kernel<P, T, L>), dim3(row_blocks(a.tokens, L)), dim3(256), 0, st,
+                       static_cast<const P*>(a.Yp), a.ldp, a.places, a.pos, a.w, a.k, static_cast<const T*>(a.R), a.ldr,
+                       static_cast<T*>(a.Y), a.ldy, a.tokens, a.cols);
   };
-  if (wide)
+  if (wide_rows(a.tokens, a.cols / kVec<P>))
     go(std::integral_constant<int, 256>{});
   else
     go(std::integral_constant<int, 64>{});
   return hipGetLastError();
 }
-hipError_t launch_expert_combine(int bf16, const CombineArgs& a, hipStream_t st) {
-  return bf16 ? combine<bf16_t>(a, st) : combine<float>(a, st);
+hipError_t launch_expert_combine(int bf16, int wide, const CombineArgs& a, hipStream_t st) {
+  if (!bf16) return combine<float, float>(a, st);
+  return wide ? combine<float, bf16_t>(a, st) : combine<bf16_t, bf16_t>(a, st);
 }
 
-template <class T>
+template <class P, class T>
 static hipError_t combine_backward(const CombineArgs& a, hipStream_t st) {
-  const bool wide = wide_rows(a.tokens, a.cols / kVec<T>);
   auto go = [&](auto lanes_c) {
     constexpr int L = decltype(lanes_c)::value;
-    hipLaunchKernelGGL((combine_backward_kernel<T, L>), dim3(row_blocks(a.tokens, L)), dim3(256), 0, st,
-                       static_cast<const T*>(a.Y), a.ldy, static_cast<const T*>(a.Yp), a.ldp, a.places, a.pos, a.w, a.k,
+    hipLaunchKernelGGL((combine_backward_kernel<P, T, L>), dim3(row_blocks(a.tokens, L)), dim3(256), 0, st,
+                       static_cast<const T*>(a.Y), a.ldy, static_cast<const P*>(a.Yp), a.ldp, a.places, a.pos, a.w, a.k,
                        static_cast<T*>(a.dYp), a.lddp, a.dw, a.tokens, a.cols);
   };
-  if (wide)
+  if (wide_rows(a.tokens, a.cols / kVec<P>))
     go(std::integral_constant<int, 256>{});
   else
     go(std::integral_constant<int, 64>{});
   return hipGetLastError();
 }
-hipError_t launch_expert_combine_backward(int bf16, const CombineArgs& a, hipStream_t st) {
-  return bf16 ? combine_backward<bf16_t>(a, st) : combine_backward<float>(a, st);
+hipError_t launch_expert_combine_backward(int bf16, int wide, const CombineArgs& a, hipStream_t st) {
+  if (!bf16) return combine_backward<float, float>(a, st);
+  return wide ? combine_backward<float, bf16_t>(a, st) : combine_backward<bf16_t, bf16_t>(a, st);
 }
 
 template <class T>
@@ -458,7 +481,7 @@ static hipError_t quantize(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, f
                            hipStream_t st) {
   const int64_t chunks = cols / kVec<T>;
   const T* x = static_cast<const T*>(X);
-  if (wide_rows(rows, chunks))
+  if (wide_quant(rows, chunks))
     hipLaunchKernelGGL((quantize_kernel<T, 256, 8>), dim3(row_blocks(rows, 256)), dim3(256), 0, st, x, ldx, Q, ldq, scale,
                        rows, cols);
   else

@@ -56,6 +56,14 @@ void set_group(LinArgs& g, int experts, const int64_t* offsets) {
   g.offsets = offsets;
 }
 
+// The product's sums, in float32, as the result.
+void set_sums(LinArgs& g, const forge_tensor* Y) {
+  g.splits = 1;
+  g.e.acc = (float*)Y->data;
+  g.e.ldacc = Y->ld;
+  g.e.acc_write = 1;
+}
+
 // (pairs of 8-bit integers stand where the kernels count bfloat16 elements)
 void set_pair_q8(LinArgs& g, int s, const forge_tensor* A, const forge_tensor* B) {
   set_pair(g, s, A->data, A->ld / 2, B->data, B->ld / 2, B->cols / 2);
@@ -73,7 +81,9 @@ int linear_q8(const forge_tensor* X, const forge_tensor* W, const forge_tensor* 
     return r;
   if (W->rows % parts) return FORGE_ERR_SHAPE;
   const int64_t out = W->rows / parts;
-  if ((r = check_mat(Y, FORGE_BF16, T, out))) return r;
+  const bool wide = offsets && !Wu && Y->dtype == FORGE_F32;  // the sums as they are
+  if ((r = check_mat(Y, wide ? FORGE_F32 : FORGE_BF16, T, out))) return r;
+  if (wide && (act != FORGE_ACT_NONE || out % 8)) return FORGE_ERR_UNSUPPORTED;
   if (bias && (r = check_mat(bias, bias->dtype == FORGE_F32 ? FORGE_F32 : FORGE_BF16, 1, out))) return r;
   if (R && (r = check_mat(R, FORGE_BF16, T, out))) return r;
   if (in >= kMaxQ8 || !fits_31(X)) return FORGE_ERR_UNSUPPORTED;
@@ -92,11 +102,15 @@ int linear_q8(const forge_tensor* X, const forge_tensor* W, const forge_tensor* 
   g.M = (int32_t)out;
   g.N = (int32_t)T;
   if (offsets) set_group(g, experts, offsets);
+  g.e.sx = X->scale;
+  g.e.sw = W->scale;
+  if (wide) {
+    set_sums(g, Y);
+    return hip_status(launch_lin_q8(L_ACC, g, st));
+  }
   g.e.act = act;
   g.e.out = Y->data;
   g.e.ldo = Y->ld;
-  g.e.sx = X->scale;
-  g.e.sw = W->scale;
   if (Wu) g.e.sw2 = Wu->scale;
   if (R) {
     g.e.in1 = R->data;
@@ -172,7 +186,7 @@ static int check_combine(const forge_tensor* Yp, const int32_t* pos, int64_t k, 
                          CombineArgs& a) {
   int r;
   if ((r = op_dtype(Y)) || (r = check_mat(Y, Y->dtype, Y->rows, Y->cols))) return r;
-  if (Yp && ((r = op_dtype(Yp)) || (r = check_mat(Yp, Y->dtype, Yp->rows, Y->cols)))) return r;
+  if (Yp && ((r = op_dtype(Yp)) || (r = check_mat(Yp, Yp->dtype == FORGE_F32 ? FORGE_F32 : Y->dtype, Yp->rows, Y->cols)))) return r;
   if (k < 1) return FORGE_ERR_SHAPE;
   if (Y->rows >= kMaxTokens || k >= kMaxRoutes || Y->rows * k >= kMaxRoutes) return FORGE_ERR_UNSUPPORTED;
   if (Y->rows > 0 && !pos) return FORGE_ERR_NULL;
@@ -206,7 +220,7 @@ int forge_expert_combine(const forge_tensor* Yp, const int32_t* pos, int64_t k, 
     a.R = R->data;
     a.ldr = R->ld;
   }
-  return hip_status(launch_expert_combine(Y->dtype == FORGE_BF16, a, (hipStream_t)stream));
+  return hip_status(launch_expert_combine(Y->dtype == FORGE_BF16, Yp->dtype == FORGE_F32, a, (hipStream_t)stream));
 }
 
 int forge_expert_combine_backward(const forge_tensor* dY, const forge_tensor* Yp, const int32_t* pos, int64_t k,
@@ -229,7 +243,7 @@ int forge_expert_combine_backward(const forge_tensor* dY, const forge_tensor* Yp
     a.places = dYp->rows;
   }
   a.dw = dweights;
-  return hip_status(launch_expert_combine_backward(dY->dtype == FORGE_BF16, a, (hipStream_t)stream));
+  return hip_status(launch_expert_combine_backward(dY->dtype == FORGE_BF16, Yp && Yp->dtype == FORGE_F32, a, (hipStream_t)stream));
 }
 
 int forge_expert_linear(const forge_tensor* X, const forge_tensor* W, int32_t experts, const int64_t* offsets,
@@ -240,7 +254,11 @@ int forge_expert_linear(const forge_tensor* X, const forge_tensor* W, int32_t ex
   if (!act_ok(act)) return FORGE_ERR_UNSUPPORTED;
   const int dt = W->dtype;
   const int64_t T = X->rows, out = W->rows / experts, in = W->cols;
-  if ((r = check_mat(X, dt, T, in)) || (r = check_stack(W, dt, experts, out, in)) || (r = check_mat(Y, dt, T, out))) return r;
+  const bool wide = dt == FORGE_BF16 && Y->dtype == FORGE_F32;  // the sums as they are
+  if ((r = check_mat(X, dt, T, in)) || (r = check_stack(W, dt, experts, out, in)) ||
+      (r = check_mat(Y, wide ? FORGE_F32 : dt, T, out)))
+    return r;
+  if (wide && (act != FORGE_ACT_NONE || Z || out % 8)) return FORGE_ERR_UNSUPPORTED;
   if (Z && (r = check_mat(Z, dt, T, out))) return r;
   const forge_tensor off = flat(offsets, (experts + 1) * 8);
   const forge_tensor* outs[2] = {Y, Z};
@@ -253,6 +271,10 @@ int forge_expert_linear(const forge_tensor* X, const forge_tensor* W, int32_t ex
   g.M = (int32_t)out;
   g.N = (int32_t)T;
   set_group(g, experts, offsets);
+  if (wide) {
+    set_sums(g, Y);
+    return hip_status(launch_lin_expert(1, L_ACC, false, g, (hipStream_t)stream));
+  }
   g.e.act = act;
   g.e.out = Y->data;
   g.e.ldo = Y->ld;
@@ -260,7 +282,7 @@ int forge_expert_linear(const forge_tensor* X, const forge_tensor* W, int32_t ex
     g.e.out2 = Z->data;
     g.e.ldo2 = Z->ld;
   }
-  return hip_status(launch_lin_expert(dt == FORGE_BF16, L_LINEAR, g, (hipStream_t)stream));
+  return hip_status(launch_lin_expert(dt == FORGE_BF16, L_LINEAR, false, g, (hipStream_t)stream));
 }
 
 int forge_expert_gated(const forge_tensor* X, const forge_tensor* Wg, const forge_tensor* Wu, int32_t experts,
@@ -297,7 +319,7 @@ int forge_expert_gated(const forge_tensor* X, const forge_tensor* Wg, const forg
     g.e.out3 = U->data;
     g.e.ldo3 = U->ld;
   }
-  return hip_status(launch_lin_expert(dt == FORGE_BF16, L_GATED, g, (hipStream_t)stream));
+  return hip_status(launch_lin_expert(dt == FORGE_BF16, L_GATED, false, g, (hipStream_t)stream));
 }
 
 int forge_expert_gated_dgrad(const forge_tensor* dY, const forge_tensor* Wd, const forge_tensor* G,
@@ -337,7 +359,7 @@ int forge_expert_gated_dgrad(const forge_tensor* dY, const forge_tensor* Wd, con
     g.e.out3 = H->data;
     g.e.ldo3 = H->ld;
   }
-  return hip_status(launch_lin_expert(dt == FORGE_BF16, L_DGATE, g, (hipStream_t)stream));
+  return hip_status(launch_lin_expert(dt == FORGE_BF16, L_DGATE, true, g, (hipStream_t)stream));
 }
 
 int forge_expert_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,
@@ -371,7 +393,7 @@ int forge_expert_dgrad_group(int32_t n_layers, const forge_tensor* dY, const for
   set_group(g, experts, offsets);
   g.e.out = dX->data;
   g.e.ldo = dX->ld;
-  return hip_status(launch_lin_expert(dt == FORGE_BF16, L_ACC, g, (hipStream_t)stream));
+  return hip_status(launch_lin_expert(dt == FORGE_BF16, L_ACC, true, g, (hipStream_t)stream));
 }
 
 // Operands of the stack's weight gradient, for W [experts * out, in] of type dt.

@@ -44,6 +44,8 @@
 // 1.06. The part's clock is what gives: 1.76 GHz at 72% busy matrix pipes.
 #pragma once
 
+#include <math.h>
+
 #include "forge_gemm_kernel.h"
 #include "forge_ops.h"
 
@@ -122,8 +124,8 @@ __device__ __forceinline__ LinArgsPtr lin_args() { return (LinArgsPtr)__builtin_
 template <class C, int EPI, bool TA, bool TB, int MODE>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::OCC, C::OCC)))
 void lin_kernel(LinArgs g) {
-  constexpr bool EXP = (MODE & LM_EXPERT) != 0, Q8 = (MODE & LM_Q8) != 0;
-  static_assert(!Q8 || (!TA && !TB && (EPI == L_LINEAR || EPI == L_GATED)), "8-bit operands: forward products");
+  constexpr bool EXP = (MODE & LM_EXPERT) != 0, Q8 = (MODE & LM_Q8) != 0, TAIL = (MODE & LM_TAIL) != 0;
+  static_assert(!Q8 || (!TA && !TB && (EPI == L_LINEAR || EPI == L_GATED || EPI == L_ACC)), "8-bit operands: forward products");
   using OA = LOper<C, C::BM, TA>;
   using OB = LOper<C, C::BN, TB>;
   constexpr bool TWO = EPI == L_GATED;              // A: BM / 2 rows of gate, then BM / 2 of up
@@ -139,10 +141,22 @@ void lin_kernel(LinArgs g) {
   const int wm = wave_u % C::WM, wn = wave_u / C::WM;
   uint8_t* const ring = smem + grp * 5 * C::SLOT;
   const uint32_t lds0 = lds_addr(smem) + (uint32_t)(grp * 5 * C::SLOT);
-  const int ntm = (epi_width<EPI>(g.M) - g.m_off + OM - 1) / OM, ntn = (g.N - g.n_off + C::BN - 1) / C::BN;
-  ExpertRows<C::BN> xr{g.offsets, g.experts, g.N, -1, 0, 0, 0};
-  int ntiles = ntm * ntn * (EPI == L_ACC && TA && !TB && !EXP ? g.splits : 1);
-  if constexpr (EXP) ntiles = ntm * xr.total();
+  constexpr int XM = TAIL ? 2 * OM : OM, XN = TAIL ? 2 * C::BN : C::BN;  // the tiles that are counted
+  const int ntm = (epi_width<EPI>(g.M) - g.m_off + XM - 1) / XM, ntn = (g.N - g.n_off + C::BN - 1) / C::BN;
+  ExpertRows<XN> xr{g.offsets, g.experts, g.N, -1, 0, 0, 0};
+  int ntiles = ntm * ntn * (EPI == L_ACC && TA && !TB && !EXP ? g.splits : 1), tail0 = 0;
+  if constexpr (EXP) {
+    ntiles = ntm * xr.total();
+    if (g.round > 0) {
+      const int full = ntiles / g.round * g.round, rem = ntiles - full;
+      const bool split = full > 0 && rem > 0 && 2 * rem <= g.round;
+      tail0 = full;
+      if constexpr (TAIL)
+        ntiles = split ? 4 * rem : 0;
+      else if (split)
+        ntiles = full;
+    }
+  }
   const LinArgsPtr ga = lin_args();
   const int nsrc = MULTI ? ga->nsrc : 1;
   int nst = (g.K[0] + C::BK - 1) / C::BK;
@@ -259,12 +273,12 @@ void lin_kernel(LinArgs g) {
       tile /= splits;
     }
     if constexpr (EXP) {
-      const int L = g_order(tile, ntiles);
+      const int L = TAIL ? tail0 + (tile >> 2) : g_order(tile, ntiles);
       int r0, t0;
       xr.find(L / ntm, lx, r0, lend, t0);
-      g_place(L - t0 * ntm, ntm, (lend - r0 + C::BN - 1) / C::BN, tm, tn);
-      lm0 = tm * OM;
-      ln0 = r0 + tn * C::BN;
+      g_place(L - t0 * ntm, ntm, (lend - r0 + XN - 1) / XN, tm, tn);
+      lm0 = tm * XM + (TAIL ? (tile & 1) * OM : 0);
+      ln0 = r0 + tn * XN + (TAIL ? (tile >> 1 & 1) * C::BN : 0);  // (past the expert's end: nothing is read or written)
     } else {
       g_tile(tile, ntm, ntn, tm, tn);
       lm0 = g.m_off + tm * OM;
@@ -715,6 +729,15 @@ void lin_kernel(LinArgs g) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) __builtin_amdgcn_raw_buffer_store_b128(x[k], r, o[k], at, 0);
       };
+      // the same for vector k alone
+      auto put_one = [&](u32x4 x, int k, void* p, int64_t ld, int blk) FORGE_INLINE {
+        const int n = 32 * (blk / CH) + e_row + k * RS, m = mw + OWB * (blk % CH) + 8 * e_col;
+        const uint32_t o = (uint32_t)n * (uint32_t)(ld * 2) + (uint32_t)(m * 2);
+        __builtin_amdgcn_raw_buffer_store_b128(x, res(p, ld, 2), m < Mw && n < rows ? o : kOOB, 0, 0);
+      };
+      // Three results of which none waits for the others': two waves per SIMD have no registers left for all
+      // vectors of a block beside the experts' rows.
+      constexpr bool EACH = EXP && EPI == L_DGATE && !C::AHEAD;
       auto process = [&](const Pre& P, int blk) FORGE_INLINE {
         // 16-byte chunk c of row r sits at chunk c ^ (r mod 16)
         static_for<0, NB>([&](auto b_c) FORGE_INLINE {
@@ -755,6 +778,10 @@ void lin_kernel(LinArgs g) {
 #pragma unroll
           for (int k = 0; k < NV; ++k) {
             f32x4 x0 = chunk(k, 2 * e_col), x1 = chunk(k, 2 * e_col + 1);
+            if constexpr (Q8) {
+              x0 = int_sums(x0) * (P.sw[0] * P.sx[k]);
+              x1 = int_sums(x1) * (P.sw[1] * P.sx[k]);
+            }
             if (e.acc_read) {
               x0 = x0 + __builtin_bit_cast(f32x4, P.a[k]);
               x1 = x1 + __builtin_bit_cast(f32x4, P.b[k]);
@@ -818,16 +845,25 @@ void lin_kernel(LinArgs g) {
               }
               epi_math<uint16_t, EPI>(act, x0, z0, a0, b0, y0, y1, y2);
               epi_math<uint16_t, EPI>(act, x1, z1, a1, b1, v0, v1, v2);
-              r0[k] = pack(y0, v0);
-              r1[k] = pack(y1, v1);
-              if constexpr (EPI != L_LINEAR) r2[k] = pack(y2, v2);
+              if constexpr (EACH) {
+                put_one(pack(y0, v0), k, e.out, e.ldo, blk);
+                put_one(pack(y1, v1), k, e.out2, e.ldo2, blk);
+                if (e.out3) put_one(pack(y2, v2), k, e.out3, e.ldo3, blk);
+                __builtin_amdgcn_sched_barrier(0);
+              } else {
+                r0[k] = pack(y0, v0);
+                r1[k] = pack(y1, v1);
+                if constexpr (EPI != L_LINEAR) r2[k] = pack(y2, v2);
+              }
             }
           };
           act_dispatch<EPI>(e.act, math);
-          put(r0, e.out, e.ldo, 2, 0, blk);
-          if (e.out2) put(r1, e.out2, e.ldo2, 2, 0, blk);
-          if constexpr (EPI != L_LINEAR) {
-            if (e.out3) put(r2, e.out3, e.ldo3, 2, 0, blk);
+          if constexpr (!EACH) {
+            put(r0, e.out, e.ldo, 2, 0, blk);
+            if (e.out2) put(r1, e.out2, e.ldo2, 2, 0, blk);
+            if constexpr (EPI != L_LINEAR) {
+              if (e.out3) put(r2, e.out3, e.ldo3, 2, 0, blk);
+            }
           }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -874,7 +910,8 @@ hipError_t lin_run(const LinArgs& g, hipStream_t st) {
   // (grouped by expert: as many as there can be, each expert's last one partly full)
   const int64_t ntn = EXP ? (g.N + C::BN - 1) / C::BN + (g.experts < g.N ? g.experts : g.N)
                           : (g.N - g.n_off + C::BN - 1) / C::BN;
-  const int64_t tiles = ntm * ntn * (EPI == L_ACC && TA && !TB && !EXP ? g.splits : 1);
+  // (of a last round: two quarters a unit fill the chip)
+  const int64_t tiles = MODE & LM_TAIL ? 2 * g.round : ntm * ntn * (EPI == L_ACC && TA && !TB && !EXP ? g.splits : 1);
   if (tiles <= 0) return hipSuccess;
   const int64_t resident = (int64_t)(C::OCC * 4 / C::NW) * g_num_cus();
   hipLaunchKernelGGL((lin_kernel<C, EPI, TA, TB, MODE>), dim3((uint32_t)(tiles < resident ? tiles : resident)), dim3(C::NT), 0,
@@ -907,6 +944,36 @@ inline bool lin_split_big(int64_t M, int64_t N, int64_t K) {
   return M >= 192 && N >= 192 && s > 0 && (K + 63) / 64 >= 48 * s;
 }
 
+// A last round of large tiles that would be at most half full: the whole rounds run as large
+// tiles over a band of tile columns (or rows, whichever band holds more of them), the rest as
+// 128x128 tiles in a second launch. (Not the cross entropy's maxima and sums: their blocks
+// follow the tile.) A tile owns its output elements either way.
+template <int EPI, bool TA, bool TB, int MODE>
+hipError_t lin_large(const LinArgs& g, hipStream_t st) {
+  constexpr int OM = EPI == L_GATED ? 128 : 256;
+  const int cus = g_num_cus(), Mw = epi_width<EPI>(g.M);
+  const int ntm = (Mw + OM - 1) / OM, ntn = (g.N + 255) / 256;
+  const int64_t tiles = (int64_t)ntm * ntn, full = tiles / cus * cus, rem = tiles - full;
+  if (EPI != L_LSE && full > 0 && rem > 0 && 2 * rem <= cus && g.K[0] >= 512) {
+    LinArgs g1 = g, g2 = g;
+    const int mb = (int)(full / ntn), nb = (int)(full / ntm);  // whole bands the rounds hold
+    if (mb * (int64_t)ntn >= nb * (int64_t)ntm) {
+      g1.M = mb * OM;
+      g2.m_off = g1.M;
+    } else {
+      g1.N = nb * 256;
+      g2.n_off = g1.N;
+    }
+    if (g1.M > 0 && g1.N > 0) {
+      hipError_t e = lin_run<LinBig, EPI, TA, TB, MODE>(g1, st);
+      if (e != hipSuccess) return e;
+      const int64_t t = (int64_t)((Mw - g2.m_off + OM / 2 - 1) / (OM / 2)) * ((g.N - g2.n_off + 127) / 128);
+      return t > cus ? lin_run<LinSmall, EPI, TA, TB, MODE>(g2, st) : lin_run<LinSplit, EPI, TA, TB, MODE>(g2, st);
+    }
+  }
+  return lin_run<LinBig, EPI, TA, TB, MODE>(g, st);
+}
+
 template <int EPI, bool TA, bool TB>
 hipError_t lin_bf16(const LinArgs& g, hipStream_t st) {
   if constexpr (EPI == L_ACC && TA && !TB) {
@@ -917,54 +984,46 @@ hipError_t lin_bf16(const LinArgs& g, hipStream_t st) {
     }
   }
   switch (lin_tile<EPI>(epi_width<EPI>(g.M), g.N)) {
-    case LT_BIG: {
-      // A last round of large tiles that would be at most half full: the whole rounds run as large
-      // tiles over a band of tile columns (or rows, whichever band holds more of them), the rest as
-      // 128x128 tiles in a second launch. (Not the cross entropy's maxima and sums: their blocks
-      // follow the tile.) A tile owns its output elements either way.
-      constexpr int OM = EPI == L_GATED ? 128 : 256;
-      const int cus = g_num_cus(), Mw = epi_width<EPI>(g.M);
-      const int ntm = (Mw + OM - 1) / OM, ntn = (g.N + 255) / 256;
-      const int64_t tiles = (int64_t)ntm * ntn, full = tiles / cus * cus, rem = tiles - full;
-      if (EPI != L_LSE && full > 0 && rem > 0 && 2 * rem <= cus && g.K[0] >= 512) {
-        LinArgs g1 = g, g2 = g;
-        const int mb = (int)(full / ntn), nb = (int)(full / ntm);  // whole bands the rounds hold
-        if (mb * (int64_t)ntn >= nb * (int64_t)ntm) {
-          g1.M = mb * OM;
-          g2.m_off = g1.M;
-        } else {
-          g1.N = nb * 256;
-          g2.n_off = g1.N;
-        }
-        if (g1.M > 0 && g1.N > 0) {
-          hipError_t e = lin_run<LinBig, EPI, TA, TB>(g1, st);
-          if (e != hipSuccess) return e;
-          const int64_t t = (int64_t)((Mw - g2.m_off + OM / 2 - 1) / (OM / 2)) * ((g.N - g2.n_off + 127) / 128);
-          return t > cus ? lin_run<LinSmall, EPI, TA, TB>(g2, st) : lin_run<LinSplit, EPI, TA, TB>(g2, st);
-        }
-      }
-      return lin_run<LinBig, EPI, TA, TB>(g, st);
-    }
+    case LT_BIG: return lin_large<EPI, TA, TB, 0>(g, st);
     case LT_SMALL: return lin_run<LinSmall, EPI, TA, TB>(g, st);
     case LT_SPLIT: return lin_run<LinSplit, EPI, TA, TB>(g, st);
     default: return lin_run<LinTiny, EPI, TA, TB>(g, st);
   }
 }
 
-// Products grouped by expert: the tiles as far as they can be told without the experts' sizes, which are
-// in device memory.
+// Products grouped by expert. Their sizes are in device memory; the host counts the tiles that sizes spread
+// exponentially around their mean would give (of b rows: 1 / (1 - e^(-b / mean)) an expert, the mean / b + 1/2 of a large
+// mean), and compares the kinds by a stage's time in us, given the rounds of the chip they take:
+//   256x256, one a unit: 1.35 a round, a last round that is at most half full 0.79 (its quarters, LM_TAIL);
+//   128x128, two a unit: 0.79 a round, 0.70 for one that is not full, 0.71 for 8-bit operands;
+//   64x64 with four groups of waves: 0.47, each further round 0.31.
+// Measured: 8 experts of 2048 rows, 4096 -> 2 x 14336 gated 2927 us against 3974, the input gradient of both
+// 3162 (3488 without the quarters) against 4828; 8 of 128 rows, 4096 -> 2 x 3584 gated 173 against 116, 8-bit
+// 99 against 57; 16 of 8 rows, 4096 -> 1792: 128x128 45, 64x64 31.
 template <int EPI, bool TA, int MODE>
-hipError_t lin_expert(const LinArgs& g, hipStream_t st) {
+hipError_t lin_expert(const LinArgs& g0, hipStream_t st) {
+  LinArgs g = g0;
   const int64_t cus = g_num_cus(), w = EPI == L_GATED ? 2 * (int64_t)g.M : g.M;
-  const int64_t used = g.experts < g.N ? g.experts : g.N, each = g.N / used;
-  auto tiles = [&](int64_t b) { return (w + b - 1) / b * used * ((each + b - 1) / b); };
-  if (each >= 128 && 2 * tiles(256) > cus) return lin_run<LinBig, EPI, TA, false, MODE>(g, st);
-  // (the gated gradient's epilogue and the experts' rows need more registers than two workgroups per unit leave)
-  if constexpr (EPI != L_DGATE) {
-    if (each >= 48 && tiles(128) > cus) return lin_run<LinSmall, EPI, TA, false, MODE>(g, st);
-  }
-  if (each >= 48) return lin_run<LinSplit, EPI, TA, false, MODE>(g, st);
-  return lin_run<LinTiny, EPI, TA, false, MODE>(g, st);
+  const double used = g.experts * (1.0 - pow(1.0 - 1.0 / g.experts, (double)g.N)), each = g.N / used;
+  auto rounds = [&](int64_t b, int64_t per_cu) {
+    const double n = -1.0 / expm1(-(double)b / each);
+    return (double)((w + b - 1) / b) * used * n / (double)(per_cu * cus);
+  };
+  const double big = rounds(256, 1), small = rounds(128, 2), tiny = rounds(64, 1);
+  const double part = big - floor(big);
+  double stages = 0.0;
+  for (int s = 0; s < g.nsrc; ++s) stages += (g.K[s] + 63) / 64;
+  const double one = 1.35 * stages + 12.0;
+  const double t_big = big >= 1.0 && part <= 0.5 ? one * floor(big) + (part > 0.0 ? 0.79 * stages + 12.0 : 0.0) : one * ceil(big);
+  const double t_small = (small <= 1.0 ? 0.70 * stages : (MODE & LM_Q8 ? 0.71 : 0.79) * stages * ceil(small)) + 5.0 * ceil(small);
+  const double t_tiny = 0.16 * stages + (0.31 * stages + 5.0) * ceil(tiny);
+  if (t_tiny < t_small && t_tiny < t_big) return lin_run<LinTiny, EPI, TA, false, MODE>(g, st);
+  if (t_small <= t_big) return lin_run<LinSmall, EPI, TA, false, MODE>(g, st);
+  // where there can be more large tiles than a round has (whatever the experts' sizes are)
+  if ((w + 255) / 256 * ((g.N + 255) / 256 + (g.experts < g.N ? g.experts : g.N)) > cus) g.round = (int32_t)cus;
+  hipError_t e = lin_run<LinBig, EPI, TA, false, MODE>(g, st);
+  if (e != hipSuccess || g.round == 0) return e;
+  return lin_run<LinSmall, EPI, TA, false, MODE | LM_TAIL>(g, st);
 }
 
 #define FORGE_LIN_FORMS(X)                                                                                  \

@@ -116,15 +116,21 @@ hipError_t run(const LinArgs& g, hipStream_t st) {
   const bool exp = MODE & LM_EXPERT;
   const int64_t used = g.experts < g.N ? g.experts : g.N;  // experts with rows, at most
   const dim3 grid((uint32_t)((g.M + 15) / 16), exp ? (uint32_t)used : 1u), block(64 * K_NW);
-  if (exp ? g.N <= 16 * used : g.N <= 16)
-    hipLaunchKernelGGL((lin_skinny_kernel<EPI, 1, MODE>), grid, block, 0, st, g);
-  else
-    hipLaunchKernelGGL((lin_skinny_kernel<EPI, 2, MODE>), grid, block, 0, st, g);
+  if constexpr (!(MODE & LM_EXPERT)) {
+    if (g.N > 16) {
+      hipLaunchKernelGGL((lin_skinny_kernel<EPI, 2, MODE>), grid, block, 0, st, g);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((lin_skinny_kernel<EPI, 1, MODE>), grid, block, 0, st, g);
   return hipGetLastError();
 }
 
 template <int MODE>
 hipError_t run(int epi, const LinArgs& g, hipStream_t st) {
+  if constexpr (MODE & LM_EXPERT) {
+    if (epi == L_ACC) return run<L_ACC, MODE>(g, st);
+  }
   return epi == L_GATED ? run<L_GATED, MODE>(g, st) : run<L_LINEAR, MODE>(g, st);
 }
 

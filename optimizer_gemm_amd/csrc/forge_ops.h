@@ -188,6 +188,9 @@ struct LinArgs {
   // Products grouped by expert: expert x owns rows offsets[x] .. offsets[x + 1] - 1 of the N rows of
   // B and of the output, and the x-th of the stacked matrices A
   int32_t experts;
+  // workgroups of a whole round of the large tiles, where a last round that is at most half full is left
+  // to the smaller ones of a second launch (LM_TAIL); 0: it is not
+  int32_t round;
   const int64_t* offsets;
   LinEpiArgs e;
 };
@@ -204,6 +207,7 @@ inline void set_pair(LinArgs& g, int s, const void* A, int64_t lda, const void* 
 // Forms of a product's kernel.
 enum LinMode {
   LM_EXPERT = 1,  // grouped by expert
+  LM_TAIL = 4,    // grouped by expert: quarters of the last round's large tiles
   LM_Q8 = 2,      // operands of 8-bit integers (LinArgs' K and pitches count pairs of them), bfloat16 output
 };
 
@@ -397,18 +401,16 @@ __host__ __device__ constexpr int epi_width(int M) {
 hipError_t launch_lin(int bf16, int epi, bool ta, bool tb, const LinArgs& g, hipStream_t st);
 // products grouped by expert (g.offsets, g.experts); forward products of 8-bit operands, grouped where
 // g.experts > 0
-hipError_t launch_lin_expert(int bf16, int epi, const LinArgs& g, hipStream_t st);
+hipError_t launch_lin_expert(int bf16, int epi, bool ta, const LinArgs& g, hipStream_t st);
 hipError_t launch_lin_q8(int epi, const LinArgs& g, hipStream_t st);
 // forward products (L_LINEAR, L_GATED) of at most kSkinny tokens, bf16 (launch_lin chooses); mode: LinMode,
 // grouped by expert any number
 constexpr int kSkinny = 32;
 hipError_t launch_lin_skinny(int mode, int epi, const LinArgs& g, hipStream_t st);
-// whether a forward product of so few tokens (rows of an expert) is one for launch_lin_skinny
+// whether a forward product of so few tokens is one for launch_lin_skinny
 bool few_tokens(int epi, const LinArgs& g);
-inline bool few_rows(const LinArgs& g) {
-  const int64_t used = g.experts < g.N ? g.experts : g.N;
-  return g.N <= 16 * used && g.M < (1 << 26);  // (a grid of fewer than 2^32 threads)
-}
+// the same of one that is grouped by expert
+bool few_rows(const LinArgs& g);
 // vocabulary entries per partial result that launch_lin(L_LSE) writes for this product
 int lin_lse_block(int bf16, int M, int N);
 
@@ -450,8 +452,9 @@ struct CombineArgs {
   int64_t lddp;
   float* dw;
 };
-hipError_t launch_expert_combine(int bf16, const CombineArgs& a, hipStream_t st);
-hipError_t launch_expert_combine_backward(int bf16, const CombineArgs& a, hipStream_t st);
+// bf16: of the tokens' side (Y, R, dYp); wide: Yp in float32 beside it
+hipError_t launch_expert_combine(int bf16, int wide, const CombineArgs& a, hipStream_t st);
+hipError_t launch_expert_combine_backward(int bf16, int wide, const CombineArgs& a, hipStream_t st);
 hipError_t launch_quantize_rows(int bf16, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, int64_t rows,
                                 int cols, hipStream_t st);
 

@@ -892,13 +892,15 @@ def expert_dispatch(X: torch.Tensor, pos: torch.Tensor, scale: Optional[torch.Te
 
 
 def expert_combine(Yp: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] = None,
-                   residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                   residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """The experts' results back to their tokens, Y[t] = sum_j weights[t, j] Yp[pos[t, j]] + residual[t], dropped
-    routes left out (forge_expert_combine); weights float32 or None for ones."""
+    routes left out (forge_expert_combine); weights float32 or None for ones. Y is of Yp's type, or bfloat16 of
+    float32 Yp with out_dtype=torch.bfloat16 (or a residual or out of that type)."""
     k = _places(pos)
     _factors(weights, pos)
     with _On(stream, Yp, pos, weights, residual, out) as on:
-        Y = _same(on, out, (pos.shape[0], Yp.shape[1]), Yp.dtype)
+        Y = _same(on, out, (pos.shape[0], Yp.shape[1]), out_dtype or (Yp if residual is None else residual).dtype)
         if Y.shape[0] != pos.shape[0]:
             raise ValueError("pos has the routes of another number of tokens")
         _check(_lib.forge_expert_combine(_ten(Yp), _ptr(pos), k, _ptr(weights), _ten(residual), _ten(Y), on.stream),
@@ -927,15 +929,16 @@ def expert_combine_backward(dY: torch.Tensor, Yp: Optional[torch.Tensor], pos: t
 
 
 def expert_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, act: str = "none", save: bool = False,
-                  out: Optional[torch.Tensor] = None, stream=None):
+                  out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, stream=None):
     """Y[r] = act(X[r] W[x]^T) for the rows r of each expert x (forge_expert_linear): X [R, in] in expert_plan's
     order, W [experts, out, in], offsets as expert_plan returned them. Rows behind offsets[-1] are
-    neither read nor written. With save=True returns (Y, Z), Z the pre-activation."""
+    neither read nor written. With save=True returns (Y, Z), Z the pre-activation. out_dtype=torch.float32 of bfloat16
+    operands, without an activation: the sums unrounded, for expert_combine."""
     a = _act(act)
     with _On(stream, X, W, offsets, out) as on:
         e = _experts(W, offsets)
         shape = (X.shape[0], W.shape[1])
-        Y = _same(on, out, shape, W.dtype)
+        Y = _same(on, out, shape, out_dtype or W.dtype)
         Z = on.empty(shape, W.dtype) if save else None
         _check(_lib.forge_expert_linear(_ten(X), _stack(W), e, offsets.data_ptr(), a, _ten(Y), _ten(Z), on.stream),
                "forge_expert_linear")
@@ -1091,13 +1094,14 @@ def gated_q8(X: torch.Tensor, x_scale: torch.Tensor, Wg: torch.Tensor, wg_scale:
 
 def expert_linear_q8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
                      offsets: torch.Tensor, act: str = "none", out: Optional[torch.Tensor] = None,
-                     stream=None) -> torch.Tensor:
+                     out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """expert_linear() of 8-bit integers (forge_expert_linear_q8): W [experts, out, in] int8 with experts * out
-    factors, X and its factors as expert_dispatch(Q, pos, scale) returned them; Y bfloat16."""
+    factors, X and its factors as expert_dispatch(Q, pos, scale) returned them; Y bfloat16, or float32 without an
+    activation, for expert_combine."""
     a = _act(act)
     with _On(stream, X, x_scale, W, w_scale, offsets, out) as on:
         e = _experts(W, offsets)
-        Y = _same(on, out, (X.shape[0], W.shape[1]), torch.bfloat16)
+        Y = _same(on, out, (X.shape[0], W.shape[1]), out_dtype)
         _check(_lib.forge_expert_linear_q8(_codes(X, x_scale, "X"), _codes(W, w_scale, "W"), e, offsets.data_ptr(), a, _ten(Y),
                                            on.stream), "forge_expert_linear_q8")
     return Y

@@ -70,7 +70,7 @@ def test_combine_refusals():
 
     assert call(pos=None) == NULL and call(pos=P + 1) == ALIGN and call(w=W + 2) == ALIGN and call(k=0) == SHAPE
     assert call(Yp=ten(0, 32, 72)) == SHAPE and call(R=ten(2, 16, 72)) == SHAPE and call(R=ten(2, 15, 64)) == SHAPE
-    assert call(Yp=ten(0, 32, 64, F32)) == DTYPE and call(R=ten(2, 16, 64, F32)) == DTYPE
+    assert call(Yp=ten(0, 32, 64), Y=ten(1, 16, 64, F32)) == DTYPE and call(R=ten(2, 16, 64, F32)) == DTYPE
     assert call(Y=ten(0, 16, 64)) == ALIAS and call(R=ten(1, 16, 64)) == ALIAS and call(w=BASE + (1 << 34)) == ALIAS
 
     def back(dY=None, Yp=0, pos=P, k=2, w=W, dYp=0, dw=BASE + (11 << 34)):
@@ -95,6 +95,7 @@ def test_product_refusals():
     assert lin(Y=ten(2, 16, 40)) == SHAPE and lin(Y=ten(2, 15, 32)) == SHAPE and lin(Z=ten(3, 16, 40)) == SHAPE
     assert lin(Y=ten(0, 16, 32)) == ALIAS and lin(Z=ten(2, 16, 32)) == ALIAS
     assert lin(off=BASE + (2 << 34)) == ALIAS
+    assert lin(Y=ten(2, 16, 32, F32), act=1) == UNSUP and lin(Y=ten(2, 16, 32, F32), Z=ten(3, 16, 32)) == UNSUP
     # one expert's part past 2^31 bytes is refused, the whole stack's is not (here: refused for its alignment only)
     assert lin(X=ten(0, 16, 65536), W=ten(1, 4 * 16384, 65536)) == UNSUP
     assert lin(X=ten(0, 1 << 24, 64), Y=ten(2, 1 << 24, 32)) == UNSUP
@@ -184,7 +185,7 @@ def test_q8_refusals():
         return L.forge_expert_linear_q8(ref(q8(0, 16, 64)), ref(W or q8(1, 128, 64)), e, off, 0, ref(Y or ten(3, 16, 32)), None)
 
     assert ex(off=None) == NULL and ex(e=0) == SHAPE and ex(e=3) == SHAPE and ex(off=OFF + 4) == ALIGN
-    assert ex(Y=ten(3, 16, 128)) == SHAPE
+    assert ex(Y=ten(3, 16, 128)) == SHAPE and ex(Y=ten(3, 16, 32, 3)) == DTYPE
     assert L.forge_expert_gated_q8(ref(q8(0, 16, 64)), ref(q8(1, 128, 64)), None, 4, OFF, 0, ref(ten(3, 16, 32)), None) == NULL
 
 

@@ -130,6 +130,26 @@ def test_dispatch_and_combine(t, k, e, d, dt):
     assert none is None and torch.equal(only[:n], dYp[:n])
 
 
+@pytest.mark.parametrize("t,k,e,d", ROWS)
+def test_float32_results_of_bfloat16_tokens(t, k, e, d):
+    """Yp in float32, the tokens' side in bfloat16: combined and back"""
+    g = gen(t + d)
+    offsets, pos = forge.expert_plan(routes(t + d, t, k, e, dropped=0.2 if t > 1 else 0.0).cuda(), e)
+    n = int(offsets[-1])
+    Yp, R, dY = rnd(g, t * k, d, dtype=F), rnd(g, t, d), rnd(g, t, d)
+    Yp[n:] = NAN
+    w = torch.rand(t, k, device="cuda", generator=g)
+    close("combine", forge.expert_combine(Yp, pos, w, out_dtype=BF), *combine64(Yp, pos, w))
+    Y = forge.expert_combine(Yp, pos, w, residual=R)
+    assert Y.dtype == BF
+    close("residual", Y, *combine64(Yp, pos, w, R))
+    dYp, dw = forge.expert_combine_backward(dY, Yp, pos, w)
+    same, _ = forge.expert_combine_backward(dY, Yp.to(BF), pos, w)
+    assert dYp.dtype == BF and torch.equal(dYp[:n], same[:n])
+    prod = torch.where((pos >= 0)[:, :, None], Yp.double()[pos.long().clamp(min=0)] * dY.double()[:, None, :], 0.0)
+    close("dw", dw, prod.sum(2), (d + 1) * U * prod.abs().sum(2))
+
+
 def test_combine_pitched_rows_and_repeats():
     g = gen(3)
     idx = routes(3, 50, 3, 6, 0.2).cuda()
@@ -178,7 +198,7 @@ def test_dispatch_takes_int8_rows_and_their_factors():
 # has lanes; hundreds of rows
 SIZES = [([1], 8, 8), ([0, 1, 0], 512, 264), ([2, 0, 3], 72, 40), ([7, 0, 0, 9], 4096, 128), ([33, 1], 136, 1032),
          ([0, 130, 0, 64, 65, 1], 264, 520), ([257, 40, 0, 300], 96, 328), ([511, 513, 1], 1000, 776), ([1000], 256, 2056),
-         ([20] * 70, 128, 136), ([0] * 65 + [3, 150] + [0] * 100 + [1], 200, 72), ([900, 10, 1300, 700], 520, 1288)]
+         ([20] * 70, 128, 136), ([2500, 1, 0, 900, 1800], 192, 2600), ([1100, 1500, 700, 1290], 128, 4360), ([0] * 65 + [3, 150] + [0] * 100 + [1], 200, 72), ([900, 10, 1300, 700], 520, 1288)]
 
 
 def stacked(g, e, o, i, dtype, std=None):
@@ -212,6 +232,9 @@ def test_products(case, dt):
     X, W, Wu = rows(R, i), stacked(g, e, o, i, dtype), stacked(g, e, o, i, dtype)
     y, dy, z, dz = expert_linear64(X[used], W, loc, act)
     close(f"linear {act}", rest(forge.expert_linear(X, W, off, act=act, out=filled(R, o, dtype=dtype))), y, dy)
+    if i % 8 == 0 and o % 8 == 0:
+        y, dy = expert_linear64(X[used], W, loc, "none")[:2]
+        close("float32 sums", rest(forge.expert_linear(X, W, off, out=filled(R, o, dtype=F))), y, dy)
     Y, Z = forge.expert_linear(X, W, off, act=act, save=True)
     close("Z", Z[used], z, dz)
     h, dh, gt, dg, u, du = expert_gated64(X[used], W, Wu, loc, act)

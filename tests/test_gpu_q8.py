@@ -130,7 +130,7 @@ def test_pitched_rows():
 
 GROUPS = [([1], 16, 8), ([0, 1, 0], 512, 264), ([2, 0, 3], 80, 40), ([7, 0, 0, 9], 4096, 128), ([33, 1], 144, 1032),
           ([0, 130, 0, 64, 65, 1], 272, 520), ([257, 40, 0, 300], 96, 328), ([511, 513, 1], 1008, 776),
-          ([20] * 70, 128, 136), ([900, 10, 1300, 700], 528, 1288)]
+          ([20] * 70, 128, 136), ([2500, 1, 0, 900, 1800], 192, 2600), ([1100, 1500, 700, 1290], 128, 4360), ([900, 10, 1300, 700], 528, 1288)]
 
 
 @pytest.mark.parametrize("case", range(len(GROUPS)))
@@ -150,6 +150,11 @@ def test_grouped_by_expert(case):
     close(f"linear {act}", out[first:n],
           *grouped(loc, lambda a, x, s: linear_q8_64(x, s, Wg[a], sg[a], None, act), X[first:n], sx[first:n]))
     assert torch.all(out[:first] == 7.0) and torch.all(out[n:] == 7.0)
+    wide = torch.full((R, o), 7.0, device="cuda")
+    forge.expert_linear_q8(X, sx, Wg, sg, off, out=wide)
+    close("float32 sums", wide[first:n],
+          *grouped(loc, lambda a, x, s: linear_q8_64(x, s, Wg[a], sg[a]), X[first:n], sx[first:n]))
+    assert torch.all(wide[:first] == 7.0) and torch.all(wide[n:] == 7.0)
     out.fill_(7.0)
     forge.expert_gated_q8(X, sx, Wg, sg, Wu, su, off, act=act, out=out)
     close(f"gated {act}", out[first:n],
