@@ -377,7 +377,8 @@ def _own_run(s):
         offsets, pos = forge.expert_plan(s["idx"], s["e"])
         xp = forge.expert_dispatch(s["X"], pos)
         hid = forge.expert_gated(xp, s["Wg"], s["Wu"], offsets, act=act)
-        return [forge.expert_combine(forge.expert_linear(hid, s["Wd"], offsets), pos, s["w"])]
+        yp = forge.expert_linear(hid, s["Wd"], offsets, out_dtype=F32)
+        return [forge.expert_combine(yp, pos, s["w"], out_dtype=s["X"].dtype)]
     if op == "block_bwd":
         dg, du, hid = forge.expert_gated_dgrad(s["dYp"], s["Wd"], s["G"], s["U"], s["offsets"], act=act)
         return [dg, du, hid, forge.expert_dgrad_group([dg, du], [s["Wg"], s["Wu"]], s["offsets"])]
