@@ -25,6 +25,8 @@ Around the linear layers: ForgeLinear takes a bias and an activation and adds a 
 its forward product's epilogue, SwiGLUBlock(joined=True) runs gate, up, activation and
 product as one kernel, and ForgeHead is a linear head whose softmax cross entropy never
 stores its logits and whose backward pass steps its weights piece by piece of the vocabulary.
+ForgeExperts is a SwiGLU block of stacked experts, each token through those a router chose for it, whose backward
+pass steps all of them. LinearQ8 and ExpertsQ8 serve a layer and a block of experts with 8-bit weights.
 """
 from __future__ import annotations
 
@@ -349,9 +351,9 @@ def grouped_linear(layers, x: torch.Tensor):
 
 
 def step_all(model: torch.nn.Module) -> None:
-    """The optimizer phase of the two-phase schedule for every ForgeLinear in `model`."""
+    """The optimizer phase of the two-phase schedule for every ForgeLinear and ForgeStack in `model`."""
     for mod in model.modules():
-        if isinstance(mod, ForgeLinear):
+        if isinstance(mod, (ForgeLinear, ForgeStack)):
             mod.step()
 
 
@@ -520,3 +522,199 @@ class ForgeHead(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, targets: torch.Tensor, reduction: str = "mean") -> torch.Tensor:
         return _LinearCrossEntropyFn.apply(x, self.weight, targets, self.ignore_index, reduction, self)
+
+
+class ForgeStack(torch.nn.Module):
+    """The stacked weights [experts, out, in] of one layer of a ForgeExperts block, with their moments and step;
+    arguments as ForgeLinear's. The stack steps as one [experts * out, in] layer, all experts in one launch;
+    an expert that no token reached steps on a gradient of zero (decay and moments included)."""
+
+    def __init__(self, experts: int, in_features: int, out_features: int, opt: str = "adamw",
+                 hyper: Optional[dict] = None, states: str = "f32", dtype: torch.dtype = torch.bfloat16, device=None,
+                 seed: int = 0, fused: bool = True):
+        super().__init__()
+        weight = torch.empty(experts, out_features, in_features, dtype=dtype, device=device)
+        torch.nn.init.normal_(weight, std=0.02)
+        self.weight = torch.nn.Parameter(weight, requires_grad=True)
+        self.opt, self.hyper, self.fused = opt, forge.make_hyper(opt, **(hyper or {})), bool(fused)
+        m, v, ms, vs = forge.new_states(self.weight.detach(), opt, states)
+        self.code = "dynamic" if states == "q8dyn" else "linear"
+        for name, t in (("m", m), ("v", v), ("m_scale", ms), ("v_scale", vs)):
+            if t is None:
+                setattr(self, name, None)
+            else:
+                self.register_buffer(name, t)
+        self.seed = (int(seed) * _SEED_MIX) & (2 ** 64 - 1)
+        self.grad32: Optional[torch.Tensor] = None
+        self._step_count = 0
+
+    @property
+    def step_count(self) -> int:
+        return self._step_count
+
+    def _update(self, x2: torch.Tensor, dy2: torch.Tensor, offsets: torch.Tensor) -> None:
+        if not self.fused:
+            g = forge.expert_wgrad(x2, dy2, offsets)
+            if self.grad32 is None:
+                self.grad32 = g
+            else:
+                self.grad32.add_(g)
+            return
+        forge.expert_wgrad_step(x2, dy2, self.weight.detach(), self.m, self.v, offsets, self.opt, self.hyper,
+                                self._step_count + 1, self.seed, self.m_scale, self.v_scale, code=self.code)
+        self._step_count += 1
+
+    def step(self) -> None:
+        """Two-phase schedule: apply the optimizer to the stored gradient and free it (nothing to do for a fused
+        stack, whose backward already stepped)."""
+        if self.fused or self.grad32 is None:
+            return
+
+        def rows(t):
+            return None if t is None else t.view(-1, t.shape[-1])
+
+        forge.optimizer_step(rows(self.grad32), rows(self.weight.detach()), rows(self.m), rows(self.v), self.opt, self.hyper,
+                             self._step_count + 1, self.seed, rows(self.m_scale), rows(self.v_scale), code=self.code)
+        self._step_count += 1
+        self.grad32 = None
+
+
+class _ExpertsFn(torch.autograd.Function):
+    """y = r + sum_j w_j down_e(act(gate_e(x)) * up_e(x)) over a token's experts e. Kept for backward: the tokens,
+    the routes, the projections G, U, and the experts' results (float32) where the routing weights want a gradient.
+    Backward: the rows' gradients, dG, dU and H from their product with the down weights, dx of both projections -
+    all on the old weights - and then the steps."""
+
+    @staticmethod
+    def forward(ctx, x, idx, w, r, wg, wu, wd, block, recorded, want_w):
+        x2 = _rows(x, wg.shape[2], wg.dtype)
+        _same_rows("routes", idx.shape[:-1], x.shape[:-1])
+        i2 = idx.reshape(-1, idx.shape[-1]).contiguous()
+        w2 = w.reshape(-1, w.shape[-1]).float().contiguous()
+        r2 = None
+        if r is not None:
+            _same_rows("a residual", r.shape[:-1], x.shape[:-1])
+            r2 = _rows(r, wd.shape[1], wd.dtype)
+        offsets, pos = forge.expert_plan(i2, wg.shape[0])
+        out = forge.expert_gated(forge.expert_dispatch(x2, pos), wg.detach(), wu.detach(), offsets, act=block.act,
+                                 save=recorded)
+        H, G, U = out if recorded else (out, None, None)
+        yp = forge.expert_linear(H, wd.detach(), offsets, out_dtype=torch.float32)
+        y = forge.expert_combine(yp, pos, w2, residual=r2, out_dtype=wd.dtype)
+        ctx.block, ctx.x_shape, ctx.w_like = block, x.shape, (w.shape, w.dtype)
+        ctx.r_shape = None if r is None else r.shape
+        ctx.counts = [L._step_count for L in (block.gate, block.up, block.down)]
+        if recorded:
+            ctx.save_for_backward(x2, pos, offsets, w2, G, U, yp if want_w else None, wg, wu, wd)
+        return y.reshape(*x.shape[:-1], wd.shape[1])
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy):
+        gate, up, down = ctx.block.gate, ctx.block.up, ctx.block.down
+        _check_unstepped((gate, up, down), ctx.counts)
+        x2, pos, offsets, w2, G, U, yp, wg, wu, wd = ctx.saved_tensors
+        wg, wu, wd = wg.detach(), wu.detach(), wd.detach()
+        dy2 = _rows(dy, wd.shape[1], wd.dtype)
+        dyp, dw = forge.expert_combine_backward(dy2, yp, pos, w2, want_dweights=ctx.needs_input_grad[2])
+        dG, dU, H = forge.expert_gated_dgrad(dyp, wd, G, U, offsets, act=ctx.block.act)
+        dx = None
+        if ctx.needs_input_grad[0]:
+            dx = forge.expert_combine(forge.expert_dgrad_group([dG, dU], [wg, wu], offsets), pos).reshape(ctx.x_shape)
+        xp = forge.expert_dispatch(x2, pos)
+        down._update(H, dyp, offsets)
+        gate._update(xp, dG, offsets)
+        up._update(xp, dU, offsets)
+        if dw is not None:
+            dw = dw.reshape(ctx.w_like[0]).to(ctx.w_like[1])
+        return (dx, None, dw, dy.reshape(ctx.r_shape) if ctx.needs_input_grad[3] else None) + (None,) * 6
+
+
+class ForgeExperts(torch.nn.Module):
+    """A SwiGLU block of `experts` stacked experts (gate, up: [experts, hidden, d], down: [experts, d, hidden]) with the
+    optimizer step fused into the backward pass: forward(x, idx, weights) is sum over j of weights[t, j] times the
+    block of expert idx[t, j] on x[t], plus `residual` if given. idx [..., k] int64 and weights [..., k] come from the
+    router (an idx outside [0, experts) drops the route); x and weights receive gradients. Arguments as
+    ForgeLinear's; `act` the gate's activation. Rows are counted on the device: no call waits for the routes, and the
+    block can be captured into a graph. Each backward call is one step of all experts; a second one of an output computed
+    before it is refused (two-phase blocks, fused=False, take it, and step with step_all())."""
+
+    def __init__(self, d: int, hidden: int, experts: int, act: str = "silu", seed: int = 0, **kw):
+        super().__init__()
+        if act not in forge.ACTS:
+            raise ValueError(f"unknown activation {act!r}; one of {', '.join(forge.ACTS)}")
+        if not 1 <= experts <= forge.MAX_EXPERTS:
+            raise ValueError(f"1..{forge.MAX_EXPERTS} experts")
+        self.act = act
+        self.gate = ForgeStack(experts, d, hidden, seed=3 * seed, **kw)
+        self.up = ForgeStack(experts, d, hidden, seed=3 * seed + 1, **kw)
+        self.down = ForgeStack(experts, hidden, d, seed=3 * seed + 2, **kw)
+
+    def forward(self, x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor,
+                residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if idx.shape != weights.shape or idx.dim() < 1:
+            raise ValueError(f"routes of shape {tuple(idx.shape)} with weights of {tuple(weights.shape)}")
+        stacks = (self.gate.weight, self.up.weight, self.down.weight)
+        return _ExpertsFn.apply(x, idx, weights, residual, *stacks, self, _differentiated(x, weights, residual, *stacks),
+                                torch.is_grad_enabled() and weights.requires_grad)
+
+
+def _quantized(W: torch.Tensor):
+    """Codes of W's shape and one factor for each row of its last dimension"""
+    q, scale = forge.quantize_rows(W.detach().reshape(-1, W.shape[-1]))
+    return q.view(W.shape), scale
+
+
+class LinearQ8(torch.nn.Module):
+    """A ForgeLinear as it is now, for serving: weights in 8 bits with a factor for each output channel, tokens
+    quantised as they come, bias and activation in the product's epilogue; no gradients."""
+
+    def __init__(self, layer: ForgeLinear):
+        super().__init__()
+        self.act = layer.act
+        q, scale = _quantized(layer.weight)
+        self.register_buffer("codes", q)
+        self.register_buffer("scale", scale)
+        self.register_buffer("bias", None if layer.bias is None else layer.bias.detach().clone())
+
+    @torch.no_grad()
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        x2 = _rows(x, self.codes.shape[1], x.dtype)
+        r2 = None
+        if residual is not None:
+            _same_rows("a residual", residual.shape[:-1], x.shape[:-1])
+            r2 = _rows(residual, self.codes.shape[0], torch.bfloat16)
+        y = forge.linear_q8(*forge.quantize_rows(x2), self.codes, self.scale, bias=self.bias, act=self.act, residual=r2)
+        return y.reshape(*x.shape[:-1], self.codes.shape[0])
+
+
+class ExpertsQ8(torch.nn.Module):
+    """A ForgeExperts block as it is now, for serving: stacks in 8 bits with a factor for each output channel, tokens
+    quantised once and sent to their experts as codes, the hidden rows quantised again; no gradients."""
+
+    def __init__(self, block: ForgeExperts):
+        super().__init__()
+        self.act = block.act
+        for name in ("gate", "up", "down"):
+            q, scale = _quantized(getattr(block, name).weight)
+            self.register_buffer(name, q)
+            self.register_buffer(name + "_scale", scale)
+
+    @torch.no_grad()
+    def forward(self, x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor,
+                residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if idx.shape != weights.shape or idx.dim() < 1:
+            raise ValueError(f"routes of shape {tuple(idx.shape)} with weights of {tuple(weights.shape)}")
+        _same_rows("routes", idx.shape[:-1], x.shape[:-1])
+        r2 = None
+        if residual is not None:
+            _same_rows("a residual", residual.shape[:-1], x.shape[:-1])
+            r2 = _rows(residual, self.down.shape[1], torch.bfloat16)
+        k = idx.shape[-1]
+        offsets, pos = forge.expert_plan(idx.reshape(-1, k).contiguous(), self.gate.shape[0])
+        q, s = forge.quantize_rows(_rows(x, self.gate.shape[2], x.dtype))
+        qp, sp = forge.expert_dispatch(q, pos, scale=s)
+        H = forge.expert_gated_q8(qp, sp, self.gate, self.gate_scale, self.up, self.up_scale, offsets, act=self.act)
+        yp = forge.expert_linear_q8(*forge.quantize_rows(H), self.down, self.down_scale, offsets, out_dtype=torch.float32)
+        y = forge.expert_combine(yp, pos, weights.reshape(-1, k).float().contiguous(), residual=r2, out_dtype=torch.bfloat16)
+        return y.reshape(*x.shape[:-1], self.down.shape[1])
