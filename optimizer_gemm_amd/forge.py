@@ -549,9 +549,56 @@ class _On:
         return t
 
 
-# torch's own short ways to the device's current stream and to the current device: a few
-# microseconds less per call than a Stream object and the checks around them, which a tensor on
+_F32 = torch.float32
+
+
+class _Here:
+    """_On's common case, a call without a stream on tensors of the current device: nothing to switch, nothing to
+    note; one object per device, which calls of all threads share."""
+
+    __slots__ = ("device", "_index")
+
+    def __init__(self, device):
+        self.device, self._index = device, device.index
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return None
+
+    @property
+    def stream(self) -> int:
+        return _raw_stream(self._index)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        if _new is not None and len(shape) == 2:
+            rows, cols = shape
+            return _new((rows, cols), (cols or 1, 1), dtype)
+        return torch.empty(*shape, dtype=dtype, device=self.device)
+
+
+_here: Dict[int, _Here] = {}
+
+
+def _on(stream, first, *others):
+    """The device and stream of a call: _On, or its common case at half the host's time"""
+    index = first.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        return _On(stream, first, *others)
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError("the tensors of a call live on one device")
+    on = _here.get(index)
+    if on is None:
+        on = _here[index] = _Here(first.device)
+    return on
+
+
+# torch's own short ways to a new tensor on the current device, to the device's current stream and to the current
+# device: a few microseconds less per call than the public ones with the checks around them, which a tensor on
 # the device makes needless (the public ones where a build of torch lacks them)
+_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
@@ -565,6 +612,8 @@ def _ten(t: Optional[torch.Tensor]):
     rows, cols = t.shape
     s0, s1 = t.stride()
     dt = _DT.get(t.dtype)
+    if s1 == 1 and rows > 1 and cols and dt is not None:
+        return ForgeTensor(t.data_ptr(), dt, 0, rows, cols, s0)
     if dt is None:
         raise ValueError(f"unsupported dtype {t.dtype}")
     if rows == 0 or cols == 0:
@@ -609,7 +658,7 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     act one of ACTS. With save=True returns (Y, Z), Z = X W^T + bias, which
     linear_act_backward needs for an activation."""
     a = _act(act)
-    with _On(stream, X, W, bias, residual, out) as on:
+    with _on(stream, X, W, bias, residual, out) as on:
         Y = _same(on, out, (X.shape[0], W.shape[0]), W.dtype)
         Z = on.empty((X.shape[0], W.shape[0]), W.dtype) if save else None
         _check(_lib.forge_linear_forward(_ten(X), _ten(W), _row(bias), a,
@@ -626,7 +675,7 @@ def linear_act_backward(dY: torch.Tensor, Z: Optional[torch.Tensor] = None, act:
     a = _act(act)
     if act != "none" and Z is None:
         raise ValueError("the gradient through an activation needs Z")
-    with _On(stream, dY, Z, dZ) as on:
+    with _on(stream, dY, Z, dZ) as on:
         T, out = dY.shape
         if act == "none" and dZ is dY:
             dZ = None  # nothing to copy
@@ -651,7 +700,7 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
     """H = act(X Wg^T) * (X Wu^T), one kernel (forge_gated_forward): X [T, in], Wg and Wu
     [hidden, in]. With save=True returns (H, G, U), the projections the backward pass reads."""
     a = _act(act)
-    with _On(stream, X, Wg, Wu, out) as on:
+    with _on(stream, X, Wg, Wu, out) as on:
         shape = (X.shape[0], Wg.shape[0])
         H = _same(on, out, shape, Wg.dtype)
         G, U = (on.empty(shape, Wg.dtype), on.empty(shape, Wg.dtype)) if save else (None, None)
@@ -666,7 +715,7 @@ def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, act: str 
     """Backward of the gated product from dH: (dG, dU, H), dG = dH * U * act'(G),
     dU = dH * act(G), H = act(G) * U (None with want_h=False)."""
     a = _act(act)
-    with _On(stream, dH, G, U) as on:
+    with _on(stream, dH, G, U) as on:
         dG, dU = on.empty(dH.shape, dH.dtype), on.empty(dH.shape, dH.dtype)
         H = on.empty(dH.shape, dH.dtype) if want_h else None
         _check(_lib.forge_gated_backward(_ten(dH), _ten(G), _ten(U), a,
@@ -680,7 +729,7 @@ def gated_dgrad(dY: torch.Tensor, Wd: torch.Tensor, G: torch.Tensor, U: torch.Te
     """gated_backward with dH = dY Wd (the linear layer behind the block, its weights as they
     are now) formed in registers and never stored (forge_gated_dgrad): (dG, dU, H)."""
     a = _act(act)
-    with _On(stream, dY, Wd, G, U) as on:
+    with _on(stream, dY, Wd, G, U) as on:
         shape = (dY.shape[0], Wd.shape[1])
         dG, dU = on.empty(shape, Wd.dtype), on.empty(shape, Wd.dtype)
         H = on.empty(shape, Wd.dtype) if want_h else None
@@ -696,7 +745,7 @@ def dgrad_group(dYs, Ws, dX: Optional[torch.Tensor] = None, stream=None) -> torc
     n = len(Ws)
     if len(dYs) != n or not 1 <= n <= MAX_GROUP:
         raise ValueError(f"a group holds 1..{MAX_GROUP} layers, each with its dY and W")
-    with _On(stream, *dYs, *Ws, dX) as on:
+    with _on(stream, *dYs, *Ws, dX) as on:
         dX = _same(on, dX, (dYs[0].shape[0], Ws[0].shape[1]), Ws[0].dtype)
         dy_a = (ForgeTensor * n)(*[_ten(t) for t in dYs])
         w_a = (ForgeTensor * n)(*[_ten(t) for t in Ws])
@@ -730,7 +779,7 @@ def linear_cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
     ignored), each token's log sum of exponentials, and total = (sum of the losses, tokens
     counted, mean); linear_cross_entropy_backward takes the last two."""
     _reduction(reduction)
-    with _On(stream, X, W, targets) as on:
+    with _on(stream, X, W, targets) as on:
         T = X.shape[0]
         _vec(targets, T, torch.int64, "targets")
         loss = on.empty((T,), torch.float32) if reduction == "none" else None
@@ -765,7 +814,7 @@ def linear_cross_entropy_backward(X: torch.Tensor, W: torch.Tensor, targets: tor
     reduction="none"; lse and total as linear_cross_entropy returned them. Works through the
     vocabulary `piece` entries at a time (0: the library's choice)."""
     _reduction(reduction)
-    with _On(stream, X, W, targets, lse, dloss, total) as on:
+    with _on(stream, X, W, targets, lse, dloss, total) as on:
         need, ws, tot = _xent_grad_args(on, X, W, targets, lse, dloss, reduction, total, piece)
         dX = on.empty(X.shape, X.dtype) if want_dx else None
         dW = on.empty(W.shape, W.dtype) if want_dw else None
@@ -788,7 +837,7 @@ def linear_cross_entropy_step(X: torch.Tensor, W: torch.Tensor, m: Optional[torc
     2^31 bytes each."""
     _reduction(reduction)
     h = _hyper(opt, hyper)
-    with _On(stream, X, W, m, v, targets, lse, dloss, m_scale, v_scale, total) as on:
+    with _on(stream, X, W, m, v, targets, lse, dloss, m_scale, v_scale, total) as on:
         need, ws, tot = _xent_grad_args(on, X, W, targets, lse, dloss, reduction, total, piece)
         dX = on.empty(X.shape, X.dtype) if want_dx else None
         _check(_lib.forge_linear_xent_step(_ten(X), _ten(W), _ref(describe(m, m_scale, code=code)),
@@ -829,8 +878,11 @@ def _stack(W: Optional[torch.Tensor]):
 
 def _experts(W: torch.Tensor, offsets: torch.Tensor, *others) -> int:
     e = W.shape[0]
-    if W.dim() != 3 or any(w.dim() != 3 or w.shape[0] != e for w in others):
-        raise ValueError("stacked matrices [experts, out, in] of the same experts wanted")
+    if W.dim() != 3:
+        raise ValueError("stacked matrices [experts, out, in] wanted")
+    for w in others:
+        if w.dim() != 3 or w.shape[0] != e:
+            raise ValueError("stacked matrices [experts, out, in] of the same experts wanted")
     _vec(offsets, e + 1, torch.int64, "offsets")
     return e
 
@@ -859,7 +911,7 @@ def expert_plan(idx: torch.Tensor, experts: int, stream=None):
         raise ValueError("a token has one route at least")
     if not 1 <= experts <= MAX_EXPERTS:
         raise ValueError(f"1..{MAX_EXPERTS} experts")
-    with _On(stream, idx) as on:
+    with _on(stream, idx) as on:
         T, k = idx.shape
         offsets, pos = on.empty((experts + 1,), torch.int64), on.empty((T, k), torch.int32)
         need = _lib.forge_expert_plan_workspace(T, k, experts)
@@ -878,7 +930,7 @@ def expert_dispatch(X: torch.Tensor, pos: torch.Tensor, scale: Optional[torch.Te
     k = _places(pos)
     if (X.dtype == torch.int8) != (scale is not None):
         raise ValueError("int8 rows come with their factors, others without")
-    with _On(stream, X, pos, scale, out) as on:
+    with _on(stream, X, pos, scale, out) as on:
         if X.shape[0] != pos.shape[0]:
             raise ValueError("pos has the routes of another number of tokens")
         Xp = _same(on, out, (pos.numel(), X.shape[1]), X.dtype)
@@ -899,7 +951,7 @@ def expert_combine(Yp: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.
     float32 Yp with out_dtype=torch.bfloat16 (or a residual or out of that type)."""
     k = _places(pos)
     _factors(weights, pos)
-    with _On(stream, Yp, pos, weights, residual, out) as on:
+    with _on(stream, Yp, pos, weights, residual, out) as on:
         Y = _same(on, out, (pos.shape[0], Yp.shape[1]), out_dtype or (Yp if residual is None else residual).dtype)
         if Y.shape[0] != pos.shape[0]:
             raise ValueError("pos has the routes of another number of tokens")
@@ -917,7 +969,7 @@ def expert_combine_backward(dY: torch.Tensor, Yp: Optional[torch.Tensor], pos: t
     _factors(weights, pos)
     if want_dweights and Yp is None:
         raise ValueError("the weights' gradient needs Yp")
-    with _On(stream, dY, Yp, pos, weights) as on:
+    with _on(stream, dY, Yp, pos, weights) as on:
         if dY.shape[0] != pos.shape[0]:
             raise ValueError("pos has the routes of another number of tokens")
         rows = pos.numel() if Yp is None else Yp.shape[0]
@@ -935,7 +987,7 @@ def expert_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, act: 
     neither read nor written. With save=True returns (Y, Z), Z the pre-activation. out_dtype=torch.float32 of bfloat16
     operands, without an activation: the sums unrounded, for expert_combine."""
     a = _act(act)
-    with _On(stream, X, W, offsets, out) as on:
+    with _on(stream, X, W, offsets, out) as on:
         e = _experts(W, offsets)
         shape = (X.shape[0], W.shape[1])
         Y = _same(on, out, shape, out_dtype or W.dtype)
@@ -950,7 +1002,7 @@ def expert_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, offsets: t
     """gated() with each row's expert's matrices (forge_expert_gated): Wg, Wu [experts, hidden, in], rows and
     offsets as in expert_linear. With save=True returns (H, G, U)."""
     a = _act(act)
-    with _On(stream, X, Wg, Wu, offsets, out) as on:
+    with _on(stream, X, Wg, Wu, offsets, out) as on:
         e = _experts(Wg, offsets, Wu)
         shape = (X.shape[0], Wg.shape[1])
         H = _same(on, out, shape, Wg.dtype)
@@ -965,7 +1017,7 @@ def expert_gated_dgrad(dY: torch.Tensor, Wd: torch.Tensor, G: torch.Tensor, U: t
     """gated_dgrad() with each row's expert's matrix (forge_expert_gated_dgrad): Wd [experts, out, hidden];
     (dG, dU, H)."""
     a = _act(act)
-    with _On(stream, dY, Wd, G, U, offsets) as on:
+    with _on(stream, dY, Wd, G, U, offsets) as on:
         e = _experts(Wd, offsets)
         shape = (dY.shape[0], Wd.shape[2])
         dG, dU = on.empty(shape, Wd.dtype), on.empty(shape, Wd.dtype)
@@ -981,7 +1033,7 @@ def expert_dgrad_group(dYs, Ws, offsets: torch.Tensor, dX: Optional[torch.Tensor
     n = len(Ws)
     if len(dYs) != n or not 1 <= n <= MAX_GROUP:
         raise ValueError(f"a group holds 1..{MAX_GROUP} layers, each with its dY and W")
-    with _On(stream, *dYs, *Ws, offsets, dX) as on:
+    with _on(stream, *dYs, *Ws, offsets, dX) as on:
         e = _experts(Ws[0], offsets, *Ws[1:])
         dX = _same(on, dX, (dYs[0].shape[0], Ws[0].shape[2]), Ws[0].dtype)
         dy_a, w_a = (ForgeTensor * n)(*[_ten(t) for t in dYs]), (ForgeTensor * n)(*[_stack(t) for t in Ws])
@@ -995,7 +1047,7 @@ def expert_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor, dW: O
     """The stack's gradient dW[x] = dY^T X over each expert's rows, float32 [experts, out, in]
     (forge_expert_wgrad): the two-phase schedule's first half (optimizer_step on the stack as one
     [experts * out, in] layer is its second)."""
-    with _On(stream, X, dY, offsets, dW) as on:
+    with _on(stream, X, dY, offsets, dW) as on:
         e = offsets.numel() - 1
         _vec(offsets, e + 1, torch.int64, "offsets")
         dW = _same(on, dW, (e, dY.shape[1], X.shape[1]), torch.float32)
@@ -1016,7 +1068,7 @@ def expert_wgrad_step(X: torch.Tensor, dY: torch.Tensor, W: torch.Tensor, m: Opt
     [experts, out, in / 64], as new_states(W) makes them. The step is that of the stack as one [experts * out, in] layer:
     same element indices and random streams. Experts without rows step on a gradient of zero."""
     h = _hyper(opt, hyper)
-    with _On(stream, X, dY, W, m, v, offsets, m_scale, v_scale) as on:
+    with _on(stream, X, dY, W, m, v, offsets, m_scale, v_scale) as on:
         e = _experts(W, offsets)
 
         def state(t, scale):
@@ -1046,11 +1098,13 @@ def expert_wgrad_step(X: torch.Tensor, dY: torch.Tensor, W: torch.Tensor, m: Opt
 # ---------------------------------------------------------------------------
 def _codes(t: torch.Tensor, scale: torch.Tensor, what: str):
     """_ten() or _stack() of int8 rows with a factor each"""
-    if t.dtype != torch.int8:
-        raise ValueError(f"{what}: int8 codes wanted")
     d = _ten(t) if t.dim() == 2 else _stack(t)
-    _vec(scale, d.rows, torch.float32, f"factors of {what}")
-    d.scale = _ptr(scale)
+    if d.dtype != I8:
+        raise ValueError(f"{what}: int8 codes wanted")
+    if scale.dtype is not _F32 or scale.numel() != d.rows or not scale.is_contiguous():
+        raise ValueError(f"factors of {what}: {d.rows} contiguous float32 values wanted")
+    if d.rows:
+        d.scale = scale.data_ptr()
     return d
 
 
@@ -1060,7 +1114,7 @@ def quantize_rows(X: torch.Tensor, stream=None):
     row of zeros has scale 0; one with an infinity or NaN has scale NaN, and so NaN for its products. Weights
     are quantised the same way, one factor per output channel: a stack [experts, out, in] as its rows
     W.reshape(-1, in)."""
-    with _On(stream, X) as on:
+    with _on(stream, X) as on:
         Q, scale = on.empty(X.shape, torch.int8), on.empty((X.shape[0],), torch.float32)
         q = _ten(Q)
         q.scale = _ptr(scale)
@@ -1074,7 +1128,7 @@ def linear_q8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale: 
     """linear() of 8-bit integers (forge_linear_q8): X [T, in] and W [out, in] int8 with a factor for each row (token,
     output channel), as quantize_rows makes them; the sums are exact, the epilogue float32, Y bfloat16."""
     a = _act(act)
-    with _On(stream, X, x_scale, W, w_scale, bias, residual, out) as on:
+    with _on(stream, X, x_scale, W, w_scale, bias, residual, out) as on:
         Y = _same(on, out, (X.shape[0], W.shape[0]), torch.bfloat16)
         _check(_lib.forge_linear_q8(_codes(X, x_scale, "X"), _codes(W, w_scale, "W"), _row(bias), a, _ten(residual), _ten(Y),
                                     on.stream), "forge_linear_q8")
@@ -1085,7 +1139,7 @@ def gated_q8(X: torch.Tensor, x_scale: torch.Tensor, Wg: torch.Tensor, wg_scale:
              wu_scale: torch.Tensor, act: str = "silu", out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """gated() of 8-bit integers (forge_gated_q8), operands as in linear_q8; H bfloat16."""
     a = _act(act)
-    with _On(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, out) as on:
+    with _on(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, out) as on:
         H = _same(on, out, (X.shape[0], Wg.shape[0]), torch.bfloat16)
         _check(_lib.forge_gated_q8(_codes(X, x_scale, "X"), _codes(Wg, wg_scale, "Wg"), _codes(Wu, wu_scale, "Wu"), a, _ten(H),
                                    on.stream), "forge_gated_q8")
@@ -1099,7 +1153,7 @@ def expert_linear_q8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_
     factors, X and its factors as expert_dispatch(Q, pos, scale) returned them; Y bfloat16, or float32 without an
     activation, for expert_combine."""
     a = _act(act)
-    with _On(stream, X, x_scale, W, w_scale, offsets, out) as on:
+    with _on(stream, X, x_scale, W, w_scale, offsets, out) as on:
         e = _experts(W, offsets)
         Y = _same(on, out, (X.shape[0], W.shape[1]), out_dtype)
         _check(_lib.forge_expert_linear_q8(_codes(X, x_scale, "X"), _codes(W, w_scale, "W"), e, offsets.data_ptr(), a, _ten(Y),
@@ -1112,7 +1166,7 @@ def expert_gated_q8(X: torch.Tensor, x_scale: torch.Tensor, Wg: torch.Tensor, wg
                     stream=None) -> torch.Tensor:
     """expert_gated() of 8-bit integers (forge_expert_gated_q8), operands as in expert_linear_q8; H bfloat16."""
     a = _act(act)
-    with _On(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, offsets, out) as on:
+    with _on(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, offsets, out) as on:
         e = _experts(Wg, offsets, Wu)
         H = _same(on, out, (X.shape[0], Wg.shape[1]), torch.bfloat16)
         _check(_lib.forge_expert_gated_q8(_codes(X, x_scale, "X"), _codes(Wg, wg_scale, "Wg"), _codes(Wu, wu_scale, "Wu"), e,
