@@ -318,6 +318,15 @@ __device__ __forceinline__ int g_order(int tile, int ntiles) {
   }
   return tile;
 }
+// The same, with the ids of a round that the tiles do not fill made contiguous per XCD too (ids first, first + 1 ..
+// of n tiles): neighbouring tiles read the same panel of weights, which one XCD's L2 then fetches once.
+__device__ __forceinline__ int g_order_part(int tile, int ntiles) {
+  const int G = gridDim.x;
+  const int round0 = (tile / G) * G, n = min(G, ntiles - round0);
+  if ((G & 7) != 0) return tile;
+  const int w = tile - round0, x = w & 7;
+  return round0 + x * (n >> 3) + min(x, n & 7) + (w >> 3);
+}
 __device__ __forceinline__ void g_place(int L, int ntm, int ntn, int& tm, int& tn) {
   constexpr int GROUP = 4;
   const int per = GROUP * ntn;

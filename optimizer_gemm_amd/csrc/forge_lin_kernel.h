@@ -273,12 +273,12 @@ void lin_kernel(LinArgs g) {
       tile /= splits;
     }
     if constexpr (EXP) {
-      const int L = TAIL ? tail0 + (tile >> 2) : g_order(tile, ntiles);
+      const int at = g_order_part(tile, ntiles), L = TAIL ? tail0 + (at >> 2) : at;
       int r0, t0;
       xr.find(L / ntm, lx, r0, lend, t0);
       g_place(L - t0 * ntm, ntm, (lend - r0 + XN - 1) / XN, tm, tn);
-      lm0 = tm * XM + (TAIL ? (tile & 1) * OM : 0);
-      ln0 = r0 + tn * XN + (TAIL ? (tile >> 1 & 1) * C::BN : 0);  // (past the expert's end: nothing is read or written)
+      lm0 = tm * XM + (TAIL ? (at & 1) * OM : 0);
+      ln0 = r0 + tn * XN + (TAIL ? (at >> 1 & 1) * C::BN : 0);  // (past the expert's end: nothing is read or written)
     } else {
       g_tile(tile, ntm, ntn, tm, tn);
       lm0 = g.m_off + tm * OM;
@@ -914,7 +914,8 @@ hipError_t lin_run(const LinArgs& g, hipStream_t st) {
   const int64_t tiles = MODE & LM_TAIL ? 2 * g.round : ntm * ntn * (EPI == L_ACC && TA && !TB && !EXP ? g.splits : 1);
   if (tiles <= 0) return hipSuccess;
   const int64_t resident = (int64_t)(C::OCC * 4 / C::NW) * g_num_cus();
-  hipLaunchKernelGGL((lin_kernel<C, EPI, TA, TB, MODE>), dim3((uint32_t)(tiles < resident ? tiles : resident)), dim3(C::NT), 0,
+  const int64_t want = EXP ? (tiles + 7) / 8 * 8 : tiles;  // (whole XCDs, for the tiles' order)
+  hipLaunchKernelGGL((lin_kernel<C, EPI, TA, TB, MODE>), dim3((uint32_t)(want < resident ? want : resident)), dim3(C::NT), 0,
                      st, g);
   return hipGetLastError();
 }
@@ -993,10 +994,13 @@ hipError_t lin_bf16(const LinArgs& g, hipStream_t st) {
 
 // Products grouped by expert. Their sizes are in device memory; the host counts the tiles that sizes spread
 // exponentially around their mean would give (of b rows: 1 / (1 - e^(-b / mean)) an expert, the mean / b + 1/2 of a large
-// mean), and compares the kinds by a stage's time in us, given the rounds of the chip they take:
-//   256x256, one a unit: 1.35 a round, a last round that is at most half full 0.79 (its quarters, LM_TAIL);
-//   128x128, two a unit: 0.79 a round, 0.70 for one that is not full, 0.71 for 8-bit operands;
-//   64x64 with four groups of waves: 0.47, each further round 0.31.
+// mean), and compares the kinds by us for each stage and each tile, given the rounds of the chip they take (fitted to
+// 78 sweeps over 8 to 64 experts, 16 to 2048 rows of each; the kind taken is within 13% of the best in all of them):
+//   256x256, one a unit: 1.45 a stage and 10 a tile; a last round that is at most half full runs as quarters
+//     (LM_TAIL), 0.79 and 12;
+//   128x128, two a unit: 1.0 a stage (8-bit 0.85) and 3 a tile; a round that is not full at least 0.7 of that;
+//   64x64 with four groups of waves: 0.31 a stage and 5 a tile, and 0.16 a stage once.
+// Epilogues that read what they write beside, and operands whose k is slow, cost 15 (8) or 20 (14) more a tile.
 // Measured: 8 experts of 2048 rows, 4096 -> 2 x 14336 gated 2927 us against 3974, the input gradient of both
 // 3162 (3488 without the quarters) against 4828; 8 of 128 rows, 4096 -> 2 x 3584 gated 173 against 116, 8-bit
 // 99 against 57; 16 of 8 rows, 4096 -> 1792: 128x128 45, 64x64 31.
@@ -1010,13 +1014,15 @@ hipError_t lin_expert(const LinArgs& g0, hipStream_t st) {
     return (double)((w + b - 1) / b) * used * n / (double)(per_cu * cus);
   };
   const double big = rounds(256, 1), small = rounds(128, 2), tiny = rounds(64, 1);
-  const double part = big - floor(big);
   double stages = 0.0;
   for (int s = 0; s < g.nsrc; ++s) stages += (g.K[s] + 63) / 64;
-  const double one = 1.35 * stages + 12.0;
-  const double t_big = big >= 1.0 && part <= 0.5 ? one * floor(big) + (part > 0.0 ? 0.79 * stages + 12.0 : 0.0) : one * ceil(big);
-  const double t_small = (small <= 1.0 ? 0.70 * stages : (MODE & LM_Q8 ? 0.71 : 0.79) * stages * ceil(small)) + 5.0 * ceil(small);
-  const double t_tiny = 0.16 * stages + (0.31 * stages + 5.0) * ceil(tiny);
+  const double more = EPI == L_DGATE ? 20.0 : TA ? 15.0 : 0.0, more_small = EPI == L_DGATE ? 14.0 : TA ? 8.0 : 0.0;
+  const double one_big = 1.45 * stages + 10.0 + more, one_small = (MODE & LM_Q8 ? 0.85 : 1.0) * stages + 3.0 + more_small;
+  const double fb = floor(big), fs = floor(small);
+  const double t_big = fb >= 1.0 && big - fb <= 0.5 ? one_big * fb + (big > fb ? 0.79 * stages + 12.0 + more_small : 0.0)
+                                                    : one_big * ceil(big);
+  const double t_small = one_small * (fs + (small > fs ? fmax(0.7, small - fs) : 0.0));
+  const double t_tiny = 0.16 * stages + (0.31 * stages + 5.0 + more_small) * ceil(tiny);
   if (t_tiny < t_small && t_tiny < t_big) return lin_run<LinTiny, EPI, TA, false, MODE>(g, st);
   if (t_small <= t_big) return lin_run<LinSmall, EPI, TA, false, MODE>(g, st);
   // where there can be more large tiles than a round has (whatever the experts' sizes are)
