@@ -27,7 +27,8 @@
  *     error nothing is launched and a negative status is returned. No entry
  *     point keeps global mutable state and calls are thread-safe, except for
  *     forge_linear_wgrad_unfused_noalloc (its per-GPU scratch; see there).
- *   - Results are deterministic: fixed reduction order, no atomics.
+ *   - Results are deterministic: fixed reduction order, no atomics (but on integer counts, whose order
+ *     does not matter).
  */
 #ifndef FORGE_H
 #define FORGE_H

@@ -276,7 +276,10 @@ void lin_kernel(LinArgs g) {
       const int at = g_order_part(tile, ntiles), L = TAIL ? tail0 + (at >> 2) : at;
       int r0, t0;
       xr.find(L / ntm, lx, r0, lend, t0);
-      g_place(L - t0 * ntm, ntm, (lend - r0 + XN - 1) / XN, tm, tn);
+      const int nt = (lend - r0 + XN - 1) / XN;
+      g_place(L - t0 * ntm, ntm, max(nt, 1), tm, tn);
+      tm = min(max(tm, 0), ntm - 1);  // (whatever offsets that are none lead to)
+      tn = min(max(tn, 0), max(nt - 1, 0));
       lm0 = tm * XM + (TAIL ? (at & 1) * OM : 0);
       ln0 = r0 + tn * XN + (TAIL ? (at >> 1 & 1) * C::BN : 0);  // (past the expert's end: nothing is read or written)
     } else {
@@ -680,7 +683,7 @@ void lin_kernel(LinArgs g) {
 #pragma unroll
           for (int k = 0; k < NV; ++k) {
             const int n = nw + 32 * (blk / CH) + e_row + k * RS;
-            P.sx[k] = e.sx[n < n_end ? n : n_end - 1];
+            P.sx[k] = e.sx[n < n_end ? n : max(n_end - 1, 0)];
           }
           const int m = mw + OWB * (blk % CH) + 8 * e_col, mc = m < Mw ? m : 0;
           P.sw[0] = load4(e.sw + sw0 + mc);

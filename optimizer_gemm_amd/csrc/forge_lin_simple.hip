@@ -115,7 +115,7 @@ __global__ __launch_bounds__(S_NT) void lin_simple_kernel(LinArgs g) {
   if constexpr (EXP) {
     int t0;
     xr.find(tn, ex, r0, n_end, t0);
-    tn -= t0;
+    tn = min(max(tn - t0, 0), max((n_end - r0 + S_B - 1) / S_B - 1, 0));  // (whatever offsets that are none lead to)
   }
   const int m0 = g.m_off + (int)(tile % tiles_m) * S_B, n0 = r0 + tn * S_B;
   f32x16 acc, acc2;

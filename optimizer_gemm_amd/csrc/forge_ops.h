@@ -233,14 +233,16 @@ struct ExpertRows {
       if (lane >= h) upto += other;
     }
   }
-  // tiles of rows of all experts; afterwards the first 64 are loaded
+  // tiles of rows of all experts (offsets that are none may claim rows twice: no more than there can be);
+  // afterwards the first 64 are loaded
   __device__ __forceinline__ int total() {
-    int n = 0;
+    int64_t n = 0;
     for (int first = (experts - 1) / 64 * 64; first >= 0; first -= 64) {
       load(first);
       n += __builtin_amdgcn_readlane(upto, 63);
     }
-    return n;
+    const int64_t most = (rows + BN - 1) / BN + min(experts, rows);
+    return (int)(n < most ? n : most);
   }
   // the expert of row tile q, its first row and its end, its first row tile
   __device__ __forceinline__ void find(int q, int& x, int& first_row, int& end_row, int& first_tile) {

@@ -296,13 +296,20 @@ def test_offsets_that_are_no_offsets_stay_inside(dt):
     g = gen(9)
     around = filled(300, 64, dtype=dtype)
     X, W = rnd(g, 100, 32, dtype=dtype), stacked(g, 4, 64, 32, dtype)
-    for o in ([-5, 10, 400, 50, 2 ** 40], [90, 20, 10, 0, -1], [2 ** 62, -2 ** 62, 2 ** 62, 7, 100], [100, 100, 100, 100, 2 ** 33]):
+    for o in ([-5, 10, 400, 50, 2 ** 40], [90, 20, 10, 0, -1], [2 ** 62, -2 ** 62, 2 ** 62, 7, 100], [100, 100, 100, 100, 2 ** 33],
+              [0, 100, 0, 100, 0], [100, 0, 100, 0, 100]):
         off = torch.tensor(o, device="cuda")
         forge.expert_linear(X, W, off, out=around[100:200])
         forge.expert_gated(X, W, W, off, out=around[100:200])
         D = rnd(g, 100, 64, dtype=dtype)
         forge.expert_dgrad_group([D], [W], off)
         forge.expert_wgrad(X, D, off)
+        if dtype == BF:
+            forge.expert_linear(X, W, off, out=filled(100, 64, dtype=F))
+            Q, s = forge.quantize_rows(X)
+            q, sw = forge.quantize_rows(W.reshape(-1, 32))
+            forge.expert_linear_q8(Q, s, q.view(4, 64, 32), sw, off, out=around[100:200])
+            forge.expert_gated_q8(Q, s, q.view(4, 64, 32), sw, q.view(4, 64, 32), sw, off, out=around[100:200])
         assert torch.all(around[:100] == 7.0) and torch.all(around[200:] == 7.0)
 
 
