@@ -572,9 +572,13 @@ class _Here:
         return _raw_stream(self._index)
 
     def empty(self, shape, dtype) -> torch.Tensor:
-        if _new is not None and len(shape) == 2:
-            rows, cols = shape
-            return _new((rows, cols), (cols or 1, 1), dtype)
+        if _new is not None:
+            n = len(shape)
+            if n == 2:
+                rows, cols = shape
+                return _new((rows, cols), (cols or 1, 1), dtype)
+            if n == 1:
+                return _new((shape[0],), (1,), dtype)
         return torch.empty(*shape, dtype=dtype, device=self.device)
 
 
@@ -612,8 +616,8 @@ def _ten(t: Optional[torch.Tensor]):
     rows, cols = t.shape
     s0, s1 = t.stride()
     dt = _DT.get(t.dtype)
-    if s1 == 1 and rows > 1 and cols and dt is not None:
-        return ForgeTensor(t.data_ptr(), dt, 0, rows, cols, s0)
+    if s1 == 1 and rows and cols and dt is not None:
+        return ForgeTensor(t.data_ptr(), dt, 0, rows, cols, s0 if rows > 1 else cols)
     if dt is None:
         raise ValueError(f"unsupported dtype {t.dtype}")
     if rows == 0 or cols == 0:
