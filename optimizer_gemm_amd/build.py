@@ -2,8 +2,10 @@
 
 Usage: python optimizer_gemm_amd/build.py   (or __graft_entry__.build()); run by path,
 since importing the package loads the library this script builds.
-The library lands in optimizer_gemm_amd/_lib/libforge.so; object files in
-optimizer_gemm_amd/_build/. Every call recompiles.
+The library lands in optimizer_gemm_amd/_lib/libforge.so, the Python calls of some of its entry
+points (csrc/forge_calls.cpp, host code against torch's C++ interface) in
+optimizer_gemm_amd/_lib/forge_calls.so; object files in optimizer_gemm_amd/_build/. Every call
+recompiles.
 
 python optimizer_gemm_amd/build.py --sanitize builds the host-checking variant,
 optimizer_gemm_amd/_build/san/libforge_san.so: AddressSanitizer and
@@ -15,10 +17,12 @@ ASAN_OPTIONS=detect_leaks=0 (the interpreter keeps its allocations to the end).
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +30,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libforge.so")
+CALLS = os.path.join(LIBDIR, "forge_calls.so")
 ARCH = os.environ.get("FORGE_OFFLOAD_ARCH", "gfx950")
 
 # every HIP source of csrc/ (the fused-step instantiations are split over several
@@ -86,12 +91,31 @@ def _compile_all(out_dir: str, extra=()) -> list:
         return list(ex.map(lambda s: _compile(s, out_dir, extra), SOURCES))
 
 
+def _build_calls() -> str:
+    """The extension module of csrc/forge_calls.cpp; its undefined symbols are the interpreter's and torch's."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "forge_calls.cpp"), "-o", tmp,
+           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for forge_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(LIBDIR, exist_ok=True)
-    objs = [o for o, _ in _compile_all(BUILD)]
-    _link(objs, LIB)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(_build_calls)
+        objs = [o for o, _ in _compile_all(BUILD)]
+        _link(objs, LIB)
+        calls.result()
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB}\nbuilt {CALLS}")
     return LIB
 
 

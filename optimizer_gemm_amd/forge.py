@@ -8,6 +8,7 @@ not built, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Dict, Optional
 
@@ -52,6 +53,18 @@ class ForgeError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {STATUS.get(status, status)} ({status_str(status)})")
         self.status = status
+
+
+def _load_calls():
+    """The module of csrc/forge_calls.cpp: entry points that take tensors as they are, at a fraction of ctypes' time."""
+    path = os.path.join(_PKG, "_lib", "forge_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"forge_calls.so not built at {path}; run `python optimizer_gemm_amd/build.py`")
+    spec = importlib.util.spec_from_file_location("forge_calls", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.load(LIB_PATH, ForgeError)
+    return mod
 
 
 def _load() -> ctypes.CDLL:
@@ -155,6 +168,7 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+_calls = _load_calls()
 
 
 def lib() -> ctypes.CDLL:
@@ -593,10 +607,19 @@ def _on(stream, first, *others):
     for t in others:
         if t is not None and t.get_device() != index:
             raise ValueError("the tensors of a call live on one device")
-    on = _here.get(index)
-    if on is None:
-        on = _here[index] = _Here(first.device)
-    return on
+    return _here.get(index) or _here_new(first)
+
+
+def _at(stream, first, *others):
+    """_on for the calls of forge_calls.cpp, which check the others' device themselves"""
+    index = first.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        return _On(stream, first, *others)
+    return _here.get(index) or _here_new(first)
+
+
+def _here_new(first) -> _Here:
+    return _here.setdefault(first.get_device(), _Here(first.device))
 
 
 # torch's own short ways to a new tensor on the current device, to the device's current stream and to the current
@@ -915,13 +938,12 @@ def expert_plan(idx: torch.Tensor, experts: int, stream=None):
         raise ValueError("a token has one route at least")
     if not 1 <= experts <= MAX_EXPERTS:
         raise ValueError(f"1..{MAX_EXPERTS} experts")
-    with _on(stream, idx) as on:
+    with _at(stream, idx) as on:
         T, k = idx.shape
         offsets, pos = on.empty((experts + 1,), torch.int64), on.empty((T, k), torch.int32)
-        need = _lib.forge_expert_plan_workspace(T, k, experts)
+        need = _calls.forge_expert_plan_workspace(T, k, experts)
         ws = on.empty((need,), torch.uint8) if need else None
-        _check(_lib.forge_expert_plan(_ptr(idx), T, k, experts, offsets.data_ptr(), _ptr(pos), _ptr(ws), need, on.stream),
-               "forge_expert_plan")
+        _calls.forge_expert_plan(idx, T, k, experts, offsets, pos, ws, need, on.stream)
     return offsets, pos
 
 
@@ -934,17 +956,16 @@ def expert_dispatch(X: torch.Tensor, pos: torch.Tensor, scale: Optional[torch.Te
     k = _places(pos)
     if (X.dtype == torch.int8) != (scale is not None):
         raise ValueError("int8 rows come with their factors, others without")
-    with _on(stream, X, pos, scale, out) as on:
+    with _at(stream, X, pos, scale, out) as on:
         if X.shape[0] != pos.shape[0]:
             raise ValueError("pos has the routes of another number of tokens")
         Xp = _same(on, out, (pos.numel(), X.shape[1]), X.dtype)
-        x, y, sp = _ten(X), _ten(Xp), None
-        if scale is not None:
-            _vec(scale, X.shape[0], torch.float32, "scale")
-            sp = on.empty((Xp.shape[0],), torch.float32)
-            x.scale, y.scale = _ptr(scale), _ptr(sp)
-        _check(_lib.forge_expert_dispatch(x, _ptr(pos), k, y, on.stream), "forge_expert_dispatch")
-    return Xp if scale is None else (Xp, sp)
+        if scale is None:
+            _calls.forge_expert_dispatch(X, pos, k, Xp, on.stream)
+            return Xp
+        sp = on.empty((Xp.shape[0],), _F32)
+        _calls.forge_expert_dispatch((X, scale), pos, k, (Xp, sp), on.stream)
+        return Xp, sp
 
 
 def expert_combine(Yp: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -955,12 +976,11 @@ def expert_combine(Yp: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.
     float32 Yp with out_dtype=torch.bfloat16 (or a residual or out of that type)."""
     k = _places(pos)
     _factors(weights, pos)
-    with _on(stream, Yp, pos, weights, residual, out) as on:
+    with _at(stream, Yp, pos, weights, residual, out) as on:
         Y = _same(on, out, (pos.shape[0], Yp.shape[1]), out_dtype or (Yp if residual is None else residual).dtype)
         if Y.shape[0] != pos.shape[0]:
             raise ValueError("pos has the routes of another number of tokens")
-        _check(_lib.forge_expert_combine(_ten(Yp), _ptr(pos), k, _ptr(weights), _ten(residual), _ten(Y), on.stream),
-               "forge_expert_combine")
+        _calls.forge_expert_combine(Yp, pos, k, weights, residual, Y, on.stream)
     return Y
 
 
@@ -973,14 +993,13 @@ def expert_combine_backward(dY: torch.Tensor, Yp: Optional[torch.Tensor], pos: t
     _factors(weights, pos)
     if want_dweights and Yp is None:
         raise ValueError("the weights' gradient needs Yp")
-    with _on(stream, dY, Yp, pos, weights) as on:
+    with _at(stream, dY, Yp, pos, weights) as on:
         if dY.shape[0] != pos.shape[0]:
             raise ValueError("pos has the routes of another number of tokens")
         rows = pos.numel() if Yp is None else Yp.shape[0]
         dYp = on.empty((rows, dY.shape[1]), dY.dtype)
         dw = on.empty(pos.shape, torch.float32) if want_dweights else None
-        _check(_lib.forge_expert_combine_backward(_ten(dY), _ten(Yp) if want_dweights else None, _ptr(pos), k, _ptr(weights),
-                                                  _ten(dYp), _ptr(dw), on.stream), "forge_expert_combine_backward")
+        _calls.forge_expert_combine_backward(dY, Yp if want_dweights else None, pos, k, weights, dYp, dw, on.stream)
     return dYp, dw
 
 
@@ -991,13 +1010,12 @@ def expert_linear(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, act: 
     neither read nor written. With save=True returns (Y, Z), Z the pre-activation. out_dtype=torch.float32 of bfloat16
     operands, without an activation: the sums unrounded, for expert_combine."""
     a = _act(act)
-    with _on(stream, X, W, offsets, out) as on:
+    with _at(stream, X, W, offsets, out) as on:
         e = _experts(W, offsets)
         shape = (X.shape[0], W.shape[1])
         Y = _same(on, out, shape, out_dtype or W.dtype)
         Z = on.empty(shape, W.dtype) if save else None
-        _check(_lib.forge_expert_linear(_ten(X), _stack(W), e, offsets.data_ptr(), a, _ten(Y), _ten(Z), on.stream),
-               "forge_expert_linear")
+        _calls.forge_expert_linear(X, W, e, offsets, a, Y, Z, on.stream)
     return (Y, Z) if save else Y
 
 
@@ -1006,13 +1024,12 @@ def expert_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, offsets: t
     """gated() with each row's expert's matrices (forge_expert_gated): Wg, Wu [experts, hidden, in], rows and
     offsets as in expert_linear. With save=True returns (H, G, U)."""
     a = _act(act)
-    with _on(stream, X, Wg, Wu, offsets, out) as on:
+    with _at(stream, X, Wg, Wu, offsets, out) as on:
         e = _experts(Wg, offsets, Wu)
         shape = (X.shape[0], Wg.shape[1])
         H = _same(on, out, shape, Wg.dtype)
         G, U = (on.empty(shape, Wg.dtype), on.empty(shape, Wg.dtype)) if save else (None, None)
-        _check(_lib.forge_expert_gated(_ten(X), _stack(Wg), _stack(Wu), e, offsets.data_ptr(), a, _ten(H), _ten(G), _ten(U),
-                                       on.stream), "forge_expert_gated")
+        _calls.forge_expert_gated(X, Wg, Wu, e, offsets, a, H, G, U, on.stream)
     return (H, G, U) if save else H
 
 
@@ -1021,13 +1038,12 @@ def expert_gated_dgrad(dY: torch.Tensor, Wd: torch.Tensor, G: torch.Tensor, U: t
     """gated_dgrad() with each row's expert's matrix (forge_expert_gated_dgrad): Wd [experts, out, hidden];
     (dG, dU, H)."""
     a = _act(act)
-    with _on(stream, dY, Wd, G, U, offsets) as on:
+    with _at(stream, dY, Wd, G, U, offsets) as on:
         e = _experts(Wd, offsets)
         shape = (dY.shape[0], Wd.shape[2])
         dG, dU = on.empty(shape, Wd.dtype), on.empty(shape, Wd.dtype)
         H = on.empty(shape, Wd.dtype) if want_h else None
-        _check(_lib.forge_expert_gated_dgrad(_ten(dY), _stack(Wd), _ten(G), _ten(U), e, offsets.data_ptr(), a, _ten(dG),
-                                             _ten(dU), _ten(H), on.stream), "forge_expert_gated_dgrad")
+        _calls.forge_expert_gated_dgrad(dY, Wd, G, U, e, offsets, a, dG, dU, H, on.stream)
     return dG, dU, H
 
 
@@ -1037,12 +1053,10 @@ def expert_dgrad_group(dYs, Ws, offsets: torch.Tensor, dX: Optional[torch.Tensor
     n = len(Ws)
     if len(dYs) != n or not 1 <= n <= MAX_GROUP:
         raise ValueError(f"a group holds 1..{MAX_GROUP} layers, each with its dY and W")
-    with _on(stream, *dYs, *Ws, offsets, dX) as on:
+    with _at(stream, *dYs, *Ws, offsets, dX) as on:
         e = _experts(Ws[0], offsets, *Ws[1:])
         dX = _same(on, dX, (dYs[0].shape[0], Ws[0].shape[2]), Ws[0].dtype)
-        dy_a, w_a = (ForgeTensor * n)(*[_ten(t) for t in dYs]), (ForgeTensor * n)(*[_stack(t) for t in Ws])
-        _check(_lib.forge_expert_dgrad_group(n, dy_a, w_a, e, offsets.data_ptr(), _ten(dX), on.stream),
-               "forge_expert_dgrad_group")
+        _calls.forge_expert_dgrad_group(n, list(dYs), list(Ws), e, offsets, dX, on.stream)
     return dX
 
 
@@ -1100,29 +1114,16 @@ def expert_wgrad_step(X: torch.Tensor, dY: torch.Tensor, W: torch.Tensor, m: Opt
 # ---------------------------------------------------------------------------
 # products of 8-bit integers
 # ---------------------------------------------------------------------------
-def _codes(t: torch.Tensor, scale: torch.Tensor, what: str):
-    """_ten() or _stack() of int8 rows with a factor each"""
-    d = _ten(t) if t.dim() == 2 else _stack(t)
-    if d.dtype != I8:
-        raise ValueError(f"{what}: int8 codes wanted")
-    if scale.dtype is not _F32 or scale.numel() != d.rows or not scale.is_contiguous():
-        raise ValueError(f"factors of {what}: {d.rows} contiguous float32 values wanted")
-    if d.rows:
-        d.scale = scale.data_ptr()
-    return d
-
-
 def quantize_rows(X: torch.Tensor, stream=None):
     """Rows to 8 bits (forge_quantize_rows): X [rows, cols] float32 or bfloat16, cols a multiple of 16; returns (Q, scale),
     int8 codes and one float32 factor per row, scale = max |x| / 127 and Q = x / scale to the nearest. A
     row of zeros has scale 0; one with an infinity or NaN has scale NaN, and so NaN for its products. Weights
     are quantised the same way, one factor per output channel: a stack [experts, out, in] as its rows
     W.reshape(-1, in)."""
-    with _on(stream, X) as on:
-        Q, scale = on.empty(X.shape, torch.int8), on.empty((X.shape[0],), torch.float32)
-        q = _ten(Q)
-        q.scale = _ptr(scale)
-        _check(_lib.forge_quantize_rows(_ten(X), q, on.stream), "forge_quantize_rows")
+    with _at(stream, X) as on:
+        shape = X.shape
+        Q, scale = on.empty(shape, torch.int8), on.empty((shape[0],), _F32)
+        _calls.forge_quantize_rows(X, (Q, scale), on.stream)
     return Q, scale
 
 
@@ -1132,10 +1133,9 @@ def linear_q8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale: 
     """linear() of 8-bit integers (forge_linear_q8): X [T, in] and W [out, in] int8 with a factor for each row (token,
     output channel), as quantize_rows makes them; the sums are exact, the epilogue float32, Y bfloat16."""
     a = _act(act)
-    with _on(stream, X, x_scale, W, w_scale, bias, residual, out) as on:
+    with _at(stream, X, x_scale, W, w_scale, bias, residual, out) as on:
         Y = _same(on, out, (X.shape[0], W.shape[0]), torch.bfloat16)
-        _check(_lib.forge_linear_q8(_codes(X, x_scale, "X"), _codes(W, w_scale, "W"), _row(bias), a, _ten(residual), _ten(Y),
-                                    on.stream), "forge_linear_q8")
+        _calls.forge_linear_q8((X, x_scale), (W, w_scale), bias, a, residual, Y, on.stream)
     return Y
 
 
@@ -1143,10 +1143,9 @@ def gated_q8(X: torch.Tensor, x_scale: torch.Tensor, Wg: torch.Tensor, wg_scale:
              wu_scale: torch.Tensor, act: str = "silu", out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """gated() of 8-bit integers (forge_gated_q8), operands as in linear_q8; H bfloat16."""
     a = _act(act)
-    with _on(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, out) as on:
+    with _at(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, out) as on:
         H = _same(on, out, (X.shape[0], Wg.shape[0]), torch.bfloat16)
-        _check(_lib.forge_gated_q8(_codes(X, x_scale, "X"), _codes(Wg, wg_scale, "Wg"), _codes(Wu, wu_scale, "Wu"), a, _ten(H),
-                                   on.stream), "forge_gated_q8")
+        _calls.forge_gated_q8((X, x_scale), (Wg, wg_scale), (Wu, wu_scale), a, H, on.stream)
     return H
 
 
@@ -1157,11 +1156,10 @@ def expert_linear_q8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_
     factors, X and its factors as expert_dispatch(Q, pos, scale) returned them; Y bfloat16, or float32 without an
     activation, for expert_combine."""
     a = _act(act)
-    with _on(stream, X, x_scale, W, w_scale, offsets, out) as on:
+    with _at(stream, X, x_scale, W, w_scale, offsets, out) as on:
         e = _experts(W, offsets)
         Y = _same(on, out, (X.shape[0], W.shape[1]), out_dtype)
-        _check(_lib.forge_expert_linear_q8(_codes(X, x_scale, "X"), _codes(W, w_scale, "W"), e, offsets.data_ptr(), a, _ten(Y),
-                                           on.stream), "forge_expert_linear_q8")
+        _calls.forge_expert_linear_q8((X, x_scale), (W, w_scale), e, offsets, a, Y, on.stream)
     return Y
 
 
@@ -1170,9 +1168,8 @@ def expert_gated_q8(X: torch.Tensor, x_scale: torch.Tensor, Wg: torch.Tensor, wg
                     stream=None) -> torch.Tensor:
     """expert_gated() of 8-bit integers (forge_expert_gated_q8), operands as in expert_linear_q8; H bfloat16."""
     a = _act(act)
-    with _on(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, offsets, out) as on:
+    with _at(stream, X, x_scale, Wg, wg_scale, Wu, wu_scale, offsets, out) as on:
         e = _experts(Wg, offsets, Wu)
         H = _same(on, out, (X.shape[0], Wg.shape[1]), torch.bfloat16)
-        _check(_lib.forge_expert_gated_q8(_codes(X, x_scale, "X"), _codes(Wg, wg_scale, "Wg"), _codes(Wu, wu_scale, "Wu"), e,
-                                          offsets.data_ptr(), a, _ten(H), on.stream), "forge_expert_gated_q8")
+        _calls.forge_expert_gated_q8((X, x_scale), (Wg, wg_scale), (Wu, wu_scale), e, offsets, a, H, on.stream)
     return H

@@ -240,3 +240,28 @@ def test_states_of_a_stack():
     assert m.shape == (8, 128) and m.dtype == torch.bfloat16 and v is None and ms is None
     with pytest.raises(ValueError):
         forge.new_states(W, "adamw", "fp4")
+
+
+def test_calls_check_their_arguments():
+    """the calls that take tensors as they are: counts, types, ranges and devices, and a status as an exception"""
+    from optimizer_gemm_amd import forge as f
+    c, t = f._calls, torch.zeros(4, 16)
+    with pytest.raises(TypeError, match="takes 3 arguments"):
+        c.forge_quantize_rows(t, t)
+    with pytest.raises(TypeError):
+        c.forge_expert_plan_workspace(1, 2, "x")
+    with pytest.raises(ValueError, match="out of range"):
+        c.forge_expert_plan_workspace(1, 2, 2 ** 31)
+    with pytest.raises(OverflowError):
+        c.forge_expert_plan_workspace(2 ** 64, 2, 1)
+    with pytest.raises(ValueError, match="a tensor wanted"):
+        c.forge_quantize_rows("x", None, 0)
+    with pytest.raises(ValueError, match="one device"):
+        c.forge_quantize_rows(t, (t.char(), t[:, 0]), 0)
+    with pytest.raises(forge.ForgeError, match="forge_quantize_rows") as e:
+        c.forge_quantize_rows(None, None, 0)
+    assert e.value.status == -1
+    with pytest.raises(forge.ForgeError) as e:
+        c.forge_expert_plan(None, 4, 2, 0, None, None, None, 0, 0)
+    assert e.value.status == -2
+    assert c.forge_expert_plan_workspace(65536, 8, 64) == f.lib().forge_expert_plan_workspace(65536, 8, 64) > 0

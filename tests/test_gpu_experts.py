@@ -289,6 +289,66 @@ def test_no_rows():
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [3, 700])
+def test_no_inner_dimension(t, dt):
+    """sums of nothing are zeros, for the rows that belong to an expert"""
+    dtype = DT[dt]
+    off = torch.tensor([0, 1, 1, t - 1], device="cuda")
+
+    def none(*shape):
+        return torch.empty(*shape, device="cuda", dtype=dtype)
+
+    def zeros(a):
+        assert torch.all(a[:t - 1] == 0)
+
+    out = filled(t, 264, dtype=dtype)
+    zeros(forge.expert_linear(none(t, 0), none(3, 264, 0), off, act="silu", out=out))
+    assert torch.all(out[t - 1:] == 7.0)
+    zeros(forge.expert_gated(none(t, 0), none(3, 264, 0), none(3, 264, 0), off))
+    zeros(forge.expert_dgrad_group([none(t, 0)], [none(3, 0, 264)], off))
+    G = filled(t, 264, dtype=dtype)
+    dG, dU, H = forge.expert_gated_dgrad(none(t, 0), none(3, 0, 264), G, G, off)
+    zeros(dG)
+    zeros(dU)
+    assert torch.all(H[:t - 1] == H[0, 0]) and float(H[0, 0]) > 48
+    if dt == "bf16":
+        zeros(forge.expert_linear(none(t, 0), none(3, 264, 0), off, out=filled(t, 264, dtype=F)))
+
+
+def test_operands_that_are_refused():
+    X, W, off = rnd(gen(1), 8, 32), rnd(gen(2), 2, 16, 32), torch.tensor([0, 4, 8], device="cuda")
+    pos = torch.arange(8, device="cuda", dtype=torch.int32).reshape(8, 1)
+    Q, s = forge.quantize_rows(X)
+    q, sw = forge.quantize_rows(W.reshape(-1, 32))
+    q = q.view(2, 16, 32)
+    for what, call in (
+            ("contiguous", lambda: forge.expert_linear(rnd(gen(1), 32, 8).t(), W, off)),
+            ("contiguous", lambda: forge.expert_linear(X, rnd(gen(2), 2, 32, 16).transpose(1, 2), off)),
+            ("one pitch", lambda: forge.expert_linear(X, rnd(gen(2), 2, 20, 32)[:, :16], off)),
+            ("two dimensions", lambda: forge.expert_linear(X[None], W, off)),
+            ("two dimensions", lambda: forge.quantize_rows(X[0])),
+            ("unsupported dtype", lambda: forge.expert_linear(X.double(), W, off)),
+            ("unsupported dtype", lambda: forge.expert_dispatch(X.half(), pos)),
+            ("one device", lambda: forge.expert_linear(X, W.cpu(), off)),
+            ("one device", lambda: forge.expert_combine(X, pos.cpu())),
+            ("one device", lambda: forge.expert_linear(X, W, off.cpu())),
+            ("offsets", lambda: forge.expert_linear(X, W, off.int())),
+            ("int8 codes", lambda: forge.linear_q8(X, s, q[0], sw[:16])),
+            ("factors", lambda: forge.linear_q8(Q, s[:7], q[0], sw[:16])),
+            ("factors", lambda: forge.linear_q8(Q, s.double(), q[0], sw[:16])),
+            ("factors", lambda: forge.expert_linear_q8(Q, s, q, sw[:31], off)),
+            ("factors", lambda: forge.expert_dispatch(Q, pos, scale=s[::2])),
+            ("contiguous vector", lambda: forge.linear_q8(Q, s, q[0], sw[:16], bias=torch.zeros(1, 16, device="cuda"))),
+            ("group holds", lambda: forge.expert_dgrad_group([X], [W, W], off))):
+        with pytest.raises(ValueError, match=what):
+            call()
+    for call in (lambda: forge.expert_linear(X.float(), W, off), lambda: forge.expert_linear(X[:, :24], W, off),
+                 lambda: forge.expert_linear(X, W, off, out=X[:, :16]), lambda: forge.expert_dispatch(X, pos, out=X)):
+        with pytest.raises(forge.ForgeError):
+            call()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_offsets_that_are_no_offsets_stay_inside(dt):
     """values outside 0 .. rows or out of order reach no memory outside the operands: the rows around the views keep
     their values, and the call returns"""

@@ -115,6 +115,17 @@ def test_largest_sums_are_exact():
         assert torch.all(Y[:, 1::2] == float(torch.tensor(-i * 128.0 * 127.0 * 2.0 ** -20).to(BF)))
 
 
+def test_no_inner_dimension():
+    for t in (2, 300):
+        X, W = codes(gen(1), t, 0), codes(gen(1), 264, 0)
+        sx, sw, b, R = scales(gen(2), t), scales(gen(2), 264), rnd(gen(3), 264), rnd(gen(4), t, 264)
+        close("act(bias) + residual", forge.linear_q8(X, sx, W, sw, bias=b, act="silu", residual=R),
+              *linear_q8_64(X, sx, W, sw, b, "silu", R))
+        assert torch.all(forge.gated_q8(X, sx, W, sw, W, sw) == 0)
+        off = torch.tensor([0, t - 1], device="cuda")
+        assert torch.all(forge.expert_linear_q8(X, sx, W[None], sw, off)[:t - 1] == 0)
+
+
 def test_pitched_rows():
     g = gen(3)
     for t in (1, 5, 300):
