@@ -467,6 +467,11 @@ int forge_expert_gated_dgrad(const forge_tensor* dY, const forge_tensor* Wd, con
                              forge_tensor* dG, forge_tensor* dU, forge_tensor* H, forge_stream_t stream);
 int forge_expert_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,
                              const int64_t* offsets, forge_tensor* dX, forge_stream_t stream);
+/* The input gradient with a workspace, as forge_linear_dgrad_group_split: sum_out is the sum of the out_l of one expert. */
+int64_t forge_expert_dgrad_group_workspace(int64_t rows, int64_t in, int64_t sum_out, int32_t experts, int32_t dtype);
+int forge_expert_dgrad_group_split(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,
+                                   const int64_t* offsets, forge_tensor* dX, void* workspace, int64_t workspace_bytes,
+                                   forge_stream_t stream);
 
 /*
  * The stack's weight gradient dW = dY^T X over each expert's rows, stored as float32 [experts * out, in] (row

@@ -167,7 +167,9 @@ PyObject* call(R (*fn)(A...), const char* name, const char* kinds, PyObject* con
   X(forge_expert_linear, "ms...mm.")                 \
   X(forge_expert_gated, "mss...mmm.")                \
   X(forge_expert_gated_dgrad, "msmm...mmm.")         \
-  X(forge_expert_dgrad_group, ".ms..m.")             \
+  X(forge_expert_dgrad_group_workspace, ".....")     \
+  X(forge_expert_dgrad_group_split, ".ms..m...")     \
+  X(forge_expert_wgrad, "mm.....")                   \
   X(forge_quantize_rows, "mm.")                      \
   X(forge_linear_q8, "mmr.mm.")                      \
   X(forge_gated_q8, "mmm.m.")                        \

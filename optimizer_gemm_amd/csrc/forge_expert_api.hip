@@ -362,14 +362,24 @@ int forge_expert_gated_dgrad(const forge_tensor* dY, const forge_tensor* Wd, con
   return hip_status(launch_lin_expert(dt == FORGE_BF16, L_DGATE, true, g, (hipStream_t)stream));
 }
 
-int forge_expert_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,
-                             const int64_t* offsets, forge_tensor* dX, forge_stream_t stream) {
+int64_t forge_expert_dgrad_group_workspace(int64_t rows, int64_t in, int64_t sum_out, int32_t experts, int32_t dtype) {
+  if (rows <= 0 || in <= 0 || sum_out <= 0 || rows >= kMaxDim || in >= kMaxDim || sum_out >= FORGE_MAX_GROUP * kMaxDim ||
+      experts < 1 || experts > FORGE_MAX_EXPERTS)
+    return 0;
+  const int64_t s = lin_expert_splits(dtype == FORGE_BF16, in, rows, experts, sum_out);
+  return s > 1 ? s * rows * in * 4 : 0;
+}
+
+static int expert_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,
+                              const int64_t* offsets, forge_tensor* dX, bool split, void* workspace,
+                              int64_t workspace_bytes, forge_stream_t stream) {
   int r;
   if (!dY || !W || !dX) return FORGE_ERR_NULL;
   if (n_layers < 1 || n_layers > FORGE_MAX_GROUP) return FORGE_ERR_SHAPE;
   if ((r = op_dtype(dX)) || (r = check_experts(experts, offsets))) return r;
   const int dt = dX->dtype;
   const int64_t T = dX->rows, in = dX->cols;
+  int64_t rows = 0;
   LinArgs g{};
   const forge_tensor off = flat(offsets, (experts + 1) * 8);
   const forge_tensor* ins[2 * FORGE_MAX_GROUP + 1];
@@ -379,21 +389,42 @@ int forge_expert_dgrad_group(int32_t n_layers, const forge_tensor* dY, const for
     if ((r = check_mat(&dY[l], dt, T, out)) || (r = check_stack(&W[l], dt, experts, out, in))) return r;
     ins[2 * l] = &dY[l];
     ins[2 * l + 1] = &W[l];
+    rows += out;
     if (out == 0) continue;  // a layer without rows adds nothing
     set_pair(g, g.nsrc++, W[l].data, W[l].ld, dY[l].data, dY[l].ld, out);
   }
   ins[2 * n_layers] = &off;
   if ((r = check_mat(dX, dt, T, in))) return r;
-  const forge_tensor* outs[1] = {dX};
-  if ((r = check_alias(outs, 1, ins, 2 * n_layers + 1))) return r;
+  const int64_t need = split ? forge_expert_dgrad_group_workspace(T, in, rows, experts, dt) : 0;
+  if ((r = check_workspace(workspace, workspace_bytes, need))) return r;
+  const forge_tensor ws = flat(workspace, need);
+  const forge_tensor* outs[2] = {dX, &ws};
+  if ((r = check_alias(outs, 2, ins, 2 * n_layers + 1))) return r;
   if (T == 0 || in == 0) return FORGE_OK;
   g.M = (int32_t)in;
   g.N = (int32_t)T;
-  g.splits = 1;
+  g.splits = need ? lin_expert_splits(dt == FORGE_BF16, in, T, experts, rows) : 1;
   set_group(g, experts, offsets);
   g.e.out = dX->data;
   g.e.ldo = dX->ld;
-  return hip_status(launch_lin_expert(dt == FORGE_BF16, L_ACC, true, g, (hipStream_t)stream));
+  if (g.splits > 1) {
+    g.e.acc = (float*)workspace;
+    g.e.ldacc = in;
+    g.e.acc_write = 1;
+  }
+  r = hip_status(launch_lin_expert(dt == FORGE_BF16, L_ACC, true, g, (hipStream_t)stream));
+  return r || g.splits <= 1 ? r : hip_status(launch_acc_join(g, (hipStream_t)stream));
+}
+
+int forge_expert_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,
+                             const int64_t* offsets, forge_tensor* dX, forge_stream_t stream) {
+  return expert_dgrad_group(n_layers, dY, W, experts, offsets, dX, false, nullptr, 0, stream);
+}
+
+int forge_expert_dgrad_group_split(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,
+                                   const int64_t* offsets, forge_tensor* dX, void* workspace, int64_t workspace_bytes,
+                                   forge_stream_t stream) {
+  return expert_dgrad_group(n_layers, dY, W, experts, offsets, dX, true, workspace, workspace_bytes, stream);
 }
 
 // Operands of the stack's weight gradient, for W [experts * out, in] of type dt.

@@ -147,6 +147,7 @@ void lin_kernel(LinArgs g) {
   int ntiles = ntm * ntn * (EPI == L_ACC && TA && !TB && !EXP ? g.splits : 1), tail0 = 0;
   if constexpr (EXP) {
     ntiles = ntm * xr.total();
+    if constexpr (MULTI && !TAIL) ntiles *= g.splits;
     if (g.round > 0) {
       const int full = ntiles / g.round * g.round, rem = ntiles - full;
       const bool split = full > 0 && rem > 0 && 2 * rem <= g.round;
@@ -164,7 +165,7 @@ void lin_kernel(LinArgs g) {
     for (int s = 1; s < nsrc; ++s) nst += (ga->K[s] + C::BK - 1) / C::BK;
   }
   // SPLIT: g.splits workgroups share a tile's k range, each writing its part of the sums
-  constexpr bool SPLIT = MULTI && !EXP;
+  constexpr bool SPLIT = MULTI && !TAIL;
   const int splits = SPLIT ? g.splits : 1;
   const int mine = (nst + C::KS * splits - 1) / (C::KS * splits);  // stages of a group
 
@@ -268,12 +269,17 @@ void lin_kernel(LinArgs g) {
   // stages 0 and 1 of a tile, into slots 0..3
   auto dma_begin = [&](int tile) FORGE_INLINE {
     int tm, tn, part = 0;
-    if constexpr (SPLIT) {
+    if constexpr (SPLIT && !EXP) {
       part = tile % splits;
       tile /= splits;
     }
     if constexpr (EXP) {
-      const int at = g_order_part(tile, ntiles), L = TAIL ? tail0 + (at >> 2) : at;
+      int at = g_order_part(tile, ntiles);
+      if constexpr (SPLIT) {  // (the tiles of one part side by side: they share panels)
+        part = at / (ntiles / splits);
+        at -= part * (ntiles / splits);
+      }
+      const int L = TAIL ? tail0 + (at >> 2) : at;
       int r0, t0;
       xr.find(L / ntm, lx, r0, lend, t0);
       const int nt = (lend - r0 + XN - 1) / XN;
@@ -914,7 +920,7 @@ hipError_t lin_run(const LinArgs& g, hipStream_t st) {
   const int64_t ntn = EXP ? (g.N + C::BN - 1) / C::BN + (g.experts < g.N ? g.experts : g.N)
                           : (g.N - g.n_off + C::BN - 1) / C::BN;
   // (of a last round: two quarters a unit fill the chip)
-  const int64_t tiles = MODE & LM_TAIL ? 2 * g.round : ntm * ntn * (EPI == L_ACC && TA && !TB && !EXP ? g.splits : 1);
+  const int64_t tiles = MODE & LM_TAIL ? 2 * g.round : ntm * ntn * (EPI == L_ACC && TA && !TB ? g.splits : 1);
   if (tiles <= 0) return hipSuccess;
   const int64_t resident = (int64_t)(C::OCC * 4 / C::NW) * g_num_cus();
   const int64_t want = EXP ? (tiles + 7) / 8 * 8 : tiles;  // (whole XCDs, for the tiles' order)
@@ -1007,27 +1013,78 @@ hipError_t lin_bf16(const LinArgs& g, hipStream_t st) {
 // Measured: 8 experts of 2048 rows, 4096 -> 2 x 14336 gated 2927 us against 3974, the input gradient of both
 // 3162 (3488 without the quarters) against 4828; 8 of 128 rows, 4096 -> 2 x 3584 gated 173 against 116, 8-bit
 // 99 against 57; 16 of 8 rows, 4096 -> 1792: 128x128 45, 64x64 31.
+struct ExpertCost {  // tiles of b rows and columns, of products `width` wide
+  double w, used, each, cus;
+  ExpertCost(int64_t width, int64_t N, int experts)
+      : w((double)width), used(experts * (1.0 - pow(1.0 - 1.0 / experts, (double)N))), each((double)N / used),
+        cus((double)g_num_cus()) {}
+  double tiles(int b) const { return ceil(w / b) * used * -1.0 / expm1(-(double)b / each); }
+};
+struct ExpertKind {
+  LinTileKind kind;
+  double us;
+};
 template <int EPI, bool TA, int MODE>
-hipError_t lin_expert(const LinArgs& g0, hipStream_t st) {
-  LinArgs g = g0;
-  const int64_t cus = g_num_cus(), w = EPI == L_GATED ? 2 * (int64_t)g.M : g.M;
-  const double used = g.experts * (1.0 - pow(1.0 - 1.0 / g.experts, (double)g.N)), each = g.N / used;
-  auto rounds = [&](int64_t b, int64_t per_cu) {
-    const double n = -1.0 / expm1(-(double)b / each);
-    return (double)((w + b - 1) / b) * used * n / (double)(per_cu * cus);
-  };
-  const double big = rounds(256, 1), small = rounds(128, 2), tiny = rounds(64, 1);
-  double stages = 0.0;
-  for (int s = 0; s < g.nsrc; ++s) stages += (g.K[s] + 63) / 64;
+ExpertKind lin_expert_kind(const ExpertCost& c, double stages) {
+  const double big = c.tiles(256) / c.cus, small = c.tiles(128) / (2 * c.cus), tiny = c.tiles(64) / c.cus;
   const double more = EPI == L_DGATE ? 20.0 : TA ? 15.0 : 0.0, more_small = EPI == L_DGATE ? 14.0 : TA ? 8.0 : 0.0;
   const double one_big = 1.45 * stages + 10.0 + more, one_small = (MODE & LM_Q8 ? 0.85 : 1.0) * stages + 3.0 + more_small;
   const double fb = floor(big), fs = floor(small);
   const double t_big = fb >= 1.0 && big - fb <= 0.5 ? one_big * fb + (big > fb ? 0.79 * stages + 12.0 + more_small : 0.0)
                                                     : one_big * ceil(big);
   const double t_small = one_small * (fs + (small > fs ? fmax(0.7, small - fs) : 0.0));
-  const double t_tiny = 0.16 * stages + (0.31 * stages + 5.0 + more_small) * ceil(tiny);
-  if (t_tiny < t_small && t_tiny < t_big) return lin_run<LinTiny, EPI, TA, false, MODE>(g, st);
-  if (t_small <= t_big) return lin_run<LinSmall, EPI, TA, false, MODE>(g, st);
+  const double t_tiny = 0.16 * stages + (0.31 * stages + 5.0 + (EPI == L_ACC ? more_small / 2 : more_small)) * ceil(tiny);
+  if (t_tiny < t_small && t_tiny < t_big) return {LT_TINY, t_tiny};
+  return t_small <= t_big ? ExpertKind{LT_SMALL, t_small} : ExpertKind{LT_BIG, t_big};
+}
+
+// Whether an input gradient's tiles are shared along k by several workgroups, whose sums launch_acc_join adds: where
+// that is a fifth faster at least, by the costs above, the join's (6 us, the parts written and read at 3 TB/s), and
+// for 128x128 tiles 0.75 of a stage's cost where a unit has one of them and 1.15 where it has two. Of two to 32
+// parts of 12 stages or more, 256x256 tiles (no more than a third of a round behind the first, which the experts'
+// sizes may make a whole one) or 128x128. Over 22 sweeps of 1 to 64 experts the choice was within 23% of the best of all
+// kinds and parts, within 9% in 20 of them. Sum of both layers, one part and several: 1 expert of 481 rows, 22320 -> 64
+// 108 us and 23; 8 of 128 rows, 28672 -> 1024 338 and 128; 7 of 53 rows, 6624 -> 1944 78 and 55;
+// 4 of 16 rows, 16384 -> 512 66 and 27; but 39 of 47 rows, 1728 -> 2824 94 and 119.
+struct ExpertSplit {
+  int parts;
+  bool big;
+};
+inline ExpertSplit lin_expert_split(int64_t M, int64_t N, int experts, int64_t K) {
+  const ExpertCost c(M, N, experts);
+  const double stages = (double)((K + 63) / 64), big = c.tiles(256) / c.cus, small = c.tiles(128) / (2 * c.cus);
+  auto fill = [](double r) { return r <= 0.5 ? 0.75 : r <= 0.8 ? 1.15 : 1.15 * (r + 0.2); };
+  const ExpertKind one = lin_expert_kind<L_ACC, true, LM_EXPERT>(c, stages);
+  ExpertSplit x{1, false};
+  double best = 0.8 * (one.kind == LT_SMALL ? fmax(one.us, (stages + 11.0) * fill(small)) : one.us);
+  for (int s : {2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+    if (stages < 12.0 * s) break;
+    const double part = ceil(stages / s), join = 6.0 + (double)(s * M * N) * 8.0 / 3e6;
+    const double t_big = (1.45 * part + 15.0) * (s * big <= 0.85 ? 1.0 : s * big + 0.15) + join;
+    const double t_small = (part + 6.0) * fill(s * small) + join;
+    if (s * big <= 1.3 && t_big < best) best = t_big, x = {s, true};
+    if (s * small <= 9.0 && t_small < best) best = t_small, x = {s, false};
+  }
+  return x;
+}
+
+template <int EPI, bool TA, int MODE>
+hipError_t lin_expert(const LinArgs& g0, hipStream_t st) {
+  LinArgs g = g0;
+  const int64_t cus = g_num_cus(), w = EPI == L_GATED ? 2 * (int64_t)g.M : g.M;
+  if constexpr (EPI == L_ACC && TA) {
+    if (g.splits > 1) {
+      int64_t k = 0;
+      for (int s = 0; s < g.nsrc; ++s) k += g.K[s];
+      return lin_expert_split(g.M, g.N, g.experts, k).big ? lin_run<LinBig, EPI, TA, false, MODE>(g, st)
+                                                          : lin_run<LinSmall, EPI, TA, false, MODE>(g, st);
+    }
+  }
+  double stages = 0.0;
+  for (int s = 0; s < g.nsrc; ++s) stages += (g.K[s] + 63) / 64;
+  const LinTileKind kind = lin_expert_kind<EPI, TA, MODE>(ExpertCost(w, g.N, g.experts), stages).kind;
+  if (kind == LT_TINY) return lin_run<LinTiny, EPI, TA, false, MODE>(g, st);
+  if (kind == LT_SMALL) return lin_run<LinSmall, EPI, TA, false, MODE>(g, st);
   // where there can be more large tiles than a round has (whatever the experts' sizes are)
   if ((w + 255) / 256 * ((g.N + 255) / 256 + (g.experts < g.N ? g.experts : g.N)) > cus) g.round = (int32_t)cus;
   hipError_t e = lin_run<LinBig, EPI, TA, false, MODE>(g, st);

@@ -309,6 +309,10 @@ int lin_splits(int bf16, int64_t M, int64_t N, int64_t K) {
   return s < 2 ? 1 : (int)s;
 }
 
+int lin_expert_splits(int bf16, int64_t M, int64_t N, int experts, int64_t K) {
+  return bf16 ? lin_expert_split(M, N, experts, K).parts : 1;
+}
+
 int lin_lse_block(int bf16, int M, int N) {
   if (!bf16) return S_B;
   switch (lin_tile<L_LSE>(M, N)) {

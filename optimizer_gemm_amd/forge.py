@@ -146,6 +146,10 @@ def _load() -> ctypes.CDLL:
                                      [P(ForgeTensor)] * 3 + [ctypes.c_void_p], ctypes.c_int),
         "forge_expert_dgrad_group": ([ctypes.c_int32] + [P(ForgeTensor)] * 2 +
                                      [ctypes.c_int32, ctypes.c_void_p, P(ForgeTensor), ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_dgrad_group_workspace": ([ctypes.c_int64] * 3 + [ctypes.c_int32] * 2, ctypes.c_int64),
+        "forge_expert_dgrad_group_split": ([ctypes.c_int32] + [P(ForgeTensor)] * 2 +
+                                           [ctypes.c_int32, ctypes.c_void_p, P(ForgeTensor), ctypes.c_void_p, ctypes.c_int64,
+                                            ctypes.c_void_p], ctypes.c_int),
         "forge_expert_wgrad": ([P(ForgeTensor)] * 2 + [ctypes.c_int32] + [ctypes.c_void_p] * 2 +
                                [ctypes.c_int64, ctypes.c_void_p], ctypes.c_int),
         "forge_expert_wgrad_step": ([P(ForgeTensor)] * 5 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
@@ -593,6 +597,9 @@ class _Here:
                 return _new((rows, cols), (cols or 1, 1), dtype)
             if n == 1:
                 return _new((shape[0],), (1,), dtype)
+            if n == 3:
+                stack, rows, cols = shape
+                return _new((stack, rows, cols), (rows * cols or 1, cols or 1, 1), dtype)
         return torch.empty(*shape, dtype=dtype, device=self.device)
 
 
@@ -1048,7 +1055,7 @@ def expert_gated_dgrad(dY: torch.Tensor, Wd: torch.Tensor, G: torch.Tensor, U: t
 
 
 def expert_dgrad_group(dYs, Ws, offsets: torch.Tensor, dX: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """dX[r] = sum_l dYs[l][r] Ws[l][x] for the rows r of each expert x (forge_expert_dgrad_group): Ws[l]
+    """dX[r] = sum_l dYs[l][r] Ws[l][x] for the rows r of each expert x (forge_expert_dgrad_group_split): Ws[l]
     [experts, out_l, in]; from the weights as they are now, before their step."""
     n = len(Ws)
     if len(dYs) != n or not 1 <= n <= MAX_GROUP:
@@ -1056,7 +1063,9 @@ def expert_dgrad_group(dYs, Ws, offsets: torch.Tensor, dX: Optional[torch.Tensor
     with _at(stream, *dYs, *Ws, offsets, dX) as on:
         e = _experts(Ws[0], offsets, *Ws[1:])
         dX = _same(on, dX, (dYs[0].shape[0], Ws[0].shape[2]), Ws[0].dtype)
-        _calls.forge_expert_dgrad_group(n, list(dYs), list(Ws), e, offsets, dX, on.stream)
+        need = _calls.forge_expert_dgrad_group_workspace(*dX.shape, sum([w.shape[1] for w in Ws]), e, _DT.get(dX.dtype, -1))
+        ws = on.empty((need,), torch.uint8) if need else None
+        _calls.forge_expert_dgrad_group_split(n, list(dYs), list(Ws), e, offsets, dX, ws, need, on.stream)
     return dX
 
 
@@ -1065,15 +1074,17 @@ def expert_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor, dW: O
     """The stack's gradient dW[x] = dY^T X over each expert's rows, float32 [experts, out, in]
     (forge_expert_wgrad): the two-phase schedule's first half (optimizer_step on the stack as one
     [experts * out, in] layer is its second)."""
-    with _on(stream, X, dY, offsets, dW) as on:
+    with _at(stream, X, dY, offsets, dW) as on:
         e = offsets.numel() - 1
         _vec(offsets, e + 1, torch.int64, "offsets")
-        dW = _same(on, dW, (e, dY.shape[1], X.shape[1]), torch.float32)
-        t = _stack(dW)
-        if t.dtype != F32 or tuple(dW.shape) != (e, dY.shape[1], X.shape[1]):
+        shape, ld = (e, dY.shape[1], X.shape[1]), X.shape[1]
+        if dW is None:
+            dW = on.empty(shape, _F32)
+        elif dW.dtype is not _F32 or tuple(dW.shape) != shape:
             raise ValueError("dW: float32 [experts, out, in] wanted")
-        _check(_lib.forge_expert_wgrad(_ten(X), _ten(dY), e, offsets.data_ptr(), t.data, t.ld, on.stream),
-               "forge_expert_wgrad")
+        else:
+            ld = _stack(dW).ld
+        _calls.forge_expert_wgrad(X, dY, e, offsets, dW, ld, on.stream)
     return dW
 
 

@@ -126,6 +126,24 @@ def test_product_refusals():
     assert dg(W1=ten(3, 160, 72)) == SHAPE and dg(dX=ten(4, 16, 72)) == SHAPE and dg(dX=ten(1, 16, 64)) == ALIAS
 
 
+def test_dgrad_group_split_refusals():
+    T, rows, cols, ws = 20, 8192, 64, BASE + (5 << 34)
+    need = L.forge_expert_dgrad_group_workspace(T, cols, rows, 4, BF16)
+    assert need > 0 and need % (T * cols * 4) == 0
+    for a in ((16384, 4096, 28672, 8, BF16), (T, cols, 512, 4, BF16), (T, cols, rows, 4, F32), (0, cols, rows, 4, BF16),
+              (T, 0, rows, 4, BF16), (T, cols, 0, 4, BF16), (T, cols, rows, 0, BF16), (T, cols, rows, 1025, BF16),
+              (1 << 40, cols, rows, 4, BF16)):
+        assert L.forge_expert_dgrad_group_workspace(*a) == 0
+    dy, w = (ForgeTensor * 1)(ten(0, T, rows)), (ForgeTensor * 1)(ten(1, 4 * rows, cols))
+
+    def call(ws=ws, n=need, dX=ten(2, T, cols), off=OFF):
+        return L.forge_expert_dgrad_group_split(1, dy, w, 4, off, ref(dX), ws, n, None)
+
+    assert call(n=need - 1) == SCRATCH and call(ws=None) == NULL and call(ws=ws + 4) == ALIGN
+    assert call(ws=BASE) == ALIAS and call(ws=BASE + (2 << 34)) == ALIAS and call(dX=ten(1, T, cols)) == ALIAS
+    assert call(ws=OFF & ~15) == ALIAS and call(off=None) == NULL
+
+
 def test_step_refusals():
     h = make_hyper("adamw")
 

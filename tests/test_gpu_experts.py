@@ -274,6 +274,36 @@ def test_products_pitched(dt):
     assert torch.all(dW[:, :, 264:] == 7.0)
 
 
+# input gradients of few tiles over a long k, which workgroups share: rows of each expert, the layers' out, in
+SPLITS = [([481], [11160, 11160], 64), ([3, 0, 700, 50], [4096, 3000, 1104], 264), ([600, 101, 0, 500], [26304], 440),
+          ([7] * 70, [1200, 1200], 72), ([9, 0, 12], [8200], 136), ([1], [6400], 8)]
+
+
+@pytest.mark.parametrize("case", range(len(SPLITS)))
+def test_input_gradient_shared_along_k(case):
+    sizes, outs, i = SPLITS[case]
+    e, g = len(sizes), gen(100 + case)
+    first, behind = (3, 5) if case % 2 else (0, 0)
+    off = sizes_to_offsets(sizes, first)
+    n = int(off[-1])
+    R = n + behind
+    assert forge.lib().forge_expert_dgrad_group_workspace(R, i, sum(outs), e, forge.forge.BF16) > 0
+    W, D = [stacked(g, e, o, i, BF, std=o ** -0.5) for o in outs], [rnd(g, R, o) for o in outs]
+    for d in D:
+        d[:first], d[n:] = NAN, NAN
+    dX = forge.expert_dgrad_group(D, W, off, dX=filled(R, i))
+    assert torch.all(dX[:first] == 7.0) and torch.all(dX[n:] == 7.0)
+    close("dX", dX[first:n], *expert_dgrad64([d[first:n] for d in D], W, off - first))
+    out = filled(R, i + 16)
+    forge.expert_dgrad_group([pitched(d) for d in D], [pitched(w) for w in W], off, dX=out[:, :i])
+    assert torch.equal(out[first:n, :i], dX[first:n]) and torch.all(out[:, i:] == 7.0)
+    # offsets that are none reach nothing outside
+    around = filled(R + 20, i)
+    for o in ([-5] + [2 ** 40] * e, [R] * e + [0], [0, R] * ((e + 1) // 2) + [R] * ((e + 1) % 2)):
+        forge.expert_dgrad_group(D, W, torch.tensor(o, device="cuda"), dX=around[10:R + 10])
+        assert torch.all(around[:10] == 7.0) and torch.all(around[R + 10:] == 7.0)
+
+
 def test_no_rows():
     W, off = rnd(gen(1), 3, 16, 24), torch.zeros(4, dtype=torch.int64, device="cuda")
     X, D = torch.empty(0, 24, device="cuda", dtype=BF), torch.empty(0, 16, device="cuda", dtype=BF)
