@@ -1380,11 +1380,20 @@ hipError_t wgrad_fused_bf16_opt(int sf, int sr, const GArgs& g, const OptArgs& a
       g, [&](auto c, const GArgs& gc) { return g_launch_opt<decltype(c), OPT>(sf, sr, gc, a, st); });
 }
 
-// The tiles of stacked layers: 256x256 for more than half a round of them, else 128x128.
+// The tiles of stacked layers, by their rounds of the chip: a round of 128x128 tiles, two a unit, holds half the
+// elements of one of 256x256 tiles and takes 0.5 to 0.75 of its time. AdamW with float32 moments, 256x256 and 128x128:
+// 44 experts of 16 rows, 704 -> 312 (2 rounds and 2) 90 us and 60; 8 of 3750, 1024 -> 1024 (1 and 1) 164 and 124; 5 of
+// 244, 128 -> 5840 (1 and 1) 51 and 28; but 8 of 951, 2024 -> 4936 (5 and 10) 488 and 646; 32 of 125, 1024 -> 512 (1 and 2)
+// 74 and 78.
+template <class C>
+static int64_t g_rounds(const GArgs& g) {
+  const int64_t resident = C::OCC * 4 / C::NW * g_num_cus();
+  return ((int64_t)g_tiles<C>(g) * g.experts + resident - 1) / resident;
+}
 template <class F>
 static hipError_t g_pick_expert(const GArgs& g, F&& f) {
-  if (2 * (int64_t)g_tiles<WgradBig>(g) * g.experts > g_num_cus()) return f(WgradBig{});
-  return f(WgradSmall{});
+  if (3 * g_rounds<WgradSmall>(g) < 4 * g_rounds<WgradBig>(g)) return f(WgradSmall{});
+  return f(WgradBig{});
 }
 
 template <int OPT>

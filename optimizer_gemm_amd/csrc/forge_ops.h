@@ -419,7 +419,7 @@ int lin_lse_block(int bf16, int M, int N);
 // parts a product of k-slow A should be cut into (1: none): too few tiles to fill the chip with,
 // a k range long enough to share
 int lin_splits(int bf16, int64_t M, int64_t N, int64_t K);
-// the same of one that is grouped by expert
+// the same of an input gradient that is grouped by expert (by rows and experts alone: the sizes are on the device)
 int lin_expert_splits(int bf16, int64_t M, int64_t N, int experts, int64_t K);
 // out = (sum of the parts' sums, in order) * scale
 hipError_t launch_acc_join(const LinArgs& g, hipStream_t st);
