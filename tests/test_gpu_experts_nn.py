@@ -311,6 +311,42 @@ def test_captured_and_replayed_with_other_routes():
             assert all(torch.equal(p, q) for p, q in zip(got, want)), n
 
 
+def test_shared_input_gradient_captured_and_on_streams():
+    """the input gradient whose tiles are shared along k, with its workspace: two streams at once, and two graphs replayed with
+    other offsets"""
+    W = [rnd(60 + j, 4, 5000, 136, std=5000 ** -0.5) for j in range(2)]
+    sets = []
+    for j, t in ((0, 300), (1, 77)):
+        assert forge.lib().forge_expert_dgrad_group_workspace(t, 136, 10000, 4, forge.forge.BF16) > 0
+        sets.append(([rnd(70 + j, t, 5000), rnd(80 + j, t, 5000)], torch.tensor([0, t // 3, t // 3, t // 2, t - 2], device="cuda")))
+    want = [forge.expert_dgrad_group(D, W, off)[:off[-1]] for D, off in sets]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        got = [forge.expert_dgrad_group(D, W, off, stream=s) for (D, off), s in zip(sets, (s1, s2))]
+        junk = [torch.full((4000, 136), float("nan"), device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[:len(b)], b) for a, b in zip(got, want))
+        del junk
+    graphs, outs = [], []
+    for D, off in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(forge.expert_dgrad_group(D, W, off))
+        graphs.append(g)
+    for n in range(4):
+        for D, off in sets:
+            D[0].copy_(rnd(90 + n, *D[0].shape))
+            t = D[0].shape[0]
+            off.copy_(torch.tensor([0, n, t // 2 + n, t - 4, t - n], device="cuda"))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for (D, off), out in zip(sets, outs):
+            m = int(off[-1])
+            assert torch.equal(out[:m], forge.expert_dgrad_group(D, W, off)[:m])
+
+
 def test_block_step_captured():
     """Forward, backward and the fused steps of a block in one graph: a replay does what the eager calls do"""
     idx, w = routed(5, 300, 2, 5)
