@@ -75,6 +75,15 @@ def test_plan_extremes():
         assert offsets[-1] == 2100 and torch.all(offsets[:-1] == 0)
 
 
+@pytest.mark.parametrize("t,k,e", [(256, 2, 1024), (171, 3, 5), (2047, 1, 1024), (1024, 2, 64), (683, 3, 1), (1, 2048, 9)])
+def test_plan_of_one_block_and_its_borders(t, k, e):
+    for n in (0.0, 0.3):
+        idx = routes(t + e, t, k, e, dropped=n)
+        off, pos = forge.expert_plan(idx.cuda(), e)
+        o, p = plan64(idx, e)
+        assert torch.equal(off.cpu(), o) and torch.equal(pos.cpu(), p)
+
+
 def test_plan_beyond_512_blocks():
     """blocks of more than one turn: 512 x 1024 routes and some"""
     idx = torch.randint(-1, 33, (600001, 1), device="cuda", generator=gen(1))
