@@ -231,8 +231,6 @@ hipError_t lin_f32(const LinArgs& g, hipStream_t st) {
   return run<STile<64>, EPI, TA, TB>(g, st);
 }
 
-namespace {
-
 // grouped by expert, by the same rule on the tiles as far as they can be told
 template <int EPI, bool TA>
 hipError_t lin_f32_expert(const LinArgs& g, hipStream_t st) {
@@ -249,8 +247,6 @@ hipError_t lin_f32_expert(const LinArgs& g, hipStream_t st) {
 // most (32 x 14336 -> 4096: 40 us against 47; 32 x 8192 -> 8192: 45 against 30), above 4 also those
 // that fill more than two rounds or less than half of one (16 x 4096 -> 14336: 32 against 22; 16 x
 // 4096 -> 4096: 11 against 17; 4 x 4096 -> 40000: 63 against 87).
-}  // namespace
-
 bool few_tokens(int epi, const LinArgs& g) {
   // (a grid of fewer than 2^32 threads)
   if (g.N > kSkinny || g.M >= (1 << 26)) return false;
