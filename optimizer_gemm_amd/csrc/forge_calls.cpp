@@ -8,6 +8,7 @@
 #include <Python.h>
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <stdexcept>
 #include <string>
@@ -227,4 +228,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "forge_calls", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_forge_calls() { return PyModule_Create(&module); }
+// torch_version: the torch that this was compiled against, whose classes the code above has inlined
+PyMODINIT_FUNC PyInit_forge_calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

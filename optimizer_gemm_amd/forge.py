@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import re
 from typing import Dict, Optional
 
 import torch
@@ -55,15 +56,31 @@ class ForgeError(RuntimeError):
         self.status = status
 
 
+class _NoCalls:
+    """In the place of forge_calls where it does not load: the calls that go through it say why, all others work."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name: str):
+        raise ImportError(f"{name}: {self._why}; run `python optimizer_gemm_amd/build.py`")
+
+
 def _load_calls():
-    """The module of csrc/forge_calls.cpp: entry points that take tensors as they are, at a fraction of ctypes' time."""
+    """The module of csrc/forge_calls.cpp: entry points that take tensors as they are, at a fraction of ctypes' time. It is
+    built against one torch's C++ interface, so with another one, or without it, the package loads all the same."""
     path = os.path.join(_PKG, "_lib", "forge_calls.so")
     if not os.path.exists(path):
-        raise ImportError(f"forge_calls.so not built at {path}; run `python optimizer_gemm_amd/build.py`")
+        return _NoCalls(f"forge_calls.so not built at {path}")
     spec = importlib.util.spec_from_file_location("forge_calls", path)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
-    mod.load(LIB_PATH, ForgeError)
+    try:
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        if not re.match(re.escape(mod.torch_version) + r"(?!\d)", torch.__version__):
+            return _NoCalls(f"forge_calls.so was built against torch {mod.torch_version}, this is {torch.__version__}")
+        mod.load(LIB_PATH, ForgeError)
+    except (ImportError, AttributeError) as e:
+        return _NoCalls(f"forge_calls.so does not load ({e})")
     return mod
 
 

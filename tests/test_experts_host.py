@@ -283,3 +283,49 @@ def test_calls_check_their_arguments():
         c.forge_expert_plan(None, 4, 2, 0, None, None, None, 0, 0)
     assert e.value.status == -2
     assert c.forge_expert_plan_workspace(65536, 8, 64) == f.lib().forge_expert_plan_workspace(65536, 8, 64) > 0
+
+
+def test_the_package_loads_without_the_python_calls(tmp_path):
+    """forge_calls.so is built against one torch's C++ interface. Where it is missing, is no module or belongs to another
+    torch, the package and every call that goes another way work; those that go through it say why they do not."""
+    import os
+    import subprocess
+    import sys
+
+    from optimizer_gemm_amd import forge as f
+
+    pkg = os.path.dirname(f.__file__)
+    assert f._calls.torch_version and torch.__version__.startswith(f._calls.torch_version)
+    check = """
+import sys, torch
+if len(sys.argv) > 2:
+    torch.__version__ = sys.argv[2]
+import optimizer_gemm_amd as forge
+from optimizer_gemm_amd import nn
+from optimizer_gemm_amd import forge as f
+assert f.__file__.startswith(sys.argv[1]), f.__file__
+assert forge.lib().forge_version() > 0 and forge.step_scalars("adamw", None, 1) is not None
+assert forge.lib().forge_expert_plan_workspace(512, 2, 16) == 0
+assert nn.ForgeLinear(16, 16).step_count == 0
+try:
+    f._calls.forge_expert_plan_workspace(512, 2, 16)
+except ImportError as e:
+    assert "forge_expert_plan_workspace" in str(e) and "build.py" in str(e), e
+    print("refused:", e)
+"""
+    for n, (calls, argv, why) in enumerate((("missing", (), "not built"), ("garbage", (), "does not load"),
+                                            ("real", ("1.2.3+cpu",), "built against torch"), ("real", (), None))):
+        root = tmp_path / str(n)
+        (root / "optimizer_gemm_amd" / "_lib").mkdir(parents=True)
+        for name in os.listdir(pkg):
+            if name.endswith(".py"):
+                os.symlink(os.path.join(pkg, name), root / "optimizer_gemm_amd" / name)
+        os.symlink(f.LIB_PATH, root / "optimizer_gemm_amd" / "_lib" / "libforge.so")
+        so = root / "optimizer_gemm_amd" / "_lib" / "forge_calls.so"
+        if calls == "garbage":
+            so.write_bytes(b"no module")
+        elif calls == "real":
+            os.symlink(os.path.join(pkg, "_lib", "forge_calls.so"), so)
+        r = subprocess.run([sys.executable, "-B", "-c", check, str(root), *argv], cwd=root, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
+        assert (why in r.stdout) if why else (r.stdout == ""), r.stdout
