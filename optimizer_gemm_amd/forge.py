@@ -502,6 +502,8 @@ def new_states(W: torch.Tensor, opt: str = "adamw", fmt: str = "f32"):
     """Zero moment slots for `opt` in format f32, bf16, q8 (linear codes) or q8dyn (dynamic
     codes; pass code="dynamic" to the step): returns (m, v, m_scale, v_scale), the moments of W's shape (a layer's
     [out, in], a stack's [experts, out, in])."""
+    if W.dim() not in (2, 3):
+        raise ValueError(f"weights [out, in] or a stack [experts, out, in] wanted, not a tensor of shape {tuple(W.shape)}")
     use_m, use_v = SLOTS[opt]
     m = v = ms = vs = None
     if fmt not in ("f32", "bf16", "q8", "q8dyn"):

@@ -329,3 +329,12 @@ except ImportError as e:
         r = subprocess.run([sys.executable, "-B", "-c", check, str(root), *argv], cwd=root, capture_output=True, text=True)
         assert r.returncode == 0, r.stderr
         assert (why in r.stdout) if why else (r.stdout == ""), r.stdout
+
+
+def test_states_are_those_of_a_layer_or_a_stack():
+    """no step takes moments of other dimensions, so none are made"""
+    for shape in ((), (128,), (2, 3, 8, 128)):
+        for fmt in ("f32", "bf16", "q8"):
+            with pytest.raises(ValueError, match="stack"):
+                forge.new_states(torch.zeros(shape, dtype=torch.bfloat16), "adamw", fmt)
+    assert forge.new_states(torch.zeros(1, 128), "adamw")[0].shape == (1, 128)
