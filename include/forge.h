@@ -410,7 +410,8 @@ int forge_linear_xent_step(const forge_tensor* X, forge_tensor* W, forge_tensor*
  * them, and the x-th of the stacked matrices. The operators' conventions above hold; in addition:
  *   - 1 <= experts <= FORGE_MAX_EXPERTS, else FORGE_ERR_SHAPE.
  *   - A stack W [experts * out, in] is one tensor (its rows a multiple of `experts`, FORGE_ERR_SHAPE); one
- *     expert's part spans less than 2^31 bytes, the whole any number.
+ *     expert's part spans less than 2^31 bytes, the whole any number. Rows span less than 2^31 bytes, those in FORGE_F32
+ *     beside FORGE_BF16 or FORGE_I8 ones less than 2^32 (less than 2^21 elements a row then).
  *   - offsets: experts + 1 int64 in device memory, ascending, within 0 .. rows. The sizes are read on the
  *     device, so no call waits for them. Other values reach no memory outside the tensors (they are held to
  *     that range and order), but the results are then unspecified.

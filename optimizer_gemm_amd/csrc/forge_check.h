@@ -203,6 +203,16 @@ int check_mat(const forge_tensor* t, int dtype, int64_t rows, int64_t cols) {
   return fits_31(t) ? FORGE_OK : FORGE_ERR_UNSUPPORTED;
 }
 
+// Float32 rows beside operands of fewer bits (sums as they are, results before they are combined): as many elements as
+// bfloat16 rows may have, so twice the bytes. Their kernels find a row by 64-bit offsets and reach 256 rows from there by
+// 32-bit ones below 2^31.
+int check_wide(const forge_tensor* t, int64_t rows, int64_t cols) {
+  int r = check_io(t, FORGE_F32);
+  if (r) return r;
+  if (t->rows != rows || t->cols != cols) return FORGE_ERR_SHAPE;
+  return fits_31(t) || (t->rows * t->ld < ((int64_t)1 << 30) && t->ld < ((int64_t)1 << 21)) ? FORGE_OK : FORGE_ERR_UNSUPPORTED;
+}
+
 bool act_ok(int act) { return act >= FORGE_ACT_NONE && act <= FORGE_ACT_GELU_TANH; }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? FORGE_OK : FORGE_ERR_HIP; }

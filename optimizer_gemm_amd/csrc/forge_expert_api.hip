@@ -82,7 +82,7 @@ int linear_q8(const forge_tensor* X, const forge_tensor* W, const forge_tensor* 
   if (W->rows % parts) return FORGE_ERR_SHAPE;
   const int64_t out = W->rows / parts;
   const bool wide = offsets && !Wu && Y->dtype == FORGE_F32;  // the sums as they are
-  if ((r = check_mat(Y, wide ? FORGE_F32 : FORGE_BF16, T, out))) return r;
+  if ((r = wide ? check_wide(Y, T, out) : check_mat(Y, FORGE_BF16, T, out))) return r;
   if (wide && (act != FORGE_ACT_NONE || out % 8)) return FORGE_ERR_UNSUPPORTED;
   if (bias && (r = check_mat(bias, bias->dtype == FORGE_F32 ? FORGE_F32 : FORGE_BF16, 1, out))) return r;
   if (R && (r = check_mat(R, FORGE_BF16, T, out))) return r;
@@ -186,7 +186,11 @@ static int check_combine(const forge_tensor* Yp, const int32_t* pos, int64_t k, 
                          CombineArgs& a) {
   int r;
   if ((r = op_dtype(Y)) || (r = check_mat(Y, Y->dtype, Y->rows, Y->cols))) return r;
-  if (Yp && ((r = op_dtype(Yp)) || (r = check_mat(Yp, Yp->dtype == FORGE_F32 ? FORGE_F32 : Y->dtype, Yp->rows, Y->cols)))) return r;
+  if (Yp) {
+    if ((r = op_dtype(Yp))) return r;
+    const bool wide = Yp->dtype == FORGE_F32 && Y->dtype == FORGE_BF16;
+    if ((r = wide ? check_wide(Yp, Yp->rows, Y->cols) : check_mat(Yp, Y->dtype, Yp->rows, Y->cols))) return r;
+  }
   if (k < 1) return FORGE_ERR_SHAPE;
   if (Y->rows >= kMaxTokens || k >= kMaxRoutes || Y->rows * k >= kMaxRoutes) return FORGE_ERR_UNSUPPORTED;
   if (Y->rows > 0 && !pos) return FORGE_ERR_NULL;
@@ -256,7 +260,7 @@ int forge_expert_linear(const forge_tensor* X, const forge_tensor* W, int32_t ex
   const int64_t T = X->rows, out = W->rows / experts, in = W->cols;
   const bool wide = dt == FORGE_BF16 && Y->dtype == FORGE_F32;  // the sums as they are
   if ((r = check_mat(X, dt, T, in)) || (r = check_stack(W, dt, experts, out, in)) ||
-      (r = check_mat(Y, wide ? FORGE_F32 : dt, T, out)))
+      (r = wide ? check_wide(Y, T, out) : check_mat(Y, dt, T, out)))
     return r;
   if (wide && (act != FORGE_ACT_NONE || Z || out % 8)) return FORGE_ERR_UNSUPPORTED;
   if (Z && (r = check_mat(Z, dt, T, out))) return r;

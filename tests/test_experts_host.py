@@ -338,3 +338,28 @@ def test_states_are_those_of_a_layer_or_a_stack():
             with pytest.raises(ValueError, match="stack"):
                 forge.new_states(torch.zeros(shape, dtype=torch.bfloat16), "adamw", fmt)
     assert forge.new_states(torch.zeros(1, 128), "adamw")[0].shape == (1, 128)
+
+
+def test_float32_rows_beside_bfloat16_hold_as_many_elements():
+    """float32 results of bfloat16 or 8-bit operands, and the combination that reads them: refused from 2^30 elements on, as
+    bfloat16 rows are, not from 2^31 bytes (the calls below that size overlap an input, so that nothing is launched)"""
+    n, P, W = 1 << 20, BASE + (9 << 34), BASE + (10 << 34)
+
+    def lin(rows, cols, q=False, ld=None):
+        Y = ten(0, rows, cols, F32, ld)  # (where X is)
+        if q:
+            return L.forge_expert_linear_q8(ref(q8(0, rows, 16)), ref(q8(1, 4 * cols, 16)), 4, OFF, 0, ref(Y), None)
+        return L.forge_expert_linear(ref(ten(0, rows, 16)), ref(ten(1, 4 * cols, 16)), 4, OFF, 0, ref(Y), None, None)
+
+    def com(rows, cols, dt=BF16):
+        return L.forge_expert_combine(ref(ten(0, rows, cols, F32)), P, 2, W, None, ref(ten(0, 16, cols, dt)), None)
+
+    def back(rows, cols):
+        return L.forge_expert_combine_backward(ref(ten(1, 16, cols)), ref(ten(0, rows, cols, F32)), P, 2, W,
+                                               ref(ten(1, rows, cols)), BASE + (11 << 34), None)
+
+    for q in (False, True):
+        assert lin(n, 512, q) == lin(n, 1016, q) == ALIAS and lin(n, 1024, q) == UNSUP and lin(n, 512, q, 1024) == UNSUP
+        assert lin(511, 512, q, 1 << 21) == UNSUP  # 256 rows of them past 2^31 bytes
+    assert com(n, 512) == com(n, 1016) == ALIAS and com(n, 1024) == UNSUP and com(n, 512, F32) == UNSUP
+    assert back(n, 512) == back(n, 1016) == ALIAS and back(n, 1024) == UNSUP

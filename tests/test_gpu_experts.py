@@ -573,3 +573,45 @@ def test_gradients_against_differences():
         dn[tt, j] -= eps
         diff = (loss(x64, up) - loss(x64, dn)) / (2 * eps)
         assert abs(diff - float(dw[tt, j])) <= 1e-7 + 300 * U * max(1.0, float(dw.abs().max()))
+
+
+# ---- rows past 2^31 bytes ------------------------------------------------------------------------------------------
+def test_float32_results_past_two_gigabytes():
+    """float32 results of bfloat16 and 8-bit operands, combined and back: 150003 rows of 4096, 2.46e9 bytes. A row of a
+    product does not depend on the others, nor, with one stage of k, on the tiles: the same bits as in calls of fewer rows."""
+    g = gen(31)
+    t, k, e, i, d = 50001, 3, 4, 64, 4096
+    off = sizes_to_offsets([40000, 0, 70000, 40003])
+    R = t * k
+    assert R * d * 4 > 2 ** 31 and int(off[-1]) == R
+    X, W = rnd(g, R, i), stacked(g, e, d, i, BF)
+    Q, s = forge.quantize_rows(X)
+    q, sw = forge.quantize_rows(W.reshape(-1, i))
+    q = q.view(W.shape)
+
+    def by_parts(whole, call):
+        for a, b, c in spans(off):
+            lo = max(b, c - 7000)
+            part = torch.zeros(e + 1, device="cuda", dtype=torch.int64)
+            part[a + 1:] = c - lo
+            assert torch.equal(whole[lo:c], call(lo, c, part))
+
+    Yp = forge.expert_linear_q8(Q, s, q, sw, off, out_dtype=F)
+    by_parts(Yp, lambda lo, hi, o: forge.expert_linear_q8(Q[lo:hi], s[lo:hi], q, sw, o, out_dtype=F))
+    del Yp
+    Yp = forge.expert_linear(X, W, off, out_dtype=F)
+    by_parts(Yp, lambda lo, hi, o: forge.expert_linear(X[lo:hi], W, o, out_dtype=F))
+    pos = torch.randperm(R, device="cuda", generator=g).to(torch.int32).reshape(t, k)
+    w, dY = torch.rand(t, k, device="cuda", generator=g), rnd(g, t, d)
+    Y = forge.expert_combine(Yp, pos, w, out_dtype=BF)
+    dYp, dw = forge.expert_combine_backward(dY, Yp, pos, w)
+    assert torch.any(pos > 2 ** 31 // (4 * d))
+    for lo in range(0, t, 10000):
+        at = slice(lo, min(t, lo + 10000))
+        close("combine", Y[at], *combine64(Yp, pos[at], w[at]))
+        rows = pos[at].long()
+        p = Yp[rows].double() * dY[at].double()[:, None, :]
+        close("dw", dw[at], p.sum(2), (d + 1) * U * p.abs().sum(2))
+        want = dY[at].double()[:, None, :] * w[at].double()[:, :, None]
+        close("dYp", dYp[rows].reshape(-1, d), want.reshape(-1, d), U * want.abs().reshape(-1, d))
+        del p, want
