@@ -41,73 +41,81 @@ __global__ __launch_bounds__(64 * K_NW) void lin_skinny_kernel(LinArgs g) {
 #pragma unroll
   for (int i = 0; i < NA; ++i)
     a[i] = static_cast<const char*>(g.A[i]) + ((int64_t)ex * g.M + (row_ok ? m0 + l16 : 0)) * g.lda[i] * 2 + 16 * q;
-  for (int n0 = r0; n0 < r1; n0 += 16 * NF) {
-  const char* b[NF];
+  auto pass = [&](const int n0) FORGE_INLINE {  // the rows from n0 on
+    const char* b[NF];
 #pragma unroll
-  for (int f = 0; f < NF; ++f) {
-    const int n = n0 + 16 * f + l16;
-    b[f] = static_cast<const char*>(g.B[0]) + (int64_t)(n < r1 ? n : r0) * g.ldb[0] * 2 + 16 * q;
-  }
-  f32x4 acc[NA][NF];
-#pragma unroll
-  for (int i = 0; i < NA; ++i)
-#pragma unroll
-    for (int f = 0; f < NF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // rows and tokens past the edge read the first row (their sums are dropped); k past the end reads 0
-  auto ld = [&](const char* p, int s) -> u32x4 {
-    return s < s1 && 32 * s + 8 * q < K ? *reinterpret_cast<const u32x4*>(p + (int64_t)s * 64) : u32x4{0u, 0u, 0u, 0u};
-  };
-  for (int s = s0; s < s1; s += K_UN) {
-    u32x4 x[NA][K_UN], y[NF][K_UN];
-#pragma unroll
-    for (int u = 0; u < K_UN; ++u) {
-#pragma unroll
-      for (int i = 0; i < NA; ++i) x[i][u] = ld(a[i], s + u);
-#pragma unroll
-      for (int f = 0; f < NF; ++f) y[f][u] = ld(b[f], s + u);
+    for (int f = 0; f < NF; ++f) {
+      const int n = n0 + 16 * f + l16;
+      b[f] = static_cast<const char*>(g.B[0]) + (int64_t)(n < r1 ? n : r0) * g.ldb[0] * 2 + 16 * q;
     }
+    f32x4 acc[NA][NF];
 #pragma unroll
-    for (int u = 0; u < K_UN; ++u)
+    for (int i = 0; i < NA; ++i)
 #pragma unroll
-      for (int i = 0; i < NA; ++i)
+      for (int f = 0; f < NF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // rows and tokens past the edge read the first row (their sums are dropped); k past the end reads 0
+    auto ld = [&](const char* p, int s) -> u32x4 {
+      return s < s1 && 32 * s + 8 * q < K ? *reinterpret_cast<const u32x4*>(p + (int64_t)s * 64) : u32x4{0u, 0u, 0u, 0u};
+    };
+    for (int s = s0; s < s1; s += K_UN) {
+      u32x4 x[NA][K_UN], y[NF][K_UN];
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
-          if constexpr (Q8)
-            acc[i][f] = __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                                                      __builtin_bit_cast(i32x4, x[i][u]), __builtin_bit_cast(i32x4, y[f][u]),
-                                                      __builtin_bit_cast(i32x4, acc[i][f]), 0, 0, 0));
-          else
-            acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[i][u]),
-                                                                __builtin_bit_cast(bf16x8, y[f][u]), acc[i][f], 0, 0, 0);
-  }
-  if (n0 > r0) __syncthreads();  // the sums before are read
-  // lane holds C[row 4 q + j][token l16]
+      for (int u = 0; u < K_UN; ++u) {
 #pragma unroll
-  for (int i = 0; i < NA; ++i)
+        for (int i = 0; i < NA; ++i) x[i][u] = ld(a[i], s + u);
 #pragma unroll
-    for (int f = 0; f < NF; ++f) *reinterpret_cast<f32x4*>(&part[wave][i][f][l16][4 * q]) = acc[i][f];
-  __syncthreads();
-  const int t = threadIdx.x, f = t >> 6, n = n0 + 16 * f + ((t >> 2) & 15), c = (t & 3) * 4;
-  if (f < NF && n < r1 && m0 + c < g.M) {
-    f32x4 sum[NA];
-#pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      sum[i] = *reinterpret_cast<const f32x4*>(&part[0][i][f][(t >> 2) & 15][c]);
-#pragma unroll
-      for (int w = 1; w < K_NW; ++w) {
-        const f32x4 p = *reinterpret_cast<const f32x4*>(&part[w][i][f][(t >> 2) & 15][c]);
-        if constexpr (Q8)
-          sum[i] = __builtin_bit_cast(f32x4, __builtin_bit_cast(i32x4, sum[i]) + __builtin_bit_cast(i32x4, p));
-        else
-          sum[i] = sum[i] + p;
+        for (int f = 0; f < NF; ++f) y[f][u] = ld(b[f], s + u);
       }
-      if constexpr (Q8)
-        sum[i] = int_sums(sum[i]) * (load4((i ? g.e.sw2 : g.e.sw) + (int64_t)ex * g.M + m0 + c) * g.e.sx[n]);
+#pragma unroll
+      for (int u = 0; u < K_UN; ++u)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+          for (int f = 0; f < NF; ++f)
+            if constexpr (Q8)
+              acc[i][f] = __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                                                        __builtin_bit_cast(i32x4, x[i][u]), __builtin_bit_cast(i32x4, y[f][u]),
+                                                        __builtin_bit_cast(i32x4, acc[i][f]), 0, 0, 0));
+            else
+              acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[i][u]),
+                                                                  __builtin_bit_cast(bf16x8, y[f][u]), acc[i][f], 0, 0, 0);
     }
-    act_dispatch<EPI>(g.e.act, [&](auto act_c) {
-      epi_vec<uint16_t, EPI, decltype(act_c)::value>(g.e, n, m0 + c, g.M, sum[0], sum[NA - 1], 1.f);
-    });
-  }
+    if constexpr (EXP) {
+      if (n0 > r0) __syncthreads();  // the sums before are read
+    }
+    // lane holds C[row 4 q + j][token l16]
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+      for (int f = 0; f < NF; ++f) *reinterpret_cast<f32x4*>(&part[wave][i][f][l16][4 * q]) = acc[i][f];
+    __syncthreads();
+    const int t = threadIdx.x, f = t >> 6, n = n0 + 16 * f + ((t >> 2) & 15), c = (t & 3) * 4;
+    if (f < NF && n < r1 && m0 + c < g.M) {
+      f32x4 sum[NA];
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        sum[i] = *reinterpret_cast<const f32x4*>(&part[0][i][f][(t >> 2) & 15][c]);
+#pragma unroll
+        for (int w = 1; w < K_NW; ++w) {
+          const f32x4 p = *reinterpret_cast<const f32x4*>(&part[w][i][f][(t >> 2) & 15][c]);
+          if constexpr (Q8)
+            sum[i] = __builtin_bit_cast(f32x4, __builtin_bit_cast(i32x4, sum[i]) + __builtin_bit_cast(i32x4, p));
+          else
+            sum[i] = sum[i] + p;
+        }
+        if constexpr (Q8)
+          sum[i] = int_sums(sum[i]) * (load4((i ? g.e.sw2 : g.e.sw) + (int64_t)ex * g.M + m0 + c) * g.e.sx[n]);
+      }
+      act_dispatch<EPI>(g.e.act, [&](auto act_c) {
+        epi_vec<uint16_t, EPI, decltype(act_c)::value>(g.e, n, m0 + c, g.M, sum[0], sum[NA - 1], 1.f);
+      });
+    }
+  };
+  // (a loop around the one pass of the other forms costs them their schedule: 1 x 4096 -> 2 x 14336 gated, 40.8 us, takes 42.8)
+  if constexpr (EXP) {
+    for (int n0 = r0; n0 < r1; n0 += 16 * NF) pass(n0);
+  } else {
+    pass(0);
   }
 }
 
