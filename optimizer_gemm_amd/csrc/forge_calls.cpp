@@ -6,7 +6,10 @@
 // of the tensors; all else in the entry points.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <ATen/ops/empty.h>
 #include <dlfcn.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
@@ -216,8 +219,37 @@ PyObject* load(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+// empty(device index, dtype, *sizes): torch.empty on that device, without the time that parsing its arguments takes (of
+// 1.25 us for a matrix); what torch.empty honours, deterministic fill and dispatch modes, at::empty does
+PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n < 2 || !THPDtype_Check(args[1])) throw std::invalid_argument("empty(device index, dtype, *sizes) wanted");
+  int64_t v[FORGE_MAX_GROUP + 1];
+  const Py_ssize_t dims = n - 2;
+  if (dims > FORGE_MAX_GROUP) throw std::invalid_argument("too many dimensions");
+  for (Py_ssize_t i = 0; i <= dims; ++i) {  // (the device's index, then the sizes)
+    v[i] = PyLong_AsLongLong(args[i ? i + 1 : 0]);
+    if (v[i] == -1 && PyErr_Occurred()) return nullptr;
+  }
+  const auto options = at::TensorOptions()
+                           .dtype(reinterpret_cast<THPDtype*>(args[1])->scalar_type)
+                           .device(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(v[0])));
+  struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+  };
+  at::Tensor t;
+  {
+    Released gil;
+    t = at::empty(at::IntArrayRef(v + 1, dims), options);
+  }
+  return THPVariable_Wrap(std::move(t));
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"load", load, METH_VARARGS, nullptr},
+    {"empty", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empty)), METH_FASTCALL, nullptr},
 #define FORGE_METHOD(NAME, KINDS) \
   {#NAME, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##NAME)), METH_FASTCALL, nullptr},
     FORGE_CALLS(FORGE_METHOD)

@@ -363,3 +363,11 @@ def test_float32_rows_beside_bfloat16_hold_as_many_elements():
         assert lin(511, 512, q, 1 << 21) == UNSUP  # 256 rows of them past 2^31 bytes
     assert com(n, 512) == com(n, 1016) == ALIAS and com(n, 1024) == UNSUP and com(n, 512, F32) == UNSUP
     assert back(n, 512) == back(n, 1016) == ALIAS and back(n, 1024) == UNSUP
+
+
+def test_new_tensors_check_their_arguments():
+    from optimizer_gemm_amd import forge as f
+    for bad in ((), (0,), (0, "float32", 3), (0, torch.float32, "x"), ("x", torch.float32, 3), (0, torch.float32, 1, 1, 1, 1, 1),
+                (0, torch.float32, -1)):
+        with pytest.raises((RuntimeError, TypeError, ValueError)):
+            f._calls.empty(*bad)

@@ -414,3 +414,45 @@ def test_one_block_trains():
     assert blk.gate.step_count == 4
     for a, b in zip(stacks(blk), W):
         assert torch.isfinite(a).all() and not torch.equal(a, b)
+
+
+# ---- what a call allocates -----------------------------------------------------------------------------------------
+@pytest.mark.parametrize("short", [True, False])
+def test_new_tensors_are_those_of_torch(short, monkeypatch):
+    """a call's new tensors honour what torch.empty does: the fill of deterministic mode and dispatch modes, by the shorter
+    way and, where forge_calls is not there, by torch.empty itself"""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    impl = forge.forge
+    assert impl._new is not None
+    if not short:
+        monkeypatch.setattr(impl, "_new", None)
+    x, W, off = rnd(1, 40, 128), rnd(2, 3, 264, 128), torch.tensor([0, 10, 10, 25], device="cuda")
+    want = forge.expert_linear(x, W, off)[:25].clone()
+
+    class Seen(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.names = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            self.names.append(str(func))
+            return func(*args, **(kwargs or {}))
+
+    with Seen() as seen:
+        y, z = forge.linear(x, W[0], save=True)
+        forge.expert_plan(torch.zeros(40, 2, device="cuda", dtype=torch.int64), 3)
+    assert sum("empty" in n for n in seen.names) == 4
+    assert y.shape == z.shape == (40, 264) and y.dtype == BF and y.is_contiguous() and y.device == x.device
+    torch.use_deterministic_algorithms(True)
+    try:
+        for _ in range(3):
+            junk = [torch.full((40, 264), 7.0, device="cuda", dtype=BF) for _ in range(8)]
+            del junk  # (what torch.empty would hand out as it is)
+            y = forge.expert_linear(x, W, off)
+            assert torch.equal(y[:25], want) and torch.isnan(y[25:]).all()
+    finally:
+        torch.use_deterministic_algorithms(False)
+    d = impl._here[0]
+    assert d.empty((3,), torch.int64).shape == (3,) and d.empty((2, 0), F).shape == (2, 0)
+    assert d.empty((2, 3, 5), F).stride() == (15, 5, 1)
