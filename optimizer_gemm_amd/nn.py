@@ -552,6 +552,16 @@ class ForgeStack(torch.nn.Module):
     def step_count(self) -> int:
         return self._step_count
 
+    def _check_step(self) -> None:
+        """What no step takes is refused by the forward pass of a training step, not at the end of its backward pass."""
+        e, o, i = self.weight.shape
+        if e * o * i >= 2 ** 32:
+            raise ValueError(f"a stack that is trained holds fewer than 2^32 weights, not [{e}, {o}, {i}]")
+        held = [self.weight, *(t for t in (self.m, self.v) if t is not None)] if self.fused else []
+        if o * i * max((t.element_size() for t in held), default=4) >= 2 ** 31:
+            what = "weights and moments span" if self.fused else "float32 gradient spans"
+            raise ValueError(f"an expert's {what} less than 2^31 bytes in a stack that is trained, not [{o}, {i}]")
+
     def _update(self, x2: torch.Tensor, dy2: torch.Tensor, offsets: torch.Tensor) -> None:
         if not self.fused:
             g = forge.expert_wgrad(x2, dy2, offsets)
@@ -637,7 +647,9 @@ class ForgeExperts(torch.nn.Module):
     router (an idx outside [0, experts) drops the route); x and weights receive gradients. Arguments as
     ForgeLinear's; `act` the gate's activation. Rows are counted on the device: no call waits for the routes, and the
     block can be captured into a graph. Each backward call is one step of all experts; a second one of an output computed
-    before it is refused (two-phase blocks, fused=False, take it, and step with step_all())."""
+    before it is refused (two-phase blocks, fused=False, take it, and step with step_all()). Sizes: routes * d and routes *
+    hidden elements span less than 2^31 bytes in the stacks' type; a stack that is trained holds fewer than 2^32 weights, and
+    one expert's weights and moments (two-phase: its float32 gradient) less than 2^31 bytes each."""
 
     def __init__(self, d: int, hidden: int, experts: int, act: str = "silu", seed: int = 0, **kw):
         super().__init__()
@@ -655,7 +667,11 @@ class ForgeExperts(torch.nn.Module):
         if idx.shape != weights.shape or idx.dim() < 1:
             raise ValueError(f"routes of shape {tuple(idx.shape)} with weights of {tuple(weights.shape)}")
         stacks = (self.gate.weight, self.up.weight, self.down.weight)
-        return _ExpertsFn.apply(x, idx, weights, residual, *stacks, self, _differentiated(x, weights, residual, *stacks),
+        recorded = _differentiated(x, weights, residual, *stacks)
+        if recorded:
+            for stack in (self.gate, self.up, self.down):
+                stack._check_step()
+        return _ExpertsFn.apply(x, idx, weights, residual, *stacks, self, recorded,
                                 torch.is_grad_enabled() and weights.requires_grad)
 
 

@@ -371,3 +371,28 @@ def test_new_tensors_check_their_arguments():
                 (0, torch.float32, -1)):
         with pytest.raises((RuntimeError, TypeError, ValueError)):
             f._calls.empty(*bad)
+
+
+def test_a_stack_that_no_step_takes_is_refused_by_the_forward_pass():
+    """the limits of the step (2^32 weights, 2^31 bytes of an expert) are checked before a training step's forward pass; a
+    forward pass without a gradient goes on (here to the check of the device)"""
+    from optimizer_gemm_amd.nn import ForgeExperts
+
+    idx, w = torch.zeros(2, 1, dtype=torch.int64, device="meta"), torch.zeros(2, 1, device="meta")
+
+    def block(d, h, e, **kw):
+        return ForgeExperts(d, h, e, device="meta", **kw), torch.zeros(2, d, dtype=torch.bfloat16, device="meta")
+
+    for args, kw, match in (((8192, 65536, 8), {"opt": "sgd"}, "fewer than 2.32 weights"),
+                            ((8192, 65536, 4), {}, "moments span less than 2.31"),
+                            ((8192, 65536, 4), {"states": "bf16", "fused": False}, "gradient spans less than 2.31"),
+                            ((8192, 131072, 2), {"opt": "sgd"}, "moments span less than 2.31")):
+        blk, x = block(*args, **kw)
+        with pytest.raises(ValueError, match=match):
+            blk(x, idx, w)
+        with torch.no_grad(), pytest.raises(ValueError, match="device tensors"):
+            blk(x, idx, w)
+    for args, kw in (((8192, 65536, 7), {"states": "bf16"}), ((8192, 65536, 7), {"opt": "sgd"}), ((8192, 65528, 7), {})):
+        blk, x = block(*args, **kw)
+        with pytest.raises(ValueError, match="device tensors"):
+            blk(x, idx, w)
