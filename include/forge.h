@@ -520,6 +520,23 @@ int forge_step_scalars(int32_t opt, const forge_hyper* hyper, int64_t step, forg
 /* Defaults of the optimizer sweep for `opt` (lr, betas, eps, decay ...). Returns a status. */
 int forge_default_hyper(int32_t opt, forge_hyper* out);
 
+/*
+ * The tiles that a call grouped by expert is cut into, so that a tuning run or a test can tell which kernel it has: the
+ * edge of the output tiles of a bfloat16 (with dtype FORGE_I8: 8-bit) product, 256, 128 or 64, or 0 for the kernel of a
+ * few rows. rows: of all experts; cols, k: columns of the result and inner dimension (FORGE_EXPERT_WGRAD, the stack's gradient
+ * and step: in and out). FORGE_EXPERT_DGRAD: without a workspace. 256-row tiles of a product are counted in rounds of one a
+ * compute unit; a last round that is at most half full runs as quarters. Negative: a status.
+ */
+typedef enum {
+  FORGE_EXPERT_LINEAR = 0,
+  FORGE_EXPERT_SUMS = 1, /* float32 results */
+  FORGE_EXPERT_GATED = 2,
+  FORGE_EXPERT_GATED_DGRAD = 3,
+  FORGE_EXPERT_DGRAD = 4,
+  FORGE_EXPERT_WGRAD = 5
+} forge_expert_product;
+int32_t forge_expert_tile(int32_t product, int64_t rows, int64_t cols, int64_t k, int32_t experts, int32_t dtype);
+
 /* The stochastic-rounding random bits of element `idx` at `step` (same hash as the kernels). */
 uint32_t forge_rand16(uint64_t seed, int64_t step, uint32_t idx);
 

@@ -522,4 +522,23 @@ int forge_expert_gated_q8(const forge_tensor* X, const forge_tensor* Wg, const f
   return linear_q8(X, Wg, Wu, experts, offsets, nullptr, act, nullptr, H, (hipStream_t)stream);
 }
 
+int32_t forge_expert_tile(int32_t product, int64_t rows, int64_t cols, int64_t k, int32_t experts, int32_t dtype) {
+  if (rows < 1 || cols < 1 || k < 0 || rows >= kMaxDim || cols >= kMaxDim || k >= kMaxDim || experts < 1 || experts > FORGE_MAX_EXPERTS)
+    return FORGE_ERR_SHAPE;
+  if (dtype != FORGE_BF16 && dtype != FORGE_I8) return FORGE_ERR_DTYPE;
+  const bool q8 = dtype == FORGE_I8;
+  switch (product) {
+    case FORGE_EXPERT_LINEAR:
+      return q8 ? lin_q8_expert_edge(L_LINEAR, cols, rows, k, experts) : lin_expert_edge(L_LINEAR, false, cols, rows, k, experts);
+    case FORGE_EXPERT_SUMS:
+      return q8 ? lin_q8_expert_edge(L_ACC, cols, rows, k, experts) : lin_expert_edge(L_ACC, false, cols, rows, k, experts);
+    case FORGE_EXPERT_GATED:
+      return q8 ? lin_q8_expert_edge(L_GATED, cols, rows, k, experts) : lin_expert_edge(L_GATED, false, cols, rows, k, experts);
+    case FORGE_EXPERT_GATED_DGRAD: return q8 ? FORGE_ERR_DTYPE : lin_expert_edge(L_DGATE, true, cols, rows, k, experts);
+    case FORGE_EXPERT_DGRAD: return q8 ? FORGE_ERR_DTYPE : lin_expert_edge(L_ACC, true, cols, rows, k, experts);
+    case FORGE_EXPERT_WGRAD: return q8 ? FORGE_ERR_DTYPE : wgrad_expert_edge(k, cols, experts);
+    default: return FORGE_ERR_UNSUPPORTED;
+  }
+}
+
 }  // extern "C"

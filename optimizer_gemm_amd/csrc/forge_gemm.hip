@@ -180,6 +180,11 @@ hipError_t launch_wgrad_store_expert_bf16(const void* X, const void* dY, const G
   });
 }
 
+int wgrad_expert_edge(int64_t out, int64_t in, int experts) {
+  const GArgs g = expert_args(nullptr, nullptr, GemmDims{0, (int32_t)out, (int32_t)in, in, out}, nullptr, experts);
+  return g_expert_small(g) ? WgradSmall::BM : WgradBig::BM;
+}
+
 template <int FB>
 static hipError_t wgrad_fused_f8(int sf, int opt, int sr, const GArgs& g, const OptArgs& a, hipStream_t st) {
   switch (opt) {

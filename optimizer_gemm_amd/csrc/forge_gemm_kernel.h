@@ -1390,10 +1390,10 @@ static int64_t g_rounds(const GArgs& g) {
   const int64_t resident = C::OCC * 4 / C::NW * g_num_cus();
   return ((int64_t)g_tiles<C>(g) * g.experts + resident - 1) / resident;
 }
+static bool g_expert_small(const GArgs& g) { return 3 * g_rounds<WgradSmall>(g) < 4 * g_rounds<WgradBig>(g); }
 template <class F>
 static hipError_t g_pick_expert(const GArgs& g, F&& f) {
-  if (3 * g_rounds<WgradSmall>(g) < 4 * g_rounds<WgradBig>(g)) return f(WgradSmall{});
-  return f(WgradBig{});
+  return g_expert_small(g) ? f(WgradSmall{}) : f(WgradBig{});
 }
 
 template <int OPT>

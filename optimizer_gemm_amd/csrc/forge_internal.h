@@ -414,6 +414,8 @@ hipError_t launch_wgrad_fused_expert_bf16(int state_fmt, int opt, int sr, const 
                                           hipStream_t stream);
 hipError_t launch_wgrad_store_expert_bf16(const void* X, const void* dY, const GemmDims& d, const int64_t* offsets,
                                           int experts, float* dW, int64_t ld_dw, hipStream_t stream);
+// edge of the tiles of bfloat16 stacks
+int wgrad_expert_edge(int64_t out, int64_t in, int experts);
 // bfloat16 / FP8 kernels (forge_gemm.hip, forge_gemm_kernel.h)
 hipError_t launch_wgrad_fused_bf16(int state_fmt, int opt, int sr, const void* X, const void* dY, const GemmDims& d,
                                    const OptArgs& a, hipStream_t stream);

@@ -1069,6 +1069,12 @@ inline ExpertSplit lin_expert_split(int64_t M, int64_t N, int experts, int64_t K
 }
 
 template <int EPI, bool TA, int MODE>
+LinTileKind lin_expert_tile(int64_t M, int64_t N, int experts, double stages) {
+  return lin_expert_kind<EPI, TA, MODE>(ExpertCost(EPI == L_GATED ? 2 * M : M, N, experts), stages).kind;
+}
+inline int lin_tile_edge(LinTileKind kind) { return kind == LT_BIG ? 256 : kind == LT_TINY ? 64 : 128; }
+
+template <int EPI, bool TA, int MODE>
 hipError_t lin_expert(const LinArgs& g0, hipStream_t st) {
   LinArgs g = g0;
   const int64_t cus = g_num_cus(), w = EPI == L_GATED ? 2 * (int64_t)g.M : g.M;
@@ -1082,7 +1088,7 @@ hipError_t lin_expert(const LinArgs& g0, hipStream_t st) {
   }
   double stages = 0.0;
   for (int s = 0; s < g.nsrc; ++s) stages += (g.K[s] + 63) / 64;
-  const LinTileKind kind = lin_expert_kind<EPI, TA, MODE>(ExpertCost(w, g.N, g.experts), stages).kind;
+  const LinTileKind kind = lin_expert_tile<EPI, TA, MODE>(g.M, g.N, g.experts, stages);
   if (kind == LT_TINY) return lin_run<LinTiny, EPI, TA, false, MODE>(g, st);
   if (kind == LT_SMALL) return lin_run<LinSmall, EPI, TA, false, MODE>(g, st);
   // where there can be more large tiles than a round has (whatever the experts' sizes are)

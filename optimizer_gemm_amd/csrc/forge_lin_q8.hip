@@ -25,13 +25,31 @@ hipError_t lin_q8(const LinArgs& g, hipStream_t st) {
 // of each matrix there (1 x 4096 -> 2 x 14336, 117 MB: 31 us against 24 with tiles; 4 of 8 experts, 470 MB: 119
 // against 96; but 5 of 16 experts, 4096 -> 2 x 1792, 73 MB: 20.6 against 22.2).
 bool q8_much_memory(const LinArgs& g, int64_t used) { return used * g.M * g.K[0] * 4 >= 96 * 1000 * 1000; }
+bool q8_few_rows(int epi, const LinArgs& g) {
+  return few_rows(g) && !(epi == L_GATED && q8_much_memory(g, g.experts < g.N ? g.experts : g.N));
+}
 
 }  // namespace
 
+int lin_q8_expert_edge(int epi, int64_t M, int64_t N, int64_t K, int experts) {
+  LinArgs g{};
+  set_pair(g, 0, nullptr, 0, nullptr, 0, K / 2);
+  g.M = (int32_t)M;
+  g.N = (int32_t)N;
+  g.experts = experts;
+  if (q8_few_rows(epi, g)) return 0;
+  const double stages = (g.K[0] + 63) / 64;
+  switch (epi) {
+    case L_LINEAR: return lin_tile_edge(lin_expert_tile<L_LINEAR, false, LM_EXPERT | LM_Q8>(M, N, experts, stages));
+    case L_ACC: return lin_tile_edge(lin_expert_tile<L_ACC, false, LM_EXPERT | LM_Q8>(M, N, experts, stages));
+    case L_GATED: return lin_tile_edge(lin_expert_tile<L_GATED, false, LM_EXPERT | LM_Q8>(M, N, experts, stages));
+    default: return FORGE_ERR_UNSUPPORTED;
+  }
+}
+
 hipError_t launch_lin_q8(int epi, const LinArgs& g, hipStream_t st) {
   if (g.experts > 0) {
-    if (few_rows(g) && !(epi == L_GATED && q8_much_memory(g, g.experts < g.N ? g.experts : g.N)))
-      return launch_lin_skinny(LM_EXPERT | LM_Q8, epi, g, st);
+    if (q8_few_rows(epi, g)) return launch_lin_skinny(LM_EXPERT | LM_Q8, epi, g, st);
     return epi == L_GATED ? lin_expert<L_GATED, false, LM_EXPERT | LM_Q8>(g, st)
            : epi == L_ACC ? lin_expert<L_ACC, false, LM_EXPERT | LM_Q8>(g, st)
                           : lin_expert<L_LINEAR, false, LM_EXPERT | LM_Q8>(g, st);

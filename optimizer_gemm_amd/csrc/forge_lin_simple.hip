@@ -305,6 +305,21 @@ int lin_splits(int bf16, int64_t M, int64_t N, int64_t K) {
   return s < 2 ? 1 : (int)s;
 }
 
+int lin_expert_edge(int epi, bool ta, int64_t M, int64_t N, int64_t K, int experts) {
+  LinArgs g{};
+  g.M = (int32_t)M;
+  g.N = (int32_t)N;
+  g.experts = experts;
+  if (!ta && few_rows(g)) return 0;
+  const double stages = (double)((K + 63) / 64);
+  if (!ta && epi == L_ACC) return lin_tile_edge(lin_expert_tile<L_ACC, false, LM_EXPERT>(M, N, experts, stages));
+#define FORGE_PICK(E, A) \
+  if (epi == E && ta == A) return lin_tile_edge(lin_expert_tile<E, A, LM_EXPERT>(M, N, experts, stages));
+  FORGE_LIN_EXPERT_FORMS(FORGE_PICK)
+#undef FORGE_PICK
+  return FORGE_ERR_UNSUPPORTED;
+}
+
 int lin_expert_splits(int bf16, int64_t M, int64_t N, int experts, int64_t K) {
   return bf16 ? lin_expert_split(M, N, experts, K).parts : 1;
 }

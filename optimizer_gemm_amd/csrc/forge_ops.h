@@ -416,6 +416,9 @@ bool few_rows(const LinArgs& g);
 // vocabulary entries per partial result that launch_lin(L_LSE) writes for this product
 int lin_lse_block(int bf16, int M, int N);
 
+// edge of the tiles that a bfloat16 or an 8-bit product by expert is cut into (0: the kernel for a few rows)
+int lin_expert_edge(int epi, bool ta, int64_t M, int64_t N, int64_t K, int experts);
+int lin_q8_expert_edge(int epi, int64_t M, int64_t N, int64_t K, int experts);
 // parts a product of k-slow A should be cut into (1: none): too few tiles to fill the chip with,
 // a k range long enough to share
 int lin_splits(int bf16, int64_t M, int64_t N, int64_t K);

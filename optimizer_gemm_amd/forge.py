@@ -172,6 +172,7 @@ def _load() -> ctypes.CDLL:
         "forge_expert_wgrad_step": ([P(ForgeTensor)] * 5 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
                                                             P(ForgeHyper), ctypes.c_int64, ctypes.c_uint64,
                                                             ctypes.c_void_p], ctypes.c_int),
+        "forge_expert_tile": ([ctypes.c_int32] + [ctypes.c_int64] * 3 + [ctypes.c_int32] * 2, ctypes.c_int32),
         "forge_quantize_rows": ([P(ForgeTensor)] * 2 + [ctypes.c_void_p], ctypes.c_int),
         "forge_linear_q8": ([P(ForgeTensor)] * 3 + [ctypes.c_int32] + [P(ForgeTensor)] * 2 + [ctypes.c_void_p],
                             ctypes.c_int),

@@ -396,3 +396,20 @@ def test_a_stack_that_no_step_takes_is_refused_by_the_forward_pass():
         blk, x = block(*args, **kw)
         with pytest.raises(ValueError, match="device tensors"):
             blk(x, idx, w)
+
+
+def test_tiles_of_a_product():
+    """which tiles a product takes is told for every kind, and refused for what is none"""
+    t = L.forge_expert_tile
+    for p in range(6):
+        for bad in ((0, 64, 64, 4), (16, 0, 64, 4), (16, 64, -1, 4), (16, 64, 64, 0), (16, 64, 64, 1025), (1 << 30, 64, 64, 4)):
+            assert t(p, *bad, BF16) == SHAPE
+        assert t(p, 16, 64, 64, 4, F32) == DTYPE
+        assert t(p, 20000, 4096, 4096, 8, BF16) in (256, 128, 64)
+        assert t(p, 20000, 4096, 4096, 8, I8) in ((256, 128, 64) if p < 3 else (DTYPE,))
+        # a few rows: forward products have a kernel of their own
+        assert t(p, 16, 4096, 4096, 8, BF16) == 0 if p < 3 else t(p, 16, 4096, 4096, 8, BF16) > 0
+    assert t(6, 16, 64, 64, 4, BF16) == UNSUP and t(-1, 16, 64, 64, 4, BF16) == UNSUP
+    assert t(1, 16, 4096, 4096, 8, I8) == 0 and t(2, 16, 4096, 14336, 8, I8) > 0  # (gated over much memory: tiles)
+    # the stack's gradient: two small rounds are taken for two large ones, five not for three
+    assert t(5, 100, 128, 1920, 40, BF16) == 128 and t(5, 100, 1088, 1800, 17, BF16) == 256
