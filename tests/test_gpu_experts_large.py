@@ -9,7 +9,7 @@ import torch
 import optimizer_gemm_amd as forge
 from _experts64 import (expert_dgrad64, expert_gated64, expert_gated_dgrad64, expert_linear64, expert_wgrad64, gated_q8_64,
                         grouped, linear_q8_64)
-from _ops64 import close
+from _ops64 import U, close, gated64, gated_back64, mm64
 
 pytestmark = pytest.mark.gpu
 
@@ -231,3 +231,124 @@ def test_step_in_several_rounds(case, fmt):
             assert torch.equal(W, W2), (opt, sr)
             for a, b in zip(st, st2):
                 assert a is None or torch.equal(a, b), (opt, sr)
+
+
+# ---- stacks past 2^31 bytes --------------------------------------------------------------------------------------
+@pytest.fixture
+def emptied():
+    yield
+    torch.cuda.empty_cache()
+
+
+def far_stack(g, e, o, i):
+    """zeros but for the last expert's matrix, which begins past 2^31 bytes"""
+    W = torch.zeros(e, o, i, device="cuda", dtype=BF)
+    W[e - 1] = rnd(g, o, i, std=i ** -0.5)
+    assert (e - 1) * o * i * 2 >= 2 ** 31
+    return W
+
+
+@pytest.mark.parametrize("rows", [[1, 2, 9], [0, 3, 70], [100, 300, 1100]])
+def test_gated_block_past_two_gigabytes(rows, emptied):
+    """the gated product and its backward pass: an expert of zeros, and the last one, for a few rows and for tiles"""
+    e, h, d = 17, 8192, 8192
+    g, n = gen(sum(rows)), sum(rows)
+    off = torch.tensor([0] * 15 + [rows[0], rows[0] + rows[1], n], device="cuda")
+    last = slice(rows[0] + rows[1], n)
+    Wg, Wu = far_stack(g, e, h, d), far_stack(g, e, h, d)
+    X = rnd(g, n, d)
+    H, G, V = forge.expert_gated(X, Wg, Wu, off, act="silu", save=True)
+    assert torch.all(H[:last.start] == 0) and torch.all(G[:last.start] == 0) and torch.all(V[:last.start] == 0)
+    h64, dh, gt, dg, u, du = gated64(X[last], Wg[-1], Wu[-1], "silu")
+    close("H", H[last], h64, dh)
+    close("G", G[last], gt, dg)
+    close("U", V[last], u, du)
+    del Wu
+    dY, G, V = rnd(g, n, h), rnd(g, n, d), rnd(g, n, d)  # (the first stack as the layer behind: [e, h, d])
+    dG, dU, H = forge.expert_gated_dgrad(dY, Wg, G, V, off, act="gelu")
+    assert torch.all(dG[:last.start] == 0) and torch.all(dU[:last.start] == 0)
+    want = gated_back64(*mm64(dY[last], Wg[-1]), G[last], V[last], "gelu")
+    for name, a, b in zip(("dG", "dU", "H"), (dG, dU, H), (want[:2], want[2:4], want[4:])):
+        close(name, a[last], *b)
+
+
+@pytest.mark.parametrize("rows", [[1, 2, 9], [100, 300, 1100]])
+def test_8_bit_products_past_two_gigabytes(rows, emptied):
+    e, o, i = 9, 16384, 16384
+    g, n = gen(sum(rows)), sum(rows)
+    off = torch.tensor([0] * 7 + [rows[0], rows[0] + rows[1], n], device="cuda")
+    last = slice(rows[0] + rows[1], n)
+    assert (e - 1) * o * i >= 2 ** 31
+
+    def stack():
+        W = torch.zeros(e, o, i, device="cuda", dtype=torch.int8)
+        W[-1] = torch.randint(-127, 128, (o, i), device="cuda", generator=g).to(torch.int8)
+        return W, (torch.rand(e, o, device="cuda", generator=g) + 0.5) * 1e-3
+
+    X, sx = torch.randint(-127, 128, (n, i), device="cuda", generator=g).to(torch.int8), torch.rand(n, device="cuda", generator=g) * 1e-2
+    (W, sw), (W2, s2) = stack(), stack()
+    for dtype in (BF, F):
+        Y = forge.expert_linear_q8(X, sx, W, sw, off, out_dtype=dtype)
+        assert torch.all(Y[:last.start] == 0)
+        close("linear", Y[last], *linear_q8_64(X[last], sx[last], W[-1], sw[-1]))
+    H = forge.expert_gated_q8(X, sx, W, sw, W2, s2, off, act="silu")
+    assert torch.all(H[:last.start] == 0)
+    close("gated", H[last], *gated_q8_64(X[last], sx[last], W[-1], sw[-1], W2[-1], s2[-1], "silu"))
+
+
+def far_gradient(g, e, o, i, dtype):
+    """rows of the first and of the last expert, and the stack's gradient, which is exact in float32"""
+    off = torch.tensor([0, 40] + [40] * (e - 2) + [107], device="cuda")
+    X = torch.randint(-4, 5, (107, i), device="cuda", generator=g).to(dtype)
+    dY = (torch.randint(-4, 5, (107, o), device="cuda", generator=g).to(F) * 2.0 ** -12).to(dtype)
+    dW = torch.zeros(e, o, i, device="cuda")
+    for x, r in ((0, slice(0, 40)), (e - 1, slice(40, 107))):
+        dW[x] = (dY[r].double().t() @ X[r].double()).float()
+    return off, X, dY, dW
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_gradient_past_two_gigabytes(dtype, emptied):
+    e, o, i = 9, 8192, 8192
+    off, X, dY, want = far_gradient(gen(1), e, o, i, dtype)
+    assert (e - 1) * o * i * 4 >= 2 ** 31
+    dW = torch.full((e, o, i), NAN, device="cuda")
+    forge.expert_wgrad(X, dY, off, dW=dW)
+    assert torch.equal(dW, want)
+
+
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "q8", "q8dyn"])
+def test_step_past_two_gigabytes(fmt, emptied):
+    """weights and moments of every format: the bits of the stand-alone optimizer pass over the stack as one layer"""
+    e, o, i = 17, 8192, 16384
+    g = gen(2)
+    off, X, dY, dW = far_gradient(g, e, o, i, BF)
+    assert (e - 1) * o * i >= 2 ** 31  # bytes of 8-bit moments, the smallest
+    W = torch.empty(e, o, i, device="cuda", dtype=BF).normal_(0.0, 0.02, generator=g)
+    code = "dynamic" if fmt == "q8dyn" else "linear"
+    st = random_states(W, "adamw", fmt, g)
+    W2, st2 = W.clone(), [None if t is None else t.clone() for t in st]
+    forge.expert_wgrad_step(X, dY, W, st[0], st[1], off, "adamw", None, 5, 99, st[2], st[3], code=code)
+    flat = [None if t is None else t.view(e * o, -1) for t in (W2, *st2)]
+    forge.optimizer_step(dW.view(e * o, i), flat[0], flat[1], flat[2], "adamw", None, 5, 99, flat[3], flat[4], code=code)
+    assert torch.equal(W, W2)
+    for a, b in zip(st, st2):
+        assert a is None or torch.equal(a, b)
+
+
+def test_float32_step_past_two_gigabytes(emptied):
+    e, o, i = 9, 4096, 16384
+    g = gen(3)
+    off, X, dY, dW = far_gradient(g, e, o, i, F)
+    assert (e - 1) * o * i * 4 >= 2 ** 31
+    W = rnd(g, e, o, i, dtype=F, std=0.02)
+    st = random_states(W, "adamw", "f32", g)
+    W2, st2 = W.clone(), [t if t is None else t.clone() for t in st]
+    forge.expert_wgrad_step(X, dY, W, st[0], st[1], off, "adamw", None, 3, 1)
+    flat = [None if t is None else t.view(e * o, -1) for t in (W2, *st2)]
+    forge.optimizer_step(dW.view(e * o, i), flat[0], flat[1], flat[2], "adamw", None, 3, 1)
+    for x in range(e):
+        # both passes round each operation of the update on its own path: a step of float32 or two
+        close("W", W[x], W2[x].double(), 8 * U * W2[x].double().abs() + 8 * U * 1e-3)
+        for a, b in zip(st[:2], st2[:2]):
+            close("moment", a[x], b[x].double(), 4 * U * b[x].double().abs() + 4 * U * 1e-6)
