@@ -533,6 +533,28 @@ def test_an_expert_without_rows_still_steps():
     assert not torch.equal(W[1], W2[1])
 
 
+# ---- the roundings of a token's gradient -------------------------------------------------------------------------------
+@pytest.mark.parametrize("k", [1, 2, 8])
+def test_gradient_of_a_token_with_several_routes(k):
+    """The input gradient of each route is a bfloat16 row (the half step of each is in the bound), their sum is float32 and
+    rounded once more"""
+    g = gen(40 + k)
+    t, e, d, h = 300, 8, 264, 520
+    offsets, pos = forge.expert_plan(routes(k, t, k, e, dropped=0.1).cuda(), e)
+    n = int(offsets[-1])
+    W = [stacked(g, e, h, d, BF), stacked(g, e, h, d, BF)]
+    D = [rnd(g, t * k, h), rnd(g, t * k, h)]
+    dX = forge.expert_combine(forge.expert_dgrad_group(D, W, offsets), pos)
+    x, dx = expert_dgrad64([a[:n] for a in D], W, offsets)
+    dx = dx + 2.0 ** -8 * (x.abs() + dx)
+    p, got = pos.long().clamp(min=0), (pos >= 0)[:, :, None]
+    rows, bound = torch.where(got, x[p.clamp(max=n - 1)], 0.0), torch.where(got, dx[p.clamp(max=n - 1)], 0.0)
+    want, bound = rows.sum(1), bound.sum(1) + (k + 1) * U * (rows.abs() + bound).sum(1)
+    close(f"dx of {k} routes", dX, want, bound)
+    print(f"[ops] relative error {float((dX.double() - want).norm() / want.norm()):.5f}, of one rounding "
+          f"{float((want.to(BF).double() - want).norm() / want.norm()):.5f}")
+
+
 # ---- a gradient against differences ------------------------------------------------------------------------------
 def test_gradients_against_differences():
     """The block's input gradient in float32 against central differences of the float64 form at the same point"""
