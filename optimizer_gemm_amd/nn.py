@@ -622,6 +622,9 @@ class _ExpertsFn(torch.autograd.Function):
     @_once
     def backward(ctx, dy):
         gate, up, down = ctx.block.gate, ctx.block.up, ctx.block.down
+        if torch.cuda.is_current_stream_capturing():
+            # steps are counted here, which no replay does: it would take the same step again, with the same random bits
+            raise RuntimeError("a block's backward pass steps and counts on the host: a graph takes the operators' calls")
         _check_unstepped((gate, up, down), ctx.counts)
         x2, pos, offsets, w2, G, U, yp, wg, wu, wd = ctx.saved_tensors
         wg, wu, wd = wg.detach(), wu.detach(), wd.detach()
@@ -646,7 +649,8 @@ class ForgeExperts(torch.nn.Module):
     block of expert idx[t, j] on x[t], plus `residual` if given. idx [..., k] int64 and weights [..., k] come from the
     router (an idx outside [0, experts) drops the route); x and weights receive gradients. Arguments as
     ForgeLinear's; `act` the gate's activation. Rows are counted on the device: no call waits for the routes, and the
-    block can be captured into a graph. Each backward call is one step of all experts; a second one of an output computed
+    forward pass can be captured into a graph, whose replays follow new ones (a backward pass that is captured is refused: replays
+    would not count their steps; the operators' calls can be captured, with the step's number as it is then). Each backward call is one step of all experts; a second one of an output computed
     before it is refused (two-phase blocks, fused=False, take it, and step with step_all()). Sizes: routes * d and routes *
     hidden elements span less than 2^31 bytes in the stacks' type; a stack that is trained holds fewer than 2^32 weights, and
     one expert's weights and moments (two-phase: its float32 gradient) less than 2^31 bytes each."""

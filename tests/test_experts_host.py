@@ -413,3 +413,17 @@ def test_tiles_of_a_product():
     assert t(1, 16, 4096, 4096, 8, I8) == 0 and t(2, 16, 4096, 14336, 8, I8) > 0  # (gated over much memory: tiles)
     # the stack's gradient: two small rounds are taken for two large ones, five not for three
     assert t(5, 100, 128, 1920, 40, BF16) == 128 and t(5, 100, 1088, 1800, 17, BF16) == 256
+
+
+def test_a_captured_backward_pass_of_a_block_is_refused(monkeypatch):
+    """its steps are counted on the host, where a replay does not come by"""
+    from types import SimpleNamespace
+
+    from optimizer_gemm_amd import nn as fnn
+
+    stack = SimpleNamespace(_step_count=0)
+    ctx = SimpleNamespace(block=SimpleNamespace(gate=stack, up=stack, down=stack), counts=[0, 0, 0])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="a graph takes the operators' calls"):
+        fnn._ExpertsFn.backward(ctx, torch.zeros(2, 8))
+    assert stack._step_count == 0
