@@ -456,3 +456,85 @@ def test_new_tensors_are_those_of_torch(short, monkeypatch):
     d = impl._here[0]
     assert d.empty((3,), torch.int64).shape == (3,) and d.empty((2, 0), F).shape == (2, 0)
     assert d.empty((2, 3, 5), F).stride() == (15, 5, 1)
+
+
+# ---- other ways to run a block -----------------------------------------------------------------------------------------
+def test_forward_passes_captured():
+    """a block's forward pass and its 8-bit form in graphs, replayed with other tokens and routes"""
+    blk = make()
+    served = ExpertsQ8(blk)
+    x, (idx, w) = rnd(1, 300, 128), routed(2, 300, 2, 5)
+
+    def both():
+        with torch.no_grad():
+            return blk(x, idx, w, residual=x), served(x, idx, w, residual=x)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for n in range(3):
+        x.copy_(rnd(20 + n, 300, 128))
+        i2, w2 = routed(30 + n, 300, 2, 5, dropped=(0.0, 1.0, 0.3)[n])
+        idx.copy_(i2), w.copy_(w2)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, both())), n
+
+
+def test_checkpointed_block_equals_the_block():
+    """under activation checkpointing the forward pass runs again before the steps: the same bits"""
+    from torch.utils.checkpoint import checkpoint
+
+    out = []
+    for again in (False, True):
+        blk = make(act="gelu")
+        x, r = rnd(1, 130, 128).requires_grad_(), rnd(2, 130, 128).requires_grad_()
+        idx, w = routed(3, 130, 2, 5)
+        w.requires_grad_()
+        y = checkpoint(blk, x, idx, w, r, use_reentrant=False) if again else blk(x, idx, w, r)
+        y.backward(rnd(4, 130, 128, std=1e-2))
+        assert blk.gate.step_count == blk.down.step_count == 1
+        out.append([y.detach(), x.grad, r.grad, w.grad, *stacks(blk), blk.up.m, blk.up.v])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_copied_and_restored_blocks():
+    """a deep copy, and a block that takes another's weights and moments, go on as the block itself"""
+    import copy
+
+    idx, w = routed(3, 70, 2, 5)
+    x, dy = rnd(1, 70, 128), rnd(4, 70, 128, std=1e-2)
+    blk = make(states="q8")
+    other = make(states="q8")
+    blk(x, idx, w).backward(dy)
+    two = copy.deepcopy(blk)
+    assert two.gate.step_count == 1
+    other.load_state_dict(blk.state_dict())
+    for s, o in ((blk.gate, other.gate), (blk.up, other.up), (blk.down, other.down)):
+        o._step_count = s.step_count
+    for b in (blk, two, other):
+        b(x, idx, w).backward(dy)
+    for s, *rest in zip(*[(b.gate, b.up, b.down) for b in (blk, two, other)]):
+        for o in rest:
+            assert torch.equal(s.weight, o.weight) and torch.equal(s.m, o.m) and torch.equal(s.v_scale, o.v_scale)
+
+
+def test_one_router_and_block_used_for_several_leading_dimensions():
+    """tokens in two dimensions with routing weights in bfloat16 or float64, gradients in their shapes and types"""
+    for dt in (BF, torch.float64):
+        blk = make()
+        x = rnd(1, 4, 9, 128).requires_grad_()
+        idx, w = routed(3, 36, 2, 5)
+        w = w.to(dt).reshape(4, 9, 2).requires_grad_()
+        y = blk(x, idx.reshape(4, 9, 2), w, residual=x)
+        y.backward(rnd(4, 4, 9, 128, std=1e-2))
+        assert y.shape == x.shape and x.grad.shape == x.shape and w.grad.shape == w.shape and w.grad.dtype == dt
+        flat = make()
+        x2, w2 = x.detach().reshape(36, 128).requires_grad_(), w.detach().float().reshape(36, 2).requires_grad_()
+        flat(x2, idx, w2, residual=x2).backward(rnd(4, 4, 9, 128, std=1e-2).reshape(36, 128))
+        assert torch.equal(x.grad.reshape(36, 128), x2.grad) and torch.equal(w.grad.reshape(36, 2), w2.grad.to(dt))
