@@ -468,6 +468,9 @@ int forge_expert_gated_dgrad(const forge_tensor* dY, const forge_tensor* Wd, con
                              forge_tensor* dG, forge_tensor* dU, forge_tensor* H, forge_stream_t stream);
 int forge_expert_dgrad_group(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,
                              const int64_t* offsets, forge_tensor* dX, forge_stream_t stream);
+/* Results that are operands of another product (H, dG, dU) are of the operands' type, which the matrix instructions take.
+ * So is each row of dX: half the bytes of float32 rows on the way to forge_expert_combine, for k + 1 roundings of a token's
+ * gradient instead of one (bfloat16: 0.0024 of it in the 2-norm, for 2 routes and for 8, against 0.0017). */
 /* The input gradient with a workspace, as forge_linear_dgrad_group_split: sum_out is the sum of the out_l of one expert. */
 int64_t forge_expert_dgrad_group_workspace(int64_t rows, int64_t in, int64_t sum_out, int32_t experts, int32_t dtype);
 int forge_expert_dgrad_group_split(int32_t n_layers, const forge_tensor* dY, const forge_tensor* W, int32_t experts,

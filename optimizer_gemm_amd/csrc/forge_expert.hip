@@ -156,8 +156,8 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const char* X, int64_t ld
 // ---- and back: Y[t] = sum_j w[t][j] Yp[pos[t][j]] + R[t] ----------------------
 // P: the type of Yp, T: that of the tokens' side (float32 sums may go with bfloat16 tokens). A lane holds the 16 bytes
 // of a P row at a time; the rows of up to eight routes are asked for before the first is used. Summed in float32 in
-// the order of the routes. 8191 tokens of 8 routes, 2048 bfloat16 columns (302 MB): 59 us,
-// 5.1 TB/s.
+// the order of the routes. 8191 tokens of 8 routes, 2048 bfloat16 columns (302 MB), by itself on three sets of rows in
+// turn: 58 us, 5.2 TB/s; right after its backward pass, whose results are still being written, 80 (both 178).
 template <class T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* X, int64_t ldx, 
 uint32_t row_blocks(int64_t rows, int lanes) { return (uint32_t)((rows * lanes + 255) / 256); }
 // Lanes of a row of so many 16-byte chunks: a wave's, or a workgroup's where a wave would go over it more than
 // twice and either that often that its loads wait for one another (8191 tokens of 8 routes, 256 chunks:
-// combination 59 us against 74), or the rows alone do not fill the chip.
+// combination by itself 59 us against 74), or the rows alone do not fill the chip.
 bool wide_rows(int64_t rows, int64_t chunks) { return chunks >= 256 || (chunks > 128 && rows < 4096); }
 // Of a row to quantise, which a wave holds in registers up to 512 chunks of: a workgroup's from there on or for few rows
 // (65528 rows of 256 chunks 78 us against 148).

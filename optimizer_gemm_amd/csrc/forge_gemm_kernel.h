@@ -1384,7 +1384,8 @@ hipError_t wgrad_fused_bf16_opt(int sf, int sr, const GArgs& g, const OptArgs& a
 // elements of one of 256x256 tiles and takes 0.5 to 0.75 of its time. AdamW with float32 moments, 256x256 and 128x128:
 // 44 experts of 16 rows, 704 -> 312 (2 rounds and 2) 90 us and 60; 8 of 3750, 1024 -> 1024 (1 and 1) 164 and 124; 5 of
 // 244, 128 -> 5840 (1 and 1) 51 and 28; but 8 of 951, 2024 -> 4936 (5 and 10) 488 and 646; 32 of 125, 1024 -> 512 (1 and 2)
-// 74 and 78.
+// 74 and 78. A tile's k range, one layer's rows, belongs to one workgroup: where tiles are few, or one layer has most rows,
+// its chain sets the time (8 of 3750 take 117 us where their bytes and products need 56; 6 of 1125, 272 -> 1320 40 and 13).
 template <class C>
 static int64_t g_rounds(const GArgs& g) {
   const int64_t resident = C::OCC * 4 / C::NW * g_num_cus();

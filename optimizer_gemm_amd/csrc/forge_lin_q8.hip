@@ -4,7 +4,7 @@
 // pairs, and a product takes half the stages of a bfloat16 one. The sums are integers until the epilogue, which
 // converts them and applies the two factors, so no tile or split changes a result's bits.
 // Measured: 8192 x 14336 -> 4096 with residual 333 us, 2890 TOP/s (bfloat16: 667 us, 1434); 777 x 4096 -> 2 x 14336
-// gated 104; 1 x 4096 -> 4096 10.4, of which the kernel takes 6.3. The choice of tiles is the bfloat16 products':
+// gated 104; 1 x 4096 -> 4096 6.3, 10.4 with the quantisation. The choice of tiles is the bfloat16 products':
 // within 5% of the best of them for 25 shapes from 1 x 4096 -> 4096 to 8192 x 14336 -> 4096, but for the one below.
 #include "forge_lin_kernel.h"
 

@@ -9,8 +9,8 @@
 // workgroup make 256 of them from a 4096-row layer, one per compute unit; the eight partial sums
 // are added in order through LDS.
 // Measured: 1 x 4096 -> 2 x 14336 gated 47.3 us for 235 MB, 5.0 TB/s, what a copy reaches (the
-// tiled kernel: 53); 1 x 4096 -> 4096 10.4 us, of which the kernel takes 8.4 and the rest is the
-// call (17). Up to 32 tokens, two fragments of 16.
+// tiled kernel: 53); 1 x 4096 -> 4096 9.4 us, of which the kernel takes 8.4 (17 with tiles). Up to
+// 32 tokens, two fragments of 16.
 // What it leaves to the tiles is measured at the choice between them.
 #include "forge_lin_kernel.h"
 

@@ -593,7 +593,8 @@ class _ExpertsFn(torch.autograd.Function):
     """y = r + sum_j w_j down_e(act(gate_e(x)) * up_e(x)) over a token's experts e. Kept for backward: the tokens,
     the routes, the projections G, U, and the experts' results (float32) where the routing weights want a gradient.
     Backward: the rows' gradients, dG, dU and H from their product with the down weights, dx of both projections -
-    all on the old weights - and then the steps."""
+    all on the old weights - and then the steps. Rounded to the stacks' type in between: H, dG, dU and the rows' gradients
+    as operands of products, and each route's dx, whose sum over a token's routes is float32 and rounded once more."""
 
     @staticmethod
     def forward(ctx, x, idx, w, r, wg, wu, wd, block, recorded, want_w):
