@@ -536,7 +536,9 @@ int32_t forge_expert_tile(int32_t product, int64_t rows, int64_t cols, int64_t k
       return q8 ? lin_q8_expert_edge(L_GATED, cols, rows, k, experts) : lin_expert_edge(L_GATED, false, cols, rows, k, experts);
     case FORGE_EXPERT_GATED_DGRAD: return q8 ? FORGE_ERR_DTYPE : lin_expert_edge(L_DGATE, true, cols, rows, k, experts);
     case FORGE_EXPERT_DGRAD: return q8 ? FORGE_ERR_DTYPE : lin_expert_edge(L_ACC, true, cols, rows, k, experts);
-    case FORGE_EXPERT_WGRAD: return q8 ? FORGE_ERR_DTYPE : wgrad_expert_edge(k, cols, experts);
+    case FORGE_EXPERT_WGRAD:
+      if (q8) return FORGE_ERR_DTYPE;
+      return k * cols * 4 < ((int64_t)1 << 31) ? wgrad_expert_edge(k, cols, experts) : FORGE_ERR_UNSUPPORTED;
     default: return FORGE_ERR_UNSUPPORTED;
   }
 }

@@ -411,6 +411,9 @@ def test_tiles_of_a_product():
         assert t(p, 16, 4096, 4096, 8, BF16) == 0 if p < 3 else t(p, 16, 4096, 4096, 8, BF16) > 0
     assert t(6, 16, 64, 64, 4, BF16) == UNSUP and t(-1, 16, 64, 64, 4, BF16) == UNSUP
     assert t(1, 16, 4096, 4096, 8, I8) == 0 and t(2, 16, 4096, 14336, 8, I8) > 0  # (gated over much memory: tiles)
+    assert t(5, 16, 1 << 29, 1 << 29, 4, BF16) == UNSUP and t(5, 16, 8192, 65536, 4, BF16) == UNSUP
+    # one row of tiles, half as wide but two a unit: as many rounds, so the small ones
+    assert t(5, 16, 0x1FFFFFFF, 1, 1024, BF16) == 128 and t(4, 16, 0x3FFFFFFF, 0x3FFFFFFF, 1024, BF16) > 0
     # the stack's gradient: two small rounds are taken for two large ones, five not for three
     assert t(5, 100, 128, 1920, 40, BF16) == 128 and t(5, 100, 1088, 1800, 17, BF16) == 256
 
